@@ -58,13 +58,15 @@ typedef enum {
 
 typedef enum {
     MOE_BF16 = 0,              /* BF16 operands, FP32 accumulate (blog post: "BF16 Standard") */
-    MOE_MXFP8_E4M3 = 1         /* OCP MXFP8: E4M3 elements, E8M0 scale per 32 along K */
+    MOE_MXFP8_E4M3 = 1,        /* OCP MXFP8: E4M3 elements, E8M0 scale per 32 along K */
+    MOE_MXFP4 = 2              /* weights in OCP MXFP4 (E2M1 elements, E8M0 scale per 32 along K),
+                                  activations in BF16, FP32 accumulate; inference */
 } moe_precision_t;
 
 /* path selection (moe_config_t.path) */
 #define MOE_PATH_AUTO 0        /* decode kernels when T*k <= 256 and inference, else prefill */
 #define MOE_PATH_PREFILL 1     /* grouped-GEMM path */
-#define MOE_PATH_DECODE 2      /* weight-streaming path; requires T*k <= 256, inference, BF16 */
+#define MOE_PATH_DECODE 2      /* weight-streaming path; requires T*k <= 256, inference, BF16 or MXFP4 */
 
 /* gated activation of the W13 output (moe_config_t.activation; nvfp4moe README,
  * "Supported kernel surface": SwiGLU, GeGLU and ReGLU FC1 epilogues): a = f(g) * u */
@@ -103,8 +105,10 @@ typedef struct {
 } moe_config_t;
 
 typedef struct {
-    const void* w13;          /* BF16 [E, 2I, d], or E4M3 codes (uint8) [E, 2I, d] */
-    const void* w2;           /* BF16 [E, d, I],  or E4M3 codes (uint8) [E, d, I]  */
+    const void* w13;          /* BF16 [E, 2I, d], or E4M3 codes (uint8) [E, 2I, d], or MXFP4 codes */
+    const void* w2;           /* BF16 [E, d, I],  or E4M3 codes (uint8) [E, d, I],  or MXFP4 codes */
+    /* MXFP4: w13, w2 and both scales are the four outputs of moe_prepare_weights, 16-byte
+     * aligned; NULL scales are MOE_ERR_INVALID_ARG */
     /* MXFP8 only (NULL for BF16): E8M0 scale bytes in the block-major layout that
      * moe_prepare_weights writes, uint8 [K/128, N, 4] with the expert matrices stacked
      * as N rows: w13_scale has N = E*2I rows of K = d, w2_scale N = E*d rows of K = I.
@@ -131,6 +135,9 @@ typedef struct {
  * experts, at most 131072 routed rows T*k; nvfp4moe README, "Limits"), choose
  * the kernels and lay out the workspace.  Host only: touches no device.
  * MXFP8 plans need d % 256 == 0 and I % 128 == 0 and run the grouped-GEMM path.
+ * MXFP4 plans need d % 128 == 0 and I % 128 == 0 and infer only, without mega; past
+ * T*k = 256 (or with path = MOE_PATH_PREFILL) each product's weights are first expanded to
+ * BF16 in the workspace (4 E I d bytes), within its stage, and the BF16 products run.
  * Shapes whose activations (T*d*2 bytes), routed intermediates (T*k*2I*2) or
  * per-expert W13 (2I*d*2) reach 2^31 bytes are refused (the kernels address them
  * with 32-bit offsets).  Returns MOE_ERR_UNSUPPORTED for shapes outside the limits,
@@ -198,10 +205,28 @@ moe_status_t moe_quantize_mxfp8(const void* v_bf16, int64_t rows, int32_t K,
  * N = E*2I rows of length K = d (w2: N = E*d rows of length K = I), the four
  * scale bytes of blocks 4g .. 4g+3 of row n are bytes [4 (g N + n), +4), i.e.
  * uint8 [K/128, N, 4] (E*2I*d/32 and E*d*I/32 bytes).  Needs d and I multiples
- * of 128 (else MOE_ERR_UNSUPPORTED).  Meant to run outside any timed region. */
+ * of 128 (else MOE_ERR_UNSUPPORTED).  Meant to run outside any timed region.
+ *
+ * On a plan with precision MOE_MXFP4 the same call quantizes to MXFP4 along K: per block of
+ * 32 the scale is the smallest power of two X with max|v| / X <= 6 (E8M0 byte clamped to
+ * [1, 254]), each element the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 to v / X with its sign,
+ * ties to the even code.  Weights that are such values already keep them exactly, so
+ * MXFP4 weights from elsewhere are brought in by way of BF16.  Outputs, 16-byte aligned:
+ * w13_q uint8 [E, I d], w2_q uint8 [E, d I / 2] (two elements a byte) and scales
+ * w13_s [E, 2I/16, ceil(d/512), 64, 4], w2_s [E, d/16, ceil(I/512), 64, 4], in the tile
+ * layout of the decode kernels: a tile is 16 rows x 128 of K, 1 KiB, its 16-byte piece
+ * 16 q + n the block 32 q .. 32 q + 31 of row n (element 2 i in the low half of byte i), the
+ * tiles of 16 rows one after another along K; byte j of scale word (tile row group, g, piece)
+ * is the scale of tile 4 g + j.  W13's tile b has gate rows 8 b .. 8 b + 7, then the same up
+ * rows; W2's tile b rows 16 b .. 16 b + 15.  Inputs are meant to be finite. */
 moe_status_t moe_prepare_weights(moe_plan_t plan, const void* w13_bf16, const void* w2_bf16,
                                  uint8_t* w13_q, uint8_t* w13_s, uint8_t* w2_q, uint8_t* w2_s,
                                  void* stream);
+
+/* The BF16 values of MXFP4 weights (exact): w13 [E, 2I, d] and w2 [E, d, I] from what
+ * moe_prepare_weights wrote on an MXFP4 plan (MOE_ERR_UNSUPPORTED on another). */
+moe_status_t moe_expand_weights(moe_plan_t plan, const moe_weights_t* w, void* w13_bf16, void* w2_bf16,
+                                void* stream);
 
 /* Prepare BF16 weights for the MXFP8 backward's input-gradient products (blog post,
  * "What it is selling": MXFP8 trains; each product quantizes its operands along its
@@ -290,6 +315,93 @@ moe_status_t moe_forward_routed(moe_plan_t plan, const void* x_rows, const int32
  * BF16 between kernels. */
 moe_status_t moe_backward(moe_plan_t plan, const void* dy, const void* x, const moe_weights_t* w,
                           void* dx, void* dw13, void* dw2, float* dscores, void* stream);
+
+/* ---- router: logits -> ids, scores, counts and balance loss, and the gradient -------------
+ * What makes the ids and scores that moe_forward takes.  With z = logits[t] [E] and
+ * s = softmax(z) or sigmoid(z), p_e = s_e / sum s (softmax: p = s):
+ *   ids[t]     the k experts of the largest key in descending order, ties to the lowest index.
+ *              The key is z_e, or with a selection bias s_e + bias_e (ordered as in 64 bits);
+ *              the bias changes the choice only, not the scores.
+ *   scores[t]  scale s_j, divided by the sum of the k chosen s with normalize = 1
+ *   counts_e   rows that chose e;  prob_sums_e = sum_t p_te;  N = sum counts / k
+ *   loss       balance_coef E / (k N^2) sum_e counts_e prob_sums_e   (0 when N = 0)
+ * mask (uint8 [T], or NULL): rows with 0 are padding.  They get ids 0 .. k-1 (valid for
+ * moe_forward) and scores 0, count nowhere, and get zero gradients.
+ * Logits of -inf are never chosen before others and score 0; a row of -inf alone scores 0.
+ * A NaN logit is chosen last, and makes the row's softmax (with sigmoid: its own score and the
+ * row's p) NaN; so does +inf with softmax.
+ * Stateless: a config, caller-owned buffers and a workspace that holds nothing between calls;
+ * calls that overlap need a workspace each. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct {
+    int32_t T;             /* rows of logits, >= 0 */
+    int32_t E;             /* experts, 1..256 */
+    int32_t k;             /* experts per token, 1..min(E, 32) */
+    int32_t score;         /* MOE_SCORE_* */
+    int32_t normalize;     /* 1: the chosen scores are divided by their sum */
+    int32_t logits_f32;    /* 1: logits and dlogits FP32, 0: BF16 */
+    float scale;           /* factor on the scores, finite */
+    float balance_coef;    /* factor of the balance loss, finite */
+} moe_router_config_t;
+
+/* Bytes of workspace that moe_router_forward needs for counts, prob_sums or loss; 0 for an
+ * invalid config. */
+size_t moe_router_workspace_bytes(const moe_router_config_t* cfg);
+
+/* logits [T, E]; bias f32 [E] or NULL; ids int32 [T, k]; scores f32 [T, k]; counts int32 [E],
+ * prob_sums f32 [E] and loss f32 [1], each of which may be NULL (all three: no workspace is
+ * needed).  Sums have a fixed order: the same call gives the same bits. */
+moe_status_t moe_router_forward(const moe_router_config_t* cfg, const void* logits, const float* bias,
+                                const uint8_t* mask, int32_t* ids, float* scores, int32_t* counts,
+                                float* prob_sums, float* loss, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* dlogits [T, E] (overwritten, the logits' type) from dscores f32 [T, k] (as moe_backward
+ * writes it; NULL: zeros) and dloss f32 [1] on the device, the gradient of the loss (NULL: the
+ * loss has none; then counts may be NULL).  ids as the forward gave them; entries outside
+ * [0, E) are left out.  counts may be summed over several batches or ranks: the loss is then
+ * that of all their rows.  The choice of experts, and so counts, is taken as constant. */
+moe_status_t moe_router_backward(const moe_router_config_t* cfg, const float* dscores, const void* logits,
+                                 const uint8_t* mask, const int32_t* ids, const int32_t* counts,
+                                 const float* dloss, void* dlogits, void* stream);
+
+/* ---- norms before and after the layer, with its gate and residual ------------------------
+ *   n = y, or with w_post  y / sqrt(mean_c y^2 + eps) * w_post
+ *   z = x + residual_scale * gate * n        (gate: 1, f32 [d] or f32 [T])
+ *   h = z / sqrt(mean_c z^2 + eps) * w_pre   (z as stored; the next block's input)
+ * One pass over memory.  x, z, dz, dx are the residual stream, BF16 or FP32; y, h and their
+ * gradients BF16; w_post, w_pre and the channel gate FP32 [d].  Sums and statistics in FP32.
+ * Device pointers are 16-byte aligned (a gate per token 4-byte). */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN 2
+typedef struct {
+    int32_t T;              /* rows, >= 0 */
+    int32_t d;              /* channels: a multiple of 8, at most 16384 */
+    int32_t gate;           /* MOE_GATE_* */
+    int32_t residual_f32;   /* 1: x, z, dz, dx FP32, 0: BF16 */
+    float eps;              /* a positive normal float */
+    float residual_scale;   /* finite */
+} moe_norm_config_t;
+
+/* Bytes of workspace that moe_norm_backward needs; 0 for an invalid config. */
+size_t moe_norm_workspace_bytes(const moe_norm_config_t* cfg);
+
+/* y NULL: only h = norm(x) (w_post, gate and z NULL).  w_pre and h NULL: only z.  gate is NULL
+ * exactly with MOE_GATE_NONE.  z may be x. */
+moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const void* y, const float* w_post,
+                              const float* gate, const float* w_pre, void* z, void* h, void* stream);
+
+/* dx, dy (of x and y) and the parameters' gradients (FP32, overwritten; each NULL exactly when
+ * its parameter is) from dz, the gradient that reaches z by way of the stream (NULL: none, with
+ * w_pre only), and dh.  z is the forward's (x where y is NULL; read with w_pre only, and may be
+ * NULL without).  y NULL: dx is the gradient of x and dy NULL.  dx may be dz.  Sums over tokens
+ * have a fixed order. */
+moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, const void* dz, const void* dh, const void* z,
+                               const void* y, const float* w_post, const float* gate, const float* w_pre,
+                               void* dx, void* dy, float* dw_post, float* dgate, float* dw_pre,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronise `stream`, copy the sticky device status word (MOE_DEV_* bits)
  * into *device_flags, and clear it when `clear` is non-zero.  Returns

@@ -119,6 +119,14 @@ __device__ __forceinline__ uint32_t e8m0_scale(float amax) {
     return (uint32_t)b;
 }
 
+// The same for E2M1 elements (largest 6) from BF16 magnitude bits: with max = m 2^e, m in
+// [1, 2), the exponent is e - 2, or e - 1 when m > 1.5; clamped to [1, 254], so that the scale
+// is a normal float (a block of zeros has scale 2^-126 and zero codes)
+__device__ __forceinline__ int e8m0_scale_e2m1(uint32_t mag) {
+    const int b = (int)(mag >> 7) - 2 + ((mag & 0x7Fu) > 0x40u ? 1 : 0);
+    return b < 1 ? 1 : (b > 254 ? 254 : b);
+}
+
 // Streaming (non-temporal) store of 16 bytes, for whole-line outputs no nearby kernel
 // reads back from cache: written through L2 as ordinary stores, they evict operand
 // lines the other workgroups of the XCD are still reading.

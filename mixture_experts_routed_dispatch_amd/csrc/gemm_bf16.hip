@@ -1101,7 +1101,26 @@ hipError_t launch_mode(const GemmArgs& g, int num_cu, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_gemm(GemmMode mode, const GemmArgs& g, int num_cu, hipStream_t s) {
+// MXFP4 weights run as BF16 ones: the matrix of the product is expanded (exactly) into
+// g.expanded first, which the next product reuses.
+static hipError_t expand_for(GemmMode mode, GemmArgs& g, hipStream_t s) {
+    const bool w13 = mode == FWD_W13;
+    if (!w13 && mode != FWD_W2) return hipErrorInvalidValue;
+    const hipError_t e =
+        w13 ? launch_mxfp4_expand(reinterpret_cast<const uint8_t*>(g.w13), g.w13_scale, g.E, 2 * g.I, g.d, g.I, true, g.expanded, s)
+            : launch_mxfp4_expand(reinterpret_cast<const uint8_t*>(g.w2), g.w2_scale, g.E, g.d, g.I, g.I, false, g.expanded, s);
+    if (w13) g.w13 = g.expanded;
+    else g.w2 = g.expanded;
+    g.w13_scale = g.w2_scale = nullptr;
+    return e;
+}
+
+hipError_t launch_gemm(GemmMode mode, const GemmArgs& args, int num_cu, hipStream_t s) {
+    GemmArgs g = args;
+    if (g.w13_scale) {
+        const hipError_t e = expand_for(mode, g, s);
+        if (e != hipSuccess) return e;
+    }
     switch (mode) {
         case FWD_W13: return launch_mode<FWD_W13>(g, num_cu, s);
         case FWD_W2: return launch_mode<FWD_W2>(g, num_cu, s);

@@ -54,6 +54,11 @@ struct GemmArgs {
     // (dy W2)[r][i] a[r][i]
     float* ds_part;
     int ds_slots;
+    // forward with MXFP4 weights (w13, w2 are codes): the scales, and room for the product's
+    // matrix as BF16, which is expanded there first
+    const uint8_t* w13_scale;
+    const uint8_t* w2_scale;
+    uint16_t* expanded;
 };
 
 // Pieces of split weight-gradient tiles in one launch (sizes their FP32 partial sums).
@@ -167,6 +172,8 @@ struct DecodeArgs {
     uint16_t* y;           // [T, d]
     int32_t* status;       // sticky routing flags
     int act;               // gated activation of decode W13
+    const uint8_t* w13_scale;  // MXFP4 weights only: w13 and w2 are codes (mxfp4.hip's layout)
+    const uint8_t* w2_scale;
 };
 
 hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
@@ -181,6 +188,18 @@ hipError_t launch_decode_w2_one(const DecodeArgs& g, int num_cu, hipStream_t s);
 int mega_chunk(int T, int k);
 hipError_t launch_mega_decode(const DecodeArgs& g, float* part, int num_cu, hipStream_t s);
 
+// MXFP4 weights (E2M1 codes, E8M0 scale per 32 along K) in the layout of the decode kernels,
+// from and to BF16 [E, N, K]; w13: N = 2I with gate and up rows interleaved by 8 in the tiles.
+// K a multiple of 128, N of 16 (w13: I of 8).
+hipError_t launch_mxfp4_pack(const uint16_t* w, int E, int N, int K, int I, bool w13, uint8_t* codes,
+                             uint8_t* scales, hipStream_t s);
+hipError_t launch_mxfp4_expand(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, int I, bool w13,
+                               uint16_t* w, hipStream_t s);
+// Decode with MXFP4 weights: W13 with the activation; W2 (into o; for one token with the
+// combine into y)
+hipError_t launch_decode4_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
+hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
+
 // block_major: scale word (g, row) (bytes of blocks 4 g .. 4 g + 3) at (g * rows + row) * 4
 // (K a multiple of 128); else scales [rows, K/32].
 // rows_dev (optional, device): convert only the first min(rows, *rows_dev) rows; the
@@ -192,6 +211,75 @@ hipError_t launch_quantize_mxfp8(const uint16_t* v, int64_t rows, int K, uint8_t
 // [rows, K/32] scales; K a multiple of 128; gather entries outside [0, rows) read row 0
 hipError_t launch_route_scales(const uint8_t* scales, int64_t rows, const int32_t* gather, int64_t R,
                                int K, uint8_t* out, hipStream_t s);
+
+// Router (router.hip): logits [T, E] (FP32 or BF16), E <= 256, k <= kMaxTopK.
+constexpr int kRouterBlocks = 256;     // workgroups, at most: rows of partial counts and sums
+struct RouterArgs {
+    int T, E, k, normalize;
+    float scale, coef;
+    const void* logits;
+    const float* bias;        // [E], or NULL: the key is the logit
+    const uint8_t* mask;      // [T], 0 leaves a row out; or NULL
+    int32_t* ids;             // [T, k]
+    float* scores;            // [T, k]
+    int32_t* counts;          // [E], each of the three may be NULL
+    float* psum;              // [E]
+    float* loss;              // [1]
+    int32_t* part_counts;     // [blocks, E rounded up to 4], or NULL: no counts, sums and loss
+    float* part_sums;
+    int vec, stride;          // set by the launcher
+};
+int router_blocks(int64_t T);
+hipError_t launch_route(RouterArgs g, bool sigmoid, bool f32, hipStream_t s);
+
+struct RouterGradArgs {
+    int T, E, k, normalize;
+    float scale, coef;
+    const void* logits;
+    const uint8_t* mask;      // [T] or NULL
+    const int32_t* ids;       // [T, k]; entries outside [0, E) are left out
+    const float* dscores;     // [T, k] or NULL: zeros
+    const int32_t* counts;    // [E], read when dloss is given
+    const float* dloss;       // [1] or NULL: no balance loss
+    void* dlogits;            // [T, E], the logits' type
+    int vec;                  // set by the launcher
+};
+hipError_t launch_route_grad(RouterGradArgs g, bool sigmoid, bool f32, hipStream_t s);
+
+// Norms around the block (norm.hip): d a multiple of 8, at most kNormMaxD.
+constexpr int kNormMaxD = 16384;
+constexpr int kNormBlocks = 256;       // workgroups of the backward, at most: rows of partial sums
+constexpr int kGateNone = 0, kGateChannel = 1, kGateToken = 2;
+struct NormArgs {
+    int T, d, gate_kind;
+    float eps, alpha;
+    const void* x;            // [T, d] residual stream (BF16 or FP32)
+    const uint16_t* y;        // [T, d] block output, or NULL
+    const float* w_post;      // [d] or NULL: y as it is
+    const float* gate;        // [d] or [T]
+    const float* w_pre;       // [d] or NULL: no h
+    void* z;                  // [T, d] (NULL without y); may be x
+    uint16_t* h;              // [T, d]
+};
+hipError_t launch_norm(const NormArgs& g, bool f32, int num_cu, hipStream_t s);
+struct NormGradArgs {
+    int T, d, gate_kind;
+    float eps, alpha;
+    const void* dz;           // [T, d] or NULL: zeros
+    const uint16_t* dh;       // [T, d], read with w_pre
+    const void* z;            // [T, d], read with w_pre
+    const uint16_t* y;        // [T, d] or NULL
+    const float* w_post;
+    const float* gate;
+    const float* w_pre;
+    void* dx;                 // [T, d]; may be dz
+    uint16_t* dy;
+    float* dw_post;           // [d]
+    float* dgate;             // [d] or [T]
+    float* dw_pre;            // [d]
+    float* part;              // [kNormBlocks, 3, d] partial column sums
+};
+hipError_t launch_norm_grad(const NormGradArgs& g, bool f32, hipStream_t s);
 
 // Scratch for moe_forward_static: one array of kStaticScratchBytes per device (the size
 // moe.h states as MOE_STATIC_SCRATCH_BYTES).  static_scratch returns the current device's

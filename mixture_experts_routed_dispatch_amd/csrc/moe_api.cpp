@@ -15,77 +15,19 @@
 
 #include "../../include/moe.h"
 #include "kernels.h"
+#include "plan.h"
 
 using namespace moe;
 
 namespace {
 
 constexpr int64_t kMaxRoutedRows = 131072;   // nvfp4moe README, "Limits"
-constexpr int kMaxExperts = 256;             // nvfp4moe README, "Limits"
-constexpr size_t kMaxProfileRecords = 4096;
 // the status region: the sticky device flags (cleared when a workspace is bound)
 constexpr int kStatusWords = 1;
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
-
-struct moe_plan_s {
-    moe_config_t cfg;
-    int64_t R;
-    bool decode;
-    // workspace offsets (bytes)
-    size_t off_status, off_m_indptr, off_gather, off_slots, off_probs;
-    size_t off_a, off_o, off_h, off_dh, off_dxp, off_xg, off_dys, off_xq, off_xs, off_xsr, off_aq, off_as;
-    // MXFP8 backward: dO and (dg, du) quantized along d and 2I (codes, block-major scales), and
-    // the weight-gradient operands in the token layout (P and Q codes and scales)
-    size_t off_doq, off_dos, off_dhq, off_dhs, off_tp, off_tps, off_tq, off_tqs;
-    size_t tp_feat, tq_feat;           // features of the largest P / Q token-layout operand
-    int64_t ntok;                      // token-layout rows: T*k + 128 E
-    size_t off_part, off_split;        // split weight-gradient tiles: partial sums, descriptors
-    size_t off_mega;                   // mega decode: FP32 partial expert outputs [T*k, I / chunk, d]
-    size_t ws_bytes;
-    char* ws;
-    size_t ws_size;
-    int num_cu;
-    bool have_saved_forward;
-    bool h_aliased;                    // recompute_h: h occupies the dxp / xg / dys region
-    bool dh_aliased;                   // BF16 training: dh occupies o's region (see below)
-    int32_t* status_word;              // device status word of the last call (workspace or static scratch)
-    // measurement-only event pairs around kernel stages (moe_profile)
-    struct ProfRec { int stage; hipEvent_t a, b; };
-    bool prof_on = false;
-    std::vector<hipEvent_t> ev_free;
-    std::vector<ProfRec> recs;
-
-    template <class T> T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
-
-    hipEvent_t take_event() {
-        hipEvent_t e = nullptr;
-        if (!ev_free.empty()) { e = ev_free.back(); ev_free.pop_back(); return e; }
-        if (hipEventCreate(&e) != hipSuccess) return nullptr;
-        return e;
-    }
-    // returns a record index, or -1 when not recording
-    int stage_begin(int stage, hipStream_t s) {
-        if (!prof_on || recs.size() >= kMaxProfileRecords) return -1;
-        ProfRec r{stage, take_event(), take_event()};
-        if (!r.a || !r.b || hipEventRecord(r.a, s) != hipSuccess) {
-            if (r.a) ev_free.push_back(r.a);
-            if (r.b) ev_free.push_back(r.b);
-            return -1;
-        }
-        recs.push_back(r);
-        return (int)recs.size() - 1;
-    }
-    void stage_end(int idx, hipStream_t s) {
-        if (idx >= 0) (void)hipEventRecord(recs[(size_t)idx].b, s);
-    }
-    ~moe_plan_s() {
-        for (auto& r : recs) { (void)hipEventDestroy(r.a); (void)hipEventDestroy(r.b); }
-        for (auto e : ev_free) (void)hipEventDestroy(e);
-    }
-};
 
 namespace {
 // launch `fn` as one profiled stage
@@ -222,7 +164,8 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     *out = nullptr;
     const moe_config_t c = *cfg;
     if (c.T < 0 || c.d <= 0 || c.I <= 0 || c.E <= 0 || c.k <= 0) return MOE_ERR_INVALID_ARG;
-    if (c.precision != MOE_BF16 && c.precision != MOE_MXFP8_E4M3) return MOE_ERR_INVALID_ARG;
+    if (c.precision != MOE_BF16 && c.precision != MOE_MXFP8_E4M3 && c.precision != MOE_MXFP4)
+        return MOE_ERR_INVALID_ARG;
     if (c.training != 0 && c.training != 1) return MOE_ERR_INVALID_ARG;
     if (c.wgrad_accumulate != 0 && c.wgrad_accumulate != 1) return MOE_ERR_INVALID_ARG;
     if (c.wgrad_accumulate && !c.training) return MOE_ERR_UNSUPPORTED;
@@ -237,6 +180,9 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     if (R > kMaxRoutedRows) return MOE_ERR_UNSUPPORTED;
     // MXFP8 kernels take K in stages of 64 codes and P tiles of 256 rows
     if (c.precision == MOE_MXFP8_E4M3 && (c.d % 256 != 0 || c.I % 128 != 0)) return MOE_ERR_UNSUPPORTED;
+    // MXFP4 weights come in tiles of 128 along K and serve inference only
+    const bool w4 = c.precision == MOE_MXFP4;
+    if (w4 && (c.training || c.d % 128 != 0 || c.I % 128 != 0)) return MOE_ERR_UNSUPPORTED;
     // MXFP8 weight gradients address a token-layout operand (features x padded rows) with
     // 32-bit offsets
     if (c.precision == MOE_MXFP8_E4M3 && c.training &&
@@ -248,11 +194,11 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
         return MOE_ERR_UNSUPPORTED;
     // small-batch inference runs the weight-streaming kernels (nvfp4moe README,
     // "MoE layer": batch-one and small-batch decode get their own launch grid)
-    const bool decode_ok = c.training == 0 && c.precision == MOE_BF16 && R > 0 &&
+    const bool decode_ok = c.training == 0 && (c.precision == MOE_BF16 || w4) && R > 0 &&
                            R <= kMaxDecodeRows;
     if (c.path == MOE_PATH_DECODE && !decode_ok) return MOE_ERR_UNSUPPORTED;
     if (c.mega != 0 && c.mega != 1) return MOE_ERR_INVALID_ARG;
-    if (c.mega && (!decode_ok || c.path == MOE_PATH_PREFILL)) return MOE_ERR_UNSUPPORTED;
+    if (c.mega && (!decode_ok || w4 || c.path == MOE_PATH_PREFILL)) return MOE_ERR_UNSUPPORTED;
 
     moe_plan_s* p = new (std::nothrow) moe_plan_s();
     if (!p) return MOE_ERR_INVALID_ARG;
@@ -322,6 +268,8 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     p->off_split = take(sizeof(int32_t) * 4 * (kMaxPieces / 2 + 1));
     p->off_part = gemms && c.training ? take(kGemmPartBytes) : 0;
     p->off_mega = c.mega ? take(sizeof(float) * (size_t)R * (c.I / mega_chunk(c.T, c.k)) * c.d) : 0;
+    const bool expand = w4 && !p->decode;
+    p->off_we = expand ? take(2 * (size_t)c.E * 2 * c.I * c.d) : 0;
     p->ws_bytes = off;
     p->ws = nullptr;
     p->ws_size = 0;
@@ -347,7 +295,7 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
         out += line;
     };
     add("moe plan: T=%d d=%d I=%d E=%d k=%d, %lld routed rows (T*k), %s, %s, %s path\n", c.T, c.d, c.I, c.E,
-        c.k, (long long)R, mx ? "MXFP8 E4M3" : "BF16", c.training ? "training" : "inference",
+        c.k, (long long)R, mx ? "MXFP8 E4M3" : c.precision == MOE_MXFP4 ? "MXFP4 weights" : "BF16", c.training ? "training" : "inference",
         p->decode ? (c.mega ? "decode (weight-streaming, mega: one fused launch)" : "decode (weight-streaming)")
                   : "grouped-GEMM");
     if (c.training)
@@ -418,6 +366,9 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
     if (c.mega)
         region("mega", sizeof(float) * (size_t)R * (c.I / mega_chunk(c.T, c.k)) * c.d, "scratch",
                "mega decode: FP32 partial expert outputs [T*k, I/chunk, d]");
+    if (c.precision == MOE_MXFP4 && !p->decode)
+        region("we", 2 * (size_t)c.E * 2 * c.I * c.d, "scratch",
+               "the weights of a product expanded to BF16: W13 [E, 2I, d], then W2 [E, d, I]");
     if (gemms && c.training)
         region("part", kGemmPartBytes, "backward", "FP32 partial sums of split weight-gradient tiles");
     add("kept from the training forward for the backward: %zu bytes (%.1f MiB)\n", saved, saved / 1048576.0);
@@ -476,22 +427,6 @@ moe_status_t moe_quantize_mxfp8(const void* v, int64_t rows, int32_t K, uint8_t*
     return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
-moe_status_t moe_prepare_weights(moe_plan_t p, const void* w13, const void* w2, uint8_t* w13_q,
-                                 uint8_t* w13_s, uint8_t* w2_q, uint8_t* w2_s, void* stream) {
-    if (!p || !w13 || !w2 || !w13_q || !w13_s || !w2_q || !w2_s) return MOE_ERR_INVALID_ARG;
-    const moe_config_t& c = p->cfg;
-    if (c.d % 128 != 0 || c.I % 128 != 0) return MOE_ERR_UNSUPPORTED;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    // block-major scales (the layout the MXFP8 GEMMs copy from)
-    if (launch_quantize_mxfp8(static_cast<const uint16_t*>(w13), (int64_t)c.E * 2 * c.I, c.d, w13_q, w13_s,
-                              true, s) != hipSuccess)
-        return MOE_ERR_HIP;
-    if (launch_quantize_mxfp8(static_cast<const uint16_t*>(w2), (int64_t)c.E * c.d, c.I, w2_q, w2_s, true,
-                              s) != hipSuccess)
-        return MOE_ERR_HIP;
-    return MOE_OK;
-}
-
 moe_status_t moe_prepare_weights_backward(moe_plan_t p, const void* w13, const void* w2, uint8_t* w13t_q,
                                           uint8_t* w13t_s, uint8_t* w2t_q, uint8_t* w2t_s, void* stream) {
     if (!p || !w13 || !w2 || !w13t_q || !w13t_s || !w2t_q || !w2t_s) return MOE_ERR_INVALID_ARG;
@@ -513,7 +448,8 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
     if (!p || !w) return MOE_ERR_INVALID_ARG;
     const moe_config_t& c = p->cfg;
     if (c.T > 0 && (!x || !ids || !scores || !y || !w->w13 || !w->w2)) return MOE_ERR_INVALID_ARG;
-    if (c.T > 0 && c.precision == MOE_MXFP8_E4M3 && (!w->w13_scale || !w->w2_scale))
+    const bool w4 = c.precision == MOE_MXFP4;
+    if (c.T > 0 && (w4 || c.precision == MOE_MXFP8_E4M3) && (!w->w13_scale || !w->w2_scale))
         return MOE_ERR_INVALID_ARG;
     if (!p->ws) return MOE_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -535,6 +471,10 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         dg.o = p->at<uint16_t>(p->off_o);
         dg.y = static_cast<uint16_t*>(y);
         dg.status = p->at<int32_t>(p->off_status);
+        if (w4) {
+            dg.w13_scale = w->w13_scale;
+            dg.w2_scale = w->w2_scale;
+        }
         if (c.mega) {
             hipError_t e = staged(p, MOE_STAGE_MEGA, s, [&] {
                 return launch_mega_decode(dg, p->at<float>(p->off_mega), p->num_cu, s);
@@ -614,6 +554,11 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
     g.x = static_cast<const uint16_t*>(x);
     g.w13 = static_cast<const uint16_t*>(w->w13);
     g.w2 = static_cast<const uint16_t*>(w->w2);
+    if (w4) {
+        g.w13_scale = w->w13_scale;
+        g.w2_scale = w->w2_scale;
+        g.expanded = p->at<uint16_t>(p->off_we);
+    }
     g.out = p->at<uint16_t>(p->off_a);
     g.out_h = (c.training && !c.recompute_h) ? p->at<uint16_t>(p->off_h) : nullptr;
     e = staged(p, MOE_STAGE_W13, s, [&] { return launch_gemm(FWD_W13, g, p->num_cu, s); });
@@ -663,7 +608,8 @@ moe_status_t moe_forward_routed(moe_plan_t p, const void* x_rows, const int32_t*
     if (c.training || p->decode) return MOE_ERR_UNSUPPORTED;
     if (p->R * c.d * 2 >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;   // 32-bit row offsets into x_rows
     if (c.T > 0 && (!x_rows || !m_indptr || !out || !w->w13 || !w->w2)) return MOE_ERR_INVALID_ARG;
-    if (c.T > 0 && mx && (!w->w13_scale || !w->w2_scale)) return MOE_ERR_INVALID_ARG;
+    const bool w4 = c.precision == MOE_MXFP4;
+    if (c.T > 0 && (mx || w4) && (!w->w13_scale || !w->w2_scale)) return MOE_ERR_INVALID_ARG;
     if (!p->ws) return MOE_ERR_WORKSPACE;
     p->have_saved_forward = false;
     p->status_word = p->at<int32_t>(p->off_status);
@@ -710,6 +656,11 @@ moe_status_t moe_forward_routed(moe_plan_t p, const void* x_rows, const int32_t*
     g.x = static_cast<const uint16_t*>(x_rows);
     g.w13 = static_cast<const uint16_t*>(w->w13);
     g.w2 = static_cast<const uint16_t*>(w->w2);
+    if (w4) {
+        g.w13_scale = w->w13_scale;
+        g.w2_scale = w->w2_scale;
+        g.expanded = p->at<uint16_t>(p->off_we);
+    }
     g.out = p->at<uint16_t>(p->off_a);
     e = staged(p, MOE_STAGE_W13, s, [&] { return launch_gemm(FWD_W13, g, p->num_cu, s); });
     if (e != hipSuccess) return MOE_ERR_HIP;

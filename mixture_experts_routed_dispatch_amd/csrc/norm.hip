@@ -1,0 +1,359 @@
+// norm.hip -- the norms before and after the routed expert layer with its gate and residual,
+// forward and backward, on gfx950.
+//
+//   n = y                                  or  y q w_post,  q = 1 / sqrt(mean_c y^2 + eps)
+//   z = x + alpha gate n                   (gate: 1, one a channel or one a token)
+//   h = z r w_pre,                         r = 1 / sqrt(mean_c z^2 + eps), z as stored
+// one pass over the rows: x and y are read once, z and h written once.  Backward, from the
+// gradients dz (of z by way of the stream) and dh:
+//   G  = dz + r (w_pre dh) - z r^3 mean_c(w_pre dh z),         dx = G
+//   dn = alpha gate G,     dgate = sum (over tokens or channels) alpha G n
+//   dy = q (w_post dn) - y q^3 mean_c(w_post dn y)             (dn itself without w_post)
+//   dw_pre = sum_t dh z r,  dw_post = sum_t dn y q
+// G is not rounded between the two norms.  r and q are computed again from z and y, which the
+// backward reads anyway: their sums ride along in the first of a row's two reductions.
+//
+// A row belongs to kW waves, each lane with kC pieces of 8 channels (16 bytes of BF16), so
+// that it stays in registers between the reductions; kW is the fewest waves that hold d.  The
+// vectors over channels are loaded once per workgroup, which walks several rows.  Memory
+// bound: the least traffic is 4 (forward) and 6 (backward) passes over [T, d].
+#include <type_traits>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+struct Vec8 { float v[8]; };
+
+__device__ __forceinline__ Vec8 ld8(const uint16_t* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    return {{bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y), bf16lo(u.z), bf16hi(u.z), bf16lo(u.w), bf16hi(u.w)}};
+}
+__device__ __forceinline__ Vec8 ld8(const float* p) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+    return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+}
+// rounds to the stored type and returns the stored values
+__device__ __forceinline__ Vec8 st8(uint16_t* p, const Vec8& x) {
+    const uint4 u = make_uint4(pack_bf16(x.v[0], x.v[1]), pack_bf16(x.v[2], x.v[3]), pack_bf16(x.v[4], x.v[5]),
+                               pack_bf16(x.v[6], x.v[7]));
+    *reinterpret_cast<uint4*>(p) = u;
+    return {{bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y), bf16lo(u.z), bf16hi(u.z), bf16lo(u.w), bf16hi(u.w)}};
+}
+__device__ __forceinline__ Vec8 st8(float* p, const Vec8& x) {
+    const f32x4_t a = {x.v[0], x.v[1], x.v[2], x.v[3]}, b = {x.v[4], x.v[5], x.v[6], x.v[7]};
+    *reinterpret_cast<f32x4_t*>(p) = a;
+    *reinterpret_cast<f32x4_t*>(p + 4) = b;
+    return x;
+}
+__device__ __forceinline__ Vec8 ld8_or(const float* p, int c, bool in, float other) {
+    if (p && in) return ld8(p + c);
+    return {{other, other, other, other, other, other, other, other}};
+}
+__device__ __forceinline__ Vec8 zero8() { return {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}}; }
+
+__device__ __forceinline__ float wave_sum(float v) {
+    auto ror = [](float x, auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value,
+                                                                     0xF, 0xF, true));
+    };
+    v += ror(v, std::integral_constant<int, 0x128>());
+    v += ror(v, std::integral_constant<int, 0x124>());
+    v += ror(v, std::integral_constant<int, 0x122>());
+    v += ror(v, std::integral_constant<int, 0x121>());
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
+// kN sums over the kW waves of a row, in wave order.  One barrier: `red` has two halves used
+// in turn, and a half is written again only after the barrier of the reduction in between.
+template <int kN, int kW, int kGroups>
+__device__ __forceinline__ void row_sums(float (&v)[kN], float (*red)[kGroups][kW][kN], int& half) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = wave_sum(v[i]);
+    if constexpr (kW > 1) {
+        const int w = (threadIdx.x >> 6) % kW, grp = (threadIdx.x >> 6) / kW;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < kN; ++i) red[half][grp][w][i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            v[i] = red[half][grp][0][i];
+#pragma unroll
+            for (int u = 1; u < kW; ++u) v[i] += red[half][grp][u][i];
+        }
+        half ^= 1;
+    }
+}
+
+constexpr int kFwdThreads = 256;
+template <typename TRes, int kW, int kC>
+__global__ __launch_bounds__(64 * kW > kFwdThreads ? 64 * kW : kFwdThreads) void norm_kernel(NormArgs g) {
+    constexpr int kThr = 64 * kW > kFwdThreads ? 64 * kW : kFwdThreads;
+    constexpr int kGroups = kThr / (64 * kW);
+    __shared__ float red[2][kGroups][kW][1];
+    int half = 0;
+    const int grp = threadIdx.x / (64 * kW), lt = threadIdx.x % (64 * kW);
+    const int d = g.d;
+    const float inv_d = 1.0f / (float)d;
+    const TRes* x = static_cast<const TRes*>(g.x);
+    TRes* z = static_cast<TRes*>(g.z);
+    Vec8 wa[kC], wp[kC];                               // alpha gate w_post, w_pre
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const int col = 8 * (lt + c * 64 * kW);
+        const bool in = col < d;
+        wa[c] = ld8_or(g.w_post, col, in, 1.0f);
+        const Vec8 gt = ld8_or(g.gate_kind == kGateChannel ? g.gate : nullptr, col, in, 1.0f);
+        wp[c] = ld8_or(g.w_pre, col, in, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wa[c].v[i] *= g.alpha * gt.v[i];
+    }
+    for (int64_t t0 = (int64_t)blockIdx.x * kGroups; t0 < g.T; t0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t t = t0 + grp;
+        const bool row = t < g.T;                       // groups past T only take part in barriers
+        Vec8 xv[kC], yv[kC];
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int col = 8 * (lt + c * 64 * kW);
+            const bool in = row && col < d;
+            xv[c] = in ? ld8(x + t * d + col) : zero8();
+            yv[c] = in && g.y ? ld8(g.y + t * d + col) : zero8();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss[0] += yv[c].v[i] * yv[c].v[i];
+        }
+        float f = 1.0f;
+        if (g.w_post) {
+            row_sums<1, kW, kGroups>(ss, red, half);
+            f = __builtin_amdgcn_rsqf(ss[0] * inv_d + g.eps);
+        }
+        if (g.gate_kind == kGateToken && row) f *= g.gate[t];
+        float sz[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int col = 8 * (lt + c * 64 * kW);
+            if (g.y) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[c].v[i] += yv[c].v[i] * f * wa[c].v[i];
+                if (row && col < d) xv[c] = st8(z + t * d + col, xv[c]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sz[0] += xv[c].v[i] * xv[c].v[i];
+        }
+        if (g.w_pre) {
+            row_sums<1, kW, kGroups>(sz, red, half);
+            const float r = __builtin_amdgcn_rsqf(sz[0] * inv_d + g.eps);
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int col = 8 * (lt + c * 64 * kW);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[c].v[i] *= r * wp[c].v[i];
+                if (row && col < d) st8(g.h + t * d + col, xv[c]);
+            }
+        }
+    }
+}
+
+constexpr int kBwdThreads = 1024;
+template <typename TRes, int kW, int kC>
+__global__ __launch_bounds__(kBwdThreads) void norm_grad_kernel(NormGradArgs g) {
+    constexpr int kGroups = kBwdThreads / (64 * kW);
+    __shared__ float red1[2][kGroups][kW][3];
+    __shared__ float red2[2][kGroups][kW][2];
+    __shared__ __attribute__((aligned(16))) float cols[kGroups > 1 ? kBwdThreads * 8 : 4];
+    int half1 = 0, half2 = 0;
+    const int grp = threadIdx.x / (64 * kW), lt = threadIdx.x % (64 * kW);
+    const int d = g.d;
+    const float inv_d = 1.0f / (float)d;
+    const TRes* dz = static_cast<const TRes*>(g.dz);
+    const TRes* z = static_cast<const TRes*>(g.z);
+    TRes* dx = static_cast<TRes*>(g.dx);
+    const bool pre = g.w_pre != nullptr, post = g.w_post != nullptr;
+    Vec8 wq[kC], gt[kC], wp[kC], a_pre[kC], a_post[kC], a_gate[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const int col = 8 * (lt + c * 64 * kW);
+        const bool in = col < d;
+        wq[c] = ld8_or(g.w_post, col, in, 1.0f);
+        gt[c] = ld8_or(g.gate_kind == kGateChannel ? g.gate : nullptr, col, in, 1.0f);
+        wp[c] = ld8_or(g.w_pre, col, in, 0.0f);
+        a_pre[c] = zero8();
+        a_post[c] = zero8();
+        a_gate[c] = zero8();
+    }
+    for (int64_t t0 = (int64_t)blockIdx.x * kGroups; t0 < g.T; t0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t t = t0 + grp;
+        const bool row = t < g.T;
+        Vec8 G[kC], zv[kC], hv[kC], yv[kC];
+        float s[3] = {0.0f, 0.0f, 0.0f};               // sums of z^2, w_pre dh z, y^2
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int col = 8 * (lt + c * 64 * kW);
+            const bool in = row && col < d;
+            G[c] = in && dz ? ld8(dz + t * d + col) : zero8();
+            zv[c] = in && pre ? ld8(z + t * d + col) : zero8();
+            hv[c] = in && pre ? ld8(g.dh + t * d + col) : zero8();
+            yv[c] = in && g.y ? ld8(g.y + t * d + col) : zero8();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[0] += zv[c].v[i] * zv[c].v[i];
+                s[1] += hv[c].v[i] * wp[c].v[i] * zv[c].v[i];
+                s[2] += yv[c].v[i] * yv[c].v[i];
+            }
+        }
+        row_sums<3, kW, kGroups>(s, red1, half1);
+        const float r = __builtin_amdgcn_rsqf(s[0] * inv_d + g.eps);
+        const float q = post ? __builtin_amdgcn_rsqf(s[2] * inv_d + g.eps) : 1.0f;
+        const float rz = r * (s[1] * inv_d) * r * r;   // in this order a row of zeros gives 0
+        const float tg = g.alpha * (g.gate_kind == kGateToken && row ? g.gate[t] : 1.0f);
+        float u[2] = {0.0f, 0.0f};                     // sums of w_post dn y, alpha G n
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int col = 8 * (lt + c * 64 * kW);
+            const bool in = row && col < d;
+            if (pre) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a_pre[c].v[i] += hv[c].v[i] * zv[c].v[i] * r;
+                    G[c].v[i] += r * wp[c].v[i] * hv[c].v[i] - zv[c].v[i] * rz;
+                }
+            }
+            if (in) st8(dx + t * d + col, G[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float m = yv[c].v[i] * q;         // the normed output before w_post
+                const float ag = g.alpha * G[c].v[i] * m * wq[c].v[i];
+                a_gate[c].v[i] += ag;
+                const float dn = tg * gt[c].v[i] * G[c].v[i];
+                a_post[c].v[i] += dn * m;
+                G[c].v[i] = dn * wq[c].v[i];
+                u[0] += G[c].v[i] * yv[c].v[i];
+                u[1] += ag;
+            }
+        }
+        if (!g.y) continue;
+        if (post || g.gate_kind == kGateToken) row_sums<2, kW, kGroups>(u, red2, half2);
+        const float qy = post ? q * (u[0] * inv_d) * q * q : 0.0f;
+        if (g.gate_kind == kGateToken && row && lt == 0) g.dgate[t] = u[1];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int col = 8 * (lt + c * 64 * kW);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) G[c].v[i] = q * G[c].v[i] - yv[c].v[i] * qy;
+            if (row && col < d) st8(g.dy + t * d + col, G[c]);
+        }
+    }
+    // column sums: the workgroup's row groups in order, then one partial row (the result
+    // itself when there is one workgroup)
+    const bool last = gridDim.x == 1;
+    auto column = [&](const Vec8 (&a)[kC], float* out, int which) {
+        if (!out) return;
+        float* dst = last ? out : g.part + ((size_t)blockIdx.x * 3 + which) * d;
+        if constexpr (kGroups > 1) {
+            __syncthreads();
+            st8(cols + threadIdx.x * 8, a[0]);
+            __syncthreads();
+            for (int c = threadIdx.x; c < 512 * kW; c += kBwdThreads) {
+                float v = cols[c];
+#pragma unroll
+                for (int u = 1; u < kGroups; ++u) v += cols[u * 512 * kW + c];
+                if (c < d) dst[c] = v;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int col = 8 * (lt + c * 64 * kW);
+                if (col < d) st8(dst + col, a[c]);
+            }
+        }
+    };
+    static_assert(kGroups == 1 || kC == 1, "one piece per lane when a workgroup holds several rows");
+    column(a_pre, pre ? g.dw_pre : nullptr, 0);
+    column(a_post, post && g.y ? g.dw_post : nullptr, 1);
+    column(a_gate, g.gate_kind == kGateChannel && g.y ? g.dgate : nullptr, 2);
+}
+
+// out[c] = sum over workgroups of part[b][which][c], in workgroup order within each of 64
+// slices and then over the slices: 64 columns per workgroup, four a thread
+constexpr int kSliceCols = 64, kSlices = 64;
+__global__ __launch_bounds__(1024) void norm_columns_kernel(NormGradArgs g, int blocks) {
+    __shared__ f32x4_t p[kSlices][kSliceCols / 4];
+    const int q = threadIdx.x % (kSliceCols / 4), slice = threadIdx.x / (kSliceCols / 4);
+    const int which = blockIdx.y, c = blockIdx.x * kSliceCols + 4 * q;
+    float* out = which == 0 ? (g.w_pre ? g.dw_pre : nullptr)
+                 : which == 1 ? (g.w_post && g.y ? g.dw_post : nullptr)
+                              : (g.gate_kind == kGateChannel && g.y ? g.dgate : nullptr);
+    if (!out) return;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (c < g.d)
+#pragma unroll 4
+        for (int b = slice; b < blocks; b += kSlices)
+            v += *reinterpret_cast<const f32x4_t*>(g.part + ((size_t)b * 3 + which) * g.d + c);
+    p[slice][q] = v;
+    __syncthreads();
+    if (threadIdx.x < kSliceCols && blockIdx.x * kSliceCols + threadIdx.x < g.d) {
+        float s = 0.0f;
+        for (int u = 0; u < kSlices; ++u) s += reinterpret_cast<const float*>(&p[u][threadIdx.x >> 2])[threadIdx.x & 3];
+        out[blockIdx.x * kSliceCols + threadIdx.x] = s;
+    }
+}
+
+template <typename TRes, int kW, int kC>
+void launch_norm_t(const NormArgs& g, int num_cu, hipStream_t s) {
+    constexpr int thr = 64 * kW > kFwdThreads ? 64 * kW : kFwdThreads;
+    const int groups = thr / (64 * kW);
+    const int64_t rows = ((int64_t)g.T + groups - 1) / groups;
+    const int64_t cap = (int64_t)num_cu * (2048 / thr);         // workgroups that fit the chip
+    const int grid = (int)(rows < cap ? rows : cap);
+    hipLaunchKernelGGL((norm_kernel<TRes, kW, kC>), dim3(grid), dim3(thr), 0, s, g);
+}
+template <typename TRes, int kW, int kC>
+int launch_norm_grad_t(const NormGradArgs& g, hipStream_t s) {
+    const int groups = kBwdThreads / (64 * kW);
+    const int64_t rows = ((int64_t)g.T + groups - 1) / groups;
+    const int grid = (int)(rows < 1 ? 1 : rows < kNormBlocks ? rows : kNormBlocks);
+    hipLaunchKernelGGL((norm_grad_kernel<TRes, kW, kC>), dim3(grid), dim3(kBwdThreads), 0, s, g);
+    return grid;
+}
+template <typename TRes> void launch_norm_d(const NormArgs& g, int num_cu, hipStream_t s) {
+    if (g.d <= 512) launch_norm_t<TRes, 1, 1>(g, num_cu, s);
+    else if (g.d <= 1024) launch_norm_t<TRes, 2, 1>(g, num_cu, s);
+    else if (g.d <= 2048) launch_norm_t<TRes, 4, 1>(g, num_cu, s);
+    else if (g.d <= 4096) launch_norm_t<TRes, 8, 1>(g, num_cu, s);
+    else if (g.d <= 8192) launch_norm_t<TRes, 16, 1>(g, num_cu, s);
+    else launch_norm_t<TRes, 16, 2>(g, num_cu, s);
+}
+template <typename TRes> int launch_norm_grad_d(const NormGradArgs& g, hipStream_t s) {
+    if (g.d <= 512) return launch_norm_grad_t<TRes, 1, 1>(g, s);
+    if (g.d <= 1024) return launch_norm_grad_t<TRes, 2, 1>(g, s);
+    if (g.d <= 2048) return launch_norm_grad_t<TRes, 4, 1>(g, s);
+    if (g.d <= 4096) return launch_norm_grad_t<TRes, 8, 1>(g, s);
+    if (g.d <= 8192) return launch_norm_grad_t<TRes, 16, 1>(g, s);
+    return launch_norm_grad_t<TRes, 16, 2>(g, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& g, bool f32, int num_cu, hipStream_t s) {
+    if (g.T == 0) return hipSuccess;
+    if (g.d % 8 != 0 || g.d > kNormMaxD) return hipErrorInvalidValue;
+    if (f32) launch_norm_d<float>(g, num_cu, s);
+    else launch_norm_d<uint16_t>(g, num_cu, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& g, bool f32, hipStream_t s) {
+    if (g.d % 8 != 0 || g.d > kNormMaxD) return hipErrorInvalidValue;
+    const int blocks = f32 ? launch_norm_grad_d<float>(g, s) : launch_norm_grad_d<uint16_t>(g, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || blocks == 1) return e;
+    const dim3 grid((g.d + kSliceCols - 1) / kSliceCols, 3);
+    hipLaunchKernelGGL(norm_columns_kernel, grid, dim3(1024), 0, s, g, blocks);
+    return hipGetLastError();
+}
+
+}  // namespace moe

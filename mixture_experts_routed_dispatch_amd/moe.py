@@ -28,6 +28,7 @@ MOE_STATIC_SCRATCH_BYTES = 32 << 20
 
 MOE_BF16 = 0
 MOE_MXFP8_E4M3 = 1
+MOE_MXFP4 = 2
 
 MOE_PATH_AUTO = 0
 MOE_PATH_PREFILL = 1
@@ -37,6 +38,8 @@ MOE_DEV_ID_OUT_OF_RANGE = 1
 MOE_DEV_ID_DUPLICATE = 2
 MOE_DEV_BAD_INDPTR = 4
 MOE_ACT_SWIGLU, MOE_ACT_GEGLU, MOE_ACT_REGLU = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_plan", "moe_workspace_bytes", "moe_bind_workspace", "moe_plan_destroy",
@@ -44,7 +47,9 @@ EXPORTS = ("moe_plan", "moe_workspace_bytes", "moe_bind_workspace", "moe_plan_de
            "moe_forward", "moe_forward_static",
            "moe_forward_routed",
            "moe_backward", "moe_get_status", "moe_status_string", "moe_profile", "moe_plan_explain",
-           "moe_profile_read")
+           "moe_profile_read", "moe_expand_weights",
+           "moe_router_workspace_bytes", "moe_router_forward", "moe_router_backward",
+           "moe_norm_workspace_bytes", "moe_norm_forward", "moe_norm_backward")
 
 STAGES = ("dispatch", "quant_x", "w13", "w2", "combine", "score_grad", "dgrad_w2", "wgrad_w2",
           "dgrad_w13", "wgrad_w13", "dx_combine", "decode_w13", "decode_w2", "wgrad_rows", "recompute_h",
@@ -70,6 +75,18 @@ class MoeWeights(ctypes.Structure):
                 ("w13_scale", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p),
                 ("w13t", ctypes.c_void_p), ("w13t_scale", ctypes.c_void_p),
                 ("w2t", ctypes.c_void_p), ("w2t_scale", ctypes.c_void_p)]
+
+
+class RouterConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("normalize", ctypes.c_int32), ("logits_f32", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("balance_coef", ctypes.c_float)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("residual_f32", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -110,6 +127,21 @@ def lib():
         L.moe_forward_routed.restype = ctypes.c_int
         L.moe_backward.argtypes = [vp, vp, vp, ctypes.POINTER(MoeWeights), vp, vp, vp, vp, vp]
         L.moe_backward.restype = ctypes.c_int
+        L.moe_expand_weights.argtypes = [vp, ctypes.POINTER(MoeWeights), vp, vp, vp]
+        L.moe_expand_weights.restype = ctypes.c_int
+        sz, router, norm = ctypes.c_size_t, ctypes.POINTER(RouterConfig), ctypes.POINTER(NormConfig)
+        L.moe_router_workspace_bytes.argtypes = [router]
+        L.moe_router_workspace_bytes.restype = sz
+        L.moe_router_forward.argtypes = [router] + [vp] * 9 + [sz, vp]
+        L.moe_router_forward.restype = ctypes.c_int
+        L.moe_router_backward.argtypes = [router] + [vp] * 8
+        L.moe_router_backward.restype = ctypes.c_int
+        L.moe_norm_workspace_bytes.argtypes = [norm]
+        L.moe_norm_workspace_bytes.restype = sz
+        L.moe_norm_forward.argtypes = [norm] + [vp] * 8
+        L.moe_norm_forward.restype = ctypes.c_int
+        L.moe_norm_backward.argtypes = [norm] + [vp] * 13 + [sz, vp]
+        L.moe_norm_backward.restype = ctypes.c_int
         L.moe_get_status.argtypes = [vp, ctypes.POINTER(i32), i32, vp]
         L.moe_get_status.restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -200,6 +232,39 @@ def moe_forward_routed(plan, x_rows, m_indptr, w: MoeWeights, out, stream=0):
 def moe_backward(plan, dy, x, w: MoeWeights, dx, dw13, dw2, dscores, stream=0):
     _ok(lib().moe_backward(plan, dy, x, ctypes.byref(w), dx, dw13, dw2, dscores, stream),
         "moe_backward")
+
+
+def moe_expand_weights(plan, w: MoeWeights, w13, w2, stream=0):
+    _ok(lib().moe_expand_weights(plan, ctypes.byref(w), w13, w2, stream), "moe_expand_weights")
+
+
+def moe_router_workspace_bytes(cfg: RouterConfig) -> int:
+    return int(lib().moe_router_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_router_forward(cfg: RouterConfig, logits, bias, mask, ids, scores, counts, prob_sums, loss, workspace,
+                       workspace_bytes, stream=0):
+    _ok(lib().moe_router_forward(ctypes.byref(cfg), logits, bias, mask, ids, scores, counts, prob_sums, loss,
+                                 workspace, workspace_bytes, stream), "moe_router_forward")
+
+
+def moe_router_backward(cfg: RouterConfig, dscores, logits, mask, ids, counts, dloss, dlogits, stream=0):
+    _ok(lib().moe_router_backward(ctypes.byref(cfg), dscores, logits, mask, ids, counts, dloss, dlogits, stream),
+        "moe_router_backward")
+
+
+def moe_norm_workspace_bytes(cfg: NormConfig) -> int:
+    return int(lib().moe_norm_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_norm_forward(cfg: NormConfig, x, y, w_post, gate, w_pre, z, h, stream=0):
+    _ok(lib().moe_norm_forward(ctypes.byref(cfg), x, y, w_post, gate, w_pre, z, h, stream), "moe_norm_forward")
+
+
+def moe_norm_backward(cfg: NormConfig, dz, dh, z, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre, workspace,
+                      workspace_bytes, stream=0):
+    _ok(lib().moe_norm_backward(ctypes.byref(cfg), dz, dh, z, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre,
+                                workspace, workspace_bytes, stream), "moe_norm_backward")
 
 
 def moe_get_status(plan, clear=True, stream=0):
@@ -321,9 +386,21 @@ class Layer:
         return dx, dw13, dw2, dscores
 
     def prepare_weights(self, w13, w2, stream=None):
+        """BF16 weights -> (w13_q, w13_s, w2_q, w2_s): MXFP8 codes and scales, or on an
+        MXFP4 layer MXFP4 ones in the decode kernels' tile layout."""
         import torch
         dev = w13.device
         E, I, d = self.E, self.I, self.d
+        if self.precision == MOE_MXFP4:
+            _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
+            _check("w2", w2, (E, d, I), torch.bfloat16, dev)
+            w13_q = torch.empty((E, I * d), dtype=torch.uint8, device=dev)
+            w13_s = torch.empty((E, 2 * I // 16, (d + 511) // 512, 64, 4), dtype=torch.uint8, device=dev)
+            w2_q = torch.empty((E, d * I // 2), dtype=torch.uint8, device=dev)
+            w2_s = torch.empty((E, d // 16, (I + 511) // 512, 64, 4), dtype=torch.uint8, device=dev)
+            moe_prepare_weights(self.plan, _ptr(w13), _ptr(w2), _ptr(w13_q), _ptr(w13_s), _ptr(w2_q), _ptr(w2_s),
+                                _stream(stream))
+            return w13_q, w13_s, w2_q, w2_s
         w13_q = torch.empty((E, 2 * I, d), dtype=torch.uint8, device=dev)
         # scales block-major: [K/128, rows, 4] (see moe_prepare_weights in include/moe.h)
         w13_s = torch.empty((d // 128, E * 2 * I, 4), dtype=torch.uint8, device=dev)
@@ -332,6 +409,22 @@ class Layer:
         moe_prepare_weights(self.plan, _ptr(w13), _ptr(w2), _ptr(w13_q), _ptr(w13_s), _ptr(w2_q),
                             _ptr(w2_s), _stream(stream))
         return w13_q, w13_s, w2_q, w2_s
+
+    def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
+        """The BF16 weights (w13, w2) that an MXFP4 layer's prepared weights stand for."""
+        import torch
+        dev = w13_q.device
+        E, I, d = self.E, self.I, self.d
+        if self.precision == MOE_MXFP4:
+            _check("w13_q", w13_q, (E, I * d), torch.uint8, dev)
+            _check("w13_s", w13_s, (E, 2 * I // 16, (d + 511) // 512, 64, 4), torch.uint8, dev)
+            _check("w2_q", w2_q, (E, d * I // 2), torch.uint8, dev)
+            _check("w2_s", w2_s, (E, d // 16, (I + 511) // 512, 64, 4), torch.uint8, dev)
+        w13 = torch.empty((E, 2 * I, d), dtype=torch.bfloat16, device=dev)
+        w2 = torch.empty((E, d, I), dtype=torch.bfloat16, device=dev)
+        w = weights(_ptr(w13_q), _ptr(w2_q), _ptr(w13_s), _ptr(w2_s))
+        moe_expand_weights(self.plan, w, _ptr(w13), _ptr(w2), _stream(stream))
+        return w13, w2
 
     def prepare_weights_backward(self, w13, w2, stream=None):
         """(w13t, w13t_scale, w2t, w2t_scale) for the MXFP8 backward: W13_e^T [d, 2I] and
@@ -349,3 +442,176 @@ class Layer:
 
     def status(self, clear=True, stream=None):
         return moe_get_status(self.plan, clear, _stream(stream))
+
+
+# ---------------------------------------------------------------- around the layer
+
+def _check(name, t, shape, dtype, device):
+    """A dense tensor of this shape and type on this device, or ValueError."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of shape %s on %s is needed, got %s %s on %s%s" % (
+            name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
+            "" if t.is_contiguous() else ", not contiguous"))
+
+
+class _OnDevice:
+    """What Router and BlockNorm share: their device, a workspace there, and calls made with
+    that device current and their outputs allocated on the stream that writes them.  As with
+    a Layer, one object per concurrently running stream (the workspace is its own)."""
+
+    def __init__(self, device, workspace_bytes):
+        import torch
+        device = torch.device(device)
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
+        self.device = device
+        self.workspace = torch.empty(max(workspace_bytes, 16), dtype=torch.uint8, device=device)
+
+    def _call(self, f, stream):
+        """f(raw stream) with this object's device current and `stream` its current stream."""
+        import torch
+        if stream is not None:
+            with torch.cuda.stream(stream):            # also makes the stream's device current
+                return f(int(stream.cuda_stream))
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return f(int(torch.cuda.current_stream().cuda_stream))
+        return f(int(torch.cuda.current_stream().cuda_stream))
+
+
+class Router(_OnDevice):
+    """Logits [T, E] (FP32 or BF16) -> ids, scores, per-expert counts and the balance loss, and
+    the gradient; see the router section of include/moe.h for the formulas."""
+
+    def __init__(self, T, E, k, score=MOE_SCORE_SOFTMAX, normalize=True, scale=1.0, balance_coef=0.0, device="cuda"):
+        self.T, self.E, self.k = T, E, k
+        self._cfg = {f32: RouterConfig(T, E, k, int(score), int(bool(normalize)), int(f32), scale, balance_coef)
+                     for f32 in (False, True)}
+        nbytes = moe_router_workspace_bytes(self._cfg[True])
+        if not nbytes:                                 # the reason, from the call that names it
+            moe_router_forward(self._cfg[True], 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+        super().__init__(device, nbytes)
+
+    def _logits_cfg(self, logits):
+        import torch
+        f32 = logits.dtype == torch.float32
+        _check("logits", logits, (self.T, self.E), torch.float32 if f32 else torch.bfloat16, self.device)
+        return self._cfg[f32]
+
+    def _check_mask(self, mask):
+        import torch
+        if mask is not None:
+            _check("mask", mask, (self.T,), torch.bool if mask.dtype == torch.bool else torch.uint8, self.device)
+
+    def forward(self, logits, bias=None, mask=None, stats=True, stream=None):
+        """(ids int32 [T, k], scores f32 [T, k], counts int32 [E], prob_sums f32 [E], loss f32 []);
+        without `stats` the last three are None and not computed."""
+        import torch
+        cfg, dev = self._logits_cfg(logits), self.device
+        if bias is not None:
+            _check("bias", bias, (self.E,), torch.float32, dev)
+        self._check_mask(mask)
+
+        def call(s):
+            ids = torch.empty((self.T, self.k), dtype=torch.int32, device=dev)
+            scores = torch.empty((self.T, self.k), dtype=torch.float32, device=dev)
+            counts = sums = loss = None
+            if stats:
+                counts = torch.empty(self.E, dtype=torch.int32, device=dev)
+                sums = torch.empty(self.E, dtype=torch.float32, device=dev)
+                loss = torch.empty((), dtype=torch.float32, device=dev)
+            moe_router_forward(cfg, _ptr(logits), _ptr(bias), _ptr(mask), _ptr(ids), _ptr(scores), _ptr(counts),
+                               _ptr(sums), _ptr(loss), _ptr(self.workspace), self.workspace.numel(), s)
+            return ids, scores, counts, sums, loss
+
+        return self._call(call, stream)
+
+    def backward(self, dscores, logits, ids, counts=None, dloss=None, mask=None, dlogits=None, stream=None):
+        """dlogits [T, E] from dscores f32 [T, k] (None: zeros) and dloss f32 [] or [1] (None: the
+        loss has no gradient; else counts are needed)."""
+        import torch
+        cfg, dev = self._logits_cfg(logits), self.device
+        _check("ids", ids, (self.T, self.k), torch.int32, dev)
+        if dscores is not None:
+            _check("dscores", dscores, (self.T, self.k), torch.float32, dev)
+        if counts is not None:
+            _check("counts", counts, (self.E,), torch.int32, dev)
+        if dloss is not None:
+            _check("dloss", dloss, dloss.shape if dloss.numel() == 1 else (), torch.float32, dev)
+        if dlogits is not None:
+            _check("dlogits", dlogits, (self.T, self.E), logits.dtype, dev)
+        self._check_mask(mask)
+
+        def call(s):
+            out = torch.empty_like(logits) if dlogits is None else dlogits
+            moe_router_backward(cfg, _ptr(dscores), _ptr(logits), _ptr(mask), _ptr(ids), _ptr(counts), _ptr(dloss),
+                                _ptr(out), s)
+            return out
+
+        return self._call(call, stream)
+
+
+class BlockNorm(_OnDevice):
+    """The norms before and after the layer with its gate and residual:
+    z = x + residual_scale * gate * rms(y; w_post), h = rms(z; w_pre); see include/moe.h."""
+
+    def __init__(self, T, d, eps=1e-6, residual_scale=1.0, gate=MOE_GATE_NONE, residual_f32=False, device="cuda"):
+        self.T, self.d, self.gate = T, d, gate
+        self.residual_f32 = bool(residual_f32)
+        self._cfg = NormConfig(T, d, int(gate), int(self.residual_f32), eps, residual_scale)
+        nbytes = moe_norm_workspace_bytes(self._cfg)
+        if not nbytes:
+            moe_norm_forward(self._cfg, 0, 0, 0, 0, 0, 0, 0)
+        super().__init__(device, nbytes)
+
+    def _check_args(self, stream_tensors, block_tensors, w_post, gate, w_pre):
+        import torch
+        res = torch.float32 if self.residual_f32 else torch.bfloat16
+        for name, t in stream_tensors:
+            if t is not None:
+                _check(name, t, (self.T, self.d), res, self.device)
+        for name, t in block_tensors:
+            if t is not None:
+                _check(name, t, (self.T, self.d), torch.bfloat16, self.device)
+        for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+            if t is not None:
+                _check(name, t, (self.d,), torch.float32, self.device)
+        if gate is not None:
+            _check("gate", gate, (self.T,) if self.gate == MOE_GATE_TOKEN else (self.d,), torch.float32, self.device)
+        return res
+
+    def forward(self, x, y=None, w_post=None, gate=None, w_pre=None, z=None, stream=None):
+        """(z, h); h is None without w_pre.  Without y, z is x itself.  z may be given (also x)."""
+        import torch
+        res = self._check_args((("x", x), ("z", z)), (("y", y),), w_post, gate, w_pre)
+
+        def call(s):
+            shape = (self.T, self.d)
+            out = z
+            if out is None and y is not None:
+                out = torch.empty(shape, dtype=res, device=self.device)
+            h = None if w_pre is None else torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            moe_norm_forward(self._cfg, _ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(out), _ptr(h), s)
+            return x if y is None else out, h
+
+        return self._call(call, stream)
+
+    def backward(self, dz, dh, z, y=None, w_post=None, gate=None, w_pre=None, dx=None, stream=None):
+        """(dx, dy, dw_post, dgate, dw_pre), None where there is no such input.  dz None: the stream
+        has no gradient but h's.  dx may be given (also dz)."""
+        import torch
+        res = self._check_args((("dz", dz), ("z", z), ("dx", dx)), (("dh", dh), ("y", y)), w_post, gate, w_pre)
+
+        def call(s):
+            def like(t):
+                return None if t is None else torch.empty_like(t)
+            out = dx
+            if out is None:
+                out = torch.empty((self.T, self.d), dtype=res, device=self.device)
+            dy, dw_post, dgate, dw_pre = like(y), like(w_post), like(gate), like(w_pre)
+            moe_norm_backward(self._cfg, _ptr(dz), _ptr(dh), _ptr(z), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                              _ptr(out), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), _ptr(self.workspace),
+                              self.workspace.numel(), s)
+            return out, dy, dw_post, dgate, dw_pre
+
+        return self._call(call, stream)

@@ -1,0 +1,172 @@
+"""Host checks of the router, the block norms and the 4-bit weights (include/moe.h): configs and
+arguments that are refused before anything reaches a device, workspace sizes, plan limits."""
+import ctypes
+
+import pytest
+
+from mixture_experts_routed_dispatch_amd import moe
+
+P = 0x1000          # an aligned address that no refused call may touch
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    if not os.path.exists(moe.LIB_PATH):
+        from mixture_experts_routed_dispatch_amd import build
+        build.build()
+    return moe.lib()
+
+
+def router(T=8, E=16, k=2, score=0, normalize=1, logits_f32=1, scale=1.0, coef=0.0):
+    return moe.RouterConfig(T, E, k, score, normalize, logits_f32, scale, coef)
+
+
+def norm(T=8, d=256, gate=0, residual_f32=0, eps=1e-6, scale=1.0):
+    return moe.NormConfig(T, d, gate, residual_f32, eps, scale)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(T=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(E=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(k=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(E=257), moe.MOE_ERR_UNSUPPORTED),
+    (dict(E=4, k=5), moe.MOE_ERR_UNSUPPORTED),
+    (dict(E=64, k=33), moe.MOE_ERR_UNSUPPORTED),
+    (dict(score=2), moe.MOE_ERR_INVALID_ARG),
+    (dict(normalize=2), moe.MOE_ERR_INVALID_ARG),
+    (dict(logits_f32=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), moe.MOE_ERR_INVALID_ARG),
+    (dict(coef=float("nan")), moe.MOE_ERR_INVALID_ARG),
+])
+def test_router_config_refusals(L, change, expect):
+    c = router(**change)
+    assert L.moe_router_workspace_bytes(ctypes.byref(c)) == 0
+    assert L.moe_router_forward(ctypes.byref(c), P, None, None, P, P, P, P, P, P, 1 << 20, None) == expect
+    assert L.moe_router_backward(ctypes.byref(c), P, P, None, P, P, P, P, None) == expect
+
+
+def test_router_argument_refusals(L):
+    c = router()
+    need = L.moe_router_workspace_bytes(ctypes.byref(c))
+    assert need >= 16 * 8
+    f = lambda *a: L.moe_router_forward(ctypes.byref(c), *a)
+    assert L.moe_router_forward(None, P, None, None, P, P, P, P, P, P, need, None) == moe.MOE_ERR_INVALID_ARG
+    assert f(None, None, None, P, P, P, P, P, P, need, None) == moe.MOE_ERR_INVALID_ARG        # logits
+    assert f(P, None, None, None, P, P, P, P, P, need, None) == moe.MOE_ERR_INVALID_ARG        # ids
+    assert f(P, None, None, P, None, P, P, P, P, need, None) == moe.MOE_ERR_INVALID_ARG        # scores
+    assert f(P, None, None, P, P, P, P, P, None, need, None) == moe.MOE_ERR_WORKSPACE
+    assert f(P, None, None, P, P, None, None, P, P, need - 1, None) == moe.MOE_ERR_WORKSPACE
+    assert f(P, None, None, P, P, P, P, P, P + 4, need, None) == moe.MOE_ERR_INVALID_ARG       # alignment
+    b = lambda *a: L.moe_router_backward(ctypes.byref(c), *a)
+    assert b(P, None, None, P, P, P, P, None) == moe.MOE_ERR_INVALID_ARG
+    assert b(P, P, None, None, P, P, P, None) == moe.MOE_ERR_INVALID_ARG
+    assert b(P, P, None, P, P, P, None, None) == moe.MOE_ERR_INVALID_ARG
+    assert b(P, P, None, P, None, P, P, None) == moe.MOE_ERR_INVALID_ARG                       # dloss, no counts
+
+
+def test_router_workspace_is_bounded(L):
+    """One partial row of counts and sums per workgroup, and at most 256 of them."""
+    c = router(T=1 << 30, E=256, k=8)
+    assert L.moe_router_workspace_bytes(ctypes.byref(c)) == 256 * 256 * 8
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(T=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(d=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(d=252), moe.MOE_ERR_UNSUPPORTED),
+    (dict(d=16392), moe.MOE_ERR_UNSUPPORTED),
+    (dict(gate=3), moe.MOE_ERR_INVALID_ARG),
+    (dict(residual_f32=2), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=0.0), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=-1e-6), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=1e-40), moe.MOE_ERR_INVALID_ARG),          # a subnormal float
+    (dict(scale=float("nan")), moe.MOE_ERR_INVALID_ARG),
+])
+def test_norm_config_refusals(L, change, expect):
+    c = norm(**change)
+    assert L.moe_norm_workspace_bytes(ctypes.byref(c)) == 0
+    assert L.moe_norm_forward(ctypes.byref(c), P, P, P, None, P, P, P, None) == expect
+    assert L.moe_norm_backward(ctypes.byref(c), P, P, P, P, P, None, P, P, P, P, None, P, P, 1 << 30, None) == expect
+
+
+def test_norm_argument_refusals(L):
+    bad = moe.MOE_ERR_INVALID_ARG
+    c, cg = norm(), norm(gate=moe.MOE_GATE_CHANNEL)
+    f = lambda cfg, *a: L.moe_norm_forward(ctypes.byref(cfg), *a, None)
+    # x, y, w_post, gate, w_pre, z, h
+    assert f(c, None, P, None, None, P, P, P) == bad
+    assert f(c, P, P, None, None, P, None, P) == bad               # y without z
+    assert f(c, P, P, None, P, P, P, P) == bad                     # a gate that the config lacks
+    assert f(cg, P, P, None, None, P, P, P) == bad                 # a gate that is missing
+    assert f(c, P, P, None, None, P, P, None) == bad               # w_pre without h
+    assert f(c, P, P, None, None, None, P, P) == bad               # h without w_pre
+    assert f(c, P, None, None, None, None, None, None) == bad      # nothing to do
+    assert f(c, P, None, P, None, P, None, P) == bad               # w_post without y
+    assert f(c, P, None, None, None, P, P, P) == bad               # z without y
+    assert f(c, P + 8, P, None, None, P, P, P) == bad              # alignment
+    need = L.moe_norm_workspace_bytes(ctypes.byref(c))
+    b = lambda cfg, *a: L.moe_norm_backward(ctypes.byref(cfg), *a, None)
+    # dz, dh, z, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre, workspace, bytes
+    assert b(c, P, P, P, P, P, None, P, P, P, P, None, P, P, need - 1) == moe.MOE_ERR_WORKSPACE
+    assert b(c, P, P, P, P, P, None, P, P, P, P, None, P, None, need) == moe.MOE_ERR_WORKSPACE
+    assert b(c, P, P, P, P, P, None, P, P, P, None, None, P, P, need) == bad     # dw_post missing
+    assert b(c, P, P, P, P, P, None, P, P, None, P, None, P, P, need) == bad     # dy missing
+    assert b(c, P, None, P, P, P, None, P, P, P, P, None, P, P, need) == bad     # dh missing
+    assert b(c, P, P, None, P, P, None, P, P, P, P, None, P, P, need) == bad     # z missing
+    assert b(c, None, None, None, P, P, None, None, P, P, P, None, None, P, need) == bad  # no gradient at all
+    assert b(c, P, P, P, None, None, None, None, P, None, None, None, None, P, need) == bad  # neither y nor w_pre
+    assert b(cg, P, P, P, P, P, None, P, P, P, P, None, P, P, need) == bad       # gate missing
+
+
+@pytest.mark.parametrize("cfg,expect", [
+    (dict(T=1, d=2048, I=768, E=128, k=8), moe.MOE_OK),
+    (dict(T=32, d=256, I=128, E=8, k=8, path=2), moe.MOE_OK),
+    (dict(T=64, d=256, I=128, E=8, k=8), moe.MOE_OK),                                # grouped-GEMM path
+    (dict(T=8, d=256, I=128, E=8, k=2, training=1), moe.MOE_ERR_UNSUPPORTED),
+    (dict(T=8, d=256, I=128, E=8, k=2, mega=1), moe.MOE_ERR_UNSUPPORTED),
+    (dict(T=8, d=192, I=128, E=8, k=2), moe.MOE_ERR_UNSUPPORTED),                    # d % 128
+    (dict(T=8, d=256, I=64, E=8, k=2), moe.MOE_ERR_UNSUPPORTED),                     # I % 128
+    (dict(T=64, d=256, I=128, E=8, k=8, path=2), moe.MOE_ERR_UNSUPPORTED),           # 512 rows
+])
+def test_mxfp4_plans(L, cfg, expect):
+    c = moe.MoeConfig(cfg["T"], cfg["d"], cfg["I"], cfg["E"], cfg["k"], moe.MOE_MXFP4, cfg.get("training", 0),
+                      cfg.get("path", 0), 0, 0, 0, cfg.get("mega", 0))
+    h = ctypes.c_void_p()
+    assert L.moe_plan(ctypes.byref(c), ctypes.byref(h)) == expect
+    if expect != moe.MOE_OK:
+        return
+    text = moe.moe_plan_explain(h.value)
+    assert "MXFP4 weights" in text
+    # past 256 routed rows the workspace holds a product's weights as BF16
+    expanded = 2 * cfg["E"] * 2 * cfg["I"] * cfg["d"]
+    assert (moe.moe_workspace_bytes(h.value) >= expanded and "\n  we " in text) == (cfg["T"] * cfg["k"] > 256)
+    w = moe.weights(P, P)
+    assert L.moe_forward(h, P, P, P, ctypes.byref(w), P, None) == moe.MOE_ERR_INVALID_ARG        # no scales
+    assert L.moe_expand_weights(h, ctypes.byref(w), P, P, None) == moe.MOE_ERR_INVALID_ARG
+    L.moe_plan_destroy(h)
+
+
+def test_expand_needs_an_mxfp4_plan(L):
+    plan = moe.moe_plan(8, 256, 128, 8, 2)
+    w = moe.weights(P, P, P, P)
+    assert L.moe_expand_weights(plan, ctypes.byref(w), P, P, None) == moe.MOE_ERR_UNSUPPORTED
+    moe.moe_plan_destroy(plan)
+
+
+def test_python_checks_name_the_tensor():
+    import torch
+    cpu = torch.device("cpu")
+    good = torch.zeros(4, 8)
+    moe._check("x", good, (4, 8), torch.float32, cpu)
+    for t in (good[:, :4], torch.zeros(8, 4).t(), good.double(), torch.zeros(4, 9)):
+        with pytest.raises(ValueError, match="x: "):
+            moe._check("x", t, (4, 8), torch.float32, cpu)
+    with pytest.raises(ValueError):
+        moe._check("x", good, (4, 8), torch.float32, torch.device("cuda", 0))
+    for bad in (dict(T=4, E=300, k=2), dict(T=4, E=8, k=9)):
+        with pytest.raises(moe.MoeError) as e:
+            moe.Router(**bad)
+        assert e.value.status == moe.MOE_ERR_UNSUPPORTED
+    with pytest.raises(moe.MoeError):
+        moe.BlockNorm(4, 100)
