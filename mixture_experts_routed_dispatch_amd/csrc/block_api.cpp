@@ -71,9 +71,12 @@ static moe_status_t router_check(const moe_router_config_t* c) {
     return MOE_OK;
 }
 
+// the loss' shares and ticket, in front of the partial counts and sums
+constexpr size_t kRouterHead = 32 * sizeof(double) + 16;
+
 size_t moe_router_workspace_bytes(const moe_router_config_t* c) {
     if (router_check(c) != MOE_OK) return 0;
-    return (size_t)router_blocks(c->T) * ((c->E + 3) & ~3) * (sizeof(int32_t) + sizeof(float));
+    return (size_t)router_blocks(c->T) * ((c->E + 3) & ~3) * (sizeof(int32_t) + sizeof(float)) + kRouterHead;
 }
 
 moe_status_t moe_router_forward(const moe_router_config_t* c, const void* logits, const float* bias,
@@ -91,8 +94,11 @@ moe_status_t moe_router_forward(const moe_router_config_t* c, const void* logits
     if (counts || prob_sums || loss) {
         if (!workspace || workspace_bytes < moe_router_workspace_bytes(c)) return MOE_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return MOE_ERR_INVALID_ARG;
-        g.part_sums = static_cast<float*>(workspace);
-        g.part_counts = static_cast<int32_t*>(workspace) + (size_t)router_blocks(c->T) * ((c->E + 3) & ~3);
+        const size_t part = (size_t)router_blocks(c->T) * ((c->E + 3) & ~3);
+        g.shares = static_cast<double*>(workspace);
+        g.ticket = reinterpret_cast<int32_t*>(g.shares + 32);
+        g.part_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + kRouterHead);
+        g.part_counts = reinterpret_cast<int32_t*>(g.part_sums + part);
     }
     const hipError_t e = launch_route(g, c->score == MOE_SCORE_SIGMOID, c->logits_f32 != 0, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;

@@ -227,7 +227,9 @@ struct RouterArgs {
     float* loss;              // [1]
     int32_t* part_counts;     // [blocks, E rounded up to 4], or NULL: no counts, sums and loss
     float* part_sums;
-    int vec, stride;          // set by the launcher
+    double* shares;           // [16, 2], with part_counts
+    int32_t* ticket;          // [1], with part_counts
+    int vec, bias_vec, stride;  // set by the launcher
 };
 int router_blocks(int64_t T);
 hipError_t launch_route(RouterArgs g, bool sigmoid, bool f32, hipStream_t s);

