@@ -18,11 +18,8 @@ moe_status_t moe_prepare_weights(moe_plan_t p, const void* w13, const void* w2, 
     if (c.d % 128 != 0 || c.I % 128 != 0) return MOE_ERR_UNSUPPORTED;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (c.precision == MOE_MXFP4) {
-        if (launch_mxfp4_pack(static_cast<const uint16_t*>(w13), c.E, 2 * c.I, c.d, c.I, true, w13_q, w13_s, s) !=
-                hipSuccess ||
-            launch_mxfp4_pack(static_cast<const uint16_t*>(w2), c.E, c.d, c.I, c.I, false, w2_q, w2_s, s) !=
-                hipSuccess)
-            return MOE_ERR_HIP;
+        const Mxfp4Args g{{mxfp4_w13(w13, w13_q, w13_s, c.E, c.I, c.d), mxfp4_w2(w2, w2_q, w2_s, c.E, c.I, c.d)}};
+        if (launch_mxfp4_pack(g, s) != hipSuccess) return MOE_ERR_HIP;
         return MOE_OK;
     }
     // block-major scales (the layout the MXFP8 GEMMs copy from)
@@ -39,14 +36,8 @@ moe_status_t moe_expand_weights(moe_plan_t p, const moe_weights_t* w, void* w13,
     if (!p || !w || !w13 || !w2 || !w->w13 || !w->w2 || !w->w13_scale || !w->w2_scale) return MOE_ERR_INVALID_ARG;
     const moe_config_t& c = p->cfg;
     if (c.precision != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    if (launch_mxfp4_expand(static_cast<const uint8_t*>(w->w13), w->w13_scale, c.E, 2 * c.I, c.d, c.I, true,
-                            static_cast<uint16_t*>(w13), s) != hipSuccess)
-        return MOE_ERR_HIP;
-    if (launch_mxfp4_expand(static_cast<const uint8_t*>(w->w2), w->w2_scale, c.E, c.d, c.I, c.I, false,
-                            static_cast<uint16_t*>(w2), s) != hipSuccess)
-        return MOE_ERR_HIP;
-    return MOE_OK;
+    const Mxfp4Args g{{mxfp4_w13(w13, w->w13, w->w13_scale, c.E, c.I, c.d), mxfp4_w2(w2, w->w2, w->w2_scale, c.E, c.I, c.d)}};
+    return launch_mxfp4_expand(g, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 // compute units of the current device, looked up once per device
@@ -133,7 +124,7 @@ static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 1
 
 size_t moe_norm_workspace_bytes(const moe_norm_config_t* c) {
     if (norm_check(c) != MOE_OK) return 0;
-    return sizeof(float) * (size_t)kNormBlocks * 3 * c->d;
+    return sizeof(float) * (size_t)kNormBlocks * 2 * c->d;
 }
 
 moe_status_t moe_norm_forward(const moe_norm_config_t* c, const void* x, const void* y, const float* w_post,

@@ -733,7 +733,6 @@ hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s) {
 }
 
 hipError_t launch_decode_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
-    if (g.w2_scale) return launch_decode4_w2(g, num_cu, s);
     return launch_decode(decode_w2<false>, decode_w2<true>, g, g.d / 16, g.I / 32, num_cu, s);
 }
 

@@ -2,8 +2,9 @@
 // T*k <= 256 routed rows.
 //
 // The same launches as with BF16 weights (decode.hip): W13 with the activation, then for one
-// token W2 with the combine, else W2 and the combine kernel; a and o are rounded to BF16 at the
-// same points.  The time is that of streaming 4.25 bits for each weight of the active experts.
+// token W2 with the combine, else W2 and a combine.  a is rounded to BF16, the operand type of
+// the W2 products; the experts' outputs o stay in FP32 until the one rounding of y.  The time is
+// that of streaming 4.25 bits for each weight of the active experts.
 //
 // A wave reads a tile (16 weight rows x 128 of K, 1 KiB in a row) with one 16-byte load per
 // lane: lane 16 q + n holds the block of 32 columns 128 s + 32 q of row n, with one scale.
@@ -17,13 +18,21 @@
 namespace moe {
 namespace {
 
-constexpr int kB = 4;                // tiles along K with loads in flight per wave
-
 // Scales of tiles s .. s + 3 of this lane's block, one byte each, from the words of a row tile
 __device__ __forceinline__ uint32_t scale_bytes(const uint32_t* words, int s, int groups) {
     const int g0 = s >> 2, g1 = g0 + 1 < groups ? g0 + 1 : g0;
     const uint32_t lo = words[g0 * 64], hi = words[g1 * 64];
     return __builtin_amdgcn_alignbit(hi, lo, 8 * (s & 3));
+}
+
+// acc += A * B for one quarter of the lanes' blocks: eight codes and their scale to BF16, exact
+__device__ __forceinline__ f32x4_t mma_quarter(bf16x8_t a, uint32_t codes, float x, f32x4_t acc) {
+    const bf16x2_t w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, x, 0);
+    const bf16x2_t w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, x, 1);
+    const bf16x2_t w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, x, 2);
+    const bf16x2_t w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, x, 3);
+    const bf16x8_t w = {w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, acc, 0, 0, 0);
 }
 
 // acc += A * B over the tiles s0 .. s1 - 1: codes and words point at this lane's piece of the
@@ -55,33 +64,167 @@ __device__ __forceinline__ f32x4_t mma_tiles(const uint8_t* codes, const uint32_
             if (s + j < s1) {
                 const float x = __uint_as_float(((sb[j / 4] >> (8 * (j & 3))) & 0xFFu) << 23);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bf16x2_t w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j][i], x, 0);
-                    const bf16x2_t w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j][i], x, 1);
-                    const bf16x2_t w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j][i], x, 2);
-                    const bf16x2_t w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j][i], x, 3);
-                    const bf16x8_t w = {w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j][i], w, acc, 0, 0, 0);
-                }
+                for (int i = 0; i < 4; ++i) acc = mma_quarter(a[j][i], c[j][i], x, acc);
             }
     }
     return acc;
 }
 
-// K split: wave w takes the tiles [S w / 4, S (w + 1) / 4)
-template <bool kSplit> __device__ __forceinline__ void wave_tiles(int S, int& s0, int& s1) {
-    const int w = threadIdx.x >> 6;
-    s0 = kSplit ? __builtin_amdgcn_readfirstlane(S * w / kWaves) : 0;
-    s1 = kSplit ? __builtin_amdgcn_readfirstlane(S * (w + 1) / kWaves) : S;
+// Many items: a wave owns (active expert, kTiles row tiles) from the first load to the last
+// store.  Its work is a sequence of units, one 16-row group of the expert's routed rows by B
+// tiles along K; the codes of the next unit (of the next item too) are loaded before the
+// current unit's products, behind its operand rows, so that the wait for those leaves them in
+// flight.  An operand row piece is four loads for each load of codes; two row tiles share
+// them.  32 tokens of the 128-expert layer (187 MB of W13, 93 MB of W2): one tile and B = 4
+// 37.2 + 22.3 us, two tiles and B = 4 (three waves a SIMD) 31.3 + 19.1, two tiles and B = 2
+// (four) 29.4 + 18.3, four tiles and B = 2 (three) 30.5 + 18.1.
+constexpr int kTiles = 2, kB = 2, kWaveWGs = 4;       // workgroups a CU
+struct Codes4 {
+    u32x4_t c[kTiles][kB];
+    uint32_t sb[kTiles];             // one byte for each of four tiles along K
+};
+struct Unit4 {
+    int item, slot, blk, e, M, e0, m0, s;
+    bool valid;
+};
+template <typename Store>
+__device__ __forceinline__ void wave_items(const DecodeSmem& sm, const void* codes_base, const void* words_base,
+                                           __amdgpu_buffer_rsrc_t ars, int nblk, int S, int row_bytes, int row_div,
+                                           Store&& store) {
+    const int lane = threadIdx.x & 63, n = lane & 15;
+    const int groups = (S + 3) / 4, per = nblk / kTiles;
+    const int items = __builtin_amdgcn_readfirstlane(sm.n_active) * per;
+    const int nw = (int)gridDim.x * kWaves;
+    auto begin = [&](int item) {
+        Unit4 u = {};
+        u.item = item;
+        u.valid = item < items;
+        if (!u.valid) return u;
+        u.slot = item / per;
+        u.blk = (item - u.slot * per) * kTiles;
+        u.e = __builtin_amdgcn_readfirstlane(sm.slot_expert[u.slot]);
+        u.e0 = __builtin_amdgcn_readfirstlane(sm.pfx[u.e]);
+        u.M = __builtin_amdgcn_readfirstlane(sm.pfx[u.e + 1]) - u.e0;
+        u.m0 = u.s = 0;
+        return u;
+    };
+    auto after = [&](Unit4 u) {
+        u.s += kB;
+        if (u.s < S) return u;
+        u.s = 0;
+        u.m0 += 16;
+        if (u.m0 < u.M) return u;
+        return begin(u.item + nw);
+    };
+    auto load = [&](const Unit4& u, Codes4& w) {
+        const size_t tile = (size_t)u.e * nblk + u.blk;
+        const uint8_t* codes = static_cast<const uint8_t*>(codes_base) + (tile * S + u.s) * 1024 + lane * 16;
+        const uint32_t* words = static_cast<const uint32_t*>(words_base) + (tile * groups + (u.s >> 2)) * 64 + lane;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+            for (int j = 0; j < kB; ++j)
+                if (u.s + j < S)
+                    w.c[t][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(codes + (size_t)(t * S + j) * 1024));
+            w.sb[t] = words[t * groups * 64];
+        }
+    };
+    Unit4 u = begin((int)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)));
+    if (!u.valid) return;
+    Codes4 cur, next;
+    load(u, cur);
+    f32x4_t acc[kTiles] = {};
+    bf16x8_t a[kB][4] = {};
+    while (true) {
+        const int m = u.m0 + n;
+        if (m < u.M) {                                  // the rows of other lanes are never stored
+            const uint32_t ao = (uint32_t)(sm.ent[u.e0 + m] / row_div) * (uint32_t)row_bytes + 64u * (lane >> 4) + 256u * u.s;
+#pragma unroll
+            for (int j = 0; j < kB; ++j)
+                if (u.s + j < S)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        a[j][i] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(ars, ao + 256u * j + 16u * i, 0, 0));
+        }
+        const Unit4 v = after(u);
+        if (v.valid) load(v, next);
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+            if (u.s + j < S)
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    const float x = __uint_as_float(((cur.sb[t] >> (8 * ((u.s & 3) + j))) & 0xFFu) << 23);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t] = mma_quarter(a[j][i], cur.c[t][j][i], x, acc[t]);
+                }
+        if (u.s + kB >= S) {
+            store(u, acc);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        if (!v.valid) return;
+        u = v;
+        cur = next;
+    }
 }
 
-template <bool kSplit, int kAct>
-__global__ __launch_bounds__(kThreads, 3) void decode4_w13(DecodeArgs g) {
+template <int kAct>
+__global__ __launch_bounds__(kThreads, kWaveWGs) void decode4_w13_wave(DecodeArgs g) {
+    __shared__ DecodeSmem sm;
+    decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, blockIdx.x == 0);
+    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4, I = g.I;
+    wave_items(sm, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), I / 8, g.d / 128, 2 * g.d, g.k,
+                     [&](const Unit4& u, f32x4_t (&acc)[kTiles]) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            float up[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) up[z] = __shfl_down(acc[t][z], 8, 16);
+            if (n < 8) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int mm = u.m0 + 4 * kq + z;
+                    if (mm < u.M)
+                        g.a[(size_t)sm.ent[u.e0 + mm] * I + (u.blk + t) * 8 + n] = (uint16_t)f32_to_bf16(act_f<kAct>(acc[t][z]) * up[z]);
+                }
+            }
+        }
+    });
+}
+
+__global__ __launch_bounds__(kThreads, kWaveWGs) void decode4_w2_wave(DecodeArgs g) {
+    __shared__ DecodeSmem sm;
+    decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, false);
+    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4, d = g.d;
+    float* o = reinterpret_cast<float*>(g.o);
+    wave_items(sm, g.w2, g.w2_scale, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * g.I * 2u), d / 16, g.I / 128, 2 * g.I, 1,
+                     [&](const Unit4& u, f32x4_t (&acc)[kTiles]) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int mm = u.m0 + 4 * kq + z;
+                if (mm < u.M) o[(size_t)sm.ent[u.e0 + mm] * d + (u.blk + t) * 16 + n] = acc[t][z];
+            }
+    });
+}
+
+// Few items: a workgroup per (active expert, row tile), its four waves a quarter of K each: all
+// of the item's loads are in flight at once, and the partial sums meet in LDS.
+constexpr int kSplitWGs = 3;
+__device__ __forceinline__ void wave_tiles(int S, int& s0, int& s1) {
+    const int w = threadIdx.x >> 6;
+    s0 = __builtin_amdgcn_readfirstlane(S * w / kWaves);
+    s1 = __builtin_amdgcn_readfirstlane(S * (w + 1) / kWaves);
+}
+
+template <int kAct>
+__global__ __launch_bounds__(kThreads, kSplitWGs) void decode4_w13_split(DecodeArgs g) {
     __shared__ DecodeSmem sm;
     __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
     int par = 0;
     const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
-    const bool lead = !kSplit || threadIdx.x < MOE_WAVE;
+    const bool lead = threadIdx.x < MOE_WAVE;
     const int d = g.d, I = g.I, k = g.k, nIB = I / 8, S = d / 128, groups = (S + 3) / 4;
     const bool one = g.T == 1;
     int items;
@@ -94,8 +237,8 @@ __global__ __launch_bounds__(kThreads, 3) void decode4_w13(DecodeArgs g) {
         items = sm.n_active * nIB;
     }
     int s0, s1;
-    wave_tiles<kSplit>(S, s0, s1);
-    for_items<kSplit>(items, nIB, [&](int slot, int ib) {
+    wave_tiles(S, s0, s1);
+    for_items<true>(items, nIB, [&](int slot, int ib) {
         int e, M, e0;
         if (!slot_info(g, sm, one, slot, e, M, e0)) return;
         auto entry = [&](int m) { return one ? e0 : sm.ent[e0 + m]; };
@@ -105,8 +248,8 @@ __global__ __launch_bounds__(kThreads, 3) void decode4_w13(DecodeArgs g) {
         for (int m0 = 0; m0 < M; m0 += 16) {
             const int m = m0 + n;
             const uint32_t ao = m < M ? (uint32_t)((entry(m) / k) * d) * 2u : kNoRow;
-            const f32x4_t acc = reduce_waves<kSplit>(
-                mma_tiles<kB>(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.T * d * 2u), ao, s0, s1), red, par);
+            const f32x4_t acc = reduce_waves<true>(
+                mma_tiles<4>(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.T * d * 2u), ao, s0, s1), red, par);
             float up[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) up[z] = __shfl_down(acc[z], 8, 16);
@@ -122,18 +265,17 @@ __global__ __launch_bounds__(kThreads, 3) void decode4_w13(DecodeArgs g) {
     });
 }
 
-template <bool kSplit>
-__global__ __launch_bounds__(kThreads, 3) void decode4_w2(DecodeArgs g) {
+__global__ __launch_bounds__(kThreads, kSplitWGs) void decode4_w2_split(DecodeArgs g) {
     __shared__ DecodeSmem sm;
     __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
     int par = 0;
     const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
-    const bool lead = !kSplit || threadIdx.x < MOE_WAVE;
+    const bool lead = threadIdx.x < MOE_WAVE;
     const int d = g.d, I = g.I, nNB = d / 16, S = I / 128, groups = (S + 3) / 4;
     decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, false);
     int s0, s1;
-    wave_tiles<kSplit>(S, s0, s1);
-    for_items<kSplit>(sm.n_active * nNB, nNB, [&](int slot, int nb) {
+    wave_tiles(S, s0, s1);
+    for_items<true>(sm.n_active * nNB, nNB, [&](int slot, int nb) {
         int e, M, e0;
         slot_info(g, sm, false, slot, e, M, e0);
         const size_t tile = (size_t)e * nNB + nb;
@@ -142,14 +284,14 @@ __global__ __launch_bounds__(kThreads, 3) void decode4_w2(DecodeArgs g) {
         for (int m0 = 0; m0 < M; m0 += 16) {
             const int m = m0 + n;
             const uint32_t ao = m < M ? (uint32_t)(sm.ent[e0 + m] * I) * 2u : kNoRow;
-            const f32x4_t acc = reduce_waves<kSplit>(
-                mma_tiles<kB>(codes, words, groups, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * I * 2u), ao, s0, s1), red,
+            const f32x4_t acc = reduce_waves<true>(
+                mma_tiles<4>(codes, words, groups, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * I * 2u), ao, s0, s1), red,
                 par);
             if (lead) {
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     const int mm = m0 + 4 * kq + z;
-                    if (mm < M) g.o[(size_t)sm.ent[e0 + mm] * d + nb * 16 + n] = (uint16_t)f32_to_bf16(acc[z]);
+                    if (mm < M) reinterpret_cast<float*>(g.o)[(size_t)sm.ent[e0 + mm] * d + nb * 16 + n] = acc[z];
                 }
             }
         }
@@ -192,25 +334,43 @@ __global__ __launch_bounds__(kThreads, 1) void decode4_w2_one(DecodeArgs g) {
         __syncthreads();
         if (tid < 8) {
             float y = 0.f;
-            for (int j = 0; j < k; ++j) y = __builtin_fmaf(sc[j], bf16_to_f32(f32_to_bf16(ov[j][tid])), y);
+            for (int j = 0; j < k; ++j) y = __builtin_fmaf(sc[j], ov[j][tid], y);
             g.y[n0 + tid] = (uint16_t)f32_to_bf16(y);
         }
         __syncthreads();
     }
 }
 
-// A workgroup per item with K split over its waves while that leaves wave slots empty, else a
-// wave per item.
+// y[t] = sum_j s[t][j] o[t*k + j] in FP32, j ascending from +0.0; four features a thread
+__global__ __launch_bounds__(kThreads) void decode4_combine(DecodeArgs g) {
+    const int t = blockIdx.y, n = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (n >= g.d) return;
+    const float* o = reinterpret_cast<const float*>(g.o) + (size_t)t * g.k * g.d + n;
+    f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int j = 0; j < g.k; ++j) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(o + (size_t)j * g.d);
+        const float s = g.scores[t * g.k + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(s, v[i], y[i]);
+    }
+    *reinterpret_cast<uint2*>(g.y + (size_t)t * g.d + n) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+}
+
+#ifndef D4_SPLIT
+#define D4_SPLIT 16
+#endif
+// nblk row tiles for each of at most `slots` active experts
 template <class K1, class K2>
 hipError_t launch4(K1 wave_kernel, K2 split_kernel, const DecodeArgs& g, int nblk, int num_cu, hipStream_t s) {
     const int R = g.T * g.k;
     const int slots = R < g.E ? R : g.E;
     const int items = slots * nblk;
-    const int cap = 3 * num_cu;
-    if (items < cap * kWaves) {
+    if (items < D4_SPLIT * num_cu) {
+        const int cap = kSplitWGs * num_cu;
         hipLaunchKernelGGL(split_kernel, dim3(items < cap ? items : cap), dim3(kThreads), 0, s, g);
     } else {
-        const int grid = (items + kWaves - 1) / kWaves;
+        const int grid = (items / kTiles + kWaves - 1) / kWaves, cap = kWaveWGs * num_cu;
         hipLaunchKernelGGL(wave_kernel, dim3(grid < cap ? grid : cap), dim3(kThreads), 0, s, g);
     }
     return hipGetLastError();
@@ -221,9 +381,9 @@ hipError_t launch4(K1 wave_kernel, K2 split_kernel, const DecodeArgs& g, int nbl
 hipError_t launch_decode4_w13(const DecodeArgs& g, int num_cu, hipStream_t s) {
     if (g.T * g.k <= 0) return hipSuccess;
     if (g.T * g.k > kMaxDecodeRows || g.d % 128 != 0 || g.I % 128 != 0) return hipErrorInvalidValue;
-    if (g.act == kActGeGLU) return launch4(decode4_w13<false, kActGeGLU>, decode4_w13<true, kActGeGLU>, g, g.I / 8, num_cu, s);
-    if (g.act == kActReGLU) return launch4(decode4_w13<false, kActReGLU>, decode4_w13<true, kActReGLU>, g, g.I / 8, num_cu, s);
-    return launch4(decode4_w13<false, kActSwiGLU>, decode4_w13<true, kActSwiGLU>, g, g.I / 8, num_cu, s);
+    if (g.act == kActGeGLU) return launch4(decode4_w13_wave<kActGeGLU>, decode4_w13_split<kActGeGLU>, g, g.I / 8, num_cu, s);
+    if (g.act == kActReGLU) return launch4(decode4_w13_wave<kActReGLU>, decode4_w13_split<kActReGLU>, g, g.I / 8, num_cu, s);
+    return launch4(decode4_w13_wave<kActSwiGLU>, decode4_w13_split<kActSwiGLU>, g, g.I / 8, num_cu, s);
 }
 
 hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
@@ -234,7 +394,10 @@ hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
         hipLaunchKernelGGL(decode4_w2_one, dim3(grid < cap ? grid : cap), dim3(kThreads), 0, s, g);
         return hipGetLastError();
     }
-    return launch4(decode4_w2<false>, decode4_w2<true>, g, g.d / 16, num_cu, s);
+    const hipError_t e = launch4(decode4_w2_wave, decode4_w2_split, g, g.d / 16, num_cu, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(decode4_combine, dim3((g.d / 4 + kThreads - 1) / kThreads, g.T), dim3(kThreads), 0, s, g);
+    return hipGetLastError();
 }
 
 }  // namespace moe

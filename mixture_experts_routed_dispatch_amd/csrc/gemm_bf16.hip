@@ -1106,9 +1106,9 @@ hipError_t launch_mode(const GemmArgs& g, int num_cu, hipStream_t s) {
 static hipError_t expand_for(GemmMode mode, GemmArgs& g, hipStream_t s) {
     const bool w13 = mode == FWD_W13;
     if (!w13 && mode != FWD_W2) return hipErrorInvalidValue;
-    const hipError_t e =
-        w13 ? launch_mxfp4_expand(reinterpret_cast<const uint8_t*>(g.w13), g.w13_scale, g.E, 2 * g.I, g.d, g.I, true, g.expanded, s)
-            : launch_mxfp4_expand(reinterpret_cast<const uint8_t*>(g.w2), g.w2_scale, g.E, g.d, g.I, g.I, false, g.expanded, s);
+    const Mxfp4Args m{{w13 ? mxfp4_w13(g.expanded, g.w13, g.w13_scale, g.E, g.I, g.d)
+                           : mxfp4_w2(g.expanded, g.w2, g.w2_scale, g.E, g.I, g.d)}};
+    const hipError_t e = launch_mxfp4_expand(m, s);
     if (w13) g.w13 = g.expanded;
     else g.w2 = g.expanded;
     g.w13_scale = g.w2_scale = nullptr;

@@ -179,7 +179,7 @@ struct DecodeArgs {
 hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
 hipError_t launch_decode_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
 // One token: W2 of all k experts and the score-weighted combine into y (a launch in place
-// of decode_w2 and combine).
+// of decode_w2 and combine); with MXFP4 weights any number of tokens.
 constexpr int kMaxTopK = 32;
 hipError_t launch_decode_w2_one(const DecodeArgs& g, int num_cu, hipStream_t s);
 // "Mega" decode: W13 + activation + W2 chunked over I in one launch (chunks of
@@ -189,14 +189,32 @@ int mega_chunk(int T, int k);
 hipError_t launch_mega_decode(const DecodeArgs& g, float* part, int num_cu, hipStream_t s);
 
 // MXFP4 weights (E2M1 codes, E8M0 scale per 32 along K) in the layout of the decode kernels,
-// from and to BF16 [E, N, K]; w13: N = 2I with gate and up rows interleaved by 8 in the tiles.
-// K a multiple of 128, N of 16 (w13: I of 8).
-hipError_t launch_mxfp4_pack(const uint16_t* w, int E, int N, int K, int I, bool w13, uint8_t* codes,
-                             uint8_t* scales, hipStream_t s);
-hipError_t launch_mxfp4_expand(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, int I, bool w13,
-                               uint16_t* w, hipStream_t s);
-// Decode with MXFP4 weights: W13 with the activation; W2 (into o; for one token with the
-// combine into y)
+// from and to BF16, one or two matrices [E, N, K] a launch (w NULL: none).  K a multiple of
+// 128, N of 16; w13: N = 2I, gate and up rows interleaved by 8 in the tiles.
+struct Mxfp4Matrix {
+    uint16_t* w;              // BF16: read by the packing, written by the expansion
+    uint8_t* codes;
+    uint32_t* scales;
+    int64_t units;            // set by the launcher
+    int E, N, K;
+    bool w13;
+};
+struct Mxfp4Args {
+    Mxfp4Matrix m[2];
+};
+hipError_t launch_mxfp4_pack(Mxfp4Args g, hipStream_t s);
+hipError_t launch_mxfp4_expand(Mxfp4Args g, hipStream_t s);
+inline Mxfp4Matrix mxfp4_w13(const void* w, const void* codes, const void* scales, int E, int I, int d) {
+    return {static_cast<uint16_t*>(const_cast<void*>(w)), static_cast<uint8_t*>(const_cast<void*>(codes)),
+            static_cast<uint32_t*>(const_cast<void*>(scales)), 0, E, 2 * I, d, true};
+}
+inline Mxfp4Matrix mxfp4_w2(const void* w, const void* codes, const void* scales, int E, int I, int d) {
+    Mxfp4Matrix m = mxfp4_w13(w, codes, scales, E, I, d);
+    m.N = d; m.K = I; m.w13 = false;
+    return m;
+}
+// Decode with MXFP4 weights: W13 with the activation; W2 with the combine into y, by way of
+// FP32 expert outputs in o ([T*k, d] floats; one token: none)
 hipError_t launch_decode4_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
 hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
 
@@ -250,7 +268,7 @@ hipError_t launch_route_grad(RouterGradArgs g, bool sigmoid, bool f32, hipStream
 
 // Norms around the block (norm.hip): d a multiple of 8, at most kNormMaxD.
 constexpr int kNormMaxD = 16384;
-constexpr int kNormBlocks = 256;       // workgroups of the backward, at most: rows of partial sums
+constexpr int kNormBlocks = 512;       // workgroups of the backward, at most: rows of partial sums
 constexpr int kGateNone = 0, kGateChannel = 1, kGateToken = 2;
 struct NormArgs {
     int T, d, gate_kind;
@@ -279,7 +297,7 @@ struct NormGradArgs {
     float* dw_post;           // [d]
     float* dgate;             // [d] or [T]
     float* dw_pre;            // [d]
-    float* part;              // [kNormBlocks, 3, d] partial column sums
+    float* part;              // [kNormBlocks, 2, d] partial column sums
 };
 hipError_t launch_norm_grad(const NormGradArgs& g, bool f32, hipStream_t s);
 

@@ -216,7 +216,9 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     const bool mxt = mx && c.training;
     // a in BF16: the BF16 path's W2 operand; MXFP8 training keeps it for the weight gradient
     p->off_a = (!mx || c.training) ? take(2 * (size_t)R * c.I) : 0;
-    p->off_o = take(2 * (size_t)R * c.d);
+    // the experts' outputs: BF16, or FP32 in the MXFP4 decode, which rounds y alone
+    p->o_bytes = (w4 && p->decode ? 4 : 2) * (size_t)R * c.d;
+    p->off_o = take(p->o_bytes);
     const size_t h_bytes = 2 * (size_t)R * 2 * c.I;
     p->off_h = (c.training && !c.recompute_h) ? take(h_bytes) : 0;
     // BF16 training takes the router gradient from the W2 data-gradient partials, so the
@@ -325,7 +327,7 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
     if (p->dh_aliased)
         region("o", 2 * (size_t)R * c.d, "fwd/bwd", "expert outputs [R, d] BF16; in the backward dh (g, u gradient [R, 2I])");
     else
-        saved_region("o", 2 * (size_t)R * c.d, "expert outputs [R, d] BF16");
+        saved_region("o", p->o_bytes, p->o_bytes == 2 * (size_t)R * c.d ? "expert outputs [R, d] BF16" : "expert outputs [R, d] FP32");
     if (c.training) {
         const size_t hb = 2 * (size_t)R * 2 * c.I;
         if (c.recompute_h)
@@ -483,7 +485,7 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         }
         hipError_t e = staged(p, MOE_STAGE_DECODE_W13, s, [&] { return launch_decode_w13(dg, p->num_cu, s); });
         if (e != hipSuccess) return MOE_ERR_HIP;
-        if (c.T == 1) {
+        if (c.T == 1 || w4) {                          // W2 with the combine
             e = staged(p, MOE_STAGE_DECODE_W2, s, [&] { return launch_decode_w2_one(dg, p->num_cu, s); });
             return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
         }

@@ -26,20 +26,27 @@ __device__ __forceinline__ int tile_row(int tile, int n, int I, bool w13) {
     return w13 ? (n < 8 ? 8 * tile + n : I + 8 * tile + n - 8) : 16 * tile + n;
 }
 
+// One launch takes both matrices: waves go over the units of the first, then the second's.
+template <typename F> __device__ __forceinline__ void for_units(const Mxfp4Args& g, F&& f) {
+    const int64_t step = (int64_t)gridDim.x * (kThreads / MOE_WAVE);
+    const int64_t total = g.m[0].units + g.m[1].units;
+    for (int64_t u = (int64_t)blockIdx.x * (kThreads / MOE_WAVE) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+         u < total; u += step) {
+        if (u < g.m[0].units) f(g.m[0], u);
+        else f(g.m[1], u - g.m[0].units);
+    }
+}
+
 // A wave takes four tiles along K of one row tile: each lane quantizes the block that is its
 // piece of each, so that codes leave as whole KiB and scales as whole words.
-__global__ __launch_bounds__(kThreads) void mxfp4_pack_kernel(const uint16_t* __restrict__ w, int E, int N, int K,
-                                                              int I, bool w13, uint8_t* __restrict__ codes,
-                                                              uint32_t* __restrict__ scales) {
+__global__ __launch_bounds__(kThreads) void mxfp4_pack_kernel(Mxfp4Args args) {
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-    const int S = K / 128, groups = (S + 3) / 4, tiles = N / 16;
-    const int64_t units = (int64_t)E * tiles * groups;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / MOE_WAVE);
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / MOE_WAVE) + (threadIdx.x >> 6); u < units; u += step) {
+    for_units(args, [&](const Mxfp4Matrix& mat, int64_t u) {
+        const int K = mat.K, N = mat.N, S = K / 128, groups = (S + 3) / 4, tiles = N / 16;
         const int64_t rt = u / groups;                  // expert and row tile
         const int g = (int)(u - rt * groups);
         const int e = (int)(rt / tiles), tile = (int)(rt - (int64_t)e * tiles);
-        const uint16_t* src = w + ((int64_t)e * N + tile_row(tile, n, I, w13)) * K + 512 * g + 32 * q;
+        const uint16_t* src = mat.w + ((int64_t)e * N + tile_row(tile, n, N / 2, mat.w13)) * K + 512 * g + 32 * q;
         uint32_t word = 0;
         uint4 v[4][4];
 #pragma unroll
@@ -75,24 +82,20 @@ __global__ __launch_bounds__(kThreads) void mxfp4_pack_kernel(const uint16_t* __
                 r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2_t, b[4 * c + 3]), x, 3);
                 out[c] = r;
             }
-            *reinterpret_cast<uint4*>(codes + ((rt * S + 4 * g + j) * 64 + lane) * 16) =
+            *reinterpret_cast<uint4*>(mat.codes + ((rt * S + 4 * g + j) * 64 + lane) * 16) =
                 make_uint4(out[0], out[1], out[2], out[3]);
             word |= (uint32_t)byte << (8 * j);
         }
-        scales[(rt * groups + g) * 64 + lane] = word;
-    }
+        mat.scales[(rt * groups + g) * 64 + lane] = word;
+    });
 }
 
 // A wave expands one tile: for each of four rounds, lanes 16 r .. 16 r + 15 write the 256
 // consecutive bytes of tile row 4 round + r.
-__global__ __launch_bounds__(kThreads) void mxfp4_expand_kernel(const uint8_t* __restrict__ codes,
-                                                                const uint32_t* __restrict__ scales, int E, int N,
-                                                                int K, int I, bool w13, uint16_t* __restrict__ w) {
+__global__ __launch_bounds__(kThreads) void mxfp4_expand_kernel(Mxfp4Args args) {
     const int lane = threadIdx.x & 63, c8 = lane & 15, q = c8 >> 2;
-    const int S = K / 128, groups = (S + 3) / 4, tiles = N / 16;
-    const int64_t units = (int64_t)E * tiles * S;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / MOE_WAVE);
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / MOE_WAVE) + (threadIdx.x >> 6); u < units; u += step) {
+    for_units(args, [&](const Mxfp4Matrix& mat, int64_t u) {
+        const int K = mat.K, N = mat.N, S = K / 128, groups = (S + 3) / 4, tiles = N / 16;
         const int64_t rt = u / S;
         const int s = (int)(u - rt * S);
         const int e = (int)(rt / tiles), tile = (int)(rt - (int64_t)e * tiles);
@@ -100,8 +103,8 @@ __global__ __launch_bounds__(kThreads) void mxfp4_expand_kernel(const uint8_t* _
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int n = 4 * r + (lane >> 4);
-            code[r] = *reinterpret_cast<const uint32_t*>(codes + (u * 64 + 16 * q + n) * 16 + 4 * (c8 & 3));
-            word[r] = scales[(rt * groups + (s >> 2)) * 64 + 16 * q + n];
+            code[r] = *reinterpret_cast<const uint32_t*>(mat.codes + (u * 64 + 16 * q + n) * 16 + 4 * (c8 & 3));
+            word[r] = mat.scales[(rt * groups + (s >> 2)) * 64 + 16 * q + n];
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -112,33 +115,34 @@ __global__ __launch_bounds__(kThreads) void mxfp4_expand_kernel(const uint8_t* _
             o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[r], x, 1));
             o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[r], x, 2));
             o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[r], x, 3));
-            *reinterpret_cast<uint4*>(w + ((int64_t)e * N + tile_row(tile, n, I, w13)) * K + 128 * s + 8 * c8) = o;
+            *reinterpret_cast<uint4*>(mat.w + ((int64_t)e * N + tile_row(tile, n, N / 2, mat.w13)) * K + 128 * s + 8 * c8) = o;
         }
-    }
+    });
 }
 
-int grid_of(int64_t units) {
-    const int64_t b = (units + kThreads / MOE_WAVE - 1) / (kThreads / MOE_WAVE);
+int grid_of(const Mxfp4Args& g) {
+    const int64_t b = (g.m[0].units + g.m[1].units + kThreads / MOE_WAVE - 1) / (kThreads / MOE_WAVE);
     return (int)(b < 8192 ? b : 8192);
+}
+bool shapes_ok(const Mxfp4Args& g) {
+    for (const Mxfp4Matrix& m : g.m)
+        if (m.w && (m.N % 16 != 0 || m.K % 128 != 0)) return false;
+    return true;
 }
 
 }  // namespace
 
-hipError_t launch_mxfp4_pack(const uint16_t* w, int E, int N, int K, int I, bool w13, uint8_t* codes,
-                             uint8_t* scales, hipStream_t s) {
-    if (N % 16 != 0 || K % 128 != 0) return hipErrorInvalidValue;
-    const int64_t units = (int64_t)E * (N / 16) * ((K / 128 + 3) / 4);
-    hipLaunchKernelGGL(mxfp4_pack_kernel, dim3(grid_of(units)), dim3(kThreads), 0, s, w, E, N, K, I, w13, codes,
-                       reinterpret_cast<uint32_t*>(scales));
+hipError_t launch_mxfp4_pack(Mxfp4Args g, hipStream_t s) {
+    if (!shapes_ok(g)) return hipErrorInvalidValue;
+    for (Mxfp4Matrix& m : g.m) m.units = m.w ? (int64_t)m.E * (m.N / 16) * ((m.K / 128 + 3) / 4) : 0;
+    hipLaunchKernelGGL(mxfp4_pack_kernel, dim3(grid_of(g)), dim3(kThreads), 0, s, g);
     return hipGetLastError();
 }
 
-hipError_t launch_mxfp4_expand(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, int I, bool w13,
-                               uint16_t* w, hipStream_t s) {
-    if (N % 16 != 0 || K % 128 != 0) return hipErrorInvalidValue;
-    const int64_t units = (int64_t)E * (N / 16) * (K / 128);
-    hipLaunchKernelGGL(mxfp4_expand_kernel, dim3(grid_of(units)), dim3(kThreads), 0, s, codes,
-                       reinterpret_cast<const uint32_t*>(scales), E, N, K, I, w13, w);
+hipError_t launch_mxfp4_expand(Mxfp4Args g, hipStream_t s) {
+    if (!shapes_ok(g)) return hipErrorInvalidValue;
+    for (Mxfp4Matrix& m : g.m) m.units = m.w ? (int64_t)m.E * (m.N / 16) * (m.K / 128) : 0;
+    hipLaunchKernelGGL(mxfp4_expand_kernel, dim3(grid_of(g)), dim3(kThreads), 0, s, g);
     return hipGetLastError();
 }
 

@@ -325,6 +325,7 @@ class Layer:
         import torch
         self.T, self.d, self.I, self.E, self.k = T, d, I, E, k
         self.precision = precision
+        self._mxfp4 = None
         self.plan = moe_plan(T, d, I, E, k, precision, int(bool(training)), path,
                              int(bool(wgrad_accumulate)), int(bool(recompute_h)), int(activation),
                              int(bool(mega)))
@@ -406,14 +407,12 @@ class Layer:
         dev = w13.device
         E, I, d = self.E, self.I, self.d
         if self.precision == MOE_MXFP4:
+            (n13, n2), stream = self._mxfp4_layout(), _stream(stream)
             _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
             _check("w2", w2, (E, d, I), torch.bfloat16, dev)
-            w13_q = torch.empty((E, I * d), dtype=torch.uint8, device=dev)
-            w13_s = torch.empty((E, 2 * I // 16, (d + 511) // 512, 64, 4), dtype=torch.uint8, device=dev)
-            w2_q = torch.empty((E, d * I // 2), dtype=torch.uint8, device=dev)
-            w2_s = torch.empty((E, d // 16, (I + 511) // 512, 64, 4), dtype=torch.uint8, device=dev)
-            moe_prepare_weights(self.plan, _ptr(w13), _ptr(w2), _ptr(w13_q), _ptr(w13_s), _ptr(w2_q), _ptr(w2_s),
-                                _stream(stream))
+            w13_q, w13_s, w2_q, w2_s = (torch.empty_strided(*n, dtype=torch.uint8, device=dev) for n in n13 + n2)
+            moe_prepare_weights(self.plan, w13.data_ptr(), w2.data_ptr(), w13_q.data_ptr(), w13_s.data_ptr(),
+                                w2_q.data_ptr(), w2_s.data_ptr(), stream)
             return w13_q, w13_s, w2_q, w2_s
         w13_q = torch.empty((E, 2 * I, d), dtype=torch.uint8, device=dev)
         # scales block-major: [K/128, rows, 4] (see moe_prepare_weights in include/moe.h)
@@ -424,16 +423,23 @@ class Layer:
                             _ptr(w2_s), _stream(stream))
         return w13_q, w13_s, w2_q, w2_s
 
+    def _mxfp4_layout(self):
+        """(codes, scales) of W13 and of W2, each as shape and strides."""
+        if self._mxfp4 is None:
+            E, I, d = self.E, self.I, self.d
+            self._mxfp4 = ((_dense(E, I * d), _dense(E, 2 * I // 16, (d + 511) // 512, 64, 4)),
+                           (_dense(E, d * I // 2), _dense(E, d // 16, (I + 511) // 512, 64, 4)))
+        return self._mxfp4
+
     def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
         """The BF16 weights (w13, w2) that an MXFP4 layer's prepared weights stand for."""
         import torch
         dev = w13_q.device
         E, I, d = self.E, self.I, self.d
         if self.precision == MOE_MXFP4:
-            _check("w13_q", w13_q, (E, I * d), torch.uint8, dev)
-            _check("w13_s", w13_s, (E, 2 * I // 16, (d + 511) // 512, 64, 4), torch.uint8, dev)
-            _check("w2_q", w2_q, (E, d * I // 2), torch.uint8, dev)
-            _check("w2_s", w2_s, (E, d // 16, (I + 511) // 512, 64, 4), torch.uint8, dev)
+            for name, t, n in zip(("w13_q", "w13_s", "w2_q", "w2_s"), (w13_q, w13_s, w2_q, w2_s),
+                                  sum(self._mxfp4_layout(), ())):
+                _check(name, t, n[0], torch.uint8, dev)
         w13 = torch.empty((E, 2 * I, d), dtype=torch.bfloat16, device=dev)
         w2 = torch.empty((E, d, I), dtype=torch.bfloat16, device=dev)
         w = weights(_ptr(w13_q), _ptr(w2_q), _ptr(w13_s), _ptr(w2_s))
@@ -460,12 +466,22 @@ class Layer:
 
 # ---------------------------------------------------------------- around the layer
 
+def _dense(*shape):
+    """(shape, strides) of a row-major tensor, for torch.empty_strided (1.2 us a call, torch.empty 1.6)."""
+    strides, n = [], 1
+    for size in reversed(shape):
+        strides.append(n)
+        n *= max(size, 1)
+    return shape, tuple(reversed(strides))
+
+
 def _check(name, t, shape, dtype, device):
     """A dense tensor of this shape and type on this device, or ValueError."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s: a contiguous %s tensor of shape %s on %s is needed, got %s %s on %s%s" % (
-            name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
-            "" if t.is_contiguous() else ", not contiguous"))
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    raise ValueError("%s: a contiguous %s tensor of shape %s on %s is needed, got %s %s on %s%s" % (
+        name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
+        "" if t.is_contiguous() else ", not contiguous"))
 
 
 class _OnDevice:
@@ -478,19 +494,20 @@ class _OnDevice:
         device = torch.device(device)
         if device.index is None:
             device = torch.device(device.type, torch.cuda.current_device())
-        self.device = device
+        self.device, self._index = device, device.index
         self.workspace = torch.empty(max(workspace_bytes, 16), dtype=torch.uint8, device=device)
+        self._workspace_ptr, self._workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
 
-    def _call(self, f, stream):
-        """f(raw stream) with this object's device current and `stream` its current stream."""
+    def _call(self, f, stream, *args):
+        """f(raw stream, *args) with this object's device current and `stream` its current stream."""
         import torch
         if stream is not None:
             with torch.cuda.stream(stream):            # also makes the stream's device current
-                return f(int(stream.cuda_stream))
-        if torch.cuda.current_device() != self.device.index:
+                return f(int(stream.cuda_stream), *args)
+        if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self.device):
-                return f(_current_stream(self.device.index))
-        return f(_current_stream(self.device.index))
+                return f(_current_stream(self._index), *args)
+        return f(_current_stream(self._index), *args)
 
 
 class Router(_OnDevice):
@@ -499,6 +516,7 @@ class Router(_OnDevice):
 
     def __init__(self, T, E, k, score=MOE_SCORE_SOFTMAX, normalize=True, scale=1.0, balance_coef=0.0, device="cuda"):
         self.T, self.E, self.k = T, E, k
+        self._per_choice, self._per_expert = _dense(T, k), _dense(E)
         self._cfg = {f32: RouterConfig(T, E, k, int(score), int(bool(normalize)), int(f32), scale, balance_coef)
                      for f32 in (False, True)}
         nbytes = moe_router_workspace_bytes(self._cfg[True])
@@ -521,24 +539,26 @@ class Router(_OnDevice):
         """(ids int32 [T, k], scores f32 [T, k], counts int32 [E], prob_sums f32 [E], loss f32 []);
         without `stats` the last three are None and not computed."""
         import torch
-        cfg, dev = self._logits_cfg(logits), self.device
+        cfg = self._logits_cfg(logits)
         if bias is not None:
-            _check("bias", bias, (self.E,), torch.float32, dev)
+            _check("bias", bias, (self.E,), torch.float32, self.device)
         self._check_mask(mask)
 
-        def call(s):
-            ids = torch.empty((self.T, self.k), dtype=torch.int32, device=dev)
-            scores = torch.empty((self.T, self.k), dtype=torch.float32, device=dev)
-            counts = sums = loss = None
-            if stats:
-                counts = torch.empty(self.E, dtype=torch.int32, device=dev)
-                sums = torch.empty(self.E, dtype=torch.float32, device=dev)
-                loss = torch.empty((), dtype=torch.float32, device=dev)
-            moe_router_forward(cfg, _ptr(logits), _ptr(bias), _ptr(mask), _ptr(ids), _ptr(scores), _ptr(counts),
-                               _ptr(sums), _ptr(loss), _ptr(self.workspace), self.workspace.numel(), s)
-            return ids, scores, counts, sums, loss
+        return self._call(self._forward, stream, cfg, logits, bias, mask, stats)
 
-        return self._call(call, stream)
+    def _forward(self, s, cfg, logits, bias, mask, stats):
+        import torch
+        new, dev, f32, i32 = torch.empty_strided, self.device, torch.float32, torch.int32
+        ids = new(*self._per_choice, dtype=i32, device=dev)
+        scores = new(*self._per_choice, dtype=f32, device=dev)
+        counts = sums = loss = None
+        if stats:
+            counts = new(*self._per_expert, dtype=i32, device=dev)
+            sums = new(*self._per_expert, dtype=f32, device=dev)
+            loss = new((), (), dtype=f32, device=dev)
+        moe_router_forward(cfg, logits.data_ptr(), _ptr(bias), _ptr(mask), ids.data_ptr(), scores.data_ptr(),
+                           _ptr(counts), _ptr(sums), _ptr(loss), self._workspace_ptr, self._workspace_bytes, s)
+        return ids, scores, counts, sums, loss
 
     def backward(self, dscores, logits, ids, counts=None, dloss=None, mask=None, dlogits=None, stream=None):
         """dlogits [T, E] from dscores f32 [T, k] (None: zeros) and dloss f32 [] or [1] (None: the
@@ -556,13 +576,14 @@ class Router(_OnDevice):
             _check("dlogits", dlogits, (self.T, self.E), logits.dtype, dev)
         self._check_mask(mask)
 
-        def call(s):
-            out = torch.empty_like(logits) if dlogits is None else dlogits
-            moe_router_backward(cfg, _ptr(dscores), _ptr(logits), _ptr(mask), _ptr(ids), _ptr(counts), _ptr(dloss),
-                                _ptr(out), s)
-            return out
+        return self._call(self._backward, stream, cfg, dscores, logits, ids, counts, dloss, mask, dlogits)
 
-        return self._call(call, stream)
+    def _backward(self, s, cfg, dscores, logits, ids, counts, dloss, mask, dlogits):
+        import torch
+        out = torch.empty_like(logits) if dlogits is None else dlogits
+        moe_router_backward(cfg, _ptr(dscores), logits.data_ptr(), _ptr(mask), ids.data_ptr(), _ptr(counts),
+                            _ptr(dloss), out.data_ptr(), s)
+        return out
 
 
 class BlockNorm(_OnDevice):
@@ -572,60 +593,66 @@ class BlockNorm(_OnDevice):
     def __init__(self, T, d, eps=1e-6, residual_scale=1.0, gate=MOE_GATE_NONE, residual_f32=False, device="cuda"):
         self.T, self.d, self.gate = T, d, gate
         self.residual_f32 = bool(residual_f32)
+        self._rows = _dense(T, d)
+        self._shape, self._channels = (T, d), (d,)
         self._cfg = NormConfig(T, d, int(gate), int(self.residual_f32), eps, residual_scale)
         nbytes = moe_norm_workspace_bytes(self._cfg)
         if not nbytes:
             moe_norm_forward(self._cfg, 0, 0, 0, 0, 0, 0, 0)
         super().__init__(device, nbytes)
 
-    def _check_args(self, stream_tensors, block_tensors, w_post, gate, w_pre):
+    def _check_args(self, y, w_post, gate, w_pre):
+        """The arguments that both directions take."""
         import torch
-        res = torch.float32 if self.residual_f32 else torch.bfloat16
-        for name, t in stream_tensors:
-            if t is not None:
-                _check(name, t, (self.T, self.d), res, self.device)
-        for name, t in block_tensors:
-            if t is not None:
-                _check(name, t, (self.T, self.d), torch.bfloat16, self.device)
-        for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-            if t is not None:
-                _check(name, t, (self.d,), torch.float32, self.device)
+        dev, f32 = self.device, torch.float32
+        if y is not None:
+            _check("y", y, self._shape, torch.bfloat16, dev)
+        if w_post is not None:
+            _check("w_post", w_post, self._channels, f32, dev)
         if gate is not None:
-            _check("gate", gate, (self.T,) if self.gate == MOE_GATE_TOKEN else (self.d,), torch.float32, self.device)
-        return res
+            _check("gate", gate, (self.T,) if self.gate == MOE_GATE_TOKEN else self._channels, f32, dev)
+        if w_pre is not None:
+            _check("w_pre", w_pre, self._channels, f32, dev)
+        return f32 if self.residual_f32 else torch.bfloat16
 
     def forward(self, x, y=None, w_post=None, gate=None, w_pre=None, z=None, stream=None):
         """(z, h); h is None without w_pre.  Without y, z is x itself.  z may be given (also x)."""
+        res = self._check_args(y, w_post, gate, w_pre)
+        _check("x", x, self._shape, res, self.device)
+        if z is not None:
+            _check("z", z, self._shape, res, self.device)
+        return self._call(self._forward, stream, res, x, y, w_post, gate, w_pre, z)
+
+    def _forward(self, s, res, x, y, w_post, gate, w_pre, z):
         import torch
-        res = self._check_args((("x", x), ("z", z)), (("y", y),), w_post, gate, w_pre)
-
-        def call(s):
-            shape = (self.T, self.d)
-            out = z
-            if out is None and y is not None:
-                out = torch.empty(shape, dtype=res, device=self.device)
-            h = None if w_pre is None else torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-            moe_norm_forward(self._cfg, _ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(out), _ptr(h), s)
-            return x if y is None else out, h
-
-        return self._call(call, stream)
+        if z is None and y is not None:
+            z = torch.empty_strided(*self._rows, dtype=res, device=self.device)
+        h = None if w_pre is None else torch.empty_strided(*self._rows, dtype=torch.bfloat16, device=self.device)
+        moe_norm_forward(self._cfg, x.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(z), _ptr(h), s)
+        return x if y is None else z, h
 
     def backward(self, dz, dh, z, y=None, w_post=None, gate=None, w_pre=None, dx=None, stream=None):
         """(dx, dy, dw_post, dgate, dw_pre), None where there is no such input.  dz None: the stream
         has no gradient but h's.  dx may be given (also dz)."""
         import torch
-        res = self._check_args((("dz", dz), ("z", z), ("dx", dx)), (("dh", dh), ("y", y)), w_post, gate, w_pre)
+        res = self._check_args(y, w_post, gate, w_pre)
+        for name, t in (("dz", dz), ("z", z), ("dx", dx)):
+            if t is not None:
+                _check(name, t, self._shape, res, self.device)
+        if dh is not None:
+            _check("dh", dh, self._shape, torch.bfloat16, self.device)
+        return self._call(self._backward, stream, res, dz, dh, z, y, w_post, gate, w_pre, dx)
 
-        def call(s):
-            def like(t):
-                return None if t is None else torch.empty_like(t)
-            out = dx
-            if out is None:
-                out = torch.empty((self.T, self.d), dtype=res, device=self.device)
-            dy, dw_post, dgate, dw_pre = like(y), like(w_post), like(gate), like(w_pre)
-            moe_norm_backward(self._cfg, _ptr(dz), _ptr(dh), _ptr(z), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre),
-                              _ptr(out), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), _ptr(self.workspace),
-                              self.workspace.numel(), s)
-            return out, dy, dw_post, dgate, dw_pre
-
-        return self._call(call, stream)
+    def _backward(self, s, res, dz, dh, z, y, w_post, gate, w_pre, dx):
+        import torch
+        like = torch.empty_like
+        if dx is None:
+            dx = torch.empty_strided(*self._rows, dtype=res, device=self.device)
+        dy = None if y is None else like(y)
+        dw_post = None if w_post is None else like(w_post)
+        dgate = None if gate is None else like(gate)
+        dw_pre = None if w_pre is None else like(w_pre)
+        moe_norm_backward(self._cfg, _ptr(dz), _ptr(dh), _ptr(z), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                          dx.data_ptr(), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), self._workspace_ptr,
+                          self._workspace_bytes, s)
+        return dx, dy, dw_post, dgate, dw_pre
