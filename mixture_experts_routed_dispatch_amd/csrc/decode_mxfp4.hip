@@ -70,232 +70,172 @@ __device__ __forceinline__ f32x4_t mma_tiles(const uint8_t* codes, const uint32_
     return acc;
 }
 
-// Many items: a wave owns (active expert, kTiles row tiles) from the first load to the last
-// store.  Its work is a sequence of units, one 16-row group of the expert's routed rows by B
-// tiles along K; the codes of the next unit (of the next item too) are loaded before the
-// current unit's products, behind its operand rows, so that the wait for those leaves them in
-// flight.  An operand row piece is four loads for each load of codes; two row tiles share
-// them.  32 tokens of the 128-expert layer (187 MB of W13, 93 MB of W2): one tile and B = 4
-// 37.2 + 22.3 us, two tiles and B = 4 (three waves a SIMD) 31.3 + 19.1, two tiles and B = 2
-// (four) 29.4 + 18.3, four tiles and B = 2 (three) 30.5 + 18.1.
-constexpr int kTiles = 2, kB = 2, kWaveWGs = 4;       // workgroups a CU
-struct Codes4 {
-    u32x4_t c[kTiles][kB];
-    uint32_t sb[kTiles];             // one byte for each of four tiles along K
-};
-struct Unit4 {
-    int item, slot, blk, e, M, e0, m0, s;
-    bool valid;
-};
-template <typename Store>
-__device__ __forceinline__ void wave_items(const DecodeSmem& sm, const void* codes_base, const void* words_base,
-                                           __amdgpu_buffer_rsrc_t ars, int nblk, int S, int row_bytes, int row_div,
-                                           Store&& store) {
-    const int lane = threadIdx.x & 63, n = lane & 15;
-    const int groups = (S + 3) / 4, per = nblk / kTiles;
-    const int items = __builtin_amdgcn_readfirstlane(sm.n_active) * per;
-    const int nw = (int)gridDim.x * kWaves;
-    auto begin = [&](int item) {
-        Unit4 u = {};
-        u.item = item;
-        u.valid = item < items;
-        if (!u.valid) return u;
-        u.slot = item / per;
-        u.blk = (item - u.slot * per) * kTiles;
-        u.e = __builtin_amdgcn_readfirstlane(sm.slot_expert[u.slot]);
-        u.e0 = __builtin_amdgcn_readfirstlane(sm.pfx[u.e]);
-        u.M = __builtin_amdgcn_readfirstlane(sm.pfx[u.e + 1]) - u.e0;
-        u.m0 = u.s = 0;
-        return u;
-    };
-    auto after = [&](Unit4 u) {
-        u.s += kB;
-        if (u.s < S) return u;
-        u.s = 0;
-        u.m0 += 16;
-        if (u.m0 < u.M) return u;
-        return begin(u.item + nw);
-    };
-    auto load = [&](const Unit4& u, Codes4& w) {
-        const size_t tile = (size_t)u.e * nblk + u.blk;
-        const uint8_t* codes = static_cast<const uint8_t*>(codes_base) + (tile * S + u.s) * 1024 + lane * 16;
-        const uint32_t* words = static_cast<const uint32_t*>(words_base) + (tile * groups + (u.s >> 2)) * 64 + lane;
+// a[entry][i0 + n] = act(g) u in BF16, from one W13 tile's D: lane l holds rows 4 (l >> 4) + z
+// of column n = l & 15, gate columns 0..7 and up columns 8..15
+template <int kAct>
+__device__ __forceinline__ void store_a(const DecodeArgs& g, const int* ent, int m0, int M, int i0, f32x4_t acc, bool lead) {
+    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
+    float up[4];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
+    for (int z = 0; z < 4; ++z) up[z] = __shfl_down(acc[z], 8, 16);
+    if (lead && n < 8) {
 #pragma unroll
-            for (int j = 0; j < kB; ++j)
-                if (u.s + j < S)
-                    w.c[t][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(codes + (size_t)(t * S + j) * 1024));
-            w.sb[t] = words[t * groups * 64];
+        for (int z = 0; z < 4; ++z) {
+            const int mm = m0 + 4 * kq + z;
+            if (mm < M) g.a[(size_t)ent[mm] * g.I + i0 + n] = (uint16_t)f32_to_bf16(act_f<kAct>(acc[z]) * up[z]);
         }
-    };
-    Unit4 u = begin((int)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)));
-    if (!u.valid) return;
-    Codes4 cur, next;
-    load(u, cur);
-    f32x4_t acc[kTiles] = {};
-    bf16x8_t a[kB][4] = {};
-    while (true) {
-        const int m = u.m0 + n;
-        if (m < u.M) {                                  // the rows of other lanes are never stored
-            const uint32_t ao = (uint32_t)(sm.ent[u.e0 + m] / row_div) * (uint32_t)row_bytes + 64u * (lane >> 4) + 256u * u.s;
+    }
+}
+// o[entry][n0 + n] in FP32, from one W2 tile's D
+__device__ __forceinline__ void store_o(const DecodeArgs& g, const int* ent, int m0, int M, int n0, f32x4_t acc) {
+    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
 #pragma unroll
-            for (int j = 0; j < kB; ++j)
-                if (u.s + j < S)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        a[j][i] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(ars, ao + 256u * j + 16u * i, 0, 0));
-        }
-        const Unit4 v = after(u);
-        if (v.valid) load(v, next);
-#pragma unroll
-        for (int j = 0; j < kB; ++j)
-            if (u.s + j < S)
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    const float x = __uint_as_float(((cur.sb[t] >> (8 * ((u.s & 3) + j))) & 0xFFu) << 23);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t] = mma_quarter(a[j][i], cur.c[t][j][i], x, acc[t]);
-                }
-        if (u.s + kB >= S) {
-            store(u, acc);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        }
-        if (!v.valid) return;
-        u = v;
-        cur = next;
+    for (int z = 0; z < 4; ++z) {
+        const int mm = m0 + 4 * kq + z;
+        if (mm < M) reinterpret_cast<float*>(g.o)[(size_t)ent[mm] * g.d + n0 + n] = acc[z];
     }
 }
 
+// One token: a workgroup per (slot, row tile), its four waves a quarter of K each: every load of
+// the launch is in flight at once, and the partial sums meet in LDS.
+constexpr int kOneWGs = 3;
 template <int kAct>
-__global__ __launch_bounds__(kThreads, kWaveWGs) void decode4_w13_wave(DecodeArgs g) {
-    __shared__ DecodeSmem sm;
-    decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, blockIdx.x == 0);
-    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4, I = g.I;
-    wave_items(sm, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), I / 8, g.d / 128, 2 * g.d, g.k,
-                     [&](const Unit4& u, f32x4_t (&acc)[kTiles]) {
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            float up[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) up[z] = __shfl_down(acc[t][z], 8, 16);
-            if (n < 8) {
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int mm = u.m0 + 4 * kq + z;
-                    if (mm < u.M)
-                        g.a[(size_t)sm.ent[u.e0 + mm] * I + (u.blk + t) * 8 + n] = (uint16_t)f32_to_bf16(act_f<kAct>(acc[t][z]) * up[z]);
-                }
-            }
-        }
-    });
+__global__ __launch_bounds__(kThreads, kOneWGs) void decode4_w13_one(DecodeArgs g) {
+    __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
+    int par = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0) decode_flags_one_token(g);
+    const int slot = blockIdx.y, e = g.ids[slot];
+    if ((unsigned)e >= (unsigned)g.E) return;
+    const int lane = threadIdx.x & 63;
+    const int S = g.d / 128, groups = (S + 3) / 4, w = threadIdx.x >> 6;
+    const int s0 = __builtin_amdgcn_readfirstlane(S * w / kWaves), s1 = __builtin_amdgcn_readfirstlane(S * (w + 1) / kWaves);
+    const size_t tile = (size_t)e * (g.I / 8) + blockIdx.x;
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(g.w13) + tile * S * 1024 + lane * 16;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w13_scale) + tile * groups * 64 + lane;
+    const f32x4_t acc = reduce_waves<true>(
+        mma_tiles<4>(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.d * 2u), (lane & 15) == 0 ? 0u : kNoRow, s0, s1), red, par);
+    store_a<kAct>(g, &slot, 0, 1, blockIdx.x * 8, acc, threadIdx.x < MOE_WAVE);
 }
 
-__global__ __launch_bounds__(kThreads, kWaveWGs) void decode4_w2_wave(DecodeArgs g) {
-    __shared__ DecodeSmem sm;
-    decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, false);
-    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4, d = g.d;
-    float* o = reinterpret_cast<float*>(g.o);
-    wave_items(sm, g.w2, g.w2_scale, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * g.I * 2u), d / 16, g.I / 128, 2 * g.I, 1,
-                     [&](const Unit4& u, f32x4_t (&acc)[kTiles]) {
+// More tokens: a workgroup's item is (active expert, kTiles row tiles), its four waves a quarter
+// of K each.  A step is one tile along K: kTiles loads of codes, and four of the routed rows
+// that all the tiles share.  Those four are what bounds the kernel when few tiles share them:
+// they occupy the address unit as long as four loads of codes.  W13 and W2 at 32 tokens of the
+// 128-expert layer, 59 experts active (99 and 49 MB):
+//   a wave for each tile over all of K            32.2 and 18.1 us
+//   a wave for two, four tiles over all of K      23.6 and 14.0, 25.1 and 13.0
+//   four, eight tiles and a quarter of K a wave   21.4 and 13.2, 21.9 and 14.0
+// While a step's products run, the next step's operands are in flight, in one of two sets of
+// registers that take turns (a copy from one to the other would wait for the loads); a third
+// set costs a workgroup a CU and is slower (23.0 and 13.1 us).
+constexpr int kTiles = 4, kDepth = 2, kWGs = 4;
+static_assert(kTiles % kWaves == 0, "a wave adds up whole tiles");
+constexpr int kNonTemporal = 2;      // the nt bit of a buffer load
+struct Operands4 {
+    u32x4_t c[kTiles];               // codes
+    uint32_t sb[kTiles];             // scales, a byte for each of four tiles along K
+    bf16x8_t a[4];                   // routed rows
+};
+struct Partials4 {
+    f32x4_t p[2][kWaves][kTiles][MOE_WAVE];
+};
+// One 16-row group (rows at byte offset ao of ars, kNoRow: none) times the item's tiles: this
+// wave's share of K.  codes and words: of the item's first row tile.
+__device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], const void* codes_base, const void* words_base,
+                                              __amdgpu_buffer_rsrc_t ars, uint32_t ao, int S, int s0, int s1) {
+    const int lane = threadIdx.x & 63, groups = (S + 3) / 4;
+    // uniform bases and offsets in scalar registers, one 32-bit lane offset each
+    const __amdgpu_buffer_rsrc_t codes = rows_rsrc(codes_base, (uint32_t)(kTiles * S) * 1024u);
+    const __amdgpu_buffer_rsrc_t words = rows_rsrc(words_base, (uint32_t)(kTiles * groups) * 256u);
+    ao += 64u * (lane >> 4);
+    uint32_t co = lane * 16, so = lane * 4;
+    auto load = [&](Operands4& w, int s) {
+        if (s >= s1) co = so = ao = kNoRow;              // past the last step: no memory is read
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
+            w.c[t] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes, co, (t * S + s) * 1024, kNonTemporal));
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const int mm = u.m0 + 4 * kq + z;
-                if (mm < u.M) o[(size_t)sm.ent[u.e0 + mm] * d + (u.blk + t) * 16 + n] = acc[t][z];
-            }
-    });
+        for (int t = 0; t < kTiles; ++t)
+            w.sb[t] = __builtin_amdgcn_raw_buffer_load_b32(words, so, (t * groups + (s >> 2)) * 256, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w.a[i] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(ars, ao + 16u * i, 256 * s, 0));
+    };
+    auto products = [&](const Operands4& w, int s) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const float x = __uint_as_float(((w.sb[t] >> (8 * (s & 3))) & 0xFFu) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t] = mma_quarter(w.a[i], w.c[t][i], x, acc[t]);
+        }
+    };
+    Operands4 w[kDepth];
+#pragma unroll
+    for (int u = 0; u < kDepth - 1; ++u) load(w[u], s0 + u);
+    for (int s = s0; s < s1; s += kDepth) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) {
+            if (s + u >= s1) return;
+            load(w[(u + kDepth - 1) % kDepth], s + u + kDepth - 1);
+            products(w[u], s + u);
+        }
+    }
 }
 
-// Few items: a workgroup per (active expert, row tile), its four waves a quarter of K each: all
-// of the item's loads are in flight at once, and the partial sums meet in LDS.
-constexpr int kSplitWGs = 3;
-__device__ __forceinline__ void wave_tiles(int S, int& s0, int& s1) {
-    const int w = threadIdx.x >> 6;
-    s0 = __builtin_amdgcn_readfirstlane(S * w / kWaves);
-    s1 = __builtin_amdgcn_readfirstlane(S * (w + 1) / kWaves);
+// The items of this workgroup, its number in the launch and every (number of workgroups)-th;
+// store(entries, how many, first row of the group, row tile, sums) by the wave that has added
+// up the tile's four partial sums, in wave order
+template <typename Store>
+__device__ __forceinline__ void run_items(const DecodeSmem& sm, Partials4& part, const void* codes, const void* words,
+                                          __amdgpu_buffer_rsrc_t ars, int nblk, int S, int row_bytes, int row_div,
+                                          Store&& store) {
+    const int lane = threadIdx.x & 63, n = lane & 15, groups = (S + 3) / 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
+    const int per = nblk / kTiles, items = __builtin_amdgcn_readfirstlane(sm.n_active) * per;
+    int half = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int slot = item / per, blk = (item - slot * per) * kTiles;
+        const int e = __builtin_amdgcn_readfirstlane(sm.slot_expert[slot]);
+        const int e0 = __builtin_amdgcn_readfirstlane(sm.pfx[e]);
+        const int M = __builtin_amdgcn_readfirstlane(sm.pfx[e + 1]) - e0;
+        const size_t tile = (size_t)e * nblk + blk;
+        for (int m0 = 0; m0 < M; m0 += 16) {
+            const uint32_t ao = m0 + n < M ? (uint32_t)(sm.ent[e0 + m0 + n] / row_div) * (uint32_t)row_bytes : kNoRow;
+            f32x4_t acc[kTiles] = {};
+            tile_products(acc, static_cast<const uint8_t*>(codes) + tile * S * 1024,
+                          static_cast<const uint8_t*>(words) + tile * groups * 256, ars, ao, S, s0, s1);
+            // one barrier: the other half is written next, and read only after the next barrier
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) part.p[half][wave][t][lane] = acc[t];
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < kTiles; t += kWaves) {
+                f32x4_t sum = part.p[half][0][t + wave][lane];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) sum += part.p[half][w][t + wave][lane];
+                store(sm.ent + e0, M, m0, blk + t + wave, sum);
+            }
+            half ^= 1;
+        }
+    }
 }
 
 template <int kAct>
-__global__ __launch_bounds__(kThreads, kSplitWGs) void decode4_w13_split(DecodeArgs g) {
+__global__ __launch_bounds__(kThreads, kWGs) void decode4_w13(DecodeArgs g) {
     __shared__ DecodeSmem sm;
-    __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
-    int par = 0;
-    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
-    const bool lead = threadIdx.x < MOE_WAVE;
-    const int d = g.d, I = g.I, k = g.k, nIB = I / 8, S = d / 128, groups = (S + 3) / 4;
-    const bool one = g.T == 1;
-    int items;
-    if (one) {
-        if (blockIdx.x == 0) decode_flags_one_token(g);
-        one_token_slots(sm, g);
-        items = k * nIB;
-    } else {
-        decode_setup(sm, g.ids, g.T, k, g.E, g.status, blockIdx.x == 0);
-        items = sm.n_active * nIB;
-    }
-    int s0, s1;
-    wave_tiles(S, s0, s1);
-    for_items<true>(items, nIB, [&](int slot, int ib) {
-        int e, M, e0;
-        if (!slot_info(g, sm, one, slot, e, M, e0)) return;
-        auto entry = [&](int m) { return one ? e0 : sm.ent[e0 + m]; };
-        const size_t tile = (size_t)e * nIB + ib;
-        const uint8_t* codes = reinterpret_cast<const uint8_t*>(g.w13) + tile * S * 1024 + lane * 16;
-        const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w13_scale) + tile * groups * 64 + lane;
-        for (int m0 = 0; m0 < M; m0 += 16) {
-            const int m = m0 + n;
-            const uint32_t ao = m < M ? (uint32_t)((entry(m) / k) * d) * 2u : kNoRow;
-            const f32x4_t acc = reduce_waves<true>(
-                mma_tiles<4>(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.T * d * 2u), ao, s0, s1), red, par);
-            float up[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) up[z] = __shfl_down(acc[z], 8, 16);
-            if (lead && n < 8) {
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int mm = m0 + 4 * kq + z;
-                    if (mm < M)
-                        g.a[(size_t)entry(mm) * I + ib * 8 + n] = (uint16_t)f32_to_bf16(act_f<kAct>(acc[z]) * up[z]);
-                }
-            }
-        }
-    });
+    __shared__ Partials4 part;
+    decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, blockIdx.x == 0);
+    run_items(sm, part, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), g.I / 8, g.d / 128, 2 * g.d, g.k,
+              [&](const int* ent, int M, int m0, int tile, f32x4_t sum) { store_a<kAct>(g, ent, m0, M, tile * 8, sum, true); });
 }
 
-__global__ __launch_bounds__(kThreads, kSplitWGs) void decode4_w2_split(DecodeArgs g) {
+__global__ __launch_bounds__(kThreads, kWGs) void decode4_w2(DecodeArgs g) {
     __shared__ DecodeSmem sm;
-    __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
-    int par = 0;
-    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
-    const bool lead = threadIdx.x < MOE_WAVE;
-    const int d = g.d, I = g.I, nNB = d / 16, S = I / 128, groups = (S + 3) / 4;
+    __shared__ Partials4 part;
     decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, false);
-    int s0, s1;
-    wave_tiles(S, s0, s1);
-    for_items<true>(sm.n_active * nNB, nNB, [&](int slot, int nb) {
-        int e, M, e0;
-        slot_info(g, sm, false, slot, e, M, e0);
-        const size_t tile = (size_t)e * nNB + nb;
-        const uint8_t* codes = reinterpret_cast<const uint8_t*>(g.w2) + tile * S * 1024 + lane * 16;
-        const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w2_scale) + tile * groups * 64 + lane;
-        for (int m0 = 0; m0 < M; m0 += 16) {
-            const int m = m0 + n;
-            const uint32_t ao = m < M ? (uint32_t)(sm.ent[e0 + m] * I) * 2u : kNoRow;
-            const f32x4_t acc = reduce_waves<true>(
-                mma_tiles<4>(codes, words, groups, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * I * 2u), ao, s0, s1), red,
-                par);
-            if (lead) {
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int mm = m0 + 4 * kq + z;
-                    if (mm < M) reinterpret_cast<float*>(g.o)[(size_t)sm.ent[e0 + mm] * d + nb * 16 + n] = acc[z];
-                }
-            }
-        }
-    });
+    run_items(sm, part, g.w2, g.w2_scale, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * g.I * 2u), g.d / 16, g.I / 128, 2 * g.I, 1,
+              [&](const int* ent, int M, int m0, int tile, f32x4_t sum) { store_o(g, ent, m0, M, tile * 16, sum); });
 }
 
 // One token: W2 of all k experts and the combine, 8 output features per workgroup.  As in the
@@ -357,22 +297,16 @@ __global__ __launch_bounds__(kThreads) void decode4_combine(DecodeArgs g) {
     *reinterpret_cast<uint2*>(g.y + (size_t)t * g.d + n) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
 }
 
-#ifndef D4_SPLIT
-#define D4_SPLIT 16
-#endif
-// nblk row tiles for each of at most `slots` active experts
-template <class K1, class K2>
-hipError_t launch4(K1 wave_kernel, K2 split_kernel, const DecodeArgs& g, int nblk, int num_cu, hipStream_t s) {
-    const int R = g.T * g.k;
-    const int slots = R < g.E ? R : g.E;
-    const int items = slots * nblk;
-    if (items < D4_SPLIT * num_cu) {
-        const int cap = kSplitWGs * num_cu;
-        hipLaunchKernelGGL(split_kernel, dim3(items < cap ? items : cap), dim3(kThreads), 0, s, g);
-    } else {
-        const int grid = (items / kTiles + kWaves - 1) / kWaves, cap = kWaveWGs * num_cu;
-        hipLaunchKernelGGL(wave_kernel, dim3(grid < cap ? grid : cap), dim3(kThreads), 0, s, g);
-    }
+// a workgroup for each item, as far as they fit the chip together (nblk a multiple of kTiles)
+template <class K> hipError_t launch_items(K kernel, const DecodeArgs& g, int nblk, int num_cu, hipStream_t s) {
+    const int R = g.T * g.k, slots = R < g.E ? R : g.E;
+    const int items = slots * (nblk / kTiles), cap = kWGs * num_cu;
+    hipLaunchKernelGGL(kernel, dim3(items < cap ? items : cap), dim3(kThreads), 0, s, g);
+    return hipGetLastError();
+}
+template <int kAct> hipError_t launch_w13(const DecodeArgs& g, int num_cu, hipStream_t s) {
+    if (g.T > 1) return launch_items(decode4_w13<kAct>, g, g.I / 8, num_cu, s);
+    hipLaunchKernelGGL(decode4_w13_one<kAct>, dim3(g.I / 8, g.k), dim3(kThreads), 0, s, g);
     return hipGetLastError();
 }
 
@@ -381,9 +315,9 @@ hipError_t launch4(K1 wave_kernel, K2 split_kernel, const DecodeArgs& g, int nbl
 hipError_t launch_decode4_w13(const DecodeArgs& g, int num_cu, hipStream_t s) {
     if (g.T * g.k <= 0) return hipSuccess;
     if (g.T * g.k > kMaxDecodeRows || g.d % 128 != 0 || g.I % 128 != 0) return hipErrorInvalidValue;
-    if (g.act == kActGeGLU) return launch4(decode4_w13_wave<kActGeGLU>, decode4_w13_split<kActGeGLU>, g, g.I / 8, num_cu, s);
-    if (g.act == kActReGLU) return launch4(decode4_w13_wave<kActReGLU>, decode4_w13_split<kActReGLU>, g, g.I / 8, num_cu, s);
-    return launch4(decode4_w13_wave<kActSwiGLU>, decode4_w13_split<kActSwiGLU>, g, g.I / 8, num_cu, s);
+    if (g.act == kActGeGLU) return launch_w13<kActGeGLU>(g, num_cu, s);
+    if (g.act == kActReGLU) return launch_w13<kActReGLU>(g, num_cu, s);
+    return launch_w13<kActSwiGLU>(g, num_cu, s);
 }
 
 hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
@@ -394,7 +328,7 @@ hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
         hipLaunchKernelGGL(decode4_w2_one, dim3(grid < cap ? grid : cap), dim3(kThreads), 0, s, g);
         return hipGetLastError();
     }
-    const hipError_t e = launch4(decode4_w2_wave, decode4_w2_split, g, g.d / 16, num_cu, s);
+    const hipError_t e = launch_items(decode4_w2, g, g.d / 16, num_cu, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(decode4_combine, dim3((g.d / 4 + kThreads - 1) / kThreads, g.T), dim3(kThreads), 0, s, g);
     return hipGetLastError();
