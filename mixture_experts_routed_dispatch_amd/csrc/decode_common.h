@@ -14,7 +14,7 @@ constexpr int kWaves = kThreads / MOE_WAVE;
 
 struct DecodeSmem {
     int ids[kMaxDecodeRows];       // expert of entry q = t*k + j (-1 when invalid)
-    int cnt[256];                  // routed rows per expert, a byte for each of the four waves
+    int cnt[256];                  // routed rows per expert
     int pfx[257];                  // entries of expert e: ent[pfx[e] .. pfx[e+1])
     int slot_expert[256];          // i-th active expert (ascending id)
     int ent[kMaxDecodeRows];       // entries grouped by expert (ascending id), ascending
@@ -31,42 +31,31 @@ __device__ void decode_setup(DecodeSmem& sm, const int32_t* __restrict__ ids, in
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const bool worker = tid < 256;
     const int R = T * k;
-    int my_e = -1;
-    if (worker) {
-        sm.cnt[tid] = 0;
-        if (tid < R) {
-            const int e = ids[tid];
-            my_e = (unsigned)e < (unsigned)E ? e : -1;
-        }
-        sm.ids[tid] = my_e;
-    }
+    if (worker) sm.cnt[tid] = 0;
     __syncthreads();
-    // the wave's entries with the same expert, by a ballot for each bit of the id; cnt[e] has a
-    // byte for each wave's count (at most 64).  (Counting the earlier entries of the expert one
-    // by one took 3 us of a launch at 256 entries.)
-    uint64_t same = __ballot(my_e >= 0);
-    for (int bit = 1; bit < 256; bit <<= 1) {
-        const uint64_t ones = __ballot((my_e & bit) != 0);
-        same &= (my_e & bit) != 0 ? ones : ~ones;
+    int my_e = -1;
+    if (worker && tid < R) {
+        const int e = ids[tid];
+        const bool ok = (unsigned)e < (unsigned)E;
+        my_e = ok ? e : -1;
+        if (ok) atomicAdd(&sm.cnt[e], 1);
+        if (report) {
+            int bad = ok ? 0 : kDevIdOutOfRange;
+            const int t = tid / k, j = tid - t * k;
+            for (int jj = 0; jj < j; ++jj)
+                if (ok && ids[t * k + jj] == e) bad |= kDevIdDuplicate;
+            if (bad) atomicOr(status, bad);
+        }
     }
-    const int rank = __popcll(same & lanemask_lt());
-    if (my_e >= 0 && rank == 0) atomicAdd(&sm.cnt[my_e], (int)((uint32_t)__popcll(same) << (8 * wave)));
-    if (report && worker && tid < R) {
-        int bad = my_e >= 0 ? 0 : kDevIdOutOfRange;
-        const int t = tid / k, j = tid - t * k;
-        for (int jj = 0; jj < j; ++jj)
-            if (my_e >= 0 && sm.ids[t * k + jj] == my_e) bad |= kDevIdDuplicate;
-        if (bad) atomicOr(status, bad);
-    }
+    if (worker && tid < R) sm.ids[tid] = my_e;
     __syncthreads();
     // active experts in ascending id (ballot ranks) and the exclusive prefix of the
     // counts over the expert ids (wave scans plus the wave totals)
-    auto bytes = [](uint32_t w) { return (int)((w & 0xFF) + (w >> 8 & 0xFF) + (w >> 16 & 0xFF) + (w >> 24)); };
     int c = 0, incl = 0;
     bool active = false;
     uint64_t b = 0;
     if (worker) {
-        c = bytes((uint32_t)sm.cnt[tid]);
+        c = sm.cnt[tid];
         active = tid < E && c > 0;
         b = __ballot(active);
         incl = c;
@@ -91,10 +80,11 @@ __device__ void decode_setup(DecodeSmem& sm, const int32_t* __restrict__ ids, in
         }
     }
     __syncthreads();
-    // entry q goes after the entries q' < q of its expert: those of earlier waves and lanes
+    // entry q goes after the entries q' < q of its expert
     if (my_e >= 0) {
-        const uint32_t before = wave > 0 ? (uint32_t)sm.cnt[my_e] & ((1u << (8 * wave)) - 1) : 0u;
-        sm.ent[sm.pfx[my_e] + bytes(before) + rank] = tid;
+        int rank = 0;
+        for (int q = 0; q < tid; ++q) rank += sm.ids[q] == my_e;
+        sm.ent[sm.pfx[my_e] + rank] = tid;
     }
     __syncthreads();
 }

@@ -3,8 +3,10 @@
 //
 // The same launches as with BF16 weights (decode.hip): W13 with the activation, then for one
 // token W2 with the combine, else W2 and a combine.  a is rounded to BF16, the operand type of
-// the W2 products; the experts' outputs o stay in FP32 until the one rounding of y.  The time is
-// that of streaming 4.25 bits for each weight of the active experts.
+// the W2 products; with one token, which leaves operand rows unused, its rounded remainder is an
+// operand row too (with more tokens the second row would cost 3.5 of 42 us).  The experts'
+// outputs o stay in FP32 until the one rounding of y.  The time is that of streaming 4.25 bits
+// for each weight of the active experts.
 //
 // A wave reads a tile (16 weight rows x 128 of K, 1 KiB in a row) with one 16-byte load per
 // lane: lane 16 q + n holds the block of 32 columns 128 s + 32 q of row n, with one scale.
@@ -71,9 +73,10 @@ __device__ __forceinline__ f32x4_t mma_tiles(const uint8_t* codes, const uint32_
 }
 
 // a[entry][i0 + n] = act(g) u in BF16, from one W13 tile's D: lane l holds rows 4 (l >> 4) + z
-// of column n = l & 15, gate columns 0..7 and up columns 8..15
-template <int kAct>
-__device__ __forceinline__ void store_a(const DecodeArgs& g, const int* ent, int m0, int M, int i0, f32x4_t acc, bool lead) {
+// of column n = l & 15, gate columns 0..7 and up columns 8..15.  kRest: the remainder too, T*k
+// rows further.
+template <int kAct, bool kRest>
+__device__ __forceinline__ void store_a(const DecodeArgs& g, const int* ent, int M, int i0, f32x4_t acc, bool lead) {
     const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
     float up[4];
 #pragma unroll
@@ -81,18 +84,15 @@ __device__ __forceinline__ void store_a(const DecodeArgs& g, const int* ent, int
     if (lead && n < 8) {
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-            const int mm = m0 + 4 * kq + z;
-            if (mm < M) g.a[(size_t)ent[mm] * g.I + i0 + n] = (uint16_t)f32_to_bf16(act_f<kAct>(acc[z]) * up[z]);
+            const int mm = 4 * kq + z;
+            if (mm < M) {
+                const float v = act_f<kAct>(acc[z]) * up[z];
+                const uint32_t hi = f32_to_bf16(v);
+                uint16_t* at = g.a + (size_t)ent[mm] * g.I + i0 + n;
+                *at = (uint16_t)hi;
+                if constexpr (kRest) at[(size_t)g.T * g.k * g.I] = (uint16_t)f32_to_bf16(v - bf16_to_f32(hi));
+            }
         }
-    }
-}
-// o[entry][n0 + n] in FP32, from one W2 tile's D
-__device__ __forceinline__ void store_o(const DecodeArgs& g, const int* ent, int m0, int M, int n0, f32x4_t acc) {
-    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
-#pragma unroll
-    for (int z = 0; z < 4; ++z) {
-        const int mm = m0 + 4 * kq + z;
-        if (mm < M) reinterpret_cast<float*>(g.o)[(size_t)ent[mm] * g.d + n0 + n] = acc[z];
     }
 }
 
@@ -114,11 +114,11 @@ __global__ __launch_bounds__(kThreads, kOneWGs) void decode4_w13_one(DecodeArgs 
     const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w13_scale) + tile * groups * 64 + lane;
     const f32x4_t acc = reduce_waves<true>(
         mma_tiles<4>(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.d * 2u), (lane & 15) == 0 ? 0u : kNoRow, s0, s1), red, par);
-    store_a<kAct>(g, &slot, 0, 1, blockIdx.x * 8, acc, threadIdx.x < MOE_WAVE);
+    store_a<kAct, true>(g, &slot, 1, blockIdx.x * 8, acc, threadIdx.x < MOE_WAVE);
 }
 
-// More tokens: a workgroup's item is (active expert, kTiles row tiles), its four waves a quarter
-// of K each.  A step is one tile along K: kTiles loads of codes, and four of the routed rows
+// More tokens: a workgroup's item is (group of entries of one expert, kTiles row tiles), its four
+// waves a quarter of K each.  A step is one tile along K: kTiles loads of codes, and four of the routed rows
 // that all the tiles share.  Those four are what bounds the kernel when few tiles share them:
 // they occupy the address unit as long as four loads of codes.  W13 and W2 at 32 tokens of the
 // 128-expert layer, 59 experts active (99 and 49 MB):
@@ -182,65 +182,138 @@ __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], const void
     }
 }
 
-// The items of this workgroup, its number in the launch and every (number of workgroups)-th;
-// store(entries, how many, first row of the group, row tile, sums) by the wave that has added
-// up the tile's four partial sums, in wave order
-template <typename Store>
-__device__ __forceinline__ void run_items(const DecodeSmem& sm, Partials4& part, const void* codes, const void* words,
-                                          __amdgpu_buffer_rsrc_t ars, int nblk, int S, int row_bytes, int row_div,
-                                          Store&& store) {
-    const int lane = threadIdx.x & 63, n = lane & 15, groups = (S + 3) / 4;
+// The routed entries sorted by expert, in groups of at most 16 entries of one expert.
+constexpr int kRows = 16;
+struct Sorted4 {
+    int cnt[256];                    // entries per expert, a byte for each of the four waves
+    int ids[kMaxDecodeRows];         // for the routing flags
+    int pfx[257];                    // entries of expert e: ent[pfx[e] .. pfx[e + 1])
+    int ent[kMaxDecodeRows];         // ascending within an expert
+    uint16_t group[256 + kMaxDecodeRows / kRows];   // expert | number of the group << 8, ascending
+    int wsum[kWaves];
+    int groups;
+};
+// Every workgroup sorts for itself; the one with `report` sets the routing flags.  An entry's rank
+// among its expert's comes from a ballot for each bit of the id, which finds the wave's entries
+// of the same expert, and the counts of the waves before.  (Comparing with every earlier entry,
+// up to 255, made W13 and W2 of 32 tokens 4.3 and 8.2 us longer.)
+__device__ __forceinline__ void sort_entries(Sorted4& sm, const DecodeArgs& g, bool report) {
+    static_assert(kThreads == 256 && kMaxDecodeRows == 256, "a thread for each expert and entry");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, R = g.T * g.k;
+    const int id = tid < R ? g.ids[tid] : -1;
+    const int e = (unsigned)id < (unsigned)g.E ? id : -1;
+    sm.cnt[tid] = 0;
+    if (report) sm.ids[tid] = e;
+    __syncthreads();
+    uint64_t same = __ballot(e >= 0);
+#pragma unroll
+    for (int bit = 1; bit < 256; bit <<= 1) {
+        const uint64_t ones = __ballot((e & bit) != 0);
+        same &= (e & bit) != 0 ? ones : ~ones;
+    }
+    const int rank = __popcll(same & lanemask_lt());
+    if (e >= 0 && rank == 0) atomicAdd(&sm.cnt[e], (int)((uint32_t)__popcll(same) << (8 * wave)));   // at most 64
+    if (report && tid < R) {
+        int bad = e >= 0 ? 0 : kDevIdOutOfRange;
+        const int t = tid / g.k, j = tid - t * g.k;
+        for (int jj = 0; jj < j; ++jj)
+            if (e >= 0 && sm.ids[t * g.k + jj] == e) bad |= kDevIdDuplicate;
+        if (bad) atomicOr(g.status, bad);
+    }
+    __syncthreads();
+    // thread tid for expert tid: prefix sums of the entries and (in the upper half) the groups
+    auto bytes = [](uint32_t w) { return (int)((w & 0xFF) + (w >> 8 & 0xFF) + (w >> 16 & 0xFF) + (w >> 24)); };
+    const int count = bytes((uint32_t)sm.cnt[tid]);
+    const int own = count | (count + kRows - 1) / kRows << 16;
+    int incl = own;
+    for (int off = 1; off < MOE_WAVE; off <<= 1) {
+        const int v = __shfl_up(incl, off, MOE_WAVE);
+        if (lane >= off) incl += v;
+    }
+    if (lane == MOE_WAVE - 1) sm.wsum[wave] = incl;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) incl += sm.wsum[w];
+    const int before = incl - own;
+    sm.pfx[tid] = before & 0xFFFF;
+    for (int i = 0; i < own >> 16; ++i) sm.group[(before >> 16) + i] = (uint16_t)(tid | i << 8);
+    if (tid == 255) {
+        sm.pfx[256] = incl & 0xFFFF;
+        sm.groups = incl >> 16;
+    }
+    __syncthreads();
+    if (e >= 0) {
+        const uint32_t earlier = wave > 0 ? (uint32_t)sm.cnt[e] & ((1u << (8 * wave)) - 1) : 0u;
+        sm.ent[sm.pfx[e] + bytes(earlier) + rank] = tid;
+    }
+    __syncthreads();
+}
+
+// The items (group of entries, kTiles row tiles) of this workgroup, its number in the launch and
+// every (number of workgroups)-th; store(entries, how many, row tile, sums) by the wave that has
+// added up the tile's four partial sums, in wave order.  row(entry): byte offset of its operand
+// row.
+template <typename Row, typename Store>
+__device__ __forceinline__ void run_items(const Sorted4& sm, Partials4& part, const void* codes, const void* words,
+                                          __amdgpu_buffer_rsrc_t ars, int nblk, int S, Row&& row, Store&& store) {
+    const int lane = threadIdx.x & 63, n = lane & 15, scale_bytes = (S + 3) / 4 * 256;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
-    const int per = nblk / kTiles, items = __builtin_amdgcn_readfirstlane(sm.n_active) * per;
+    const int per = nblk / kTiles, items = __builtin_amdgcn_readfirstlane(sm.groups) * per;
     int half = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int slot = item / per, blk = (item - slot * per) * kTiles;
-        const int e = __builtin_amdgcn_readfirstlane(sm.slot_expert[slot]);
-        const int e0 = __builtin_amdgcn_readfirstlane(sm.pfx[e]);
-        const int M = __builtin_amdgcn_readfirstlane(sm.pfx[e + 1]) - e0;
+        const int q = item / per, blk = (item - q * per) * kTiles;
+        const int group = __builtin_amdgcn_readfirstlane((int)sm.group[q]), e = group & 255, m0 = (group >> 8) * kRows;
+        const int first = __builtin_amdgcn_readfirstlane(sm.pfx[e]) + m0;
+        const int left = __builtin_amdgcn_readfirstlane(sm.pfx[e + 1]) - first, M = left < kRows ? left : kRows;
         const size_t tile = (size_t)e * nblk + blk;
-        for (int m0 = 0; m0 < M; m0 += 16) {
-            const uint32_t ao = m0 + n < M ? (uint32_t)(sm.ent[e0 + m0 + n] / row_div) * (uint32_t)row_bytes : kNoRow;
-            f32x4_t acc[kTiles] = {};
-            tile_products(acc, static_cast<const uint8_t*>(codes) + tile * S * 1024,
-                          static_cast<const uint8_t*>(words) + tile * groups * 256, ars, ao, S, s0, s1);
-            // one barrier: the other half is written next, and read only after the next barrier
+        const uint32_t ao = n < M ? row(sm.ent[first + n]) : kNoRow;
+        f32x4_t acc[kTiles] = {};
+        tile_products(acc, static_cast<const uint8_t*>(codes) + tile * S * 1024,
+                      static_cast<const uint8_t*>(words) + tile * scale_bytes, ars, ao, S, s0, s1);
+        // one barrier: the other half is written next, and read only after the next barrier
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) part.p[half][wave][t][lane] = acc[t];
-            __syncthreads();
+        for (int t = 0; t < kTiles; ++t) part.p[half][wave][t][lane] = acc[t];
+        __syncthreads();
 #pragma unroll
-            for (int t = 0; t < kTiles; t += kWaves) {
-                f32x4_t sum = part.p[half][0][t + wave][lane];
+        for (int t = 0; t < kTiles; t += kWaves) {
+            f32x4_t sum = part.p[half][0][t + wave][lane];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) sum += part.p[half][w][t + wave][lane];
-                store(sm.ent + e0, M, m0, blk + t + wave, sum);
-            }
-            half ^= 1;
+            for (int w = 1; w < kWaves; ++w) sum += part.p[half][w][t + wave][lane];
+            store(sm.ent + first, M, blk + t + wave, sum);
         }
+        half ^= 1;
     }
 }
 
 template <int kAct>
 __global__ __launch_bounds__(kThreads, kWGs) void decode4_w13(DecodeArgs g) {
-    __shared__ DecodeSmem sm;
+    __shared__ Sorted4 sm;
     __shared__ Partials4 part;
-    decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, blockIdx.x == 0);
-    run_items(sm, part, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), g.I / 8, g.d / 128, 2 * g.d, g.k,
-              [&](const int* ent, int M, int m0, int tile, f32x4_t sum) { store_a<kAct>(g, ent, m0, M, tile * 8, sum, true); });
+    sort_entries(sm, g, blockIdx.x == 0);
+    run_items(sm, part, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), g.I / 8, g.d / 128,
+              [&](int entry) { return (uint32_t)(entry / g.k * g.d) * 2u; },
+              [&](const int* ent, int M, int tile, f32x4_t sum) { store_a<kAct, false>(g, ent, M, tile * 8, sum, true); });
 }
 
 __global__ __launch_bounds__(kThreads, kWGs) void decode4_w2(DecodeArgs g) {
-    __shared__ DecodeSmem sm;
+    __shared__ Sorted4 sm;
     __shared__ Partials4 part;
-    decode_setup(sm, g.ids, g.T, g.k, g.E, g.status, false);
-    run_items(sm, part, g.w2, g.w2_scale, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * g.I * 2u), g.d / 16, g.I / 128, 2 * g.I, 1,
-              [&](const int* ent, int M, int m0, int tile, f32x4_t sum) { store_o(g, ent, m0, M, tile * 16, sum); });
+    sort_entries(sm, g, false);
+    float* o = reinterpret_cast<float*>(g.o);
+    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4, d = g.d;
+    run_items(sm, part, g.w2, g.w2_scale, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * g.I * 2u), d / 16, g.I / 128,
+              [&](int entry) { return (uint32_t)(entry * g.I) * 2u; },
+              [&](const int* ent, int M, int tile, f32x4_t sum) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            if (4 * kq + z < M) o[(size_t)ent[4 * kq + z] * d + tile * 16 + n] = sum[z];
+    });
 }
 
 // One token: W2 of all k experts and the combine, 8 output features per workgroup.  As in the
 // BF16 kernel, experts 2p and 2p + 1 share one MFMA: columns 0..7 are rows n0 .. n0 + 7 of
-// expert 2p, columns 8..15 the same rows of expert 2p + 1, A row 0 is a_2p and row 1 a_2p+1.
+// expert 2p, columns 8..15 the same rows of expert 2p + 1, A row 0 is a_2p and row 1 a_2p+1, rows
+// 2 and 3 their remainders.
 __global__ __launch_bounds__(kThreads, 1) void decode4_w2_one(DecodeArgs g) {
     __shared__ float ov[kMaxTopK][8];
     __shared__ float sc[kMaxTopK];
@@ -262,12 +335,12 @@ __global__ __launch_bounds__(kThreads, 1) void decode4_w2_one(DecodeArgs g) {
             const size_t tile = (size_t)e * nNB + (n0 >> 4);
             const uint8_t* codes = reinterpret_cast<const uint8_t*>(g.w2) + tile * S * 1024 + piece * 16;
             const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w2_scale) + tile * groups * 64 + piece;
-            const bool rv = (n == 0 && vx) || (n == 1 && vy);
-            const uint32_t ao = rv ? (uint32_t)((2 * p + n) * I) * 2u : kNoRow;
-            const f32x4_t acc = mma_tiles<8>(codes, words, groups, rows_rsrc(g.a, (uint32_t)k * I * 2u), ao, 0, S);
+            const bool rv = n < 4 && (n & 1 ? vy : vx);
+            const uint32_t ao = rv ? (uint32_t)((2 * p + (n & 1) + (n & 2 ? k : 0)) * I) * 2u : kNoRow;
+            const f32x4_t acc = mma_tiles<8>(codes, words, groups, rows_rsrc(g.a, (uint32_t)k * I * 4u), ao, 0, S);
             if (kq == 0) {
-                if (n < 8 && 2 * p < k) ov[2 * p][n] = vx ? acc[0] : 0.f;
-                if (n >= 8 && 2 * p + 1 < k) ov[2 * p + 1][n - 8] = vy ? acc[1] : 0.f;
+                if (n < 8 && 2 * p < k) ov[2 * p][n] = vx ? acc[0] + acc[2] : 0.f;
+                if (n >= 8 && 2 * p + 1 < k) ov[2 * p + 1][n - 8] = vy ? acc[1] + acc[3] : 0.f;
             }
         }
         if (tid < k) sc[tid] = score;
@@ -299,8 +372,8 @@ __global__ __launch_bounds__(kThreads) void decode4_combine(DecodeArgs g) {
 
 // a workgroup for each item, as far as they fit the chip together (nblk a multiple of kTiles)
 template <class K> hipError_t launch_items(K kernel, const DecodeArgs& g, int nblk, int num_cu, hipStream_t s) {
-    const int R = g.T * g.k, slots = R < g.E ? R : g.E;
-    const int items = slots * (nblk / kTiles), cap = kWGs * num_cu;
+    const int R = g.T * g.k, groups = R < g.E + R / kRows ? R : g.E + R / kRows;   // at most
+    const int items = groups * (nblk / kTiles), cap = kWGs * num_cu;
     hipLaunchKernelGGL(kernel, dim3(items < cap ? items : cap), dim3(kThreads), 0, s, g);
     return hipGetLastError();
 }

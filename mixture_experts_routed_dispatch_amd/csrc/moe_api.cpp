@@ -215,7 +215,9 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     const bool mx = c.precision == MOE_MXFP8_E4M3;
     const bool mxt = mx && c.training;
     // a in BF16: the BF16 path's W2 operand; MXFP8 training keeps it for the weight gradient
-    p->off_a = (!mx || c.training) ? take(2 * (size_t)R * c.I) : 0;
+    // (one token's MXFP4 decode keeps the remainder of its rounding as well)
+    p->a_bytes = (w4 && p->decode && c.T == 1 ? 4 : 2) * (size_t)R * c.I;
+    p->off_a = (!mx || c.training) ? take(p->a_bytes) : 0;
     // the experts' outputs: BF16, or FP32 in the MXFP4 decode, which rounds y alone
     p->o_bytes = (w4 && p->decode ? 4 : 2) * (size_t)R * c.d;
     p->off_o = take(p->o_bytes);
@@ -322,8 +324,9 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
     saved_region("slots", sizeof(int32_t) * (size_t)R, "routed row of each (t, j) [T, k]");
     saved_region("probs", sizeof(float) * (size_t)R, "score of each routed row [R]");
     if (!mx || c.training)
-        saved_region("a", 2 * (size_t)R * c.I, mx ? "SwiGLU output [R, I] BF16 (weight-gradient operand)"
-                                                  : "SwiGLU output [R, I] BF16");
+        saved_region("a", p->a_bytes, mx ? "SwiGLU output [R, I] BF16 (weight-gradient operand)"
+                                      : p->a_bytes == 2 * (size_t)R * c.I ? "SwiGLU output [R, I] BF16"
+                                                                          : "SwiGLU output [R, I] BF16 and its remainder");
     if (p->dh_aliased)
         region("o", 2 * (size_t)R * c.d, "fwd/bwd", "expert outputs [R, d] BF16; in the backward dh (g, u gradient [R, 2I])");
     else

@@ -24,7 +24,7 @@ struct moe_plan_s {
     int64_t ntok;                      // token-layout rows: T*k + 128 E
     size_t off_part, off_split;        // split weight-gradient tiles: partial sums, descriptors
     size_t off_we;                     // MXFP4 on the grouped-GEMM path: a product's weights as BF16
-    size_t o_bytes;                    // of the region of expert outputs
+    size_t a_bytes, o_bytes;           // of the regions of W13 outputs and expert outputs
     size_t off_mega;                   // mega decode: FP32 partial expert outputs [T*k, I / chunk, d]
     size_t ws_bytes;
     char* ws;
