@@ -37,16 +37,25 @@ __device__ __forceinline__ f32x4_t mma_quarter(bf16x8_t a, uint32_t codes, float
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, acc, 0, 0, 0);
 }
 
-// acc += A * B over the tiles s0 .. s1 - 1: codes and words point at this lane's piece of the
-// row tile's first tile, ars / ao as for mma_line_pairs (the row's byte offset; kNoRow: zeros)
-template <int B>
+// One token: acc += A * B over the tiles s0 .. s1 - 1 of a row tile, with kRowsUsed operand rows
+// (1 or 4).  codes and words point at this lane's piece of the first tile; row(r): byte offset
+// of operand row r in ars (kNoRow: zeros).  The rows come through LDS (`stage`, this wave's own),
+// 64 consecutive pieces a load: as MFMA operands straight from memory, with 60 of 64 lanes
+// masked, they are four loads for each load of codes.
+template <int kRowsUsed, int B> struct Stage4 {
+    static constexpr int kRow = B * 256 + 16;          // bytes; padded: the rows' pieces meet different banks
+    char b[kRowsUsed * kRow];
+};
+template <int kRowsUsed, int B, typename Row>
 __device__ __forceinline__ f32x4_t mma_tiles(const uint8_t* codes, const uint32_t* words, int groups,
-                                             __amdgpu_buffer_rsrc_t ars, uint32_t ao, int s0, int s1) {
+                                             __amdgpu_buffer_rsrc_t ars, Row&& row, Stage4<kRowsUsed, B>& stage, int s0, int s1) {
+    static_assert(B % 4 == 0, "whole loads of a row");
+    constexpr int kLoads = kRowsUsed * B / 4;          // of 1 KiB
+    const int lane = threadIdx.x & 63;
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    ao += 64u * ((threadIdx.x & 63) >> 4);
+    const char* mine = stage.b + (lane & (kRowsUsed - 1)) * Stage4<kRowsUsed, B>::kRow + 64 * (lane >> 4);
     for (int s = s0; s < s1; s += B) {
-        u32x4_t c[B];
-        bf16x8_t a[B][4];
+        u32x4_t c[B], x[kLoads];
         uint32_t sb[(B + 3) / 4];
 #pragma unroll
         for (int j = 0; j < B; ++j)
@@ -54,20 +63,27 @@ __device__ __forceinline__ f32x4_t mma_tiles(const uint8_t* codes, const uint32_
 #pragma unroll
         for (int j = 0; j < B; j += 4)
             if (s + j < s1) sb[j / 4] = scale_bytes(words, s + j, groups);
+        // past s1 a row's pieces belong to the next wave's tiles, or the resource's end: not used
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-            if (s + j < s1)
+        for (int p = 0; p < kLoads; ++p) {
+            const int at = p % (B / 4) * 1024 + lane * 16;
+            x[p] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ars, row(p / (B / 4)) + 256u * s + at, 0, 0));
+        }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    a[j][i] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                               ars, ao + 256u * (uint32_t)(s + j) + 16u * i, 0, 0));
+        for (int p = 0; p < kLoads; ++p)
+            *reinterpret_cast<u32x4_t*>(stage.b + p / (B / 4) * Stage4<kRowsUsed, B>::kRow + p % (B / 4) * 1024 + lane * 16) = x[p];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int j = 0; j < B; ++j)
             if (s + j < s1) {
-                const float x = __uint_as_float(((sb[j / 4] >> (8 * (j & 3))) & 0xFFu) << 23);
+                const float f = __uint_as_float(((sb[j / 4] >> (8 * (j & 3))) & 0xFFu) << 23);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc = mma_quarter(a[j][i], c[j][i], x, acc);
+                for (int i = 0; i < 4; ++i)
+                    acc = mma_quarter(*reinterpret_cast<const bf16x8_t*>(mine + 256 * j + 16 * i), c[j][i], f, acc);
             }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
     return acc;
 }
@@ -102,6 +118,7 @@ constexpr int kOneWGs = 3;
 template <int kAct>
 __global__ __launch_bounds__(kThreads, kOneWGs) void decode4_w13_one(DecodeArgs g) {
     __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
+    __shared__ __attribute__((aligned(16))) Stage4<1, 4> stage[kWaves];
     int par = 0;
     if (blockIdx.x == 0 && blockIdx.y == 0) decode_flags_one_token(g);
     const int slot = blockIdx.y, e = g.ids[slot];
@@ -113,7 +130,7 @@ __global__ __launch_bounds__(kThreads, kOneWGs) void decode4_w13_one(DecodeArgs 
     const uint8_t* codes = reinterpret_cast<const uint8_t*>(g.w13) + tile * S * 1024 + lane * 16;
     const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w13_scale) + tile * groups * 64 + lane;
     const f32x4_t acc = reduce_waves<true>(
-        mma_tiles<4>(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.d * 2u), (lane & 15) == 0 ? 0u : kNoRow, s0, s1), red, par);
+        mma_tiles(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.d * 2u), [](int) { return 0u; }, stage[w], s0, s1), red, par);
     store_a<kAct, true>(g, &slot, 1, blockIdx.x * 8, acc, threadIdx.x < MOE_WAVE);
 }
 
@@ -315,6 +332,7 @@ __global__ __launch_bounds__(kThreads, kWGs) void decode4_w2(DecodeArgs g) {
 // expert 2p, columns 8..15 the same rows of expert 2p + 1, A row 0 is a_2p and row 1 a_2p+1, rows
 // 2 and 3 their remainders.
 __global__ __launch_bounds__(kThreads, 1) void decode4_w2_one(DecodeArgs g) {
+    __shared__ __attribute__((aligned(16))) Stage4<4, 8> stage[kWaves];
     __shared__ float ov[kMaxTopK][8];
     __shared__ float sc[kMaxTopK];
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, kq = lane >> 4;
@@ -335,9 +353,10 @@ __global__ __launch_bounds__(kThreads, 1) void decode4_w2_one(DecodeArgs g) {
             const size_t tile = (size_t)e * nNB + (n0 >> 4);
             const uint8_t* codes = reinterpret_cast<const uint8_t*>(g.w2) + tile * S * 1024 + piece * 16;
             const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w2_scale) + tile * groups * 64 + piece;
-            const bool rv = n < 4 && (n & 1 ? vy : vx);
-            const uint32_t ao = rv ? (uint32_t)((2 * p + (n & 1) + (n & 2 ? k : 0)) * I) * 2u : kNoRow;
-            const f32x4_t acc = mma_tiles<8>(codes, words, groups, rows_rsrc(g.a, (uint32_t)k * I * 4u), ao, 0, S);
+            auto row = [&](int r) {
+                return (r & 1 ? vy : vx) ? (uint32_t)((2 * p + (r & 1) + (r & 2 ? k : 0)) * I) * 2u : kNoRow;
+            };
+            const f32x4_t acc = mma_tiles(codes, words, groups, rows_rsrc(g.a, (uint32_t)k * I * 4u), row, stage[wave], 0, S);
             if (kq == 0) {
                 if (n < 8 && 2 * p < k) ov[2 * p][n] = vx ? acc[0] + acc[2] : 0.f;
                 if (n >= 8 && 2 * p + 1 < k) ov[2 * p + 1][n - 8] = vy ? acc[1] + acc[3] : 0.f;

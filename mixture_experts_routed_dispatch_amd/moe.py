@@ -326,6 +326,7 @@ class Layer:
         self.T, self.d, self.I, self.E, self.k = T, d, I, E, k
         self.precision = precision
         self._mxfp4 = None
+        self._rows = _dense(T, d)
         self.plan = moe_plan(T, d, I, E, k, precision, int(bool(training)), path,
                              int(bool(wgrad_accumulate)), int(bool(recompute_h)), int(activation),
                              int(bool(mega)))
@@ -362,7 +363,7 @@ class Layer:
     def forward(self, x, ids, scores, w13, w2, w13_scale=None, w2_scale=None, y=None, stream=None):
         import torch
         if y is None:
-            y = torch.empty((self.T, self.d), dtype=torch.bfloat16, device=x.device)
+            y = torch.empty_strided(*self._rows, dtype=torch.bfloat16, device=x.device)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward(self.plan, _ptr(x), _ptr(ids), _ptr(scores), w, _ptr(y), _stream(stream))
         return y
