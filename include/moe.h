@@ -328,7 +328,7 @@ moe_status_t moe_backward(moe_plan_t plan, const void* dy, const void* x, const 
  * mask (uint8 [T], or NULL): rows with 0 are padding.  They get ids 0 .. k-1 (valid for
  * moe_forward) and scores 0, count nowhere, and get zero gradients.
  * Logits of -inf are never chosen before others and score 0; a row of -inf alone scores 0.
- * A NaN logit is chosen last, and makes the row's softmax (with sigmoid: its own score and the
+ * A NaN logit counts as -inf in the choice, and makes the row's softmax (with sigmoid: its own score and the
  * row's p) NaN; so does +inf with softmax.
  * Stateless: a config, caller-owned buffers and a workspace that holds nothing between calls;
  * calls that overlap need a workspace each. */

@@ -21,9 +21,10 @@
 // The choice, k <= kFastK: the k-th largest of the 16 lanes' maxima is a bound that at least k
 // keys reach and few do (with 256 random keys about 11 for k = 8, 21 for k = 12).  Those
 // candidates' indices go to LDS in ascending order, one or two to a lane, and each counts the
-// ones before it, which is its place: about 250 instructions where taking the maximum k = 8
-// times is 900 (16384 x 256, sigmoid, bias: see route_kernel).  More than kCand candidates (ties,
-// rows of one value) and larger k take the maximum k times.
+// ones before it, which is its place.  More than kCand candidates (ties, rows of one value) and
+// larger k take the row's maximum k times.  16384 x 256 in BF16 with sigmoid, bias and k = 8:
+// 12.0 us, against 32.4 by taking the maximum 8 times; 800 vector instructions a wave issue for
+// 6 us of it, the rest is the latency of one pass (its 9.5 MB take 1.9 us).
 //
 // With a bias the keys s + b have to be ordered as in exact arithmetic.  They are compared in
 // FP32; where two that matter lie closer than FP32's error, they are computed again in 64
@@ -261,7 +262,6 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-
 // keys that FP32 rounding may have brought into a wrong order lie this close (relative to
 // the larger of 1 and the key): a score is off by at most 3e-7 and the sum's rounding adds
 // 6e-8 of the key, so two keys by less than 7.2e-7
@@ -282,6 +282,7 @@ __device__ __forceinline__ int find_candidates(const float key[kV], int k, int i
     float mine = key[0];
 #pragma unroll
     for (int i = 1; i < kV; ++i) mine = __builtin_fmaxf(mine, key[i]);
+    mine = choice_key(mine);
     int above = 0;
     count_above<15>(mine, above);
     // the smallest maximum with fewer than k above it is the k-th largest of the 16
@@ -435,8 +436,11 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
         if (k <= kFastK) n = find_candidates<kV>(z, k, i0, E, kBias ? kNear : 0.0f, sel[row]);
         if (!__ballot(n > kCand)) {
             wave_fence();
-            if (__ballot(n > 16)) place_candidates<2, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], keys64[kBias ? row : 0], id, place, sc);
-            else place_candidates<1, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], keys64[kBias ? row : 0], id, place, sc);
+            double* k64 = keys64[kBias ? row : 0];
+            if (__ballot(n > 16))
+                place_candidates<2, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place, sc);
+            else
+                place_candidates<1, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place, sc);
         } else {
             uint32_t key[kV];
 #pragma unroll
@@ -445,19 +449,19 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
             const uint32_t last = take_top<kV>(key, k, i0, sel[row]);
             wave_fence();
             if constexpr (kBias) {
-                // is every neighbour in the order, and everything left behind the last one,
-                // either further off than FP32 rounding reaches, or the same logit and bias
-                // (a true tie, which the index has settled)?
+                // is every neighbour in the order, and everything around the last one, either
+                // further off than FP32 rounding reaches, or the same logit and bias (a true
+                // tie, which the index has settled)?
                 bool near = false;
                 const int e_last = sel[row][k - 1];
                 const float z_last = ld_logit(g.logits, t * E + e_last, kF32), b_last = g.bias[e_last];
                 const float k_last = key_value(last);
-                const float floor_key = k_last - kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(k_last));
+                const float reach = kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(k_last));
 #pragma unroll 1
                 for (int i = 0; i < kV && i0 + i < E; ++i) {
                     const float zi = ld_logit(g.logits, t * E + i0 + i, kF32), bi = g.bias[i0 + i];
                     const float ki = choice_key(one_score<kSig>(zi, base, inv) + bi);
-                    near |= ki >= floor_key && ki <= k_last && !(zi == z_last && bi == b_last);
+                    near |= __builtin_fabsf(ki - k_last) <= reach && !(zi == z_last && bi == b_last);
                 }
                 for (int j = l16; j + 1 < k; j += 16) {
                     const int ea = sel[row][j], eb = sel[row][j + 1];
@@ -528,8 +532,8 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
 // Counts, sums and loss from the workgroups' partial rows: 16 experts per workgroup, a thread
 // four of them in every 64th row, then the lanes and the waves in a fixed order.  The loss
 // needs every expert: each workgroup leaves its share, and the last one to do so (a ticket that
-// route_kernel has cleared) adds the shares in order.  (One workgroup reading all 512 KB of a
-// 256-expert batch took 7.4 us.)
+// route_kernel has cleared) adds the shares in order.  5.6 us for the 512 KB of 256 workgroups and
+// experts (one workgroup for all of it: 7.4 us).
 __global__ __launch_bounds__(kThreads) void route_final_kernel(RouterArgs g, int blocks) {
     __shared__ float ps[4][16];
     __shared__ int cs[4][16];

@@ -210,6 +210,43 @@ def test_near_ties_with_a_bias_are_ordered_exactly(moe):
         assert np.array_equal(r.forward(z2.to(dev()), bias=b2.to(dev()))[0].cpu().numpy(), ri)
 
 
+@pytest.mark.parametrize("k", [3, 8, 12, 20])
+def test_few_near_pairs_with_a_bias(moe, k):
+    """Keys that are spread but for pairs a few 2^-24 apart, at every place of the order."""
+    import torch
+    T, E = 300, 96
+    g = torch.Generator().manual_seed(40 + k)
+    for score in (0, 1):
+        z = torch.randn(T, E, generator=g)
+        s = torch.from_numpy(scores64(z.double().numpy(), score)[0])
+        # one bias for all rows: pairs are made in the logits of sigmoid scores, or of softmax rows by
+        # equal logits with biases that differ by a rounding
+        b = torch.randn(E, generator=g) * 0.1
+        if score == 1:
+            target = s[:, 0::2] + b[0::2].double() - b[1::2].double()
+            ok = (target > 0.01) & (target < 0.99)
+            other = torch.log(target.clamp(0.01, 0.99) / (1 - target.clamp(0.01, 0.99)))
+            z[:, 1::2] = torch.where(ok, other, z[:, 1::2].double()).float()
+        else:
+            b[1::2] = torch.nextafter(b[0::2], torch.full_like(b[0::2], 9.0))
+            z[:, 1::2] = z[:, 0::2] - 1e-7 * torch.rand(T, E // 2, generator=g)
+        ri = ref_forward(z, b, None, k, score, True, 1.0, 0.0)[0]
+        got = moe.Router(T, E, k, score=score).forward(z.to(dev()), bias=b.to(dev()))[0].cpu().numpy()
+        assert np.array_equal(got, ri)
+
+
+def test_nan_logits_are_chosen_last(moe):
+    """Whole lanes of NaN (20 of 64 logits) with k = 12, sigmoid: the largest of the others are chosen."""
+    import torch
+    T, E, k = 8, 64, 12
+    z, _, _ = make(T, E, torch.float32, 12)
+    z[:, 8:28] = float("nan")
+    ids = moe.Router(T, E, k, score=1).forward(z.to(dev()))[0].cpu().numpy()
+    clean = z.clone()
+    clean[:, 8:28] = float("-inf")
+    assert np.array_equal(ids, ref_forward(clean, None, None, k, 1, True, 1.0, 0.0)[0])
+
+
 @pytest.mark.parametrize("score", [0, 1])
 @pytest.mark.parametrize("bias", [False, True])
 def test_infinities_and_nan(moe, score, bias):
