@@ -9,6 +9,8 @@
 
 using namespace moe;
 
+static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
 extern "C" {
 
 moe_status_t moe_prepare_weights(moe_plan_t p, const void* w13, const void* w2, uint8_t* w13_q,
@@ -18,6 +20,8 @@ moe_status_t moe_prepare_weights(moe_plan_t p, const void* w13, const void* w2, 
     if (c.d % 128 != 0 || c.I % 128 != 0) return MOE_ERR_UNSUPPORTED;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (c.precision == MOE_MXFP4) {
+        if (!aligned16(w13) || !aligned16(w2) || !aligned16(w13_q) || !aligned16(w13_s) || !aligned16(w2_q) || !aligned16(w2_s))
+            return MOE_ERR_INVALID_ARG;
         const Mxfp4Args g{{mxfp4_w13(w13, w13_q, w13_s, c.E, c.I, c.d), mxfp4_w2(w2, w2_q, w2_s, c.E, c.I, c.d)}};
         if (launch_mxfp4_pack(g, s) != hipSuccess) return MOE_ERR_HIP;
         return MOE_OK;
@@ -36,6 +40,9 @@ moe_status_t moe_expand_weights(moe_plan_t p, const moe_weights_t* w, void* w13,
     if (!p || !w || !w13 || !w2 || !w->w13 || !w->w2 || !w->w13_scale || !w->w2_scale) return MOE_ERR_INVALID_ARG;
     const moe_config_t& c = p->cfg;
     if (c.precision != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
+    if (!aligned16(w->w13) || !aligned16(w->w2) || !aligned16(w->w13_scale) || !aligned16(w->w2_scale) || !aligned16(w13) ||
+        !aligned16(w2))
+        return MOE_ERR_INVALID_ARG;
     const Mxfp4Args g{{mxfp4_w13(w13, w->w13, w->w13_scale, c.E, c.I, c.d), mxfp4_w2(w2, w->w2, w->w2_scale, c.E, c.I, c.d)}};
     return launch_mxfp4_expand(g, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -120,7 +127,6 @@ static moe_status_t norm_check(const moe_norm_config_t* c) {
     if (c->d % 8 != 0 || c->d > kNormMaxD) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
-static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 size_t moe_norm_workspace_bytes(const moe_norm_config_t* c) {
     if (norm_check(c) != MOE_OK) return 0;

@@ -374,8 +374,8 @@ __global__ __launch_bounds__(kThreads, 1) void decode4_w2_one(DecodeArgs g) {
 }
 
 // y[t] = sum_j s[t][j] o[t*k + j] in FP32, j ascending from +0.0; four features a thread
-__global__ __launch_bounds__(kThreads) void decode4_combine(DecodeArgs g) {
-    const int t = blockIdx.y, n = (blockIdx.x * kThreads + threadIdx.x) * 4;
+__global__ __launch_bounds__(MOE_WAVE) void decode4_combine(DecodeArgs g) {
+    const int t = blockIdx.y, n = (blockIdx.x * MOE_WAVE + threadIdx.x) * 4;
     if (n >= g.d) return;
     const float* o = reinterpret_cast<const float*>(g.o) + (size_t)t * g.k * g.d + n;
     f32x4_t y = {0.f, 0.f, 0.f, 0.f};
@@ -422,7 +422,7 @@ hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
     }
     const hipError_t e = launch_items(decode4_w2, g, g.d / 16, num_cu, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(decode4_combine, dim3((g.d / 4 + kThreads - 1) / kThreads, g.T), dim3(kThreads), 0, s, g);
+    hipLaunchKernelGGL(decode4_combine, dim3((g.d / 4 + MOE_WAVE - 1) / MOE_WAVE, g.T), dim3(MOE_WAVE), 0, s, g);
     return hipGetLastError();
 }
 

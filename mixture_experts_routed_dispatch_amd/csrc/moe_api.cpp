@@ -448,6 +448,12 @@ moe_status_t moe_prepare_weights_backward(moe_plan_t p, const void* w13, const v
     return MOE_OK;
 }
 
+// the kernels read MXFP4 codes 16 bytes and scales a word at a time
+static bool mxfp4_aligned(const moe_weights_t* w) {
+    auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    return aligned(w->w13) && aligned(w->w2) && aligned(w->w13_scale) && aligned(w->w2_scale);
+}
+
 moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const float* scores,
                          const moe_weights_t* w, void* y, void* stream) {
     if (!p || !w) return MOE_ERR_INVALID_ARG;
@@ -456,6 +462,7 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
     const bool w4 = c.precision == MOE_MXFP4;
     if (c.T > 0 && (w4 || c.precision == MOE_MXFP8_E4M3) && (!w->w13_scale || !w->w2_scale))
         return MOE_ERR_INVALID_ARG;
+    if (c.T > 0 && w4 && !mxfp4_aligned(w)) return MOE_ERR_INVALID_ARG;
     if (!p->ws) return MOE_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     p->have_saved_forward = false;
@@ -615,6 +622,7 @@ moe_status_t moe_forward_routed(moe_plan_t p, const void* x_rows, const int32_t*
     if (c.T > 0 && (!x_rows || !m_indptr || !out || !w->w13 || !w->w2)) return MOE_ERR_INVALID_ARG;
     const bool w4 = c.precision == MOE_MXFP4;
     if (c.T > 0 && (mx || w4) && (!w->w13_scale || !w->w2_scale)) return MOE_ERR_INVALID_ARG;
+    if (c.T > 0 && w4 && !mxfp4_aligned(w)) return MOE_ERR_INVALID_ARG;
     if (!p->ws) return MOE_ERR_WORKSPACE;
     p->have_saved_forward = false;
     p->status_word = p->at<int32_t>(p->off_status);

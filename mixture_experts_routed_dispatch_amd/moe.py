@@ -363,7 +363,7 @@ class Layer:
     def forward(self, x, ids, scores, w13, w2, w13_scale=None, w2_scale=None, y=None, stream=None):
         import torch
         if y is None:
-            y = torch.empty_strided(*self._rows, dtype=torch.bfloat16, device=x.device)
+            y = _new(self._rows, torch.bfloat16, x.device)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward(self.plan, _ptr(x), _ptr(ids), _ptr(scores), w, _ptr(y), _stream(stream))
         return y
@@ -411,7 +411,7 @@ class Layer:
             (n13, n2), stream = self._mxfp4_layout(), _stream(stream)
             _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
             _check("w2", w2, (E, d, I), torch.bfloat16, dev)
-            w13_q, w13_s, w2_q, w2_s = (torch.empty_strided(*n, dtype=torch.uint8, device=dev) for n in n13 + n2)
+            w13_q, w13_s, w2_q, w2_s = (_new(n, torch.uint8, dev) for n in n13 + n2)
             moe_prepare_weights(self.plan, w13.data_ptr(), w2.data_ptr(), w13_q.data_ptr(), w13_s.data_ptr(),
                                 w2_q.data_ptr(), w2_s.data_ptr(), stream)
             return w13_q, w13_s, w2_q, w2_s
@@ -468,12 +468,18 @@ class Layer:
 # ---------------------------------------------------------------- around the layer
 
 def _dense(*shape):
-    """(shape, strides) of a row-major tensor, for torch.empty_strided (1.2 us a call, torch.empty 1.6)."""
+    """(shape, strides) of a row-major tensor."""
     strides, n = [], 1
     for size in reversed(shape):
         strides.append(n)
         n *= max(size, 1)
     return shape, tuple(reversed(strides))
+
+
+def _new(rows, dtype, device):
+    """An uninitialised tensor of _dense's shape and strides (1.2 us a call, torch.empty 1.6)."""
+    import torch
+    return torch.empty_strided(*rows, dtype=dtype, device=device)
 
 
 def _check(name, t, shape, dtype, device):
@@ -549,14 +555,12 @@ class Router(_OnDevice):
 
     def _forward(self, s, cfg, logits, bias, mask, stats):
         import torch
-        new, dev, f32, i32 = torch.empty_strided, self.device, torch.float32, torch.int32
-        ids = new(*self._per_choice, dtype=i32, device=dev)
-        scores = new(*self._per_choice, dtype=f32, device=dev)
+        dev, f32, i32 = self.device, torch.float32, torch.int32
+        ids, scores = _new(self._per_choice, i32, dev), _new(self._per_choice, f32, dev)
         counts = sums = loss = None
         if stats:
-            counts = new(*self._per_expert, dtype=i32, device=dev)
-            sums = new(*self._per_expert, dtype=f32, device=dev)
-            loss = new((), (), dtype=f32, device=dev)
+            counts, sums = _new(self._per_expert, i32, dev), _new(self._per_expert, f32, dev)
+            loss = _new(((), ()), f32, dev)
         moe_router_forward(cfg, logits.data_ptr(), _ptr(bias), _ptr(mask), ids.data_ptr(), scores.data_ptr(),
                            _ptr(counts), _ptr(sums), _ptr(loss), self._workspace_ptr, self._workspace_bytes, s)
         return ids, scores, counts, sums, loss
@@ -627,8 +631,8 @@ class BlockNorm(_OnDevice):
     def _forward(self, s, res, x, y, w_post, gate, w_pre, z):
         import torch
         if z is None and y is not None:
-            z = torch.empty_strided(*self._rows, dtype=res, device=self.device)
-        h = None if w_pre is None else torch.empty_strided(*self._rows, dtype=torch.bfloat16, device=self.device)
+            z = _new(self._rows, res, self.device)
+        h = None if w_pre is None else _new(self._rows, torch.bfloat16, self.device)
         moe_norm_forward(self._cfg, x.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(z), _ptr(h), s)
         return x if y is None else z, h
 
@@ -648,7 +652,7 @@ class BlockNorm(_OnDevice):
         import torch
         like = torch.empty_like
         if dx is None:
-            dx = torch.empty_strided(*self._rows, dtype=res, device=self.device)
+            dx = _new(self._rows, res, self.device)
         dy = None if y is None else like(y)
         dw_post = None if w_post is None else like(w_post)
         dgate = None if gate is None else like(gate)

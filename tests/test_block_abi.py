@@ -144,6 +144,13 @@ def test_mxfp4_plans(L, cfg, expect):
     w = moe.weights(P, P)
     assert L.moe_forward(h, P, P, P, ctypes.byref(w), P, None) == moe.MOE_ERR_INVALID_ARG        # no scales
     assert L.moe_expand_weights(h, ctypes.byref(w), P, P, None) == moe.MOE_ERR_INVALID_ARG
+    for i in range(4):                                   # codes and scales are 16-byte aligned
+        w = moe.weights(*[P + 8 * (i == j) for j in range(4)])
+        assert L.moe_forward(h, P, P, P, ctypes.byref(w), P, None) == moe.MOE_ERR_INVALID_ARG
+        assert L.moe_expand_weights(h, ctypes.byref(w), P, P, None) == moe.MOE_ERR_INVALID_ARG
+    assert L.moe_prepare_weights(h, P, P, P + 8, P, P, P, None) == moe.MOE_ERR_INVALID_ARG
+    w = moe.weights(P, P, P, P)
+    assert L.moe_forward(h, P, P, P, ctypes.byref(w), P, None) == moe.MOE_ERR_WORKSPACE
     L.moe_plan_destroy(h)
 
 
