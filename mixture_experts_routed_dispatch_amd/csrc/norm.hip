@@ -160,6 +160,18 @@ __global__ __launch_bounds__(64 * kW > kFwdThreads ? 64 * kW : kFwdThreads) void
     }
 }
 
+// the parameters' gradients of column c from its sum: a_pre (which 0) or a_out (1) of
+// norm_grad_kernel
+__device__ __forceinline__ void finish_column(const NormGradArgs& g, int which, int c, float sum) {
+    if (which == 0) {
+        g.dw_pre[c] = sum;
+        return;
+    }
+    const bool channel = g.gate_kind == kGateChannel;
+    if (g.w_post) g.dw_post[c] = channel ? g.gate[c] * sum : sum;
+    if (channel) g.dgate[c] = g.w_post ? g.w_post[c] * sum : sum;
+}
+
 // Workgroups of 512 threads, two a CU, so that one loads while the other waits at a barrier
 // (8192 x 2048 in BF16: 39.0 us against 41.0 with one of 1024; 4099 x 4096 with an FP32 stream:
 // 57.3 against 61.6, 5.3 TB/s of its 302 MB).  Loading the next row ahead takes the registers
@@ -253,7 +265,9 @@ __global__ __launch_bounds__(bwd_threads<kW>(), 4) void norm_grad_kernel(NormGra
             if (row && col < d) st8(g.dy + t * d + col, G[c]);
         }
     }
-    // column sums: the workgroup's row groups in order, then one partial row
+    // column sums: the workgroup's row groups in order, then one partial row (with one workgroup
+    // the sums themselves)
+    const bool last = gridDim.x == 1;
     auto column = [&](const Vec8 (&a)[kC], int which) {
         float* dst = g.part + ((size_t)blockIdx.x * 2 + which) * d;
         if constexpr (kGroups > 1) {
@@ -264,13 +278,21 @@ __global__ __launch_bounds__(bwd_threads<kW>(), 4) void norm_grad_kernel(NormGra
                 float v = cols[c];
 #pragma unroll
                 for (int u = 1; u < kGroups; ++u) v += cols[u * kCols + c];
-                if (c < d) dst[c] = v;
+                if (c >= d) continue;
+                if (last) finish_column(g, which, c, v);
+                else dst[c] = v;
             }
         } else {
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
                 const int col = 8 * (lt + c * 64 * kW);
-                if (col < d) st8(dst + col, a[c]);
+                if (col >= d) continue;
+                if (!last) {
+                    st8(dst + col, a[c]);
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) finish_column(g, which, col + i, a[c].v[i]);
             }
         }
     };
@@ -286,8 +308,7 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormGradArgs g, int 
     __shared__ f32x4_t p[kSlices][kSliceCols / 4];
     const int q = threadIdx.x % (kSliceCols / 4), slice = threadIdx.x / (kSliceCols / 4);
     const int which = blockIdx.y, c = blockIdx.x * kSliceCols + 4 * q;
-    const bool out = which == 1, channel = g.gate_kind == kGateChannel;
-    if (out ? !g.y || !(g.w_post || channel) : !g.w_pre) return;
+    if (which == 1 ? !g.y || !(g.w_post || g.gate_kind == kGateChannel) : !g.w_pre) return;
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
     if (c < g.d)
 #pragma unroll 4
@@ -299,12 +320,7 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormGradArgs g, int 
     if (threadIdx.x >= kSliceCols || col >= g.d) return;
     float s = 0.0f;
     for (int u = 0; u < kSlices; ++u) s += reinterpret_cast<const float*>(&p[u][threadIdx.x >> 2])[threadIdx.x & 3];
-    if (!out) {
-        g.dw_pre[col] = s;
-        return;
-    }
-    if (g.w_post) g.dw_post[col] = channel ? g.gate[col] * s : s;
-    if (channel) g.dgate[col] = g.w_post ? g.w_post[col] * s : s;
+    finish_column(g, which, col, s);
 }
 
 template <typename TRes, int kW, int kC>
@@ -320,8 +336,10 @@ template <typename TRes, int kW, int kC>
 int launch_norm_grad_t(const NormGradArgs& g, hipStream_t s) {
     constexpr int thr = bwd_threads<kW>(), groups = thr / (64 * kW);
     const int64_t rows = ((int64_t)g.T + groups - 1) / groups;
+    // two passes of one workgroup cost no more than the second launch that several need (33 rows
+    // of 256 in two launches 5.9 us in a graph, 32 rows in four passes 7.3) and spare the host it
     constexpr int cap = kNormBlocks * kBwdThreads / thr;
-    const int grid = (int)(rows < cap ? rows : cap);
+    const int grid = (int)(rows <= 2 ? 1 : rows < cap ? rows : cap);
     hipLaunchKernelGGL((norm_grad_kernel<TRes, kW, kC>), dim3(grid), dim3(thr), 0, s, g);
     return grid;
 }
@@ -356,7 +374,7 @@ hipError_t launch_norm_grad(const NormGradArgs& g, bool f32, hipStream_t s) {
     if (g.d % 8 != 0 || g.d > kNormMaxD) return hipErrorInvalidValue;
     const int blocks = f32 ? launch_norm_grad_d<float>(g, s) : launch_norm_grad_d<uint16_t>(g, s);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !(g.w_pre || g.w_post || g.gate_kind == kGateChannel)) return e;
+    if (e != hipSuccess || blocks == 1 || !(g.w_pre || g.w_post || g.gate_kind == kGateChannel)) return e;
     const dim3 grid((g.d + kSliceCols - 1) / kSliceCols, 2);
     hipLaunchKernelGGL(norm_columns_kernel, grid, dim3(1024), 0, s, g, blocks);
     return hipGetLastError();

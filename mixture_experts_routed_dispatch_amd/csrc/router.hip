@@ -312,26 +312,24 @@ __device__ __forceinline__ int find_candidates(const float key[kV], int k, int i
     return total;
 }
 
-// Where each candidate of a row (n of them, kH to a lane) comes in the order: id, place and score
-// of this lane's ones; place >= k: not chosen.  With a bias FP32 keys order the candidates only
+// Where each candidate of a row (n of them, kH to a lane) comes in the order: id and place of this
+// lane's ones; place >= k: not chosen.  With a bias FP32 keys order the candidates only
 // where every other key is further off than kNear; otherwise (a tie too) 64 bits do.
 template <int kH, int kV, bool kF32, bool kSig, bool kBias>
 __device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t, int i0, int n, float base, float inv,
                                                  const int* list, float* keys, double* keys64, int (&id)[2],
-                                                 int (&place)[2], float (&sc)[2]) {
+                                                 int (&place)[2]) {
     const int l16 = threadIdx.x & 15;
     const int64_t row = t * g.E;
     float own[kH];
     id[1] = 0;
     place[1] = g.k;
-    sc[1] = 0.0f;
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
         const int c = l16 + 16 * h;
         id[h] = c < n ? list[c] : 0;
         const float z = ld_logit(g.logits, row + id[h], kF32);
-        sc[h] = one_score<kSig>(z, base, inv);
-        own[h] = choice_key(kBias ? sc[h] + g.bias[id[h]] : z);
+        own[h] = choice_key(kBias ? one_score<kSig>(z, base, inv) + g.bias[id[h]] : z);
         keys[c] = c < n ? own[h] : NAN;                 // compares with nothing
         place[h] = c < n ? 0 : g.k;
     }
@@ -429,18 +427,21 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
         if constexpr (kBias)
 #pragma unroll
             for (int i = 0; i < kV; ++i) z[i] += s[i];  // keys from here on
-        // this lane's entries of the row's choice: expert and place (k or more: not chosen)
-        int id[2], place[2];
-        float sc[2];
         int n = kCand + 1;
         if (k <= kFastK) n = find_candidates<kV>(z, k, i0, E, kBias ? kNear : 0.0f, sel[row]);
         if (!__ballot(n > kCand)) {
             wave_fence();
             double* k64 = keys64[kBias ? row : 0];
+            int id[2], place[2];
             if (__ballot(n > 16))
-                place_candidates<2, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place, sc);
+                place_candidates<2, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place);
             else
-                place_candidates<1, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place, sc);
+                place_candidates<1, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place);
+            wave_fence();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (place[h] < k) sel[row][place[h]] = id[h];
+            wave_fence();
         } else {
             uint32_t key[kV];
 #pragma unroll
@@ -477,20 +478,22 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
                     wave_fence();
                 }
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                place[h] = l16 + 16 * h;
-                id[h] = place[h] < k ? sel[row][place[h]] : 0;
-                sc[h] = one_score<kSig>(ld_logit(g.logits, t * E + id[h], kF32), base, inv);
-            }
         }
-        float total = 0.0f;
+        // sel holds the choice in order: lane j takes the j-th (and j + 16-th), so that the sum
+        // of the scores does not depend on how the row's choice was found
+        int id[2];
+        float sc[2], total = 0.0f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) total += place[h] < k ? sc[h] : 0.0f;
+        for (int h = 0; h < 2; ++h) {
+            const int j = l16 + 16 * h;
+            id[h] = j < k ? sel[row][j] : 0;
+            sc[h] = j < k ? one_score<kSig>(ld_logit(g.logits, t * E + id[h], kF32), base, inv) : 0.0f;
+            total += sc[h];
+        }
         total = row_sum(total);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int j = place[h];
+            const int j = l16 + 16 * h;
             if (j < k && in) {
                 float w = sc[h];
                 if (g.normalize) w = total == 0.0f ? 0.0f : w / total;
@@ -721,9 +724,13 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
     }
 }
 
-// Workgroups of 1024 threads once there are more rows than one pass of the smaller ones over
-// the chip: the same rows in flight with a quarter of the partial sums.
-bool wide_blocks(int64_t T) { return T > (int64_t)kRouterBlocks * kRows; }
+// Up to kOneBlock rows go to one workgroup, which needs no second launch for its sums: 64 rows of
+// 128 logits take 7.8 us in a graph (two passes, 128 rows, 11.3; 129 rows in two launches 8.6)
+// and 2.7 us less of the host.  Workgroups of 1024 threads there, and once there are more rows
+// than one pass of the smaller ones over the chip: the same rows in flight with a quarter of
+// the partial sums.
+constexpr int kOneBlock = 64;
+bool wide_blocks(int64_t T) { return (T > kRows && T <= kOneBlock) || T > (int64_t)kRouterBlocks * kRows; }
 
 // logits per lane, and whether rows are made of aligned pieces of the widest load
 int per_lane(int E) { return E <= 64 ? 4 : E <= 128 ? 8 : 16; }
@@ -758,6 +765,7 @@ void launch_route_grad_v(const RouterGradArgs& g, int grid, bool sig, bool f32, 
 }  // namespace
 
 int router_blocks(int64_t T) {
+    if (T <= kOneBlock) return 1;
     const int rows = wide_blocks(T) ? kWide / 16 : kRows;
     const int64_t b = (T + rows - 1) / rows;
     return (int)(b < 1 ? 1 : b < kRouterBlocks ? b : kRouterBlocks);

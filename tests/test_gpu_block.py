@@ -143,6 +143,7 @@ def test_offsets_past_32_bits(moe):
     """Rows that start more than 2^31 elements (2^32 bytes) into their tensors: the last rows equal
     those of a short call on the same values."""
     import torch
+    torch.manual_seed(17)
     T, E, k, n = (1 << 23) + 37, 256, 4, 70
     z = torch.zeros(T, E, dtype=torch.bfloat16, device=dev())
     z[-n:] = torch.randn(n, E, device=dev()).bfloat16()
@@ -178,6 +179,7 @@ def test_offsets_past_32_bits(moe):
 def test_4bit_weights_past_32_bits(moe):
     """Codes of more than 2^31 bytes: the last expert's output against float64 on its expanded weights."""
     import torch
+    torch.manual_seed(18)
     d, I, E, k = 4096, 2048, 256, 2
     w13 = torch.zeros(E, 2 * I, d, dtype=torch.bfloat16, device=dev())
     w2 = torch.zeros(E, d, I, dtype=torch.bfloat16, device=dev())

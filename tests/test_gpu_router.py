@@ -235,6 +235,26 @@ def test_few_near_pairs_with_a_bias(moe, k):
         assert np.array_equal(got, ri)
 
 
+@pytest.mark.parametrize("bias", [False, True])
+def test_rows_do_not_depend_on_their_neighbours(moe, bias):
+    """The bits of a row are the same alone and between rows of ties, of one value or of NaN."""
+    import torch
+    E, k, n = 256, 8, 40
+    g = torch.Generator().manual_seed(71)
+    rows = torch.randn(n, E, generator=g)
+    b = (torch.randn(E, generator=g) * 0.05).to(dev()) if bias else None
+    odd = torch.stack([torch.zeros(E), torch.randint(0, 2, (E,), generator=g).float(), torch.full((E,), float("nan"))])
+    mixed = torch.cat([torch.cat([r[None], odd]) for r in rows])
+    for score in (0, 1):
+        a = moe.Router(n, E, k, score=score).forward(rows.to(dev()), bias=b, stats=False)
+        c = moe.Router(4 * n, E, k, score=score).forward(mixed.to(dev()), bias=b, stats=False)
+        assert torch.equal(a[0], c[0][::4]) and torch.equal(a[1], c[1][::4])
+        one = moe.Router(1, E, k, score=score)
+        for t in range(5):
+            x = one.forward(rows[t:t + 1].to(dev()), bias=b, stats=False)
+            assert torch.equal(x[0][0], a[0][t]) and torch.equal(x[1][0], a[1][t])
+
+
 def test_nan_logits_are_chosen_last(moe):
     """Whole lanes of NaN (20 of 64 logits) with k = 12, sigmoid: the largest of the others are chosen."""
     import torch
