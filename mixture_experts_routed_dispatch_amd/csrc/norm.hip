@@ -17,8 +17,9 @@
 // that it stays in registers between the reductions; kW is the fewest waves that hold d.  The
 // vectors over channels are loaded once per workgroup, which walks several rows.  Memory
 // bound: the least traffic is 4 (forward) and 6 (backward) passes over [T, d]; 8192 x 2048 in
-// BF16, post norm, gate and pre norm: forward 22.0 us (6.1 TB/s), backward 39.0 us (5.2 TB/s)
-// and 5.0 us for the column sums' second stage.
+// BF16, post norm, gate and pre norm: forward 23.6 us (5.7 TB/s), backward 39.0 us (5.2 TB/s)
+// and 4.8 us for the column sums' second stage.  Stores past the caches gain the forward 2 us
+// here, cost it 4 us of 36 at 4099 x 4096 with an FP32 stream, and slow whoever reads h next.
 #include <type_traits>
 
 #include "common.h"
@@ -55,6 +56,35 @@ __device__ __forceinline__ Vec8 ld8_or(const float* p, int c, bool in, float oth
     return {{other, other, other, other, other, other, other, other}};
 }
 __device__ __forceinline__ Vec8 zero8() { return {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}}; }
+
+// 8 channels as they lie in memory.  A row's pieces are all loaded, from a place that exists
+// whatever the lane, before the first is unpacked: an unpacked load on one side of a branch
+// would be waited for there, one piece after the other.
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> {
+    uint4 u = {0, 0, 0, 0};
+    __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ Vec8 get(bool in) const {
+        const uint4 w = {in ? u.x : 0, in ? u.y : 0, in ? u.z : 0, in ? u.w : 0};
+        return {{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y), bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)}};
+    }
+};
+template <> struct Raw8<float> {
+    f32x4_t a = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const f32x4_t*>(p);
+        b = *reinterpret_cast<const f32x4_t*>(p + 4);
+    }
+    __device__ __forceinline__ Vec8 get(bool in) const {
+        Vec8 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x.v[i] = in ? a[i] : 0.0f;
+            x.v[4 + i] = in ? b[i] : 0.0f;
+        }
+        return x;
+    }
+};
 
 __device__ __forceinline__ float wave_sum(float v) {
     auto ror = [](float x, auto ctrl) {
@@ -119,12 +149,20 @@ __global__ __launch_bounds__(64 * kW > kFwdThreads ? 64 * kW : kFwdThreads) void
         const bool row = t < g.T;                       // groups past T only take part in barriers
         Vec8 xv[kC], yv[kC];
         float ss[1] = {0.0f};
+        Raw8<TRes> rx[kC];
+        Raw8<uint16_t> ry[kC];
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int col = 8 * (lt + c * 64 * kW);
-            const bool in = row && col < d;
-            xv[c] = in ? ld8(x + t * d + col) : zero8();
-            yv[c] = in && g.y ? ld8(g.y + t * d + col) : zero8();
+            const int64_t at = row && col < d ? t * d + col : 0;
+            rx[c].load(x + at);
+            if (g.y) ry[c].load(g.y + at);
+        }
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const bool in = row && 8 * (lt + c * 64 * kW) < d;
+            xv[c] = rx[c].get(in);
+            yv[c] = ry[c].get(in);
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss[0] += yv[c].v[i] * yv[c].v[i];
         }
@@ -210,15 +248,26 @@ __global__ __launch_bounds__(bwd_threads<kW>(), 4) void norm_grad_kernel(NormGra
         const bool row = t < g.T;
         Vec8 G[kC], zv[kC], hv[kC], yv[kC];
         float s[3] = {0.0f, 0.0f, 0.0f};               // sums of z^2, w_pre dh z, y^2
+        Raw8<TRes> rg[kC], rzv[kC];
+        Raw8<uint16_t> rh[kC], ry[kC];
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int col = 8 * (lt + c * 64 * kW);
-            const bool in = row && col < d;
-            const int64_t at = t * d + col;
-            G[c] = in && dz ? ld8(dz + at) : zero8();
-            zv[c] = in && pre ? ld8(z + at) : zero8();
-            hv[c] = in && pre ? ld8(g.dh + at) : zero8();
-            yv[c] = in && g.y ? ld8(g.y + at) : zero8();
+            const int64_t at = row && col < d ? t * d + col : 0;
+            if (dz) rg[c].load(dz + at);
+            if (pre) {
+                rzv[c].load(z + at);
+                rh[c].load(g.dh + at);
+            }
+            if (g.y) ry[c].load(g.y + at);
+        }
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const bool in = row && 8 * (lt + c * 64 * kW) < d;
+            G[c] = rg[c].get(in);
+            zv[c] = rzv[c].get(in);
+            hv[c] = rh[c].get(in);
+            yv[c] = ry[c].get(in);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 s[0] += zv[c].v[i] * zv[c].v[i];
@@ -328,7 +377,10 @@ void launch_norm_t(const NormArgs& g, int num_cu, hipStream_t s) {
     constexpr int thr = 64 * kW > kFwdThreads ? 64 * kW : kFwdThreads;
     const int groups = thr / (64 * kW);
     const int64_t rows = ((int64_t)g.T + groups - 1) / groups;
-    const int64_t cap = (int64_t)num_cu * (2048 / thr);         // workgroups that fit the chip
+    // Half of the waves that fit a CU, with more rows each, but two workgroups: 8192 x 2048 in BF16
+    // 23.6 us against 25.3 with all waves (28.3 with four times as many), 16384 x 4096 97 against
+    // 103; 2048 x 7168, of 1024 threads a workgroup, 20.4 with two workgroups, 23.1 with one.
+    const int64_t cap = (int64_t)num_cu * (1024 / thr > 2 ? 1024 / thr : 2);
     const int grid = (int)(rows < cap ? rows : cap);
     hipLaunchKernelGGL((norm_kernel<TRes, kW, kC>), dim3(grid), dim3(thr), 0, s, g);
 }

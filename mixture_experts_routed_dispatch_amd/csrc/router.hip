@@ -725,7 +725,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
 }
 
 // Up to kOneBlock rows go to one workgroup, which needs no second launch for its sums: 64 rows of
-// 128 logits take 7.8 us in a graph (two passes, 128 rows, 11.3; 129 rows in two launches 8.6)
+// 128 logits take 7.0 us in a graph (two passes, 128 rows, 11.3; 65 rows in two launches 8.4)
 // and 2.7 us less of the host.  Workgroups of 1024 threads there, and once there are more rows
 // than one pass of the smaller ones over the chip: the same rows in flight with a quarter of
 // the partial sums.
