@@ -272,7 +272,7 @@ __device__ __forceinline__ void sort_entries(Sorted4& sm, const DecodeArgs& g, b
 template <typename Row, typename Store>
 __device__ __forceinline__ void run_items(const Sorted4& sm, Partials4& part, const void* codes, const void* words,
                                           __amdgpu_buffer_rsrc_t ars, int nblk, int S, Row&& row, Store&& store) {
-    const int lane = threadIdx.x & 63, n = lane & 15, scale_bytes = (S + 3) / 4 * 256;
+    const int lane = threadIdx.x & 63, n = lane & 15, word_bytes = (S + 3) / 4 * 256;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
     const int per = nblk / kTiles, items = __builtin_amdgcn_readfirstlane(sm.groups) * per;
@@ -286,7 +286,7 @@ __device__ __forceinline__ void run_items(const Sorted4& sm, Partials4& part, co
         const uint32_t ao = n < M ? row(sm.ent[first + n]) : kNoRow;
         f32x4_t acc[kTiles] = {};
         tile_products(acc, static_cast<const uint8_t*>(codes) + tile * S * 1024,
-                      static_cast<const uint8_t*>(words) + tile * scale_bytes, ars, ao, S, s0, s1);
+                      static_cast<const uint8_t*>(words) + tile * word_bytes, ars, ao, S, s0, s1);
         // one barrier: the other half is written next, and read only after the next barrier
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) part.p[half][wave][t][lane] = acc[t];

@@ -11,6 +11,7 @@ with torch (PyTorch supplies device memory and streams, nothing else).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -325,11 +326,16 @@ class Layer:
         import torch
         self.T, self.d, self.I, self.E, self.k = T, d, I, E, k
         self.precision = precision
-        self._mxfp4 = None
         self._rows = _dense(T, d)
         self.plan = moe_plan(T, d, I, E, k, precision, int(bool(training)), path,
                              int(bool(wgrad_accumulate)), int(bool(recompute_h)), int(activation),
                              int(bool(mega)))
+        # MXFP4: shape and strides of W13's and W2's (codes, scales)
+        self._mxfp4 = None
+        if precision == MOE_MXFP4:
+            self._mxfp4 = ((_dense(E, I * d), _dense(E, 2 * I // 16, (d + 511) // 512, 64, 4)),
+                           (_dense(E, d * I // 2), _dense(E, d // 16, (I + 511) // 512, 64, 4)))
+            self._mxfp4_sizes = [math.prod(shape) for shape, _ in sum(self._mxfp4, ())]
         nbytes = moe_workspace_bytes(self.plan)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         moe_bind_workspace(self.plan, _ptr(self.workspace), self.workspace.numel())
@@ -364,6 +370,8 @@ class Layer:
         import torch
         if y is None:
             y = _new(self._rows, torch.bfloat16, x.device)
+        if self._mxfp4 is not None:
+            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x, ids, scores, y)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward(self.plan, _ptr(x), _ptr(ids), _ptr(scores), w, _ptr(y), _stream(stream))
         return y
@@ -376,6 +384,8 @@ class Layer:
         import torch
         if out is None:
             out = torch.empty((self.T * self.k, self.d), dtype=torch.bfloat16, device=x_rows.device)
+        if self._mxfp4 is not None:
+            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward_routed(self.plan, _ptr(x_rows), _ptr(m_indptr), w, _ptr(out), _stream(stream))
         return out
@@ -408,7 +418,8 @@ class Layer:
         dev = w13.device
         E, I, d = self.E, self.I, self.d
         if self.precision == MOE_MXFP4:
-            (n13, n2), stream = self._mxfp4_layout(), _stream(stream)
+            (n13, n2), stream = self._mxfp4, _stream(stream)
+            dev = torch.device("cuda", torch.cuda.current_device())
             _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
             _check("w2", w2, (E, d, I), torch.bfloat16, dev)
             w13_q, w13_s, w2_q, w2_s = (_new(n, torch.uint8, dev) for n in n13 + n2)
@@ -424,13 +435,24 @@ class Layer:
                             _ptr(w2_s), _stream(stream))
         return w13_q, w13_s, w2_q, w2_s
 
-    def _mxfp4_layout(self):
-        """(codes, scales) of W13 and of W2, each as shape and strides."""
-        if self._mxfp4 is None:
-            E, I, d = self.E, self.I, self.d
-            self._mxfp4 = ((_dense(E, I * d), _dense(E, 2 * I // 16, (d + 511) // 512, 64, 4)),
-                           (_dense(E, d * I // 2), _dense(E, d // 16, (I + 511) // 512, 64, 4)))
-        return self._mxfp4
+    def _check_mxfp4(self, w13_q, w13_s, w2_q, w2_s, *others):
+        """Prepared weights of this layer's shapes, they and the other tensors on the current
+        device, or ValueError (a missing scale is left to the call).  The kernels address them by
+        the plan's sizes."""
+        import torch
+        index, right = torch.cuda.current_device(), True
+        for t, n in zip((w13_q, w13_s, w2_q, w2_s), self._mxfp4_sizes):
+            if t is not None:
+                right = right and t.numel() == n and t.is_contiguous() and t.get_device() == index
+        for t in others:
+            right = right and (t is None or t.get_device() == index)
+        if right:
+            return
+        dev, layout = torch.device("cuda", index), sum(self._mxfp4, ())
+        for name, t, (shape, _) in zip(("w13_q", "w13_s", "w2_q", "w2_s"), (w13_q, w13_s, w2_q, w2_s), layout):
+            if t is not None:
+                _check(name, t, shape, torch.uint8, dev)
+        raise ValueError("the current device is %s, x, ids, scores or the output is elsewhere" % dev)
 
     def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
         """The BF16 weights (w13, w2) that an MXFP4 layer's prepared weights stand for."""
@@ -438,9 +460,7 @@ class Layer:
         dev = w13_q.device
         E, I, d = self.E, self.I, self.d
         if self.precision == MOE_MXFP4:
-            for name, t, n in zip(("w13_q", "w13_s", "w2_q", "w2_s"), (w13_q, w13_s, w2_q, w2_s),
-                                  sum(self._mxfp4_layout(), ())):
-                _check(name, t, n[0], torch.uint8, dev)
+            self._check_mxfp4(w13_q, w13_s, w2_q, w2_s)
         w13 = torch.empty((E, 2 * I, d), dtype=torch.bfloat16, device=dev)
         w2 = torch.empty((E, d, I), dtype=torch.bfloat16, device=dev)
         w = weights(_ptr(w13_q), _ptr(w2_q), _ptr(w13_s), _ptr(w2_s))

@@ -214,3 +214,29 @@ def test_weight_refusals(moe):
         layer.forward(torch.zeros(1, 256, dtype=torch.bfloat16, device=dev()),
                       torch.zeros(1, 1, dtype=torch.int32, device=dev()), torch.ones(1, 1, device=dev()), packed[0],
                       packed[2])                       # the scales are missing
+
+
+def test_weights_of_other_shapes_are_refused(moe):
+    """The kernels address the weights by the plan's sizes: codes and scales in the wrong places,
+    another layer's, or tensors on the host never reach them."""
+    import torch
+    for T, path in ((1, 0), (4, 0), (4, moe.MOE_PATH_PREFILL)):
+        layer = moe.Layer(T, 256, 128, 4, 2, precision=moe.MOE_MXFP4, path=path)
+        w = [torch.zeros(4, 256, 256, dtype=torch.bfloat16, device=dev()), torch.zeros(4, 256, 128, dtype=torch.bfloat16, device=dev())]
+        w13, s13, w2, s2 = layer.prepare_weights(*w)
+        x = torch.zeros(T, 256, dtype=torch.bfloat16, device=dev())
+        ids = torch.tensor([[0, 3]] * T, dtype=torch.int32, device=dev())
+        scores = torch.ones(T, 2, device=dev())
+        good = (x, ids, scores, w13, w2, s13, s2)
+        assert not layer.forward(*good).any()
+        for at, bad in ((3, s13), (4, w13), (5, w2), (6, s2[:1]), (3, w13[:3]), (4, w2.cpu()), (0, x.cpu()), (2, scores.cpu()),
+                        (3, w13[:1].expand(4, -1))):
+            args = list(good)
+            args[at] = bad
+            with pytest.raises(ValueError):
+                layer.forward(*args)
+        if path:
+            rows = torch.zeros(2 * T, 256, dtype=torch.bfloat16, device=dev())
+            m_indptr = torch.zeros(5, dtype=torch.int32, device=dev())
+            with pytest.raises(ValueError):
+                layer.forward_routed(rows, m_indptr, w13, s13, w2, s2)
