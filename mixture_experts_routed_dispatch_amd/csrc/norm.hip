@@ -17,7 +17,7 @@
 // that it stays in registers between the reductions; kW is the fewest waves that hold d.  The
 // vectors over channels are loaded once per workgroup, which walks several rows.  Memory
 // bound: the least traffic is 4 (forward) and 6 (backward) passes over [T, d]; 8192 x 2048 in
-// BF16, post norm, gate and pre norm: forward 23.6 us (5.7 TB/s), backward 39.0 us (5.2 TB/s)
+// BF16, post norm, gate and pre norm: forward 23.6 us (5.7 TB/s), backward 37.7 us (5.3 TB/s)
 // and 4.8 us for the column sums' second stage.  Stores past the caches gain the forward 2 us
 // here, cost it 4 us of 36 at 4099 x 4096 with an FP32 stream, and slow whoever reads h next.
 #include <type_traits>
@@ -64,9 +64,9 @@ template <typename T> struct Raw8;
 template <> struct Raw8<uint16_t> {
     uint4 u = {0, 0, 0, 0};
     __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ Vec8 get(bool in) const {
-        const uint4 w = {in ? u.x : 0, in ? u.y : 0, in ? u.z : 0, in ? u.w : 0};
-        return {{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y), bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)}};
+    __device__ __forceinline__ void keep(bool in) { u = {in ? u.x : 0, in ? u.y : 0, in ? u.z : 0, in ? u.w : 0}; }
+    __device__ __forceinline__ Vec8 get() const {
+        return {{bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y), bf16lo(u.z), bf16hi(u.z), bf16lo(u.w), bf16hi(u.w)}};
     }
 };
 template <> struct Raw8<float> {
@@ -75,31 +75,28 @@ template <> struct Raw8<float> {
         a = *reinterpret_cast<const f32x4_t*>(p);
         b = *reinterpret_cast<const f32x4_t*>(p + 4);
     }
-    __device__ __forceinline__ Vec8 get(bool in) const {
-        Vec8 x;
+    __device__ __forceinline__ void keep(bool in) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x.v[i] = in ? a[i] : 0.0f;
-            x.v[4 + i] = in ? b[i] : 0.0f;
+            a[i] = in ? a[i] : 0.0f;
+            b[i] = in ? b[i] : 0.0f;
         }
-        return x;
     }
+    __device__ __forceinline__ Vec8 get() const { return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}}; }
 };
 
+// v plus its value kBy lanes further in the row of 16
+template <int kBy> __device__ __forceinline__ float plus_rotated(float v) {
+    return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + kBy, 0xF, 0xF, true));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-    auto ror = [](float x, auto ctrl) {
-        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value,
-                                                                     0xF, 0xF, true));
-    };
-    v += ror(v, std::integral_constant<int, 0x128>());
-    v += ror(v, std::integral_constant<int, 0x124>());
-    v += ror(v, std::integral_constant<int, 0x122>());
-    v += ror(v, std::integral_constant<int, 0x121>());
+    v = plus_rotated<1>(plus_rotated<2>(plus_rotated<4>(plus_rotated<8>(v))));
     v += __shfl_xor(v, 16, 64);
     return v + __shfl_xor(v, 32, 64);
 }
 
-// kN sums over the kW waves of a row, in wave order.  One barrier: `red` has two halves used
+// kN sums over the kW waves of a row: every lane takes the sum of one wave, and rotations by
+// kW / 2, .., 1 add them in the same order in all lanes.  One barrier: `red` has two halves used
 // in turn, and a half is written again only after the barrier of the reduction in between.
 template <int kN, int kW, int kGroups>
 __device__ __forceinline__ void row_sums(float (&v)[kN], float (*red)[kGroups][kW][kN], int& half) {
@@ -113,9 +110,11 @@ __device__ __forceinline__ void row_sums(float (&v)[kN], float (*red)[kGroups][k
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            v[i] = red[half][grp][0][i];
-#pragma unroll
-            for (int u = 1; u < kW; ++u) v[i] += red[half][grp][u][i];
+            v[i] = red[half][grp][threadIdx.x % kW][i];
+            if constexpr (kW >= 16) v[i] = plus_rotated<8>(v[i]);
+            if constexpr (kW >= 8) v[i] = plus_rotated<4>(v[i]);
+            if constexpr (kW >= 4) v[i] = plus_rotated<2>(v[i]);
+            v[i] = plus_rotated<1>(v[i]);
         }
         half ^= 1;
     }
@@ -161,8 +160,10 @@ __global__ __launch_bounds__(64 * kW > kFwdThreads ? 64 * kW : kFwdThreads) void
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const bool in = row && 8 * (lt + c * 64 * kW) < d;
-            xv[c] = rx[c].get(in);
-            yv[c] = ry[c].get(in);
+            rx[c].keep(in);
+            ry[c].keep(in);
+            xv[c] = rx[c].get();
+            yv[c] = ry[c].get();
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss[0] += yv[c].v[i] * yv[c].v[i];
         }
@@ -210,17 +211,19 @@ __device__ __forceinline__ void finish_column(const NormGradArgs& g, int which, 
     if (channel) g.dgate[c] = g.w_post ? g.w_post[c] * sum : sum;
 }
 
-// Workgroups of 512 threads, two a CU, so that one loads while the other waits at a barrier
-// (8192 x 2048 in BF16: 39.0 us against 41.0 with one of 1024; 4099 x 4096 with an FP32 stream:
-// 57.3 against 61.6, 5.3 TB/s of its 302 MB).  Loading the next row ahead takes the registers
-// of the second workgroup and is slower (50.0 and 64.0 us).
+// Workgroups of 512 threads, two a CU, so that one loads while the other waits at a barrier.  What
+// stays of a row from its first reduction on stays packed (8 registers for h and y instead of 16),
+// and only one sum is left for the second (dgate_t and the mean of w_post dn y differ by a
+// factor), so that the next row's loads fit besides the second workgroup: 8192 x 2048 in BF16
+// 37.7 us (39.0 without them; one workgroup of 1024 threads 37.1), 4099 x 4096 with an FP32 stream
+// 56.6 us (57.4; 58.4), 5.6 and 5.6 TB/s of what they move, the partial sums of 8 and 17 MB among it.
 constexpr int kBwdThreads = 512;
 template <int kW> constexpr int bwd_threads() { return 64 * kW > kBwdThreads ? 64 * kW : kBwdThreads; }
 template <typename TRes, int kW, int kC>
 __global__ __launch_bounds__(bwd_threads<kW>(), 4) void norm_grad_kernel(NormGradArgs g) {
     constexpr int kThr = bwd_threads<kW>(), kGroups = kThr / (64 * kW), kCols = 512 * kW;
     __shared__ float red1[2][kGroups][kW][3];
-    __shared__ float red2[2][kGroups][kW][2];
+    __shared__ float red2[2][kGroups][kW][1];
     __shared__ __attribute__((aligned(16))) float cols[kGroups > 1 ? kThr * 8 : 4];
     int half1 = 0, half2 = 0;
     const int grp = threadIdx.x / (64 * kW), lt = threadIdx.x % (64 * kW);
@@ -232,85 +235,101 @@ __global__ __launch_bounds__(bwd_threads<kW>(), 4) void norm_grad_kernel(NormGra
     const bool pre = g.w_pre != nullptr, post = g.w_post != nullptr;
     // a_pre: sum_t dh z r;  a_out: sum_t alpha gate_t G y q (gate_t: of a gate per token, else 1),
     // from which a gate per channel and w_post give dw_post = gate a_out, dgate = w_post a_out
-    Vec8 wq[kC], gt[kC], wp[kC], a_pre[kC], a_out[kC];
+    Vec8 wg[kC], wp[kC], a_pre[kC], a_out[kC];          // wg: w_post times the gate per channel
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
         const int col = 8 * (lt + c * 64 * kW);
         const bool in = col < d;
-        wq[c] = ld8_or(g.w_post, col, in, 1.0f);
-        gt[c] = ld8_or(g.gate_kind == kGateChannel ? g.gate : nullptr, col, in, 1.0f);
+        wg[c] = ld8_or(g.w_post, col, in, 1.0f);
+        const Vec8 gt = ld8_or(g.gate_kind == kGateChannel ? g.gate : nullptr, col, in, 1.0f);
         wp[c] = ld8_or(g.w_pre, col, in, 0.0f);
         a_pre[c] = a_out[c] = zero8();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wg[c].v[i] *= gt.v[i];
     }
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    for (int64_t t0 = (int64_t)blockIdx.x * kGroups; t0 < g.T; t0 += step) {
-        const int64_t t = t0 + grp;
-        const bool row = t < g.T;
-        Vec8 G[kC], zv[kC], hv[kC], yv[kC];
-        float s[3] = {0.0f, 0.0f, 0.0f};               // sums of z^2, w_pre dh z, y^2
-        Raw8<TRes> rg[kC], rzv[kC];
-        Raw8<uint16_t> rh[kC], ry[kC];
+    struct Row {
+        Raw8<TRes> dz[kC], z[kC];
+        Raw8<uint16_t> h[kC], y[kC];
+    };
+    auto load = [&](Row& w, int64_t t) {
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int col = 8 * (lt + c * 64 * kW);
-            const int64_t at = row && col < d ? t * d + col : 0;
-            if (dz) rg[c].load(dz + at);
+            const int64_t at = t < g.T && col < d ? t * d + col : 0;
+            if (dz) w.dz[c].load(dz + at);
             if (pre) {
-                rzv[c].load(z + at);
-                rh[c].load(g.dh + at);
+                w.z[c].load(z + at);
+                w.h[c].load(g.dh + at);
             }
-            if (g.y) ry[c].load(g.y + at);
+            if (g.y) w.y[c].load(g.y + at);
         }
+    };
+    // the next row's loads are out while this one's sums and stores run, where its 16 to 24
+    // registers are there
+    constexpr bool kAhead = kC == 1;
+    Row next;
+    if constexpr (kAhead) load(next, (int64_t)blockIdx.x * kGroups + grp);
+    for (int64_t t0 = (int64_t)blockIdx.x * kGroups; t0 < g.T; t0 += step) {
+        const int64_t t = t0 + grp;
+        const bool row = t < g.T;
+        Row w;
+        if constexpr (kAhead) w = next;
+        else load(w, t);
+        float s[3] = {0.0f, 0.0f, 0.0f};               // sums of z^2, w_pre dh z, y^2
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const bool in = row && 8 * (lt + c * 64 * kW) < d;
-            G[c] = rg[c].get(in);
-            zv[c] = rzv[c].get(in);
-            hv[c] = rh[c].get(in);
-            yv[c] = ry[c].get(in);
+            w.dz[c].keep(in); w.z[c].keep(in); w.h[c].keep(in); w.y[c].keep(in);
+            const Vec8 zv = w.z[c].get(), hv = w.h[c].get(), yv = w.y[c].get();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                s[0] += zv[c].v[i] * zv[c].v[i];
-                s[1] += hv[c].v[i] * wp[c].v[i] * zv[c].v[i];
-                s[2] += yv[c].v[i] * yv[c].v[i];
+                s[0] += zv.v[i] * zv.v[i];
+                s[1] += hv.v[i] * wp[c].v[i] * zv.v[i];
+                s[2] += yv.v[i] * yv.v[i];
             }
         }
+        if constexpr (kAhead) load(next, t + step);
         row_sums<3, kW, kGroups>(s, red1, half1);
         const float r = __builtin_amdgcn_rsqf(s[0] * inv_d + g.eps);
         const float q = post ? __builtin_amdgcn_rsqf(s[2] * inv_d + g.eps) : 1.0f;
         const float rz = r * (s[1] * inv_d) * r * r;   // in this order a row of zeros gives 0
         const float tg = g.alpha * (g.gate_kind == kGateToken && row ? g.gate[t] : 1.0f);
-        float u[2] = {0.0f, 0.0f};                     // sums of w_post dn y, G n
+        const float tq = tg * q;
+        float u[1] = {0.0f};                           // sum of w_post gate_c G y
+        Vec8 G[kC];
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int col = 8 * (lt + c * 64 * kW);
+            G[c] = w.dz[c].get();
             if (pre) {
+                const Vec8 zv = w.z[c].get(), hv = w.h[c].get();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float hr = hv[c].v[i] * r;
-                    a_pre[c].v[i] += hr * zv[c].v[i];
-                    G[c].v[i] += wp[c].v[i] * hr - zv[c].v[i] * rz;
+                    const float hr = hv.v[i] * r;
+                    a_pre[c].v[i] += hr * zv.v[i];
+                    G[c].v[i] += wp[c].v[i] * hr - zv.v[i] * rz;
                 }
             }
             if (row && col < d) st8(dx + t * d + col, G[c]);
+            const Vec8 yv = w.y[c].get();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float gw = G[c].v[i] * wq[c].v[i];
-                a_out[c].v[i] += G[c].v[i] * tg * (yv[c].v[i] * q);
-                G[c].v[i] = gw * gt[c].v[i] * tg;
-                u[0] += G[c].v[i] * yv[c].v[i];
-                u[1] += gw * yv[c].v[i];
+                a_out[c].v[i] += G[c].v[i] * tq * yv.v[i];
+                G[c].v[i] *= wg[c].v[i];
+                u[0] += G[c].v[i] * yv.v[i];
             }
         }
         if (!g.y) continue;
-        if (post || g.gate_kind == kGateToken) row_sums<2, kW, kGroups>(u, red2, half2);
-        const float qy = post ? q * (u[0] * inv_d) * q * q : 0.0f;
-        if (g.gate_kind == kGateToken && row && lt == 0) g.dgate[t] = g.alpha * q * u[1];
+        if (post || g.gate_kind == kGateToken) row_sums<1, kW, kGroups>(u, red2, half2);
+        const float qy = post ? q * (tg * u[0] * inv_d) * q * q : 0.0f;
+        if (g.gate_kind == kGateToken && row && lt == 0) g.dgate[t] = g.alpha * q * u[0];
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int col = 8 * (lt + c * 64 * kW);
+            const Vec8 yv = w.y[c].get();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) G[c].v[i] = q * G[c].v[i] - yv[c].v[i] * qy;
+            for (int i = 0; i < 8; ++i) G[c].v[i] = tq * G[c].v[i] - yv.v[i] * qy;
             if (row && col < d) st8(g.dy + t * d + col, G[c]);
         }
     }
