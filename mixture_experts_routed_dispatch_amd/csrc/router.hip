@@ -18,13 +18,15 @@
 // that a wave works on four rows and every reduction over a row stays within 16 lanes, where
 // DPP rotations do it without LDS.
 //
-// The choice, k <= kFastK: the k-th largest of the 16 lanes' maxima is a bound that at least k
-// keys reach and few do (with 256 random keys about 11 for k = 8, 21 for k = 12).  Those
-// candidates' indices go to LDS in ascending order, one or two to a lane, and each counts the
-// ones before it, which is its place.  More than kCand candidates (ties, rows of one value) and
-// larger k take the row's maximum k times.  16384 x 256 in BF16 with sigmoid, bias and k = 8:
-// 12.0 us, against 32.4 by taking the maximum 8 times; 800 vector instructions a wave issue for
-// 6 us of it, the rest is the latency of one pass (its 9.5 MB take 1.9 us).
+// The choice.  A bound that at least k keys reach and few do is the k-th largest of the 16 lanes'
+// maxima for k <= 8 (of 256 random keys about 11 reach it for k = 8), or of their two largest each
+// for k <= 20 (about 18 for k = 16).  Those candidates' indices go to LDS in ascending order, one or
+// two to a lane, and each counts the ones before it, which is its place.  With larger k, or more than
+// kCand candidates (ties, rows of one value), the row's maximum is taken k times; a bias then takes
+// the last of those as the bound.  16384 x 256 in BF16 with sigmoid, bias and k = 8: 12.0 us, against
+// 32.4 by taking the maximum 8 times; 800 vector instructions a wave issue for 6 us of it, the rest
+// is the latency of one pass (its 9.5 MB take 1.9 us).  k = 16 with the second launch 23.8 us, and
+// 113 while all of k > 12 took the maxima and settled near keys for the whole row.
 //
 // With a bias the keys s + b have to be ordered as in exact arithmetic.  They are compared in
 // FP32; where two that matter lie closer than FP32's error, they are computed again in 64
@@ -86,7 +88,13 @@ __device__ __forceinline__ float ld_logit(const void* p, int64_t i, bool f32) {
     return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
-// kV logits from index i0 of the row at element offset `row`; -inf past E.  vec: rows start
+// The logits of a lane: kV from index first(l16) on, the second 8 of 16 from the row's second half.
+// So the 16 lanes' pieces follow one another, and rows of 129 to 255 fill all lanes too.
+template <int kV> __device__ __forceinline__ int first(int l16) { return l16 * (kV < 8 ? kV : 8); }
+// i-th of them relative to the first
+__device__ __forceinline__ constexpr int ahead(int i) { return i + (i >= 8 ? 120 : 0); }
+
+// A lane's kV logits of the row at element offset `row`; -inf past E.  vec: rows start
 // on, and E is a multiple of, the widest piece used here (16 bytes, 8 for kV = 4 in BF16).
 template <int kV, bool kF32>
 __device__ __forceinline__ void load_row(const void* p, int64_t row, int i0, int E, bool vec, float z[kV]) {
@@ -95,7 +103,7 @@ __device__ __forceinline__ void load_row(const void* p, int64_t row, int i0, int
 #pragma unroll
             for (int c = 0; c < kV; c += 4) {
                 f32x4_t v = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (i0 + c < E) v = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + row + i0 + c);
+                if (ahead(c) < E - i0) v = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + row + i0 + ahead(c));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) z[c + i] = v[i];
             }
@@ -107,14 +115,14 @@ __device__ __forceinline__ void load_row(const void* p, int64_t row, int i0, int
 #pragma unroll
             for (int c = 0; c < kV; c += 8) {
                 uint4 v = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-                if (i0 + c < E) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + row + i0 + c);
+                if (ahead(c) < E - i0) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + row + i0 + ahead(c));
                 z[c] = bf16lo(v.x); z[c + 1] = bf16hi(v.x); z[c + 2] = bf16lo(v.y); z[c + 3] = bf16hi(v.y);
                 z[c + 4] = bf16lo(v.z); z[c + 5] = bf16hi(v.z); z[c + 6] = bf16lo(v.w); z[c + 7] = bf16hi(v.w);
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) z[i] = i0 + i < E ? ld_logit(p, row + i0 + i, kF32) : -INFINITY;
+        for (int i = 0; i < kV; ++i) z[i] = ahead(i) < E - i0 ? ld_logit(p, row + i0 + ahead(i), kF32) : -INFINITY;
     }
 }
 
@@ -124,9 +132,9 @@ __device__ __forceinline__ void store_row(void* p, int64_t row, int i0, int E, b
         if constexpr (kF32) {
 #pragma unroll
             for (int c = 0; c < kV; c += 4)
-                if (i0 + c < E) {
+                if (ahead(c) < E - i0) {
                     const f32x4_t v = {z[c], z[c + 1], z[c + 2], z[c + 3]};
-                    *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + i0 + c) = v;
+                    *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + i0 + ahead(c)) = v;
                 }
         } else if constexpr (kV == 4) {
             if (i0 < E)
@@ -135,17 +143,17 @@ __device__ __forceinline__ void store_row(void* p, int64_t row, int i0, int E, b
         } else {
 #pragma unroll
             for (int c = 0; c < kV; c += 8)
-                if (i0 + c < E)
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + row + i0 + c) =
+                if (ahead(c) < E - i0)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + row + i0 + ahead(c)) =
                         make_uint4(pack_bf16(z[c], z[c + 1]), pack_bf16(z[c + 2], z[c + 3]),
                                    pack_bf16(z[c + 4], z[c + 5]), pack_bf16(z[c + 6], z[c + 7]));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kV; ++i)
-            if (i0 + i < E) {
-                if constexpr (kF32) static_cast<float*>(p)[row + i0 + i] = z[i];
-                else static_cast<uint16_t*>(p)[row + i0 + i] = (uint16_t)f32_to_bf16(z[i]);
+            if (ahead(i) < E - i0) {
+                if constexpr (kF32) static_cast<float*>(p)[row + i0 + ahead(i)] = z[i];
+                else static_cast<uint16_t*>(p)[row + i0 + ahead(i)] = (uint16_t)f32_to_bf16(z[i]);
             }
     }
 }
@@ -184,23 +192,20 @@ template <bool kSig> __device__ __forceinline__ float one_score(float z, float b
 // become 0.  Returns the last one's key.
 template <int kV>
 __device__ __forceinline__ uint32_t take_top(uint32_t key[kV], int k, int i0, int* sel) {
-    const int lane = threadIdx.x & 63, l16 = lane & 15, grp = lane >> 4;
     uint32_t m = 0;
     for (int j = 0; j < k; ++j) {
         uint32_t mine = key[0];
 #pragma unroll
         for (int i = 1; i < kV; ++i) mine = mine > key[i] ? mine : key[i];
         m = row_max_u32(mine);
-        const uint64_t b = __ballot(mine == m);
-        const uint32_t half = grp & 2 ? (uint32_t)(b >> 32) : (uint32_t)b;
-        const uint32_t field = (grp & 1 ? half >> 16 : half) & 0xFFFFu;
-        int li = 0;
+        int at = 1 << 20;                               // the first of them in this lane, then in the row
 #pragma unroll
-        for (int i = kV - 1; i >= 0; --i) li = key[i] == m ? i : li;
-        if (l16 == __builtin_ctz(field)) sel[j] = i0 + li;
-        else li = -1;
+        for (int i = kV - 1; i >= 0; --i) at = key[i] == m ? ahead(i) : at;
+        at += i0;
+        const int best = (int)~row_max_u32(~(uint32_t)at);
+        if (at == best) sel[j] = best;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) key[i] = li == i ? 0u : key[i];
+        for (int i = 0; i < kV; ++i) key[i] = ahead(i) == best - i0 ? 0u : key[i];
     }
     return m;
 }
@@ -218,13 +223,14 @@ __device__ __forceinline__ double exact_sum(const void* logits, int64_t row, int
     if constexpr (kSig) return 1.0;
     float top = -INFINITY;
 #pragma unroll 1
-    for (int i = 0; i < kV && i0 + i < E; ++i) top = __builtin_fmaxf(top, ld_logit(logits, row + i0 + i, f32));
+    for (int i = 0; i < kV; ++i)
+        if (ahead(i) < E - i0) top = __builtin_fmaxf(top, ld_logit(logits, row + i0 + ahead(i), f32));
     top = row_max(top);
     zmax = top == -INFINITY ? 0.0f : top;
     double sum = 0.0;
 #pragma unroll 1
     for (int i = 0; i < kV; ++i) {
-        const float z = i0 + i < E ? ld_logit(logits, row + i0 + i, f32) : -INFINITY;
+        const float z = ahead(i) < E - i0 ? ld_logit(logits, row + i0 + ahead(i), f32) : -INFINITY;
         sum += exp((double)z - (double)zmax);
     }
     for (int o = 8; o; o >>= 1) sum += __shfl_xor(sum, o, 16);
@@ -242,9 +248,10 @@ __device__ __forceinline__ void take_top_exact(const RouterArgs& g, int64_t row,
         int at = 1 << 20;
 #pragma unroll 1
         for (int i = 0; i < kV; ++i) {
-            if (i0 + i >= g.E || (taken >> i & 1)) continue;
-            const double key = exact_key<kSig>(ld_logit(g.logits, row + i0 + i, f32), g.bias[i0 + i], zmax, sum);
-            if (key > m || at == 1 << 20) { m = key; at = i0 + i; }
+            const int e = i0 + ahead(i);
+            if (e >= g.E || (taken >> i & 1)) continue;
+            const double key = exact_key<kSig>(ld_logit(g.logits, row + e, f32), g.bias[e], zmax, sum);
+            if (key > m || at == 1 << 20) { m = key; at = e; }
         }
         for (int o = 8; o; o >>= 1) {
             const double om = __shfl_xor(m, o, 16);
@@ -252,7 +259,8 @@ __device__ __forceinline__ void take_top_exact(const RouterArgs& g, int64_t row,
             if (oa != 1 << 20 && (at == 1 << 20 || om > m || (om == m && oa < at))) { m = om; at = oa; }
         }
         if ((threadIdx.x & 15) == 0) sel[j] = at;
-        if (at >= i0 && at < i0 + kV) taken |= 1u << (at - i0);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) taken |= ahead(i) == at - i0 ? 1u << i : 0u;
     }
 }
 
@@ -267,49 +275,81 @@ __device__ __forceinline__ void wave_fence() {
 // 6e-8 of the key, so two keys by less than 7.2e-7
 constexpr float kNear = 2e-6f;
 
-constexpr int kFastK = 12;               // largest k of the candidate way
+constexpr int kOneK = 8, kTwoK = 20;     // largest k with bounds from the lanes' first one and two
 constexpr int kCand = 32;                // candidates a row, at most
 
-// one rotation's share of `above` (lanes of the row whose value is larger)
-template <int kN> __device__ __forceinline__ void count_above(float v, int& above) {
+// how many of the other 15 lanes' values are larger than v
+template <int kN = 15> __device__ __forceinline__ void count_above(float v, int& above) {
     above += __uint_as_float(dpp<0x120 + kN>(__float_as_uint(v))) > v;
     if constexpr (kN > 1) count_above<kN - 1>(v, above);
 }
-// Indices of the row's candidates into list, ascending; returns how many there are (more than
-// kCand: the list is not to be used).  slack: how far below the bound a key still counts.
-template <int kV>
-__device__ __forceinline__ int find_candidates(const float key[kV], int k, int i0, int E, float slack, int* list) {
-    float mine = key[0];
+// the same of two values a lane, which pass by one lane at a time (side by side they take 30
+// registers)
+template <int kN = 15>
+__device__ __forceinline__ void count_above(float a, float b, float ra, float rb, int& above_a, int& above_b) {
+    ra = __uint_as_float(dpp<0x121>(__float_as_uint(ra)));
+    rb = __uint_as_float(dpp<0x121>(__float_as_uint(rb)));
+    above_a += (ra > a) + (rb > a);
+    above_b += (ra > b) + (rb > b);
+    if constexpr (kN > 1) count_above<kN - 1>(a, b, ra, rb, above_a, above_b);
+}
+// A bound that at least k of the row's keys reach: the k-th largest of the lanes' largest keys, or
+// of their two largest.  It is the smallest of those with fewer than k above it.
+template <int kV> __device__ __forceinline__ float bound_of(const float key[kV], int k) {
+    if (__builtin_expect(k <= kOneK, 1)) {
+        float a = key[0];
 #pragma unroll
-    for (int i = 1; i < kV; ++i) mine = __builtin_fmaxf(mine, key[i]);
-    mine = choice_key(mine);
-    int above = 0;
-    count_above<15>(mine, above);
-    // the smallest maximum with fewer than k above it is the k-th largest of the 16
-    float bound = -row_max(above < k ? -mine : -INFINITY);
+        for (int i = 1; i < kV; ++i) a = __builtin_fmaxf(a, key[i]);
+        a = choice_key(a);
+        int above = 0;
+        count_above(a, above);
+        return -row_max(above < k ? -a : -INFINITY);
+    }
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        b = key[i] > a ? a : __builtin_fmaxf(b, key[i]);
+        a = __builtin_fmaxf(a, key[i]);
+    }
+    int above_a = 0, above_b = a > b;
+    count_above(a, b, a, b, above_a, above_b);
+    return -row_max(above_b < k ? -b : above_a < k ? -a : -INFINITY);
+}
+// Indices of the row's candidates, which reach the bound, into list, ascending; returns how many
+// there are (more than kCand: the list is not to be used).  slack: how far below the bound a key
+// still counts.
+template <int kV>
+__device__ __forceinline__ int find_candidates(const float key[kV], float bound, int i0, int E, float slack, int* list) {
     bound -= slack * __builtin_fmaxf(1.0f, __builtin_fabsf(bound));
     if (!(bound > -INFINITY)) bound = -INFINITY;        // +inf gives NaN: then every key counts
     uint32_t m = 0;                                     // a NaN key is a candidate, which counts as -inf
 #pragma unroll
     for (int i = kV - 1; i >= 0; --i) m = m + m + !(key[i] < bound);
-    const int room = E - i0;                            // logits of this lane that exist
-    if (room < kV) m &= room > 0 ? (1u << room) - 1 : 0u;
-    const int n = __builtin_popcount(m);
-    int incl = n;                                       // row_shr: the lanes below, 0 past the row
-    incl += (int)dpp<0x111>((uint32_t)incl);
-    incl += (int)dpp<0x112>((uint32_t)incl);
-    incl += (int)dpp<0x114>((uint32_t)incl);
-    incl += (int)dpp<0x118>((uint32_t)incl);
-    const int total = (int)row_max_u32((uint32_t)incl);
-    int pos = incl - n;
+    auto exist = [&](int room) { return room > 7 ? 0xFFu : room > 0 ? (1u << room) - 1 : 0u; };
+    uint32_t all = exist(E - i0);
+    if constexpr (kV == 16) all |= exist(E - i0 - 128) << 8;
+    m &= all;
+    // candidates of the lanes below, of each half of the row: row_shr, 0 past the row
+    const uint32_t n = (uint32_t)__builtin_popcount(m & 0xFF) | (uint32_t)__builtin_popcount(m >> 8) << 16;
+    uint32_t incl = n;
+    incl += dpp<0x111>(incl);
+    incl += dpp<0x112>(incl);
+    incl += dpp<0x114>(incl);
+    incl += dpp<0x118>(incl);
+    const uint32_t total = row_max_u32(incl);           // the last lane's, in both halves
+    const int sum = (int)((total & 0xFFFF) + (total >> 16));
+    int pos = (int)((incl - n) & 0xFFFF);
+    // where the second half's go less where they would go if they followed the lane's first ones
+    const int jump = kV == 16 ? (int)((total & 0xFFFF) + (incl >> 16) - (n >> 16) - (incl & 0xFFFF)) : 0;
     while (__ballot(m != 0)) {
         if (m) {
-            if (pos < kCand) list[pos] = i0 + __builtin_ctz(m);
+            const int i = __builtin_ctz(m), at = pos + (i < 8 ? 0 : jump);
+            if (at < kCand) list[at] = i0 + ahead(i);
             ++pos;
             m &= m - 1;
         }
     }
-    return total;
+    return sum;
 }
 
 // Where each candidate of a row (n of them, kH to a lane) comes in the order: id and place of this
@@ -355,7 +395,7 @@ __device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t,
         bool near = false;
 #pragma unroll
         for (int h = 0; h < kH; ++h) near |= close[h] > 1 && place[h] < g.k;
-        if (!__ballot(near)) return;
+        if (__builtin_expect(!__ballot(near), 1)) return;
         float zmax;
         const double sum = exact_sum<kV, kSig>(g.logits, row, i0, g.E, zmax, kF32);
         double own64[kH];
@@ -405,7 +445,7 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
     __shared__ double part[4][2];
     static_assert(kMaxTopK <= kCand, "sel holds a row's choice too");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = tid & 15, row = tid >> 4;
-    const int E = g.E, k = g.k, i0 = l16 * kV;
+    const int E = g.E, k = g.k, i0 = first<kV>(l16);
     if (tid < 256) cnt[tid] = 0;
     __syncthreads();
     float acc[kV];
@@ -428,12 +468,34 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) z[i] += s[i];  // keys from here on
         int n = kCand + 1;
-        if (k <= kFastK) n = find_candidates<kV>(z, k, i0, E, kBias ? kNear : 0.0f, sel[row]);
-        if (!__ballot(n > kCand)) {
+        if (k <= kTwoK) n = find_candidates<kV>(z, bound_of<kV>(z, k), i0, E, kBias ? kNear : 0.0f, sel[row]);
+        bool placed = !__ballot(n > kCand);
+        uint32_t last = 0;                              // the k-th largest key, where the maxima were taken
+        if (__builtin_expect(!placed, 0)) {
+            uint32_t key[kV];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) key[i] = ahead(i) < E - i0 ? order_key(z[i]) : 0u;
+            wave_fence();
+            last = take_top<kV>(key, k, i0, sel[row]);
+            wave_fence();
+            if constexpr (kBias) {
+                // that key is the best bound; the candidates go to 64 bits only if they have to
+                int* list = reinterpret_cast<int*>(keys[row]);
+                n = find_candidates<kV>(z, key_value(last), i0, E, kNear, list);
+                placed = !__ballot(n > kCand);
+                wave_fence();
+                if (placed) {
+                    sel[row][l16] = list[l16];
+                    sel[row][l16 + 16] = list[l16 + 16];
+                }
+                wave_fence();
+            }
+        }
+        if (__builtin_expect(placed, 1)) {
             wave_fence();
             double* k64 = keys64[kBias ? row : 0];
             int id[2], place[2];
-            if (__ballot(n > 16))
+            if (__builtin_expect(__ballot(n > 16) != 0, 0))
                 place_candidates<2, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place);
             else
                 place_candidates<1, kV, kF32, kSig, kBias>(g, t, i0, n, base, inv, sel[row], keys[row], k64, id, place);
@@ -443,12 +505,6 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
                 if (place[h] < k) sel[row][place[h]] = id[h];
             wave_fence();
         } else {
-            uint32_t key[kV];
-#pragma unroll
-            for (int i = 0; i < kV; ++i) key[i] = i0 + i < E ? order_key(z[i]) : 0u;
-            wave_fence();
-            const uint32_t last = take_top<kV>(key, k, i0, sel[row]);
-            wave_fence();
             if constexpr (kBias) {
                 // is every neighbour in the order, and everything around the last one, either
                 // further off than FP32 rounding reaches, or the same logit and bias (a true
@@ -459,8 +515,10 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
                 const float k_last = key_value(last);
                 const float reach = kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(k_last));
 #pragma unroll 1
-                for (int i = 0; i < kV && i0 + i < E; ++i) {
-                    const float zi = ld_logit(g.logits, t * E + i0 + i, kF32), bi = g.bias[i0 + i];
+                for (int i = 0; i < kV; ++i) {
+                    const int e = i0 + ahead(i);
+                    if (e >= E) continue;
+                    const float zi = ld_logit(g.logits, t * E + e, kF32), bi = g.bias[e];
                     const float ki = choice_key(one_score<kSig>(zi, base, inv) + bi);
                     near |= __builtin_fabsf(ki - k_last) <= reach && !(zi == z_last && bi == b_last);
                 }
@@ -510,7 +568,7 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
     for (int i = 0; i < kV; ++i) {
         acc[i] += __shfl_xor(acc[i], 16, 64);
         acc[i] += __shfl_xor(acc[i], 32, 64);
-        if (lane < 16) sums[wave][i0 + i] = acc[i];
+        if (lane < 16) sums[wave][i0 + ahead(i)] = acc[i];
     }
     __syncthreads();
     int c = 0;
@@ -605,7 +663,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
     __shared__ __attribute__((aligned(16))) float shared[16 * kStep];   // counts
     __shared__ int64_t part[kThreads / MOE_WAVE];
     const int tid = threadIdx.x, l16 = tid & 15, row = tid >> 4;
-    const int E = g.E, k = g.k, i0 = l16 * kV;
+    const int E = g.E, k = g.k, i0 = first<kV>(l16);
     // b_e of this lane's experts
     float bal[kV];
 #pragma unroll
@@ -626,6 +684,8 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
         }
     };
     load((int64_t)blockIdx.x * kRows);
+    // where expert e's entry lies: by lane, as the lanes hold the logits
+    auto slot = [](int e) { return kV == 16 ? (e >> 3 & 15) * kStep + (e >> 7) * 8 + (e & 7) : e / kV * kStep + e % kV; };
     const int x0 = l16 * kStep;                           // padded, so that the lanes' pieces meet few banks twice
     if (g.dloss) {
         // every count is read once by the workgroup and shared: reading kV of them per lane from
@@ -634,7 +694,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
         int64_t n = c;
         for (int o = 32; o; o >>= 1) n += __shfl_xor((long long)n, o, 64);
         if ((tid & 63) == 0) part[tid >> 6] = n;
-        if (tid < 16 * kV) shared[tid / kV * kStep + tid % kV] = (float)c;
+        if (tid < 16 * kV) shared[slot(tid)] = (float)c;
         __syncthreads();
         n = 0;
         for (int w = 0; w < kThreads / MOE_WAVE; ++w) n += part[w];
@@ -704,7 +764,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
                 r = kSig ? gj[h] : sj[h] * gj[h];
                 own += kSig ? 0.0f : r;
             }
-            if (id[h] >= 0) ex[id[h] / kV * kStep + id[h] % kV] = r;
+            if (id[h] >= 0) ex[slot(id[h])] = r;
         }
         wave_fence();
         if constexpr (!kSig) {

@@ -425,3 +425,29 @@ def test_run_to_run_streams_and_graphs(moe):
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
         eager = step(r, zs[(i + 1) % 3])
         assert all(torch.equal(a, b) for a, b in zip(eager, want[(i + 1) % 3]))
+
+
+@pytest.mark.parametrize("E", [20, 61, 96, 129, 136, 160, 200, 255, 256])
+def test_choice_over_experts_and_k(moe, E):
+    """Every way to the choice: all k around its borders, rows with and without many ties (BF16 and
+    whole-number logits), with and without a bias, FP32 keys a rounding apart among them."""
+    import torch
+    T = 70
+    for k in (1, 7, 8, 9, 12, 15, 16, 17, 20, 21, 24, 31, 32):
+        if k > E:
+            continue
+        g = torch.Generator().manual_seed(100 * E + k)
+        z = torch.randn(T, E, generator=g)
+        z[1::4] = z[1::4].bfloat16().float()
+        z[2::8] = torch.randint(-1, 2, (len(z[2::8]), E), generator=g).float()
+        z[3::8] = z[3::8].sort(1, descending=True)[0]      # the largest side by side
+        z[7::8] = z[7::8].sort(1)[0]
+        z[4::8] = 0.3 + 1e-7 * torch.randn(len(z[4::8]), E, generator=g)
+        b = torch.randn(E, generator=g) * 0.02
+        b[::5] = 0.0
+        for score in (0, 1):
+            for bias in (None, b):
+                ri = ref_forward(z, bias, None, k, score, True, 1.0, 0.0)[0]
+                r = moe.Router(T, E, k, score=score)
+                got = r.forward(z.to(dev()), bias=None if bias is None else bias.to(dev()), stats=False)[0].cpu().numpy()
+                assert np.array_equal(got, ri), (E, k, score, bias is None)
