@@ -210,6 +210,22 @@ __device__ __forceinline__ void finish_column(const NormGradArgs& g, int which, 
     if (g.w_post) g.dw_post[c] = channel ? g.gate[c] * sum : sum;
     if (channel) g.dgate[c] = g.w_post ? g.w_post[c] * sum : sum;
 }
+// the same of columns c .. c + 7
+__device__ __forceinline__ void finish_columns(const NormGradArgs& g, int which, int c, const Vec8& sum) {
+    if (which == 0) {
+        st8(g.dw_pre + c, sum);
+        return;
+    }
+    const bool channel = g.gate_kind == kGateChannel;
+    Vec8 w = ld8_or(g.w_post, c, true, 1.0f), gt = ld8_or(channel ? g.gate : nullptr, c, true, 1.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w.v[i] *= sum.v[i];
+        gt.v[i] *= sum.v[i];
+    }
+    if (g.w_post) st8(g.dw_post + c, gt);
+    if (channel) st8(g.dgate + c, w);
+}
 
 // Workgroups of 512 threads, two a CU, so that one loads while the other waits at a barrier.  What
 // stays of a row from its first reduction on stays packed (8 registers for h and y instead of 16),
@@ -355,12 +371,8 @@ __global__ __launch_bounds__(bwd_threads<kW>(), 4) void norm_grad_kernel(NormGra
             for (int c = 0; c < kC; ++c) {
                 const int col = 8 * (lt + c * 64 * kW);
                 if (col >= d) continue;
-                if (!last) {
-                    st8(dst + col, a[c]);
-                    continue;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) finish_column(g, which, col + i, a[c].v[i]);
+                if (last) finish_columns(g, which, col, a[c]);
+                else st8(dst + col, a[c]);
             }
         }
     };
