@@ -293,7 +293,7 @@ def moe_profile_read(plan) -> dict:
 # ---------------------------------------------------------------- torch plumbing
 
 def _ptr(t) -> int:
-    return 0 if t is None else int(t.data_ptr())
+    return 0 if t is None else t.data_ptr()
 
 
 _raw_stream = None
@@ -335,7 +335,7 @@ class Layer:
         if precision == MOE_MXFP4:
             self._mxfp4 = ((_dense(E, I * d), _dense(E, 2 * I // 16, (d + 511) // 512, 64, 4)),
                            (_dense(E, d * I // 2), _dense(E, d // 16, (I + 511) // 512, 64, 4)))
-            self._mxfp4_sizes = [math.prod(shape) for shape, _ in sum(self._mxfp4, ())]
+            self._mxfp4_sizes = tuple(math.prod(shape) for shape, _ in sum(self._mxfp4, ()))
         nbytes = moe_workspace_bytes(self.plan)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         moe_bind_workspace(self.plan, _ptr(self.workspace), self.workspace.numel())
@@ -385,7 +385,7 @@ class Layer:
         if out is None:
             out = torch.empty((self.T * self.k, self.d), dtype=torch.bfloat16, device=x_rows.device)
         if self._mxfp4 is not None:
-            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out)
+            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out, out)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward_routed(self.plan, _ptr(x_rows), _ptr(m_indptr), w, _ptr(out), _stream(stream))
         return out
@@ -435,24 +435,24 @@ class Layer:
                             _ptr(w2_s), _stream(stream))
         return w13_q, w13_s, w2_q, w2_s
 
-    def _check_mxfp4(self, w13_q, w13_s, w2_q, w2_s, *others):
-        """Prepared weights of this layer's shapes, they and the other tensors on the current
-        device, or ValueError (a missing scale is left to the call).  The kernels address them by
-        the plan's sizes."""
+    def _check_mxfp4(self, w13_q, w13_s, w2_q, w2_s, a, b, c, d):
+        """Prepared weights of this layer's sizes, they and the four other tensors on the current
+        device, or ValueError (a missing tensor is left to the call, which refuses it): the kernels
+        address them by the plan's sizes."""
         import torch
-        index, right = torch.cuda.current_device(), True
-        for t, n in zip((w13_q, w13_s, w2_q, w2_s), self._mxfp4_sizes):
-            if t is not None:
-                right = right and t.numel() == n and t.is_contiguous() and t.get_device() == index
-        for t in others:
-            right = right and (t is None or t.get_device() == index)
-        if right:
+        index = torch.cuda.current_device()
+        try:
+            if ((w13_q.numel(), w13_s.numel(), w2_q.numel(), w2_s.numel()) == self._mxfp4_sizes
+                    and w13_q.is_contiguous() and w13_s.is_contiguous() and w2_q.is_contiguous() and w2_s.is_contiguous()
+                    and index == w13_q.get_device() == w13_s.get_device() == w2_q.get_device() == w2_s.get_device()
+                    == a.get_device() == b.get_device() == c.get_device() == d.get_device()):
+                return
+        except AttributeError:
             return
         dev, layout = torch.device("cuda", index), sum(self._mxfp4, ())
         for name, t, (shape, _) in zip(("w13_q", "w13_s", "w2_q", "w2_s"), (w13_q, w13_s, w2_q, w2_s), layout):
-            if t is not None:
-                _check(name, t, shape, torch.uint8, dev)
-        raise ValueError("the current device is %s, x, ids, scores or the output is elsewhere" % dev)
+            _check(name, t, shape, torch.uint8, dev)
+        raise ValueError("the current device is %s; x, ids, scores or the output is elsewhere" % dev)
 
     def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
         """The BF16 weights (w13, w2) that an MXFP4 layer's prepared weights stand for."""
@@ -460,7 +460,7 @@ class Layer:
         dev = w13_q.device
         E, I, d = self.E, self.I, self.d
         if self.precision == MOE_MXFP4:
-            self._check_mxfp4(w13_q, w13_s, w2_q, w2_s)
+            self._check_mxfp4(w13_q, w13_s, w2_q, w2_s, w13_q, w13_s, w2_q, w2_s)
         w13 = torch.empty((E, 2 * I, d), dtype=torch.bfloat16, device=dev)
         w2 = torch.empty((E, d, I), dtype=torch.bfloat16, device=dev)
         w = weights(_ptr(w13_q), _ptr(w2_q), _ptr(w13_s), _ptr(w2_s))
