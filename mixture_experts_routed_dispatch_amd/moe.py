@@ -330,7 +330,8 @@ class Layer:
         self.plan = moe_plan(T, d, I, E, k, precision, int(bool(training)), path,
                              int(bool(wgrad_accumulate)), int(bool(recompute_h)), int(activation),
                              int(bool(mega)))
-        # MXFP4: shape and strides of W13's and W2's (codes, scales)
+        # shapes and strides of W13 and W2, and with MXFP4 of their (codes, scales)
+        self._weights = _dense(E, 2 * I, d), _dense(E, d, I)
         self._mxfp4 = None
         if precision == MOE_MXFP4:
             self._mxfp4 = ((_dense(E, I * d), _dense(E, 2 * I // 16, (d + 511) // 512, 64, 4)),
@@ -457,12 +458,9 @@ class Layer:
     def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
         """The BF16 weights (w13, w2) that an MXFP4 layer's prepared weights stand for."""
         import torch
-        dev = w13_q.device
-        E, I, d = self.E, self.I, self.d
-        if self.precision == MOE_MXFP4:
+        if self._mxfp4 is not None:
             self._check_mxfp4(w13_q, w13_s, w2_q, w2_s, w13_q, w13_s, w2_q, w2_s)
-        w13 = torch.empty((E, 2 * I, d), dtype=torch.bfloat16, device=dev)
-        w2 = torch.empty((E, d, I), dtype=torch.bfloat16, device=dev)
+        w13, w2 = (_new(n, torch.bfloat16, w13_q.device) for n in self._weights)
         w = weights(_ptr(w13_q), _ptr(w2_q), _ptr(w13_s), _ptr(w2_s))
         moe_expand_weights(self.plan, w, _ptr(w13), _ptr(w2), _stream(stream))
         return w13, w2
