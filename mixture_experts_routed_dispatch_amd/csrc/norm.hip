@@ -20,8 +20,6 @@
 // BF16, post norm, gate and pre norm: forward 23.6 us (5.7 TB/s), backward 37.7 us (5.3 TB/s)
 // and 4.8 us for the column sums' second stage.  Stores past the caches gain the forward 2 us
 // here, cost it 4 us of 36 at 4099 x 4096 with an FP32 stream, and slow whoever reads h next.
-#include <type_traits>
-
 #include "common.h"
 #include "kernels.h"
 
