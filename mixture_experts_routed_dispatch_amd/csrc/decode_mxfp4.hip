@@ -3,9 +3,9 @@
 //
 // The same launches as with BF16 weights (decode.hip): W13 with the activation, then for one
 // token W2 with the combine, else W2 and a combine.  a is rounded to BF16, the operand type of
-// the W2 products; with one token, which leaves operand rows unused, its rounded remainder is an
-// operand row too (with more tokens the second row would cost 3.5 of 42 us).  The experts'
-// outputs o stay in FP32 until the one rounding of y.  The time is that of streaming 4.25 bits
+// the W2 products, and its remainder, rounded too, is an operand row of its own: 16 bits of a, so
+// that a token's y is as exact beside others as alone.  The experts' outputs o stay in FP32 until
+// the one rounding of y.  The time is that of streaming 4.25 bits
 // for each weight of the active experts: 128 experts of d = 2048, I = 768, k = 8, one token 5.2 and
 // 4.8 us for 13.4 and 6.7 MB, where starting and the chain of loads are what is left; 32 tokens on
 // 59 experts 22.2, 13.4 and (combine) 3.9 us for 99 and 49 MB (4.5 and 3.7 TB/s).
@@ -91,9 +91,8 @@ __device__ __forceinline__ f32x4_t mma_tiles(const uint8_t* codes, const uint32_
 }
 
 // a[entry][i0 + n] = act(g) u in BF16, from one W13 tile's D: lane l holds rows 4 (l >> 4) + z
-// of column n = l & 15, gate columns 0..7 and up columns 8..15.  kRest: the remainder too, T*k
-// rows further.
-template <int kAct, bool kRest>
+// of column n = l & 15, gate columns 0..7 and up columns 8..15.  The remainder goes T*k rows further.
+template <int kAct>
 __device__ __forceinline__ void store_a(const DecodeArgs& g, const int* ent, int M, int i0, f32x4_t acc, bool lead) {
     const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
     float up[4];
@@ -108,7 +107,7 @@ __device__ __forceinline__ void store_a(const DecodeArgs& g, const int* ent, int
                 const uint32_t hi = f32_to_bf16(v);
                 uint16_t* at = g.a + (size_t)ent[mm] * g.I + i0 + n;
                 *at = (uint16_t)hi;
-                if constexpr (kRest) at[(size_t)g.T * g.k * g.I] = (uint16_t)f32_to_bf16(v - bf16_to_f32(hi));
+                at[(size_t)g.T * g.k * g.I] = (uint16_t)f32_to_bf16(v - bf16_to_f32(hi));
             }
         }
     }
@@ -133,7 +132,7 @@ __global__ __launch_bounds__(kThreads, kOneWGs) void decode4_w13_one(DecodeArgs 
     const uint32_t* words = reinterpret_cast<const uint32_t*>(g.w13_scale) + tile * groups * 64 + lane;
     const f32x4_t acc = reduce_waves<true>(
         mma_tiles(codes, words, groups, rows_rsrc(g.x, (uint32_t)g.d * 2u), [](int) { return 0u; }, stage[w], s0, s1), red, par);
-    store_a<kAct, true>(g, &slot, 1, blockIdx.x * 8, acc, threadIdx.x < MOE_WAVE);
+    store_a<kAct>(g, &slot, 1, blockIdx.x * 8, acc, threadIdx.x < MOE_WAVE);
 }
 
 // More tokens: a workgroup's item is (group of entries of one expert, kTiles row tiles), its four
@@ -151,25 +150,27 @@ __global__ __launch_bounds__(kThreads, kOneWGs) void decode4_w13_one(DecodeArgs 
 constexpr int kTiles = 4, kDepth = 2, kWGs = 4;
 static_assert(kTiles % kWaves == 0, "a wave adds up whole tiles");
 constexpr int kNonTemporal = 2;      // the nt bit of a buffer load
-struct Operands4 {
+template <int kSets> struct Operands4 {
     u32x4_t c[kTiles];               // codes
     uint32_t sb[kTiles];             // scales, a byte for each of four tiles along K
-    bf16x8_t a[4];                   // routed rows
+    bf16x8_t a[kSets][4];            // routed rows
 };
 struct Partials4 {
     f32x4_t p[2][kWaves][kTiles][MOE_WAVE];
 };
 // One 16-row group (rows at byte offset ao of ars, kNoRow: none) times the item's tiles: this
-// wave's share of K.  codes and words: of the item's first row tile.
+// wave's share of K.  codes and words: of the item's first row tile.  kSets = 2: plus the rows
+// set_bytes further, the remainders.
+template <int kSets>
 __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], const void* codes_base, const void* words_base,
-                                              __amdgpu_buffer_rsrc_t ars, uint32_t ao, int S, int s0, int s1) {
+                                              __amdgpu_buffer_rsrc_t ars, uint32_t ao, int set_bytes, int S, int s0, int s1) {
     const int lane = threadIdx.x & 63, groups = (S + 3) / 4;
     // uniform bases and offsets in scalar registers, one 32-bit lane offset each
     const __amdgpu_buffer_rsrc_t codes = rows_rsrc(codes_base, (uint32_t)(kTiles * S) * 1024u);
     const __amdgpu_buffer_rsrc_t words = rows_rsrc(words_base, (uint32_t)(kTiles * groups) * 256u);
     ao += 64u * (lane >> 4);
     uint32_t co = lane * 16, so = lane * 4;
-    auto load = [&](Operands4& w, int s) {
+    auto load = [&](Operands4<kSets>& w, int s) {
         if (s >= s1) co = so = ao = kNoRow;              // past the last step: no memory is read
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
@@ -178,18 +179,23 @@ __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], const void
         for (int t = 0; t < kTiles; ++t)
             w.sb[t] = __builtin_amdgcn_raw_buffer_load_b32(words, so, (t * groups + (s >> 2)) * 256, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w.a[i] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(ars, ao + 16u * i, 256 * s, 0));
+        for (int h = 0; h < kSets; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w.a[h][i] = __builtin_bit_cast(
+                    bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(ars, ao + 16u * i, 256 * s + h * set_bytes, 0));
     };
-    auto products = [&](const Operands4& w, int s) {
+    auto products = [&](const Operands4<kSets>& w, int s) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             const float x = __uint_as_float(((w.sb[t] >> (8 * (s & 3))) & 0xFFu) << 23);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t] = mma_quarter(w.a[i], w.c[t][i], x, acc[t]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < kSets; ++h) acc[t] = mma_quarter(w.a[h][i], w.c[t][i], x, acc[t]);
         }
     };
-    Operands4 w[kDepth];
+    Operands4<kSets> w[kDepth];
 #pragma unroll
     for (int u = 0; u < kDepth - 1; ++u) load(w[u], s0 + u);
     for (int s = s0; s < s1; s += kDepth) {
@@ -203,7 +209,7 @@ __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], const void
 }
 
 // The routed entries sorted by expert, in groups of at most 16 entries of one expert.
-constexpr int kRows = 16;
+constexpr int kRows = 16, kHalf = 8;
 struct Sorted4 {
     int cnt[256];                    // entries per expert, a byte for each of the four waves
     int ids[kMaxDecodeRows];         // for the routing flags
@@ -271,10 +277,13 @@ __device__ __forceinline__ void sort_entries(Sorted4& sm, const DecodeArgs& g, b
 // The items (group of entries, kTiles row tiles) of this workgroup, its number in the launch and
 // every (number of workgroups)-th; store(entries, how many, row tile, sums) by the wave that has
 // added up the tile's four partial sums, in wave order.  row(entry): byte offset of its operand
-// row.
-template <typename Row, typename Store>
+// row.  kRest: every row has a remainder rest_bytes further.  Those of up to 8 entries are operand rows
+// 8 .. 15 of the same loads and MFMAs, and store adds the two halves of the sums; groups of more
+// entries have a second set of operands.  (W2 in groups of 8 entries throughout: 256 entries of 8
+// experts, d = 4096, I = 1024, 50.8 us a call against 48.4; without remainders 43.5.)
+template <bool kRest, typename Row, typename Store>
 __device__ __forceinline__ void run_items(const Sorted4& sm, Partials4& part, const void* codes, const void* words,
-                                          __amdgpu_buffer_rsrc_t ars, int nblk, int S, Row&& row, Store&& store) {
+                                          __amdgpu_buffer_rsrc_t ars, int rest_bytes, int nblk, int S, Row&& row, Store&& store) {
     const int lane = threadIdx.x & 63, n = lane & 15, word_bytes = (S + 3) / 4 * 256;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
@@ -286,10 +295,14 @@ __device__ __forceinline__ void run_items(const Sorted4& sm, Partials4& part, co
         const int first = __builtin_amdgcn_readfirstlane(sm.pfx[e]) + m0;
         const int left = __builtin_amdgcn_readfirstlane(sm.pfx[e + 1]) - first, M = left < kRows ? left : kRows;
         const size_t tile = (size_t)e * nblk + blk;
-        const uint32_t ao = n < M ? row(sm.ent[first + n]) : kNoRow;
+        const bool both = kRest && M <= kHalf;
+        const int m = both ? n % kHalf : n;
+        const uint32_t ao = m < M ? row(sm.ent[first + m]) + (m < n ? (uint32_t)rest_bytes : 0u) : kNoRow;
         f32x4_t acc[kTiles] = {};
-        tile_products(acc, static_cast<const uint8_t*>(codes) + tile * S * 1024,
-                      static_cast<const uint8_t*>(words) + tile * word_bytes, ars, ao, S, s0, s1);
+        const uint8_t* c0 = static_cast<const uint8_t*>(codes) + tile * S * 1024;
+        const uint8_t* w0 = static_cast<const uint8_t*>(words) + tile * word_bytes;
+        if (!kRest || both) tile_products<1>(acc, c0, w0, ars, ao, 0, S, s0, s1);
+        else tile_products<2>(acc, c0, w0, ars, ao, rest_bytes, S, s0, s1);
         // one barrier: the other half is written next, and read only after the next barrier
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) part.p[half][wave][t][lane] = acc[t];
@@ -310,9 +323,9 @@ __global__ __launch_bounds__(kThreads, kWGs) void decode4_w13(DecodeArgs g) {
     __shared__ Sorted4 sm;
     __shared__ Partials4 part;
     sort_entries(sm, g, blockIdx.x == 0);
-    run_items(sm, part, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), g.I / 8, g.d / 128,
-              [&](int entry) { return (uint32_t)(entry / g.k * g.d) * 2u; },
-              [&](const int* ent, int M, int tile, f32x4_t sum) { store_a<kAct, false>(g, ent, M, tile * 8, sum, true); });
+    run_items<false>(sm, part, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), 0, g.I / 8, g.d / 128,
+                     [&](int entry) { return (uint32_t)(entry / g.k * g.d) * 2u; },
+                     [&](const int* ent, int M, int tile, f32x4_t sum) { store_a<kAct>(g, ent, M, tile * 8, sum, true); });
 }
 
 __global__ __launch_bounds__(kThreads, kWGs) void decode4_w2(DecodeArgs g) {
@@ -320,13 +333,15 @@ __global__ __launch_bounds__(kThreads, kWGs) void decode4_w2(DecodeArgs g) {
     __shared__ Partials4 part;
     sort_entries(sm, g, false);
     float* o = reinterpret_cast<float*>(g.o);
-    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4, d = g.d;
-    run_items(sm, part, g.w2, g.w2_scale, rows_rsrc(g.a, (uint32_t)(g.T * g.k) * g.I * 2u), d / 16, g.I / 128,
-              [&](int entry) { return (uint32_t)(entry * g.I) * 2u; },
-              [&](const int* ent, int M, int tile, f32x4_t sum) {
+    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4, d = g.d, set = g.T * g.k * g.I * 2;
+    run_items<true>(sm, part, g.w2, g.w2_scale, rows_rsrc(g.a, 2u * set), set, d / 16, g.I / 128,
+                    [&](int entry) { return (uint32_t)(entry * g.I) * 2u; },
+                    [&](const int* ent, int M, int tile, f32x4_t sum) {
 #pragma unroll
-        for (int z = 0; z < 4; ++z)
-            if (4 * kq + z < M) o[(size_t)ent[4 * kq + z] * d + tile * 16 + n] = sum[z];
+        for (int z = 0; z < 4; ++z) {
+            const float rest = __shfl_xor(sum[z], 32, MOE_WAVE);       // rows 8 .. 15 at rows 0 .. 7
+            if (4 * kq + z < M) o[(size_t)ent[4 * kq + z] * d + tile * 16 + n] = M <= kHalf ? sum[z] + rest : sum[z];
+        }
     });
 }
 

@@ -215,8 +215,8 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     const bool mx = c.precision == MOE_MXFP8_E4M3;
     const bool mxt = mx && c.training;
     // a in BF16: the BF16 path's W2 operand; MXFP8 training keeps it for the weight gradient
-    // (one token's MXFP4 decode keeps the remainder of its rounding as well)
-    p->a_bytes = (w4 && p->decode && c.T == 1 ? 4 : 2) * (size_t)R * c.I;
+    // (the MXFP4 decode keeps the remainder of its rounding as well)
+    p->a_bytes = (w4 && p->decode ? 4 : 2) * (size_t)R * c.I;
     p->off_a = (!mx || c.training) ? take(p->a_bytes) : 0;
     // the experts' outputs: BF16, or FP32 in the MXFP4 decode, which rounds y alone
     p->o_bytes = (w4 && p->decode ? 4 : 2) * (size_t)R * c.d;
