@@ -391,7 +391,8 @@ __global__ __launch_bounds__(kThreads, 1) void decode4_w2_one(DecodeArgs g) {
     }
 }
 
-// y[t] = sum_j s[t][j] o[t*k + j] in FP32, j ascending from +0.0; four features a thread
+// y[t] = sum_j s[t][j] o[t*k + j] in FP32, j ascending from +0.0; four features a thread.  Entries
+// of invalid ids add nothing (no product has written their o)
 __global__ __launch_bounds__(MOE_WAVE) void decode4_combine(DecodeArgs g) {
     const int t = blockIdx.y, n = (blockIdx.x * MOE_WAVE + threadIdx.x) * 4;
     if (n >= g.d) return;
@@ -401,8 +402,9 @@ __global__ __launch_bounds__(MOE_WAVE) void decode4_combine(DecodeArgs g) {
     for (int j = 0; j < g.k; ++j) {
         const f32x4_t v = *reinterpret_cast<const f32x4_t*>(o + (size_t)j * g.d);
         const float s = g.scores[t * g.k + j];
+        const bool valid = (unsigned)g.ids[t * g.k + j] < (unsigned)g.E;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(s, v[i], y[i]);
+        for (int i = 0; i < 4; ++i) y[i] = valid ? __builtin_fmaf(s, v[i], y[i]) : y[i];
     }
     *reinterpret_cast<uint2*>(g.y + (size_t)t * g.d + n) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
 }

@@ -240,3 +240,23 @@ def test_weights_of_other_shapes_are_refused(moe):
             m_indptr = torch.zeros(5, dtype=torch.int32, device=dev())
             with pytest.raises(ValueError):
                 layer.forward_routed(rows, m_indptr, w13, s13, w2, s2)
+
+
+@pytest.mark.parametrize("T", [1, 2, 6, 32])
+def test_entries_of_invalid_ids_add_nothing(moe, T):
+    """y of a batch with ids out of range is that of the same batch with their scores 0, whatever an
+    earlier call left in the workspace (here NaN in every word)."""
+    import torch
+    inp = inputs.generate(T, 256, 128, 16, 4, "uniform", seed=3)
+    t, layer, packed, e13, e2, y = run4(moe, inp)
+    a, s13, c, s2 = packed
+    bad, scores = t["ids"].clone(), t["scores"].clone()
+    bad[0, 1], bad[-1, 3], bad[T // 2, 0] = 16, -1, 1 << 30
+    scores[0, 1] = scores[-1, 3] = scores[T // 2, 0] = 0
+    want = layer.forward(t["x"], t["ids"], scores, a, c, s13, s2)
+    layer.workspace.fill_(255)
+    torch.cuda.synchronize()
+    moe.moe_bind_workspace(layer.plan, layer.workspace.data_ptr(), layer.workspace.numel())
+    got = layer.forward(t["x"], bad, t["scores"], a, c, s13, s2)
+    assert torch.equal(got, want)
+    assert layer.status() == (moe.MOE_ERR_ROUTING, moe.MOE_DEV_ID_OUT_OF_RANGE)
