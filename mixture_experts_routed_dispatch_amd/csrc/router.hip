@@ -354,7 +354,8 @@ __device__ __forceinline__ int find_candidates(const float key[kV], float bound,
 
 // Where each candidate of a row (n of them, kH to a lane) comes in the order: id and place of this
 // lane's ones; place >= k: not chosen.  With a bias FP32 keys order the candidates only
-// where every other key is further off than kNear; otherwise (a tie too) 64 bits do.
+// where every other key is further off than kNear; otherwise (a tie too, and among infinite keys,
+// whose differences say nothing) 64 bits do.
 template <int kH, int kV, bool kF32, bool kSig, bool kBias>
 __device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t, int i0, int n, float base, float inv,
                                                  const int* list, float* keys, double* keys64, int (&id)[2],
@@ -385,7 +386,6 @@ __device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t,
                 if constexpr (kBias) {
                     place[h] += v[u] > own[h];
                     close[h] += __builtin_fabsf(v[u] - own[h]) <= kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(own[h]));
-                    if (own[h] == -INFINITY) close[h] += v[u] == own[h];
                 } else {
                     place[h] += v[u] > own[h] || (v[u] == own[h] && c + u < l16 + 16 * h);
                 }
@@ -394,7 +394,7 @@ __device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t,
     if constexpr (kBias) {
         bool near = false;
 #pragma unroll
-        for (int h = 0; h < kH; ++h) near |= close[h] > 1 && place[h] < g.k;
+        for (int h = 0; h < kH; ++h) near |= (close[h] > 1 || __builtin_fabsf(own[h]) == INFINITY) && place[h] < g.k;
         if (__builtin_expect(!__ballot(near), 1)) return;
         float zmax;
         const double sum = exact_sum<kV, kSig>(g.logits, row, i0, g.E, zmax, kF32);
