@@ -327,9 +327,11 @@ moe_status_t moe_backward(moe_plan_t plan, const void* dy, const void* x, const 
  *   loss       balance_coef E / (k N^2) sum_e counts_e prob_sums_e   (0 when N = 0)
  * mask (uint8 [T], or NULL): rows with 0 are padding.  They get ids 0 .. k-1 (valid for
  * moe_forward) and scores 0, count nowhere, and get zero gradients.
- * Logits of -inf are never chosen before others and score 0; a row of -inf alone scores 0.
- * A NaN logit counts as -inf in the choice, and makes the row's softmax (with sigmoid: its own score and the
- * row's p) NaN; so does +inf with softmax.
+ * A logit of -inf has the key -inf, with a bias too: it is never chosen before others, and scores 0; a
+ * row of -inf alone scores 0.  (A low finite logit is like any other: with a bias its key is s + bias.)
+ * A NaN key counts as -inf in the choice.  A NaN logit has one, and makes the row's softmax (with sigmoid:
+ * its own score and the row's p) NaN; so does +inf with softmax.  With softmax and a bias all keys of such
+ * a row are NaN: its ids are 0 .. k-1.  Biases may be infinite.
  * Stateless: a config, caller-owned buffers and a workspace that holds nothing between calls;
  * calls that overlap need a workspace each. */
 #define MOE_SCORE_SOFTMAX 0

@@ -3,7 +3,7 @@
 //
 // With z = logits[t], s = softmax(z) or sigmoid(z), p_e = s_e / sum_e' s_e' (softmax: p = s):
 //   ids      the k experts of the largest key, descending, ties to the lowest index; the key
-//            is z_e itself, or s_e + bias_e when a selection bias is given
+//            is z_e itself, or s_e + bias_e when a selection bias is given (-inf where z_e is)
 //   scores   scale s_j, divided by the sum of the chosen s with `normalize`
 //   counts_e tokens that chose e;  P_e = sum_t p_te  (rows that the mask leaves out count
 //            nowhere; N = sum counts / k rows remain)
@@ -69,6 +69,8 @@ __device__ __forceinline__ float row_sum(float v) {
 // what a key counts as in the choice: NaN as -inf
 __device__ __forceinline__ float choice_key(float f) { return f != f ? -INFINITY : f; }
 __device__ __forceinline__ double choice_key(double f) { return f != f ? -(double)INFINITY : f; }
+// the score as it enters a biased key: a logit of -inf stays behind the others whatever its bias
+template <typename T> __device__ __forceinline__ T key_score(T s, float z) { return z == -INFINITY ? -(T)INFINITY : s; }
 // unsigned number that orders like the (choice) key; 0 stays free for logits that are taken
 // or past E
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -215,7 +217,7 @@ template <bool kSig> __device__ __forceinline__ double exact_key(float z, float 
     double s;
     if constexpr (kSig) s = 1.0 / (1.0 + exp(-(double)z));
     else s = exp((double)z - (double)zmax) / sum;
-    return choice_key(s + (double)b);
+    return choice_key(key_score(s, z) + (double)b);
 }
 template <int kV, bool kSig>
 __device__ __forceinline__ double exact_sum(const void* logits, int64_t row, int i0, int E, float& zmax, bool f32) {
@@ -370,7 +372,7 @@ __device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t,
         const int c = l16 + 16 * h;
         id[h] = c < n ? list[c] : 0;
         const float z = ld_logit(g.logits, row + id[h], kF32);
-        own[h] = choice_key(kBias ? one_score<kSig>(z, base, inv) + g.bias[id[h]] : z);
+        own[h] = choice_key(kBias ? key_score(one_score<kSig>(z, base, inv), z) + g.bias[id[h]] : z);
         keys[c] = c < n ? own[h] : NAN;                 // compares with nothing
         place[h] = c < n ? 0 : g.k;
     }
@@ -463,10 +465,13 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) acc[i] += kSig ? s[i] * inv : s[i];
         }
-        if constexpr (kBias) load_row<kV, true>(g.bias, 0, i0, E, g.bias_vec, z);
-        if constexpr (kBias)
+        if constexpr (kBias) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) s[i] = key_score(s[i], z[i]);
+            load_row<kV, true>(g.bias, 0, i0, E, g.bias_vec, z);
 #pragma unroll
             for (int i = 0; i < kV; ++i) z[i] += s[i];  // keys from here on
+        }
         int n = kCand + 1;
         if (k <= kTwoK) n = find_candidates<kV>(z, bound_of<kV>(z, k), i0, E, kBias ? kNear : 0.0f, sel[row]);
         // the ways marked unlikely lie behind the usual one, which a wave walks through once: in their
@@ -521,15 +526,15 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
                     const int e = i0 + ahead(i);
                     if (e >= E) continue;
                     const float zi = ld_logit(g.logits, t * E + e, kF32), bi = g.bias[e];
-                    const float ki = choice_key(one_score<kSig>(zi, base, inv) + bi);
+                    const float ki = choice_key(key_score(one_score<kSig>(zi, base, inv), zi) + bi);
                     near |= __builtin_fabsf(ki - k_last) <= reach && !(zi == z_last && bi == b_last);
                 }
                 for (int j = l16; j + 1 < k; j += 16) {
                     const int ea = sel[row][j], eb = sel[row][j + 1];
                     const float za = ld_logit(g.logits, t * E + ea, kF32), zb = ld_logit(g.logits, t * E + eb, kF32);
                     const float ba = g.bias[ea], bb = g.bias[eb];
-                    const float ka = choice_key(one_score<kSig>(za, base, inv) + ba);
-                    const float kb = choice_key(one_score<kSig>(zb, base, inv) + bb);
+                    const float ka = choice_key(key_score(one_score<kSig>(za, base, inv), za) + ba);
+                    const float kb = choice_key(key_score(one_score<kSig>(zb, base, inv), zb) + bb);
                     near |= !(ka - kb > kNear * __builtin_fmaxf(1.0f, __builtin_fabsf(ka))) && !(za == zb && ba == bb);
                 }
                 if (__ballot(near)) {

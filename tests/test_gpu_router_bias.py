@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests.gpu_util import dev, say
-from tests.test_gpu_router import REL, ref_forward
+from tests.test_gpu_router import REL, ref_forward, scores64
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -56,3 +56,65 @@ def test_infinite_biases(moe, E):
                     continue
                 for score in (0, 1):
                     compare(moe, z, b, k, score)
+
+
+def ref_keys(z, b, score):
+    """Keys with a bias: s + b, -inf for logits of -inf, and NaN as -inf."""
+    z, b = z.double().numpy(), b.double().numpy()
+    with np.errstate(all="ignore"):
+        key = scores64(z, score)[0] + b
+    return np.where((z == -np.inf) | np.isnan(key), -np.inf, key)
+
+
+@pytest.mark.parametrize("E,k", [(8, 3), (24, 4), (40, 4), (61, 20), (128, 8), (256, 8), (256, 32)])
+def test_logits_of_minus_infinity_stay_behind_whatever_their_bias(moe, E, k):
+    """Disabled experts have the largest biases, +inf among them; every number of live experts from
+    none to all, in one piece or spread."""
+    import torch
+    g = torch.Generator().manual_seed(E + k)
+    live = sorted({0, 1, 2, k - 1, k, k + 1, E // 4, E // 2, E - 1, E})
+    z = torch.randn(2 * len(live), E, generator=g)
+    for t, n in enumerate(live):
+        z[2 * t, torch.randperm(E, generator=g)[n:]] = -INF
+        z[2 * t + 1, n:] = -INF
+    for biases in (torch.linspace(-1, 1, E), torch.linspace(1, -1, E), torch.randn(E, generator=g)):
+        for pin in (False, True):
+            b = biases.clone()
+            if pin:
+                b[E // 2] = INF
+            for score in (0, 1):
+                r = moe.Router(len(z), E, k, score=score)
+                ids, w, counts, _, _ = r.forward(z.to(dev()), bias=b.to(dev()))
+                ids, w = ids.cpu().numpy(), w.cpu().numpy()
+                want = np.argsort(-ref_keys(z, b, score), axis=1, kind="stable")[:, :k]
+                assert np.array_equal(ids, want), (E, k, score, pin)
+                assert np.array_equal(counts.cpu().numpy(), np.bincount(want.ravel(), minlength=E))
+                off = np.take_along_axis(z.numpy(), ids.astype(np.int64), 1) == -np.inf
+                assert (w[off] == 0).all() and np.isfinite(w).all()
+                assert (np.abs(w.sum(1)[1:] - 1)[~off[1:].all(1)] <= 1e-5).all()
+
+
+@pytest.mark.parametrize("E", [24, 100, 256])
+def test_nan_and_infinite_logits_with_a_bias(moe, E):
+    """A NaN logit comes with those of -inf, by index; with softmax its row has no other keys, nor has a
+    row with +inf: ids 0 .. k-1.  With sigmoid +inf has a score of 1."""
+    import torch
+    T, k = 12, 5
+    g = torch.Generator().manual_seed(E)
+    z = torch.randn(T, E, generator=g)
+    b = torch.randn(E, generator=g)
+    top = int(b.argmax())
+    z[0, top] = float("nan")
+    z[1, top], z[1, (top + 1) % E] = -INF, float("nan")
+    z[2, k - 1:] = float("nan")
+    z[3, k - 1:] = -INF
+    z[4, 3:] = float("nan")
+    z[4, 9::2] = -INF
+    z[5, 7] = INF
+    z[6, 7], z[6, top] = INF, float("nan")
+    for score in (0, 1):
+        r = moe.Router(T, E, k, score=score)
+        ids = r.forward(z.to(dev()), bias=b.to(dev()), stats=False)[0].cpu().numpy()
+        assert np.array_equal(ids, np.argsort(-ref_keys(z, b, score), axis=1, kind="stable")[:, :k]), score
+        if score == 0:
+            assert (ids[[0, 1, 2, 4, 5, 6]] == np.arange(k)).all()
