@@ -118,3 +118,30 @@ def test_nan_and_infinite_logits_with_a_bias(moe, E):
         assert np.array_equal(ids, np.argsort(-ref_keys(z, b, score), axis=1, kind="stable")[:, :k]), score
         if score == 0:
             assert (ids[[0, 1, 2, 4, 5, 6]] == np.arange(k)).all()
+
+
+@pytest.mark.parametrize("k", [2, 8, 24])
+def test_scores_far_below_the_rows_maximum(moe, k):
+    """Experts that the bias chose 40 to 80 below the maximum (sigmoid: below 0).  The logits are multiples
+    of 2^-8 and the maximum is 0, so that differences are exact and what is left is e^x: with u = 2^-24,
+    e^x by the hardware's exp2 (1 ulp, 2 u) with its argument's rounding made up for (2 u more), one
+    factor (u; with sigmoid an addition and a reciprocal, 3 u), the sum of k of them (5 u and the terms'
+    own 7 u) and the quotient (u): within 20 u.  With e^x from an argument rounded to 24 bits they are
+    80 u off."""
+    import torch
+    T, E = 400, 64
+    g = torch.Generator().manual_seed(k)
+    z = torch.zeros(T, E)
+    low = torch.randperm(E - 1, generator=g)[:k] + 1
+    z[:, low] = -(40 * 256 + torch.randint(0, 40 * 256, (T, k), generator=g)) / 256.0
+    b = torch.zeros(E)
+    b[low] = 10.0
+    for score in (0, 1):
+        ids, w, _, _, _ = moe.Router(T, E, k, score=score).forward(z.to(dev()), bias=b.to(dev()), stats=False)
+        ids = ids.cpu().numpy().astype(np.int64)
+        assert (np.sort(ids, 1) == np.sort(low.numpy())).all()
+        s = np.take_along_axis(scores64(z.double().numpy(), score)[0], ids, 1)
+        want = s / s.sum(1, keepdims=True)
+        off = (np.abs(w.cpu().numpy() - want) / want).max() * 2.0 ** 24
+        print("  %s, k = %d: %.1f u" % (("softmax", "sigmoid")[score], k, off), flush=True)
+        assert off <= 20
