@@ -283,10 +283,14 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// keys that FP32 rounding may have brought into a wrong order lie this close (relative to
-// the larger of 1 and the key): a score is off by at most 3e-7 and the sum's rounding adds
-// 6e-8 of the key, so two keys by less than 7.2e-7
-constexpr float kNear = 2e-6f;
+// Keys that FP32 rounding may have brought into a wrong order lie this close (relative to the larger
+// of 1 and the key).  With u = 2^-24, softmax: e^x is off by (3 |x| + 2) u, the row's sum by its 15 + 4
+// additions and the terms' errors weighted with p (sum p |x| < 3.4 for 256 terms), 31 u, the
+// reciprocal and the product by 2 u.  Two scores add up to at most 1, so all that is common to a row or
+// relative to a score comes to 35 u in their difference, p |x| <= 0.4 to 3 u, and the rounding of two
+// keys to 2 u of the key: 40 u = 2.4e-6.  (A row that rounds the same way in one lane reaches
+// 8.8e-7; with sigmoid it is 10 u.)  The bound and two thirds of it:
+constexpr float kNear = 4e-6f;
 
 constexpr int kOneK = 8, kTwoK = 20;     // largest k with bounds from the lanes' first one and two
 constexpr int kCand = 32;                // candidates a row, at most

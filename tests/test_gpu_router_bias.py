@@ -145,3 +145,23 @@ def test_scores_far_below_the_rows_maximum(moe, k):
         off = (np.abs(w.cpu().numpy() - want) / want).max() * 2.0 ** 24
         print("  %s, k = %d: %.1f u" % (("softmax", "sigmoid")[score], k, off), flush=True)
         assert off <= 20
+
+
+@pytest.mark.parametrize("k", [2, 8, 20])
+def test_one_dominant_score_next_to_biased_small_ones(moe, k):
+    """Rows whose sum loses the most to rounding (the lane of the score near 1 adds terms just under
+    half a step), and biases that lift small scores to within 1e-6 of the large one, above and below."""
+    import torch
+    E, T = 256, 96
+    g = torch.Generator().manual_seed(60 + k)
+    z = torch.full((T, E), -80.0)
+    z[:, 0] = 0.0
+    share = 0.5 + 0.5 * torch.rand(T, 1, generator=g)
+    z[:, [*range(1, 8), *range(128, 136)]] = torch.log(2.0 ** -24 * share)
+    low = torch.arange(20, 20 + 2 * k)
+    z[:, low] = -17 - torch.rand(T, len(low), generator=g)
+    b = torch.zeros(E)
+    b[low] = 1.0 + 1e-6 * (2 * torch.rand(len(low), generator=g) - 1)
+    z[T // 2:] = torch.randn(T - T // 2, E, generator=g) * 3
+    z[T // 2:, 0] = 16.0
+    compare(moe, z, b, k, 0)
