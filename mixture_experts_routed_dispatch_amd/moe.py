@@ -318,7 +318,8 @@ def _stream(stream) -> int:
 
 
 class Layer:
-    """One plan plus its torch-allocated workspace; all compute goes through libmoe."""
+    """One plan plus its torch-allocated workspace; all compute goes through libmoe.  Tensors that a
+    call makes come from the memory of the stream that writes them (`stream`, else the current one)."""
 
     def __init__(self, T, d, I, E, k, precision=MOE_BF16, training=False, path=MOE_PATH_AUTO,
                  device="cuda", wgrad_accumulate=False, recompute_h=False, activation=MOE_ACT_SWIGLU,
@@ -357,12 +358,12 @@ class Layer:
 
     def dispatch(self, ids, scores, stream=None):
         import torch
-        dev = ids.device
+        dev, i32 = ids.device, torch.int32
         R = self.T * self.k
-        m_indptr = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
-        gather = torch.empty(max(R, 1), dtype=torch.int32, device=dev)
-        slots = torch.empty((self.T, self.k), dtype=torch.int32, device=dev)
-        probs = torch.empty(max(R, 1), dtype=torch.float32, device=dev)
+        m_indptr = _new(_dense(self.E + 1), i32, dev, stream)
+        gather = _new(_dense(max(R, 1)), i32, dev, stream)
+        slots = _new(_dense(self.T, self.k), i32, dev, stream)
+        probs = _new(_dense(max(R, 1)), torch.float32, dev, stream)
         moe_dispatch(self.plan, _ptr(ids), _ptr(scores), _ptr(m_indptr), _ptr(gather),
                      _ptr(slots), _ptr(probs), _stream(stream))
         return m_indptr, gather[:R], slots, probs[:R]
@@ -370,7 +371,7 @@ class Layer:
     def forward(self, x, ids, scores, w13, w2, w13_scale=None, w2_scale=None, y=None, stream=None):
         import torch
         if y is None:
-            y = _new(self._rows, torch.bfloat16, x.device)
+            y = _new(self._rows, torch.bfloat16, x.device, stream)
         if self._mxfp4 is not None:
             self._check_mxfp4(w13, w13_scale, w2, w2_scale, x, ids, scores, y)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
@@ -384,7 +385,7 @@ class Layer:
         plans take the prepared weights and their scales."""
         import torch
         if out is None:
-            out = torch.empty((self.T * self.k, self.d), dtype=torch.bfloat16, device=x_rows.device)
+            out = _new(_dense(self.T * self.k, self.d), torch.bfloat16, x_rows.device, stream)
         if self._mxfp4 is not None:
             self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out, out)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
@@ -399,13 +400,13 @@ class Layer:
         import torch
         dev = dy.device
         if dx is None:
-            dx = torch.empty((self.T, self.d), dtype=torch.bfloat16, device=dev)
+            dx = _new(self._rows, torch.bfloat16, dev, stream)
         if dw13 is None:
-            dw13 = torch.empty((self.E, 2 * self.I, self.d), dtype=torch.bfloat16, device=dev)
+            dw13 = _new(self._weights[0], torch.bfloat16, dev, stream)
         if dw2 is None:
-            dw2 = torch.empty((self.E, self.d, self.I), dtype=torch.bfloat16, device=dev)
+            dw2 = _new(self._weights[1], torch.bfloat16, dev, stream)
         if dscores is None:
-            dscores = torch.empty((self.T, self.k), dtype=torch.float32, device=dev)
+            dscores = _new(_dense(self.T, self.k), torch.float32, dev, stream)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), 0, _ptr(w13t), _ptr(w13t_scale), _ptr(w2t),
                     _ptr(w2t_scale))
         moe_backward(self.plan, _ptr(dy), _ptr(x), w, _ptr(dx), _ptr(dw13), _ptr(dw2), _ptr(dscores),
@@ -419,19 +420,19 @@ class Layer:
         dev = w13.device
         E, I, d = self.E, self.I, self.d
         if self.precision == MOE_MXFP4:
-            (n13, n2), stream = self._mxfp4, _stream(stream)
+            n13, n2 = self._mxfp4
             dev = torch.device("cuda", torch.cuda.current_device())
             _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
             _check("w2", w2, (E, d, I), torch.bfloat16, dev)
-            w13_q, w13_s, w2_q, w2_s = (_new(n, torch.uint8, dev) for n in n13 + n2)
+            w13_q, w13_s, w2_q, w2_s = (_new(n, torch.uint8, dev, stream) for n in n13 + n2)
             moe_prepare_weights(self.plan, w13.data_ptr(), w2.data_ptr(), w13_q.data_ptr(), w13_s.data_ptr(),
-                                w2_q.data_ptr(), w2_s.data_ptr(), stream)
+                                w2_q.data_ptr(), w2_s.data_ptr(), _stream(stream))
             return w13_q, w13_s, w2_q, w2_s
-        w13_q = torch.empty((E, 2 * I, d), dtype=torch.uint8, device=dev)
+        w13_q = _new(self._weights[0], torch.uint8, dev, stream)
         # scales block-major: [K/128, rows, 4] (see moe_prepare_weights in include/moe.h)
-        w13_s = torch.empty((d // 128, E * 2 * I, 4), dtype=torch.uint8, device=dev)
-        w2_q = torch.empty((E, d, I), dtype=torch.uint8, device=dev)
-        w2_s = torch.empty((I // 128, E * d, 4), dtype=torch.uint8, device=dev)
+        w13_s = _new(_dense(d // 128, E * 2 * I, 4), torch.uint8, dev, stream)
+        w2_q = _new(self._weights[1], torch.uint8, dev, stream)
+        w2_s = _new(_dense(I // 128, E * d, 4), torch.uint8, dev, stream)
         moe_prepare_weights(self.plan, _ptr(w13), _ptr(w2), _ptr(w13_q), _ptr(w13_s), _ptr(w2_q),
                             _ptr(w2_s), _stream(stream))
         return w13_q, w13_s, w2_q, w2_s
@@ -460,7 +461,7 @@ class Layer:
         import torch
         if self._mxfp4 is not None:
             self._check_mxfp4(w13_q, w13_s, w2_q, w2_s, w13_q, w13_s, w2_q, w2_s)
-        w13, w2 = (_new(n, torch.bfloat16, w13_q.device) for n in self._weights)
+        w13, w2 = (_new(n, torch.bfloat16, w13_q.device, stream) for n in self._weights)
         w = weights(_ptr(w13_q), _ptr(w2_q), _ptr(w13_s), _ptr(w2_s))
         moe_expand_weights(self.plan, w, _ptr(w13), _ptr(w2), _stream(stream))
         return w13, w2
@@ -471,10 +472,10 @@ class Layer:
         import torch
         dev = w13.device
         E, I, d = self.E, self.I, self.d
-        w13t = torch.empty((E, d, 2 * I), dtype=torch.uint8, device=dev)
-        w13t_s = torch.empty((2 * I // 128, E * d, 4), dtype=torch.uint8, device=dev)
-        w2t = torch.empty((E, I, d), dtype=torch.uint8, device=dev)
-        w2t_s = torch.empty((d // 128, E * I, 4), dtype=torch.uint8, device=dev)
+        w13t = _new(_dense(E, d, 2 * I), torch.uint8, dev, stream)
+        w13t_s = _new(_dense(2 * I // 128, E * d, 4), torch.uint8, dev, stream)
+        w2t = _new(_dense(E, I, d), torch.uint8, dev, stream)
+        w2t_s = _new(_dense(d // 128, E * I, 4), torch.uint8, dev, stream)
         moe_prepare_weights_backward(self.plan, _ptr(w13), _ptr(w2), _ptr(w13t), _ptr(w13t_s), _ptr(w2t),
                                      _ptr(w2t_s), _stream(stream))
         return w13t, w13t_s, w2t, w2t_s
@@ -494,9 +495,14 @@ def _dense(*shape):
     return shape, tuple(reversed(strides))
 
 
-def _new(rows, dtype, device):
-    """An uninitialised tensor of _dense's shape and strides (1.2 us a call, torch.empty 1.6)."""
+def _new(rows, dtype, device, stream=None):
+    """An uninitialised tensor of _dense's shape and strides (1.2 us a call, torch.empty 1.6), from the
+    memory of `stream` where it is given: a block of the current stream's may still be in use there by
+    work that was enqueued before its last owner let it go, and `stream` does not wait for that."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty_strided(*rows, dtype=dtype, device=device)
     return torch.empty_strided(*rows, dtype=dtype, device=device)
 
 

@@ -1,0 +1,74 @@
+"""Calls with a `stream`: what they allocate comes from that stream's memory, which is free of work that
+other streams have not finished.  (A wrong pool shows as wrong values only when such work is late, so
+the pool itself is looked up.)"""
+import pytest
+
+from mixture_experts_routed_dispatch_amd import inputs
+from tests.gpu_util import dev, device_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import torch
+    assert torch.cuda.is_available()
+    from mixture_experts_routed_dispatch_amd import moe
+    moe.lib()
+    return moe
+
+
+def pool(address):
+    """The raw stream whose memory this address is part of."""
+    import torch
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= address < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not torch's memory: %x" % address)
+
+
+def flat(out):
+    return [t for t in (out if isinstance(out, (tuple, list)) else [out]) if t is not None]
+
+
+def both(f):
+    """f(None) on the current stream and f(a stream): equal, each from its own stream's memory."""
+    import torch
+    want = flat(f(None))
+    torch.cuda.synchronize()
+    assert all(pool(t.data_ptr()) == torch.cuda.current_stream().cuda_stream for t in want)
+    s = torch.cuda.Stream()
+    got = flat(f(s))
+    assert all(pool(t.data_ptr()) == s.cuda_stream for t in got), [t.shape for t in got]
+    s.synchronize()
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+    return want
+
+
+def test_layer_with_4bit_weights(moe):
+    T, d, I, E, k = 6, 256, 128, 8, 2
+    t = device_inputs(inputs.generate(T, d, I, E, k, "uniform", seed=1))
+    layer = moe.Layer(T, d, I, E, k, precision=moe.MOE_MXFP4)
+    a, s13, c, s2 = both(lambda s: layer.prepare_weights(t["w13"], t["w2"], stream=s))
+    both(lambda s: layer.expand_weights(a, s13, c, s2, stream=s))
+    both(lambda s: layer.forward(t["x"], t["ids"], t["scores"], a, c, s13, s2, stream=s))
+    full = moe.Layer(T, d, I, E, k, precision=moe.MOE_MXFP4, path=moe.MOE_PATH_PREFILL)
+    both(lambda s: full.forward(t["x"], t["ids"], t["scores"], a, c, s13, s2, stream=s))
+    m_indptr, gather, _, _ = both(lambda s: full.dispatch(t["ids"], t["scores"], stream=s))
+    rows = t["x"][gather.long()].contiguous()
+    both(lambda s: full.forward_routed(rows, m_indptr, a, c, s13, s2, stream=s))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_training_layer(moe, mx):
+    T, d, I, E, k = 40, 256, 128, 8, 2
+    t = device_inputs(inputs.generate(T, d, I, E, k, "uniform", seed=2, with_dy=True))
+    layer = moe.Layer(T, d, I, E, k, precision=moe.MOE_MXFP8_E4M3 if mx else moe.MOE_BF16, training=True)
+    w, scales, back = (t["w13"], t["w2"]), (), {}
+    if mx:
+        q13, s13, q2, s2 = both(lambda s: layer.prepare_weights(t["w13"], t["w2"], stream=s))
+        names = ("w13t", "w13t_scale", "w2t", "w2t_scale")
+        back = dict(zip(names, both(lambda s: layer.prepare_weights_backward(t["w13"], t["w2"], stream=s))))
+        w, scales = (q13, q2), (s13, s2)
+    both(lambda s: layer.forward(t["x"], t["ids"], t["scores"], *w, *scales, stream=s))
+    both(lambda s: layer.backward(t["dy"], t["x"], *w, stream=s, **back))
