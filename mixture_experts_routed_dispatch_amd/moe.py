@@ -517,8 +517,9 @@ def _check(name, t, shape, dtype, device):
 
 class _OnDevice:
     """What Router and BlockNorm share: their device, a workspace there, and calls made with
-    that device current and their outputs allocated on the stream that writes them.  As with
-    a Layer, one object per concurrently running stream (the workspace is its own)."""
+    that device current and their outputs allocated on the stream that writes them.  The workspace
+    belongs to the stream that the object was made on.  Calls on other streams, and captured ones, take
+    one of their own from their stream's (the graph's) memory, so that calls of one object may overlap."""
 
     def __init__(self, device, workspace_bytes):
         import torch
@@ -526,8 +527,18 @@ class _OnDevice:
         if device.index is None:
             device = torch.device(device.type, torch.cuda.current_device())
         self.device, self._index = device, device.index
-        self.workspace = torch.empty(max(workspace_bytes, 16), dtype=torch.uint8, device=device)
-        self._workspace_ptr, self._workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
+        self._workspace_bytes = max(workspace_bytes, 16)
+        with torch.cuda.device(device):
+            self.workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=device)
+            # a graph's memory is not kept for other calls: no stream is the object's own then
+            self._own = None if torch.cuda.is_current_stream_capturing() else _current_stream(self._index)
+
+    def _room(self, s):
+        """The workspace of a call on raw stream s.  (0, the default stream, is never captured.)"""
+        import torch
+        if s == self._own and not (s and torch.cuda.is_current_stream_capturing()):
+            return self.workspace
+        return torch.empty(self._workspace_bytes, dtype=torch.uint8, device=self.device)
 
     def _call(self, f, stream, *args):
         """f(raw stream, *args) with this object's device current and `stream` its current stream."""
@@ -581,12 +592,13 @@ class Router(_OnDevice):
         import torch
         dev, f32, i32 = self.device, torch.float32, torch.int32
         ids, scores = _new(self._per_choice, i32, dev), _new(self._per_choice, f32, dev)
-        counts = sums = loss = None
+        counts = sums = loss = room = None
         if stats:
+            room = self._room(s)
             counts, sums = _new(self._per_expert, i32, dev), _new(self._per_expert, f32, dev)
             loss = _new(((), ()), f32, dev)
         moe_router_forward(cfg, logits.data_ptr(), _ptr(bias), _ptr(mask), ids.data_ptr(), scores.data_ptr(),
-                           _ptr(counts), _ptr(sums), _ptr(loss), self._workspace_ptr, self._workspace_bytes, s)
+                           _ptr(counts), _ptr(sums), _ptr(loss), _ptr(room), self._workspace_bytes, s)
         return ids, scores, counts, sums, loss
 
     def backward(self, dscores, logits, ids, counts=None, dloss=None, mask=None, dlogits=None, stream=None):
@@ -681,7 +693,8 @@ class BlockNorm(_OnDevice):
         dw_post = None if w_post is None else like(w_post)
         dgate = None if gate is None else like(gate)
         dw_pre = None if w_pre is None else like(w_pre)
+        room = self._room(s)
         moe_norm_backward(self._cfg, _ptr(dz), _ptr(dh), _ptr(z), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre),
-                          dx.data_ptr(), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), self._workspace_ptr,
+                          dx.data_ptr(), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), room.data_ptr(),
                           self._workspace_bytes, s)
         return dx, dy, dw_post, dgate, dw_pre

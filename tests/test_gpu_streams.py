@@ -72,3 +72,85 @@ def test_training_layer(moe, mx):
         w, scales = (q13, q2), (s13, s2)
     both(lambda s: layer.forward(t["x"], t["ids"], t["scores"], *w, *scales, stream=s))
     both(lambda s: layer.backward(t["dy"], t["x"], *w, stream=s, **back))
+
+
+def around(moe, T):
+    """(object, what it computes on a stream, its workspace's bytes in use) of a router and a norm."""
+    import torch
+    g = torch.Generator(device=dev()).manual_seed(T)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev())
+    d, E, k = 512, 64, 4
+    z, x, y, dz, dh = rn(T, E), rn(T, d).bfloat16(), rn(T, d).bfloat16(), rn(T, d).bfloat16(), rn(T, d).bfloat16()
+    w, gate = 1 + 0.1 * rn(d), rn(d)
+    r = moe.Router(T, E, k, balance_coef=0.01)
+    n = moe.BlockNorm(T, d, gate=moe.MOE_GATE_CHANNEL)
+    return [(r, lambda s=None: r.forward(z, stream=s)),
+            (n, lambda s=None: n.backward(dz, dh, x, y, w_post=w, gate=gate, w_pre=w, stream=s))]
+
+
+@pytest.fixture
+def rooms(moe, monkeypatch):
+    """Addresses of the workspaces that the calls were given, newest last."""
+    seen = []
+    router, norm = moe.moe_router_forward, moe.moe_norm_backward
+    monkeypatch.setattr(moe, "moe_router_forward", lambda *a: (seen.append(a[9]), router(*a))[1])
+    monkeypatch.setattr(moe, "moe_norm_backward", lambda *a: (seen.append(a[13]), norm(*a))[1])
+    return seen
+
+
+def test_workspaces_of_router_and_norm(moe, rooms):
+    """The object's own on the stream that it was made on, and nowhere else: not on other streams, not
+    in a capture, not when a stream of its own is captured."""
+    import torch
+    for o, f in around(moe, 300):
+        want = flat(f())
+        torch.cuda.synchronize()
+        assert rooms[-1] == o.workspace.data_ptr()
+        s = torch.cuda.Stream()
+        got = flat(f(s))
+        assert rooms[-1] != o.workspace.data_ptr() and pool(rooms[-1]) == s.cuda_stream
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        made = around(moe, 300)
+        for o, f in made:
+            f()
+            assert rooms[-1] == o.workspace.data_ptr() and pool(rooms[-1]) == s.cuda_stream
+        s.synchronize()
+    for o, f in made:
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+            f()
+            assert rooms[-1] != o.workspace.data_ptr()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        inner = moe.Router(300, 64, 4)
+    z = torch.randn(300, 64, device=dev())
+    inner.forward(z)
+    assert rooms[-1] != inner.workspace.data_ptr()
+
+
+def test_one_object_on_streams_and_in_graphs_at_once(moe):
+    import torch
+    for o, f in around(moe, 5000):
+        want = flat(f())
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        graphs = []
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                graphs.append((g, flat(f())))
+        for _ in range(3):
+            for _, out in graphs:
+                for t in out:
+                    t.zero_()
+            torch.cuda.synchronize()
+            got = []
+            for s, (g, out) in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+            got = [flat(f(streams[2])), flat(f())]
+            torch.cuda.synchronize()
+            for out in got + [out for _, out in graphs]:
+                assert all(torch.equal(a, b) for a, b in zip(out, want))
