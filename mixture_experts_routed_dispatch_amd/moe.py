@@ -373,7 +373,7 @@ class Layer:
         if y is None:
             y = _new(self._rows, torch.bfloat16, x.device, stream)
         if self._mxfp4 is not None:
-            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x, ids, scores, y)
+            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x, ids, scores, y, stream)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward(self.plan, _ptr(x), _ptr(ids), _ptr(scores), w, _ptr(y), _stream(stream))
         return y
@@ -387,7 +387,7 @@ class Layer:
         if out is None:
             out = _new(_dense(self.T * self.k, self.d), torch.bfloat16, x_rows.device, stream)
         if self._mxfp4 is not None:
-            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out, out)
+            self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out, out, stream)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward_routed(self.plan, _ptr(x_rows), _ptr(m_indptr), w, _ptr(out), _stream(stream))
         return out
@@ -422,6 +422,8 @@ class Layer:
         if self.precision == MOE_MXFP4:
             n13, n2 = self._mxfp4
             dev = torch.device("cuda", torch.cuda.current_device())
+            if stream is not None:
+                _check_stream(stream, dev.index)
             _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
             _check("w2", w2, (E, d, I), torch.bfloat16, dev)
             w13_q, w13_s, w2_q, w2_s = (_new(n, torch.uint8, dev, stream) for n in n13 + n2)
@@ -437,12 +439,14 @@ class Layer:
                             _ptr(w2_s), _stream(stream))
         return w13_q, w13_s, w2_q, w2_s
 
-    def _check_mxfp4(self, w13_q, w13_s, w2_q, w2_s, a, b, c, d):
-        """Prepared weights of this layer's sizes, they and the four other tensors on the current
-        device, or ValueError (a missing tensor is left to the call, which refuses it): the kernels
-        address them by the plan's sizes."""
+    def _check_mxfp4(self, w13_q, w13_s, w2_q, w2_s, a, b, c, d, stream):
+        """Prepared weights of this layer's sizes, they, the four other tensors and the stream on the
+        current device, or ValueError (a missing tensor is left to the call, which refuses it): the
+        kernels address them by the plan's sizes."""
         import torch
         index = torch.cuda.current_device()
+        if stream is not None:
+            _check_stream(stream, index)
         try:
             if ((w13_q.numel(), w13_s.numel(), w2_q.numel(), w2_s.numel()) == self._mxfp4_sizes
                     and w13_q.is_contiguous() and w13_s.is_contiguous() and w2_q.is_contiguous() and w2_s.is_contiguous()
@@ -460,7 +464,7 @@ class Layer:
         """The BF16 weights (w13, w2) that an MXFP4 layer's prepared weights stand for."""
         import torch
         if self._mxfp4 is not None:
-            self._check_mxfp4(w13_q, w13_s, w2_q, w2_s, w13_q, w13_s, w2_q, w2_s)
+            self._check_mxfp4(w13_q, w13_s, w2_q, w2_s, w13_q, w13_s, w2_q, w2_s, stream)
         w13, w2 = (_new(n, torch.bfloat16, w13_q.device, stream) for n in self._weights)
         w = weights(_ptr(w13_q), _ptr(w2_q), _ptr(w13_s), _ptr(w2_s))
         moe_expand_weights(self.plan, w, _ptr(w13), _ptr(w2), _stream(stream))
@@ -506,6 +510,12 @@ def _new(rows, dtype, device, stream=None):
     return torch.empty_strided(*rows, dtype=dtype, device=device)
 
 
+def _check_stream(stream, index):
+    """A stream of device `index`, or ValueError."""
+    if stream.device.index != index:
+        raise ValueError("a stream of cuda:%d is needed, got one of %s" % (index, stream.device))
+
+
 def _check(name, t, shape, dtype, device):
     """A dense tensor of this shape and type on this device, or ValueError."""
     if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
@@ -544,6 +554,7 @@ class _OnDevice:
         """f(raw stream, *args) with this object's device current and `stream` its current stream."""
         import torch
         if stream is not None:
+            _check_stream(stream, self._index)
             with torch.cuda.stream(stream):            # also makes the stream's device current
                 return f(int(stream.cuda_stream), *args)
         if torch.cuda.current_device() != self._index:
