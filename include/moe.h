@@ -331,7 +331,7 @@ moe_status_t moe_backward(moe_plan_t plan, const void* dy, const void* x, const 
  * row of -inf alone scores 0.  (A low finite logit is like any other: with a bias its key is s + bias.)
  * A NaN key counts as -inf in the choice.  A NaN logit has one, and makes the row's softmax (with sigmoid:
  * its own score and the row's p) NaN; so does +inf with softmax.  With softmax and a bias all keys of such
- * a row are NaN: its ids are 0 .. k-1.  Biases may be infinite.
+ * a row are NaN: its ids are 0 .. k-1.  Biases may be infinite.  A score s below 2^-126 counts as 0.
  * Stateless: a config, caller-owned buffers and a workspace that holds nothing between calls;
  * calls that overlap need a workspace each. */
 #define MOE_SCORE_SOFTMAX 0

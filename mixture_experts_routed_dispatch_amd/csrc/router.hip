@@ -680,7 +680,7 @@ __global__ __launch_bounds__(kThreads) void route_final_kernel(RouterArgs g, int
 template <int kV, bool kF32, bool kSig>
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) {
     constexpr int kStep = kV + 4;
-    // p_j ds_j (softmax), ds_j (sigmoid) of the chosen
+    // of the chosen, by way of the scores: p_j ds_j (softmax), s_j (1 - s_j) ds_j (sigmoid)
     __shared__ __attribute__((aligned(16))) float extra[kRows][16 * kStep];
     __shared__ __attribute__((aligned(16))) float shared[16 * kStep];   // counts
     __shared__ int64_t part[kThreads / MOE_WAVE];
@@ -773,19 +773,15 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
             dot += gj[h] * vj[h];
         }
         dot = row_sum(dot);
-        const float inv_total = total == 0.0f ? 0.0f : 1.0f / total;
         float own = 0.0f;
         wave_fence();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float r;
-            if (g.normalize) {
-                // softmax: p_j ds_j = v_j (g_j - dot), whose sum over j is zero
-                r = (gj[h] - dot) * (kSig ? inv_total : vj[h]);
-            } else {
-                r = kSig ? gj[h] : sj[h] * gj[h];
-                own += kSig ? 0.0f : r;
-            }
+            // normalize: s_j ds_j = v_j (g_j - dot), whose sum over j is zero (1 / total alone may be too
+            // large for a product)
+            float r = g.normalize ? vj[h] * (gj[h] - dot) : sj[h] * gj[h];
+            if constexpr (kSig) r *= one_score<true>(-zj[h], 0.0f, 0.0f);    // 1 - s_j does not cancel
+            else own += r;
             if (id[h] >= 0) ex[slot(id[h])] = r;
         }
         wave_fence();
@@ -794,11 +790,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouterGradArgs g) 
         }
         float out[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const float x = ex[x0 + i];
-            if constexpr (kSig) out[i] = ((bal[i] - pb) * inv + x) * f[i];
-            else out[i] = f[i] * inv * (bal[i] - pb) + x;
-        }
+        for (int i = 0; i < kV; ++i) out[i] = f[i] * inv * (bal[i] - pb) + ex[x0 + i];
         if (!live) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) out[i] = 0.0f;

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests.gpu_util import dev, say
-from tests.test_gpu_router import REL, ref_forward, scores64
+from tests.test_gpu_router import REL, ref_backward, ref_forward, scores64
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -165,3 +165,27 @@ def test_one_dominant_score_next_to_biased_small_ones(moe, k):
     z[T // 2:] = torch.randn(T - T // 2, E, generator=g) * 3
     z[T // 2:, 0] = 16.0
     compare(moe, z, b, k, 0)
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gradient_of_the_smallest_sigmoid_scores(moe, normalize):
+    """Rows whose scores are all near FP32's smallest normal number, 2^-126: their reciprocal sums times a
+    gradient of 100 pass its largest.  Bars as in tests/test_gpu_router.py: 2e-5 of the row's largest term."""
+    import torch
+    T, E, k = 200, 24, 4
+    g = torch.Generator().manual_seed(5)
+    z = -86.5 - 0.6 * torch.rand(T, E, generator=g)
+    z[T // 2:] = -60 - 20 * torch.rand(T - T // 2, E, generator=g)
+    ds = 100 * torch.randn(T, k, generator=g)
+    r = moe.Router(T, E, k, score=1, normalize=normalize, balance_coef=20.0)
+    ids, w, counts, _, _ = r.forward(z.to(dev()))
+    ri, rw, rc, _, _ = ref_forward(z, None, None, k, 1, normalize, 1.0, 20.0)
+    assert np.array_equal(ids.cpu().numpy(), ri)
+    assert (np.abs(w.cpu().numpy() - rw) <= REL * np.abs(rw)).all()
+    for dloss in (None, 3.0):
+        got = r.backward(ds.to(dev()), z.to(dev()), ids, counts, dloss=None if dloss is None else torch.tensor(dloss, device=dev()))
+        ref = ref_backward(z, None, ri.copy(), rc, ds, dloss, k, 1, normalize, 1.0, 20.0)
+        got = got.double().cpu().numpy()
+        assert np.isfinite(got).all()
+        top = 2 * np.abs(ds.numpy()).max(1, keepdims=True) * (1 if normalize else rw.max(1, keepdims=True))
+        assert (np.abs(got - ref) <= 2e-5 * top + (0 if dloss is None else 2e-5 * 20.0)).all()
