@@ -179,7 +179,7 @@ struct DecodeArgs {
 hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
 hipError_t launch_decode_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
 // One token: W2 of all k experts and the score-weighted combine into y (a launch in place
-// of decode_w2 and combine); with MXFP4 weights any number of tokens.
+// of decode_w2 and combine).
 constexpr int kMaxTopK = 32;
 hipError_t launch_decode_w2_one(const DecodeArgs& g, int num_cu, hipStream_t s);
 // "Mega" decode: W13 + activation + W2 chunked over I in one launch (chunks of
@@ -214,7 +214,8 @@ inline Mxfp4Matrix mxfp4_w2(const void* w, const void* codes, const void* scales
     return m;
 }
 // Decode with MXFP4 weights: W13 with the activation; W2 with the combine into y, by way of
-// FP32 expert outputs in o ([T*k, d] floats; one token: none)
+// FP32 expert outputs in o ([T*k, d] floats; one token: none).  a holds 2 T*k rows of I: the rounded
+// values, then their remainders.
 hipError_t launch_decode4_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
 hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
 
