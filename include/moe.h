@@ -137,7 +137,9 @@ typedef struct {
  * MXFP8 plans need d % 256 == 0 and I % 128 == 0 and run the grouped-GEMM path.
  * MXFP4 plans need d % 128 == 0 and I % 128 == 0 and infer only, without mega; past
  * T*k = 256 (or with path = MOE_PATH_PREFILL) each product's weights are first expanded to
- * BF16 in the workspace (4 E I d bytes), within its stage, and the BF16 products run.
+ * BF16 in the workspace (4 E I d bytes), within its stage, and the BF16 products run: all experts'
+ * weights pass through memory three times a call, so that batches a little past 256 routed rows are
+ * served faster by several calls of up to 256, or by BF16 weights.
  * Shapes whose activations (T*d*2 bytes), routed intermediates (T*k*2I*2) or
  * per-expert W13 (2I*d*2) reach 2^31 bytes are refused (the kernels address them
  * with 32-bit offsets).  Returns MOE_ERR_UNSUPPORTED for shapes outside the limits,

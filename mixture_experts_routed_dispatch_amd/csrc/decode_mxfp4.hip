@@ -7,8 +7,9 @@
 // that a token's y is as exact beside others as alone.  The experts' outputs o stay in FP32 until
 // the one rounding of y.  The time is that of streaming 4.25 bits
 // for each weight of the active experts: 128 experts of d = 2048, I = 768, k = 8, one token 5.2 and
-// 4.8 us for 13.4 and 6.7 MB, where starting and the chain of loads are what is left; 32 tokens on
-// 59 experts 22.2, 13.4 and (combine) 3.9 us for 99 and 49 MB (4.5 and 3.7 TB/s).
+// 4.7 us for 13.4 and 6.7 MB, where starting and the chain of loads are what is left; 32 tokens on
+// 59 experts 22.0, 15.5 and (combine) 4.5 us for 99 and 49 MB (4.5 and 3.2 TB/s).  The remainders
+// cost W2 2.1 us of that.
 //
 // A wave reads a tile (16 weight rows x 128 of K, 1 KiB in a row) with one 16-byte load per
 // lane: lane 16 q + n holds the block of 32 columns 128 s + 32 q of row n, with one scale.
@@ -140,6 +141,7 @@ __global__ __launch_bounds__(kThreads, kOneWGs) void decode4_w13_one(DecodeArgs 
 // that all the tiles share.  Those four are what bounds the kernel when few tiles share them:
 // they occupy the address unit as long as four loads of codes.  W13 and W2 at 32 tokens of the
 // 128-expert layer, 59 experts active (99 and 49 MB):
+//   (W2 without the remainders of a)
 //   a wave for each tile over all of K            32.2 and 18.1 us
 //   a wave for two, four tiles over all of K      23.6 and 14.0, 25.1 and 13.0
 //   four, eight tiles and a quarter of K a wave   21.4 and 13.2, 21.9 and 14.0

@@ -231,6 +231,9 @@ __device__ __forceinline__ void finish_columns(const NormGradArgs& g, int which,
 // factor), so that the next row's loads fit besides the second workgroup: 8192 x 2048 in BF16
 // 37.7 us (39.0 without them; one workgroup of 1024 threads 37.1), 4099 x 4096 with an FP32 stream
 // 56.6 us (57.4; 58.4), 5.6 and 5.6 TB/s of what they move, the partial sums of 8 and 17 MB among it.
+// One rule for both: what 1024 threads gain at the first they lose at the second.  Past d = 8192 a lane
+// holds 16 channels, for which 128 registers are too few (19 spilled, 47 with an FP32 stream):
+// 2048 x 16384 takes 118 and 180 us, 3.4 TB/s.
 constexpr int kBwdThreads = 512;
 template <int kW> constexpr int bwd_threads() { return 64 * kW > kBwdThreads ? 64 * kW : kBwdThreads; }
 template <typename TRes, int kW, int kC>

@@ -23,10 +23,12 @@
 // for k <= 20 (about 18 for k = 16).  Those candidates' indices go to LDS in ascending order, one or
 // two to a lane, and each counts the ones before it, which is its place.  With larger k, or more than
 // kCand candidates (ties, rows of one value), the row's maximum is taken k times; a bias then takes
-// the last of those as the bound.  16384 x 256 in BF16 with sigmoid, bias and k = 8: 12.0 us, against
-// 32.4 by taking the maximum 8 times; 800 vector instructions a wave issue for 6 us of it, the rest
-// is the latency of one pass (its 9.5 MB take 1.9 us).  k = 16 with the second launch 23.8 us, and
-// 113 while all of k > 12 took the maxima and settled near keys for the whole row.
+// the last of those as the bound.  16384 x 256 in BF16 with sigmoid, bias and k = 8: 12.0 to 13.6 us
+// (card to card), against 32.4 by taking the maximum 8 times; 800 vector instructions a wave issue for
+// 6 us of it, the rest is the latency of one pass (its 9.5 MB take 1.9 us), in which the candidates'
+// logits and then the chosen ones' are fetched again from memory.  k = 16 with the second launch
+// 22.2 us, and 113 while all of k > 12 took the maxima and settled near keys for the whole row; k = 32,
+// which takes the maxima, 214.
 //
 // With a bias the keys s + b have to be ordered as in exact arithmetic.  They are compared in
 // FP32; where two that matter lie closer than FP32's error, they are computed again in 64

@@ -1,6 +1,7 @@
 """MXFP4 expert weights: the conversion against its definition in numpy, and the layer on them
 against the float64 oracle on the same (expanded, hence exact) weights, with the BF16 bars of
-tests/gpu_util.py: the products take exact BF16 weights and round a and o where the BF16 layer does.
+tests/gpu_util.py: the products take exact BF16 weights, and round a and o no further than the BF16
+layer does (a's remainder: tests/test_gpu_mxfp4_activation.py).
 """
 import numpy as np
 import pytest
