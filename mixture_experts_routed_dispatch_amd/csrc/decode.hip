@@ -829,6 +829,7 @@ hipError_t launch_decode(K1 wave_kernel, K2 split_kernel, const DecodeArgs& g, i
 }
 
 hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s) {
+    if (g.w13_scale) return launch_decode4_w13(g, num_cu, s);
     // many items per workgroup (many tokens) and a wave's K share within kPipePairs pairs:
     // the pipelined kernel, two workgroups per CU
     const int R = g.T * g.k;
@@ -849,6 +850,7 @@ hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s) {
 }
 
 hipError_t launch_decode_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
+    if (g.w2_scale) return launch_decode4_w2(g, num_cu, s);
     return launch_decode(decode_w2<false>, decode_w2<true>, g, g.d / 16, g.I / 32, num_cu, s);
 }
 

@@ -176,6 +176,7 @@ struct DecodeArgs {
     const uint8_t* w2_scale;
 };
 
+// With MXFP4 weights W2 is combined into y as well (decode_mxfp4.hip).
 hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
 hipError_t launch_decode_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
 // One token: W2 of all k experts and the score-weighted combine into y (a launch in place

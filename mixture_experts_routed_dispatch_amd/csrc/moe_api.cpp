@@ -486,10 +486,6 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         if (w4) {
             dg.w13_scale = w->w13_scale;
             dg.w2_scale = w->w2_scale;
-            hipError_t e = staged(p, MOE_STAGE_DECODE_W13, s, [&] { return launch_decode4_w13(dg, p->num_cu, s); });
-            if (e != hipSuccess) return MOE_ERR_HIP;
-            e = staged(p, MOE_STAGE_DECODE_W2, s, [&] { return launch_decode4_w2(dg, p->num_cu, s); });   // with the combine
-            return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
         }
         if (c.mega) {
             hipError_t e = staged(p, MOE_STAGE_MEGA, s, [&] {
@@ -499,12 +495,13 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         }
         hipError_t e = staged(p, MOE_STAGE_DECODE_W13, s, [&] { return launch_decode_w13(dg, p->num_cu, s); });
         if (e != hipSuccess) return MOE_ERR_HIP;
-        if (c.T == 1) {
+        if (c.T == 1 && !w4) {
             e = staged(p, MOE_STAGE_DECODE_W2, s, [&] { return launch_decode_w2_one(dg, p->num_cu, s); });
             return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
         }
         e = staged(p, MOE_STAGE_DECODE_W2, s, [&] { return launch_decode_w2(dg, p->num_cu, s); });
         if (e != hipSuccess) return MOE_ERR_HIP;
+        if (w4) return MOE_OK;                         // combined
         e = staged(p, MOE_STAGE_COMBINE, s, [&] {
             return launch_combine(dg.o, nullptr, scores, c.T, c.k, c.d, dg.y, s);
         });
