@@ -106,10 +106,15 @@ def _segments(g, R, E):
     return torch.cat([torch.zeros(1, dtype=torch.int32, device=DEV), ends])
 
 
+def _pow2(e):
+    """2^e in 64 bits, exactly (a power function need not be)."""
+    return (e.long() + 1023 << 52).view(torch.float64)
+
+
 def _e4m3(q):
     """The nearest E4M3 values to q (64 bits), ties to even, in 32 bits (exact)."""
     _, e = torch.frexp(q)
-    step = torch.ldexp(torch.ones_like(q), (e - 1).clamp(min=-6) - 3)
+    step = _pow2((e - 1).clamp(min=-6) - 3)
     return ((q / step).round() * step).clamp(-TOP, TOP).float()
 
 
@@ -277,8 +282,8 @@ def _columns8(v):
     top = b.abs().amax(1, keepdim=True)
     m, e = torch.frexp(top)                                   # top = m 2^e, m in [0.5, 1)
     s = torch.where(top > 0, e - 9 + (m > 0.875).int(), -127).clamp(-127, 127)    # smallest 2^s with top / 2^s <= 448
-    q = _e4m3(torch.ldexp(b, -s).double())
-    return torch.ldexp(q, s).flatten(0, 1)[:n]
+    q = _e4m3(b.double() * _pow2(-s))
+    return (q.double() * _pow2(s)).float().flatten(0, 1)[:n]
 
 
 def _plain_product8_grad(st):
@@ -441,10 +446,9 @@ def _columns64(v):
     b[:n] = v.double()
     b = b.view(-1, 32, N)
     top = b.abs().amax(1, keepdim=True)
-    s = torch.where(top > 0, torch.ceil(torch.log2(top / 448)), torch.zeros_like(top))
-    s = torch.where(top > 448 * torch.exp2(s), s + 1, s)          # the logarithm's own rounding
-    s = torch.where((top > 0) & (top <= 224 * torch.exp2(s)), s - 1, s)
-    return (_nearest64(b / torch.exp2(s)) * torch.exp2(s)).view(-1, N)[:n]
+    powers = torch.tensor([2.0 ** i for i in range(-160, 161)], dtype=torch.float64, device=DEV)
+    s = powers[torch.searchsorted(powers * 448, top).clamp(max=320)]     # the smallest with top / s <= 448
+    return (_nearest64(b / s) * s).view(-1, N)[:n]
 
 
 def _exact_product8_grad(st):
