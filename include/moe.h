@@ -59,14 +59,16 @@ typedef enum {
 typedef enum {
     MOE_BF16 = 0,              /* BF16 operands, FP32 accumulate (blog post: "BF16 Standard") */
     MOE_MXFP8_E4M3 = 1,        /* OCP MXFP8: E4M3 elements, E8M0 scale per 32 along K */
-    MOE_MXFP4 = 2              /* weights in OCP MXFP4 (E2M1 elements, E8M0 scale per 32 along K),
+    MOE_MXFP4 = 2,             /* weights in OCP MXFP4 (E2M1 elements, E8M0 scale per 32 along K),
                                   activations in BF16, FP32 accumulate; inference */
+    MOE_FP8_BLOCK128 = 3       /* E4M3 with FP32 scales: weights one per 128 x 128, activations one per
+                                  row and 128 of K, quantized in the call; FP32 accumulate; inference */
 } moe_precision_t;
 
 /* path selection (moe_config_t.path) */
 #define MOE_PATH_AUTO 0        /* decode kernels when T*k <= 256 and inference, else prefill */
 #define MOE_PATH_PREFILL 1     /* grouped-GEMM path */
-#define MOE_PATH_DECODE 2      /* weight-streaming path; requires T*k <= 256, inference, BF16 or MXFP4 */
+#define MOE_PATH_DECODE 2      /* weight-streaming path; requires T*k <= 256, inference, not MXFP8 */
 
 /* gated activation of the W13 output (moe_config_t.activation; nvfp4moe README,
  * "Supported kernel surface": SwiGLU, GeGLU and ReGLU FC1 epilogues): a = f(g) * u */
@@ -107,6 +109,10 @@ typedef struct {
 typedef struct {
     const void* w13;          /* BF16 [E, 2I, d], or E4M3 codes (uint8) [E, 2I, d], or MXFP4 codes */
     const void* w2;           /* BF16 [E, d, I],  or E4M3 codes (uint8) [E, d, I],  or MXFP4 codes */
+    /* FP8_BLOCK128: w13 and w2 are E4M3 codes, the scales FP32 in row-major order, w13_scale
+     * [E, 2I/128, d/128] (gate squares first) and w2_scale [E, d/128, I/128], each of the 128 x 128 square
+     * of its matrix: the layout in which such checkpoints hold them, and which moe_prepare_weights writes.
+     * All four, x and y 16-byte aligned; NULL scales are MOE_ERR_INVALID_ARG */
     /* MXFP4: w13, w2 and both scales are the four outputs of moe_prepare_weights, 16-byte
      * aligned; NULL scales are MOE_ERR_INVALID_ARG */
     /* MXFP8 only (NULL for BF16): E8M0 scale bytes in the block-major layout that
@@ -140,6 +146,7 @@ typedef struct {
  * BF16 in the workspace (4 E I d bytes), within its stage, and the BF16 products run: all experts'
  * weights pass through memory three times a call, so that batches a little past 256 routed rows are
  * served faster by several calls of up to 256, or by BF16 weights.
+ * FP8_BLOCK128 plans need d % 128 == 0 and I % 128 == 0 and infer only, without mega.
  * Shapes whose activations (T*d*2 bytes), routed intermediates (T*k*2I*2) or
  * per-expert W13 (2I*d*2) reach 2^31 bytes are refused (the kernels address them
  * with 32-bit offsets).  Returns MOE_ERR_UNSUPPORTED for shapes outside the limits,
@@ -220,13 +227,19 @@ moe_status_t moe_quantize_mxfp8(const void* v_bf16, int64_t rows, int32_t K,
  * 16 q + n the block 32 q .. 32 q + 31 of row n (element 2 i in the low half of byte i), the
  * tiles of 16 rows one after another along K; byte j of scale word (tile row group, g, piece)
  * is the scale of tile 4 g + j.  W13's tile b has gate rows 8 b .. 8 b + 7, then the same up
- * rows; W2's tile b rows 16 b .. 16 b + 15.  Inputs are meant to be finite. */
+ * rows; W2's tile b rows 16 b .. 16 b + 15.  Inputs are meant to be finite.
+ *
+ * On a plan with precision MOE_FP8_BLOCK128 it quantizes each 128 x 128 square of the matrices with
+ * moe_quantize_block128's rule: codes uint8 w13_q [E, 2I, d], w2_q [E, d, I], and w13_s, w2_s FP32
+ * [E, 2I/128, d/128] and [E, d/128, I/128], 16-byte aligned.  Codes and scales from elsewhere need no
+ * preparation, whatever their scales. */
 moe_status_t moe_prepare_weights(moe_plan_t plan, const void* w13_bf16, const void* w2_bf16,
                                  uint8_t* w13_q, uint8_t* w13_s, uint8_t* w2_q, uint8_t* w2_s,
                                  void* stream);
 
-/* The BF16 values of MXFP4 weights (exact): w13 [E, 2I, d] and w2 [E, d, I] from what
- * moe_prepare_weights wrote on an MXFP4 plan (MOE_ERR_UNSUPPORTED on another). */
+/* The BF16 values of MXFP4 weights (exact) or FP8_BLOCK128 weights (code times scale, rounded): w13
+ * [E, 2I, d] and w2 [E, d, I] from what moe_prepare_weights wrote on such a plan
+ * (MOE_ERR_UNSUPPORTED on another). */
 moe_status_t moe_expand_weights(moe_plan_t plan, const moe_weights_t* w, void* w13_bf16, void* w2_bf16,
                                 void* stream);
 
@@ -246,6 +259,9 @@ moe_status_t moe_prepare_weights_backward(moe_plan_t plan, const void* w13_bf16,
  * SwiGLU epilogue, [MXFP8: re-quantize the SwiGLU output], grouped W2 GEMM,
  * score-weighted combine in FP32 with j ascending from +0.0 and one rounding
  * to BF16 (nvfp4moe README, "MoE layer": the timed path).  y is BF16 [T, d].
+ * With FP8_BLOCK128 every product's operands are in 8 bits on either path: x by
+ * moe_quantize_block128's rule, and the activation's output a, from its FP32 value, by the same
+ * rule along I.  The decode path adds up y from FP32 expert outputs, the other from BF16 ones.
  * BF16 plans take BF16 weights; MXFP8 plans take the prepared codes in w13 / w2
  * and their E8M0 scales in w13_scale / w2_scale (moe_prepare_weights layout;
  * NULL scales are MOE_ERR_INVALID_ARG).  Plans with T*k <= 256 (BF16, inference)
@@ -288,7 +304,7 @@ moe_status_t moe_forward_static(moe_plan_t plan, const void* x, const int32_t* i
  * expert is then taken as empty (out is not written) and MOE_DEV_BAD_INDPTR is set
  * (moe_get_status).  Inference plans on the grouped-GEMM path (cfg.path =
  * MOE_PATH_PREFILL, or AUTO with T*k > 256) with T*k*d*2 < 2^31; others return
- * MOE_ERR_UNSUPPORTED.  MXFP8 plans take prepared weights with their scales (as
+ * MOE_ERR_UNSUPPORTED.  FP8_BLOCK128 plans quantize the rows as they stand.  MXFP8 plans take prepared weights with their scales (as
  * moe_forward does) and quantize the m_indptr[E] rows of x_rows as they stand, with
  * moe_quantize_mxfp8's rule, before W13.  It uses the plan's dispatch and intermediate workspace, which the
  * next call overwrites. */
@@ -317,6 +333,54 @@ moe_status_t moe_forward_routed(moe_plan_t plan, const void* x_rows, const int32
  * BF16 between kernels. */
 moe_status_t moe_backward(moe_plan_t plan, const void* dy, const void* x, const moe_weights_t* w,
                           void* dx, void* dw13, void* dw2, float* dscores, void* stream);
+
+/* ---- products with weights in blocks of 128 ------------------------------------------------
+ * Rows in BF16 times weights in E4M3, for projections beside the experts (E = 1) and for experts of any
+ * form (rows in expert order):
+ *   y[r] = W_e x[r],   dx[r] = W_e^T dy[r],   dW_e = sum_r dy[r] x[r]^T     for the rows r of expert e
+ * A block with largest magnitude m has the FP32 scale s = max(m / 448, 2^-100), rounded once, and each
+ * element v the code E4M3(v / s): the nearest to the exact quotient, ties to even.  A block that holds an
+ * infinity or NaN has the scale NaN, and so is all that is computed from it.  x is quantized along K and,
+ * for dx, dy along N, a block being 128 elements of a row; a weight's block is 128 x 128.  A product is
+ * the sum over blocks of (sum of code products) x scale x scale, in FP32, rounded once to BF16.
+ * For dW the operands are quantized along the expert's rows instead, in MXFP8: blocks of 32 rows,
+ * counted from the expert's first, by moe_quantize_mxfp8's rule (which makes an infinity or NaN finite). */
+typedef struct {
+    int32_t R;                 /* rows, 0 .. 2^24 */
+    int32_t N;                 /* outputs; a multiple of 128 */
+    int32_t K;                 /* inputs; a multiple of 128; N K < 2^31 */
+    int32_t E;                 /* matrices, 1..256 */
+    int32_t training;          /* 1: with moe_product_backward; max(N, K) (R + 128 E) < 2^32 */
+    int32_t wgrad_accumulate;  /* 1: dW = bf16(dW + bf16(gradient)); training only */
+} moe_product_config_t;
+
+/* BF16 rows [rows, K] to codes uint8 [rows, K] and scales f32 [rows, K/128], by the rule above. */
+moe_status_t moe_quantize_block128(const void* v_bf16, int64_t rows, int32_t K, uint8_t* codes, float* scales,
+                                   void* stream);
+
+/* Bytes of workspace of moe_product_forward and (training) moe_product_backward; 0 for an invalid
+ * config.  It holds nothing between calls; calls that overlap need one each. */
+size_t moe_product_workspace_bytes(const moe_product_config_t* cfg);
+
+/* BF16 weights [E, N, K] to codes uint8 [E, N, K] and scales f32 [E, N/128, K/128], and back. */
+moe_status_t moe_product_prepare_weights(const moe_product_config_t* cfg, const void* w_bf16, uint8_t* w_q, float* w_s,
+                                         void* stream);
+moe_status_t moe_product_expand_weights(const moe_product_config_t* cfg, const uint8_t* w_q, const float* w_s,
+                                        void* w_bf16, void* stream);
+
+/* x, y BF16 [R, K], [R, N]; m_indptr int32 [E+1] on the device, the experts' first rows: from 0, not
+ * falling, at most R (NULL with E = 1: all rows).  Rows behind m_indptr[E] are not written.  An m_indptr
+ * that breaks this is caught on the device: no row is written, and MOE_DEV_BAD_INDPTR is set in *status
+ * (device int32, or NULL).  All pointers but m_indptr, scales and status 16-byte aligned. */
+moe_status_t moe_product_forward(const moe_product_config_t* cfg, const void* x, const int32_t* m_indptr,
+                                 const uint8_t* w_q, const float* w_s, void* y, int32_t* status, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* dx BF16 [R, K] and dw BF16 [E, N, K] (+0.0 for experts with no row), either of which may be NULL; x is
+ * read for dw, the weights for dx.  With a broken m_indptr every expert counts as empty. */
+moe_status_t moe_product_backward(const moe_product_config_t* cfg, const void* dy, const void* x,
+                                  const int32_t* m_indptr, const uint8_t* w_q, const float* w_s, void* dx, void* dw,
+                                  int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- router: logits -> ids, scores, counts and balance loss, and the gradient -------------
  * What makes the ids and scores that moe_forward takes.  With z = logits[t] [E] and

@@ -1,0 +1,75 @@
+// block128.h -- what the kernels on E4M3 codes with one FP32 scale per 128 share: a block's scale
+// and the codes of its values.
+#pragma once
+
+#include <type_traits>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+// The scale of a block from the bits of its largest magnitude (magnitudes of floats order like
+// their bits, infinities and NaN above all): amax / 448 rounded once, at least 2^-100, which keeps
+// the quotients' remainders below exact; NaN for a block that holds an infinity or NaN, so that
+// what is computed from it is NaN.
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+    if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    return __builtin_fmaxf(__uint_as_float(amax_bits) / 448.0f, 0x1p-100f);
+}
+
+// v / s for |v| <= 448 s (1 + 2^-24), as a float that rounds to the same E4M3 value as the exact
+// quotient does (nearest, ties to even).  q is within an ulp of the quotient.  Where it is not the
+// quotient itself and its last bit is 0, it goes one ulp towards the quotient: E4M3 values and the
+// midpoints between them have that bit 0, so none of them lies between the result and the
+// quotient.  The sign of the remainder v - q s is that of the exact one, which fma rounds once.
+// inv = 1 / s within an ulp.
+__device__ __forceinline__ float block_quotient(float v, float s, float inv) {
+    const float a = __builtin_fabsf(v);
+    float q = a * inv;
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, a), inv, q);
+    const float rest = __builtin_fmaf(-q, s, a);
+    uint32_t b = __float_as_uint(q);
+    const uint32_t towards = rest > 0.0f ? b + 1 : b - 1;      // rest < 0 only where q > 0
+    b = rest != 0.0f && (b & 1) == 0 ? towards : b;
+    return __builtin_copysignf(__uint_as_float(b), v);
+}
+
+// Codes of four values.  With a NaN scale they are some E4M3 numbers: what is multiplied with that
+// scale is NaN whatever they are.
+__device__ __forceinline__ uint32_t block_codes4(float a, float b, float c, float d, float s, float inv) {
+    return e4m3_pack4(block_quotient(a, s, inv), block_quotient(b, s, inv), block_quotient(c, s, inv),
+                      block_quotient(d, s, inv));
+}
+// largest magnitude, as bits, of eight BF16 values
+__device__ __forceinline__ uint32_t bf16_amax_bits(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t h = w[i] & 0x7FFF0000u, l = (w[i] << 16) & 0x7FFF0000u;
+        hi = hi > h ? hi : h;
+        lo = lo > l ? lo : l;
+    }
+    return hi > lo ? hi : lo;
+}
+__device__ __forceinline__ uint2 block_codes8(uint4 v, float s, float inv) {
+    return make_uint2(block_codes4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y), s, inv),
+                      block_codes4(bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w), s, inv));
+}
+// maximum over the 16 lanes of a DPP row, in all of them
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    auto turn = [](uint32_t x, auto ctrl) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xF, 0xF, true);
+    };
+    uint32_t o;
+    o = turn(v, std::integral_constant<int, 0x128>()); v = v > o ? v : o;
+    o = turn(v, std::integral_constant<int, 0x124>()); v = v > o ? v : o;
+    o = turn(v, std::integral_constant<int, 0x122>()); v = v > o ? v : o;
+    o = turn(v, std::integral_constant<int, 0x121>()); v = v > o ? v : o;
+    return v;
+}
+
+}  // namespace
+}  // namespace moe

@@ -1,6 +1,5 @@
 // block_api.cpp -- C entry points around the routed expert layer (include/moe.h): 4-bit
 // weights, the router and the norms.  Checks of arguments and launches only.
-#include <atomic>
 #include <cmath>
 
 #include "../../include/moe.h"
@@ -26,6 +25,12 @@ moe_status_t moe_prepare_weights(moe_plan_t p, const void* w13, const void* w2, 
         if (launch_mxfp4_pack(g, s) != hipSuccess) return MOE_ERR_HIP;
         return MOE_OK;
     }
+    if (c.precision == MOE_FP8_BLOCK128) {
+        if (!aligned16(w13) || !aligned16(w2) || !aligned16(w13_q) || !aligned16(w13_s) || !aligned16(w2_q) || !aligned16(w2_s))
+            return MOE_ERR_INVALID_ARG;
+        const Block128Pair g{{block128(w13, w13_q, w13_s, c.E, 2 * c.I, c.d), block128(w2, w2_q, w2_s, c.E, c.d, c.I)}};
+        return launch_block128_pack(g, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    }
     // block-major scales (the layout the MXFP8 GEMMs copy from)
     if (launch_quantize_mxfp8(static_cast<const uint16_t*>(w13), (int64_t)c.E * 2 * c.I, c.d, w13_q, w13_s,
                               true, s) != hipSuccess)
@@ -39,24 +44,16 @@ moe_status_t moe_prepare_weights(moe_plan_t p, const void* w13, const void* w2, 
 moe_status_t moe_expand_weights(moe_plan_t p, const moe_weights_t* w, void* w13, void* w2, void* stream) {
     if (!p || !w || !w13 || !w2 || !w->w13 || !w->w2 || !w->w13_scale || !w->w2_scale) return MOE_ERR_INVALID_ARG;
     const moe_config_t& c = p->cfg;
-    if (c.precision != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
+    if (c.precision != MOE_MXFP4 && c.precision != MOE_FP8_BLOCK128) return MOE_ERR_UNSUPPORTED;
     if (!aligned16(w->w13) || !aligned16(w->w2) || !aligned16(w->w13_scale) || !aligned16(w->w2_scale) || !aligned16(w13) ||
         !aligned16(w2))
         return MOE_ERR_INVALID_ARG;
+    if (c.precision == MOE_FP8_BLOCK128) {
+        const Block128Pair b{{block128(w13, w->w13, w->w13_scale, c.E, 2 * c.I, c.d), block128(w2, w->w2, w->w2_scale, c.E, c.d, c.I)}};
+        return launch_block128_expand(b, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    }
     const Mxfp4Args g{{mxfp4_w13(w13, w->w13, w->w13_scale, c.E, c.I, c.d), mxfp4_w2(w2, w->w2, w->w2_scale, c.E, c.I, c.d)}};
     return launch_mxfp4_expand(g, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
-}
-
-// compute units of the current device, looked up once per device
-static int device_cus() {
-    constexpr int kDevices = 64;
-    static std::atomic<int> known[kDevices];
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
-    if (dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
-    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
-    return n;
 }
 
 static moe_status_t router_check(const moe_router_config_t* c) {

@@ -210,72 +210,6 @@ __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], const void
     }
 }
 
-// The routed entries sorted by expert, in groups of at most 16 entries of one expert.
-constexpr int kRows = 16, kHalf = 8;
-struct Sorted4 {
-    int cnt[256];                    // entries per expert, a byte for each of the four waves
-    int ids[kMaxDecodeRows];         // for the routing flags
-    int pfx[257];                    // entries of expert e: ent[pfx[e] .. pfx[e + 1])
-    int ent[kMaxDecodeRows];         // ascending within an expert
-    uint16_t group[256 + kMaxDecodeRows / kRows];   // expert | number of the group << 8, ascending
-    int wsum[kWaves];
-    int groups;
-};
-// Every workgroup sorts for itself; the one with `report` sets the routing flags.  An entry's rank
-// among its expert's comes from a ballot for each bit of the id, which finds the wave's entries
-// of the same expert, and the counts of the waves before.  (Comparing with every earlier entry,
-// up to 255, made W13 and W2 of 32 tokens 4.3 and 8.2 us longer.)
-__device__ __forceinline__ void sort_entries(Sorted4& sm, const DecodeArgs& g, bool report) {
-    static_assert(kThreads == 256 && kMaxDecodeRows == 256, "a thread for each expert and entry");
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, R = g.T * g.k;
-    const int id = tid < R ? g.ids[tid] : -1;
-    const int e = (unsigned)id < (unsigned)g.E ? id : -1;
-    sm.cnt[tid] = 0;
-    if (report) sm.ids[tid] = e;
-    __syncthreads();
-    uint64_t same = __ballot(e >= 0);
-#pragma unroll
-    for (int bit = 1; bit < 256; bit <<= 1) {
-        const uint64_t ones = __ballot((e & bit) != 0);
-        same &= (e & bit) != 0 ? ones : ~ones;
-    }
-    const int rank = __popcll(same & lanemask_lt());
-    if (e >= 0 && rank == 0) atomicAdd(&sm.cnt[e], (int)((uint32_t)__popcll(same) << (8 * wave)));   // at most 64
-    if (report && tid < R) {
-        int bad = e >= 0 ? 0 : kDevIdOutOfRange;
-        const int t = tid / g.k, j = tid - t * g.k;
-        for (int jj = 0; jj < j; ++jj)
-            if (e >= 0 && sm.ids[t * g.k + jj] == e) bad |= kDevIdDuplicate;
-        if (bad) atomicOr(g.status, bad);
-    }
-    __syncthreads();
-    // thread tid for expert tid: prefix sums of the entries and (in the upper half) the groups
-    auto bytes = [](uint32_t w) { return (int)((w & 0xFF) + (w >> 8 & 0xFF) + (w >> 16 & 0xFF) + (w >> 24)); };
-    const int count = bytes((uint32_t)sm.cnt[tid]);
-    const int own = count | (count + kRows - 1) / kRows << 16;
-    int incl = own;
-    for (int off = 1; off < MOE_WAVE; off <<= 1) {
-        const int v = __shfl_up(incl, off, MOE_WAVE);
-        if (lane >= off) incl += v;
-    }
-    if (lane == MOE_WAVE - 1) sm.wsum[wave] = incl;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) incl += sm.wsum[w];
-    const int before = incl - own;
-    sm.pfx[tid] = before & 0xFFFF;
-    for (int i = 0; i < own >> 16; ++i) sm.group[(before >> 16) + i] = (uint16_t)(tid | i << 8);
-    if (tid == 255) {
-        sm.pfx[256] = incl & 0xFFFF;
-        sm.groups = incl >> 16;
-    }
-    __syncthreads();
-    if (e >= 0) {
-        const uint32_t earlier = wave > 0 ? (uint32_t)sm.cnt[e] & ((1u << (8 * wave)) - 1) : 0u;
-        sm.ent[sm.pfx[e] + bytes(earlier) + rank] = tid;
-    }
-    __syncthreads();
-}
-
 // The items (group of entries, kTiles row tiles) of this workgroup, its number in the launch and
 // every (number of workgroups)-th; store(entries, how many, row tile, sums) by the wave that has
 // added up the tile's four partial sums, in wave order.  row(entry): byte offset of its operand
@@ -283,8 +217,9 @@ __device__ __forceinline__ void sort_entries(Sorted4& sm, const DecodeArgs& g, b
 // 8 .. 15 of the same loads and MFMAs, and store adds the two halves of the sums; groups of more
 // entries have a second set of operands.  (W2 in groups of 8 entries throughout: 256 entries of 8
 // experts, d = 4096, I = 1024, 50.8 us a call against 48.4; without remainders 43.5.)
+constexpr int kHalf = 8;
 template <bool kRest, typename Row, typename Store>
-__device__ __forceinline__ void run_items(const Sorted4& sm, Partials4& part, const void* codes, const void* words,
+__device__ __forceinline__ void run_items(const Sorted& sm, Partials4& part, const void* codes, const void* words,
                                           __amdgpu_buffer_rsrc_t ars, int rest_bytes, int nblk, int S, Row&& row, Store&& store) {
     const int lane = threadIdx.x & 63, n = lane & 15, word_bytes = (S + 3) / 4 * 256;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -322,7 +257,7 @@ __device__ __forceinline__ void run_items(const Sorted4& sm, Partials4& part, co
 
 template <int kAct>
 __global__ __launch_bounds__(kThreads, kWGs) void decode4_w13(DecodeArgs g) {
-    __shared__ Sorted4 sm;
+    __shared__ Sorted sm;
     __shared__ Partials4 part;
     sort_entries(sm, g, blockIdx.x == 0);
     run_items<false>(sm, part, g.w13, g.w13_scale, rows_rsrc(g.x, (uint32_t)g.T * g.d * 2u), 0, g.I / 8, g.d / 128,
@@ -331,7 +266,7 @@ __global__ __launch_bounds__(kThreads, kWGs) void decode4_w13(DecodeArgs g) {
 }
 
 __global__ __launch_bounds__(kThreads, kWGs) void decode4_w2(DecodeArgs g) {
-    __shared__ Sorted4 sm;
+    __shared__ Sorted sm;
     __shared__ Partials4 part;
     sort_entries(sm, g, false);
     float* o = reinterpret_cast<float*>(g.o);
@@ -443,7 +378,10 @@ hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
         return hipGetLastError();
     }
     const hipError_t e = launch_items(decode4_w2, g, g.d / 16, num_cu, s);
-    if (e != hipSuccess) return e;
+    return e != hipSuccess ? e : launch_decode4_combine(g, s);
+}
+
+hipError_t launch_decode4_combine(const DecodeArgs& g, hipStream_t s) {
     hipLaunchKernelGGL(decode4_combine, dim3((g.d / 4 + MOE_WAVE - 1) / MOE_WAVE, g.T), dim3(MOE_WAVE), 0, s, g);
     return hipGetLastError();
 }

@@ -1,0 +1,428 @@
+// gemm_block128.hip -- grouped products of E4M3 operands with one FP32 scale per 128 (rows) and per
+// 128 x 128 (weights) on gfx950:
+//
+//   D[r][n] = sum over groups g of 128 of K   xs[g][r] ws_e[n/128][g]  sum_k P_e[n][k] Q[r][k]
+//
+// for the rows r of each expert e (m_indptr), P_e its matrix of codes [Np, K] and Q the rows' codes:
+//
+//   mode       P                          Q                      K    output
+//   B128_W13   W13_e, gate/up row pairs   xq[gather[r]]          d    a = f(g) u quantized along I: codes [R, I],
+//                                                                     scales [I/128, R]
+//   B128_PLAIN rows of a matrix           routed rows            Kp   BF16 [R, Np]: W2, and a product's forward
+//                                                                     and input gradient
+//
+// The inner sum is one v_mfma_f32_16x16x128_f8f6f4 with a zero third operand; its four results a
+// lane are multiplied with their scale and added in FP32.  The rows are the instruction's columns: a
+// lane's results belong to one row, and to one 128 x 128 square of P, so that they share one factor.
+// The vector unit's four FMAs take half the time of the instruction.  Accumulators are operands of
+// the vector unit and lie in its registers, which limits a wave to 128 x 64 outputs (the MXFP8
+// products, whose scales the matrix unit applies, have 128 x 128).
+//
+// Workgroup tile 256 (P) x TQ (rows), waves of 128 x 64, a stage of 128 K in LDS while the next one
+// is copied into the other buffer by direct global-to-LDS copies, one continuous stream of stages per
+// workgroup over its tiles (the next tile's first stage is copied during the last of this one).
+// LDS rows are 128 bytes, 16-byte chunk c of row r at slot c ^ (r & 7): eight consecutive rows' same
+// chunks meet all banks once.
+#include "block128.h"
+
+namespace moe {
+namespace {
+
+constexpr int TP = 256, TK = 128;
+constexpr int kPBytes = TP * TK;
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// Order of an expert's tiles: as in the MXFP8 products, groups of kQGroup row tiles, inside a group
+// the P tiles with the group's row tiles fastest, so that the tiles that an XCD runs at a time share
+// operands in its L2.
+constexpr int kQGroup = 6;
+__device__ __forceinline__ void tile_order(int local, int nQt, int nPt, int& pt, int& qt) {
+    const int gi = local / (kQGroup * nPt);
+    const int rem = local - gi * kQGroup * nPt;
+    const int left = nQt - gi * kQGroup;
+    const int gsz = left < kQGroup ? left : kQGroup;
+    pt = rem / gsz;
+    qt = gi * kQGroup + (rem - pt * gsz);
+}
+
+struct Tile {
+    int e, mb, rows, pt, qt;
+};
+
+template <int MODE, int kAct, int TQ>
+__global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs g) {
+    constexpr int kWaves = TQ / 64 * 2, kThr = kWaves * MOE_WAVE;
+    constexpr int kBuf = kPBytes + TQ * TK;              // a stage: P then Q
+    constexpr int kSlot = TQ * 4 + 256;                  // its scales: TQ words of Q, 64 of P
+    constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = TQ * TK / 1024 / kWaves;   // of 1 KiB a wave
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf];
+    __shared__ __attribute__((aligned(1024))) char lsc[2 * kSlot];
+    __shared__ uint32_t tops[2][TQ];                     // B128_W13: magnitudes of a row's two halves
+    __shared__ int cum[257], mptr[257];
+    __shared__ int gsrc[2][TQ];                          // B128_W13: tokens of the next two tiles' rows
+    __shared__ int wtot[4];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wp = wave & 1, wq = wave >> 1;
+    const int E = g.E, K = g.K, groups = K / TK;
+    const int nPt = MODE == B128_W13 ? g.Np / 128 : (g.Np + TP - 1) / TP;
+    const int prows = MODE == B128_W13 ? 2 * g.Np : g.Np;        // P rows of an expert
+
+    // ---- tiles of expert e are cum[e] .. cum[e+1]-1
+    for (int i = tid; i <= E; i += kThr) mptr[i] = g.m_indptr ? g.m_indptr[i] : i == 0 ? 0 : (int)g.R;
+    __syncthreads();
+    if (g.check) {
+        const bool bad = tid <= E && (tid == 0 ? mptr[0] != 0 : mptr[tid] < mptr[tid - 1] || mptr[tid] > (int)g.R);
+        if (__syncthreads_or(bad)) {
+            if (blockIdx.x == 0 && tid == 0 && g.status) atomicOr(g.status, kDevBadIndptr);
+            return;
+        }
+    }
+    if (tid < 256) {
+        int incl = tid < E ? (mptr[tid + 1] - mptr[tid] + TQ - 1) / TQ * nPt : 0;
+        for (int off = 1; off < MOE_WAVE; off <<= 1) {
+            const int u = __shfl_up(incl, off, MOE_WAVE);
+            if (lane >= off) incl += u;
+        }
+        if (lane == MOE_WAVE - 1) wtot[wave] = incl;
+        cum[tid + 1] = incl;
+    }
+    if (tid == 0) cum[0] = 0;
+    __syncthreads();
+    if (tid < 256)
+        for (int w = 0; w < wave; ++w) cum[tid + 1] += wtot[w];
+    __syncthreads();
+    const int total = cum[E], G = gridDim.x;
+    const int vid = (G % 8 == 0) ? (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8) : (int)blockIdx.x;
+    if (vid >= total) return;
+
+    auto coords = [&](int tile) {
+        // largest e with cum[e] <= tile = number of e in [1, E) with cum[e] <= tile
+        int lo = 0;
+#pragma unroll
+        for (int base = 1; base < 257; base += 64) {
+            const int e = base + lane;
+            lo += __builtin_popcountll(__ballot(e < E && cum[e] <= tile));
+        }
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        Tile c;
+        c.e = lo;
+        c.mb = __builtin_amdgcn_readfirstlane(mptr[lo]);
+        c.rows = __builtin_amdgcn_readfirstlane(mptr[lo + 1]) - c.mb;
+        tile_order(tile - __builtin_amdgcn_readfirstlane(cum[lo]), (c.rows + TQ - 1) / TQ, nPt, c.pt, c.qt);
+        return c;
+    };
+    // row of P behind tile row r (clamped to the last)
+    auto p_row = [&](const Tile& c, int r) {
+        if constexpr (MODE == B128_W13) {
+            // 16-row pieces: gate rows 128 pt + 16 j .., then the up rows of the same outputs
+            const int i = c.pt * 128 + (r >> 5) * 16 + (r & 15);
+            return (r & 16) ? g.Np + i : i;
+        } else {
+            const int p = c.pt * TP + r;
+            return p < g.Np ? p : g.Np - 1;
+        }
+    };
+    // routed row behind tile row r (clamped to the expert's last)
+    auto routed_row = [&](const Tile& c, int r) {
+        const int rr = c.qt * TQ + r;
+        return c.mb + (rr < c.rows ? rr : c.rows - 1);
+    };
+
+    // ------------------------------------------------------------ copies
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds;
+    const uint32_t lsc0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lsc;
+    auto dma16 = [&](uint32_t dst, uint32_t voff, const char* base) {
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :: "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(base) : "memory");
+    };
+    auto dma4 = [&](uint32_t dst, uint32_t voff, const char* base) {
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2"
+                     :: "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(base) : "memory");
+    };
+    // A wave copies the tokens of the rows whose data it copies itself, a tile ahead.
+    auto gather_dma = [&](const Tile& c, int slot) {
+        if constexpr (MODE == B128_W13) {
+            const int r = 8 * kQCopies * wave + lane % (8 * kQCopies);
+            const uint32_t dst = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) int*)&gsrc[slot][8 * kQCopies * wave];
+            if (lane < 8 * kQCopies) dma4(dst, (uint32_t)routed_row(c, r) * 4u, reinterpret_cast<const char*>(g.gather));
+        }
+    };
+    // Data: a wave copies consecutive 1 KiB pieces of either operand; lane l fetches 16 bytes that land
+    // at piece + 16 l = row l / 8 of the piece, slot l % 8.  Scales: waves 0 .. TQ/64 - 1 one word
+    // each of 64 rows, the others the words of the two squares of P that the tile meets.
+    uint32_t pvoff[kPCopies], qvoff[kQCopies], svoff;
+    const char *pbase = nullptr, *qbase = nullptr, *sbase = nullptr;
+    const bool q_scales = wave < TQ / 64;
+    size_t sstep = 0;                                    // bytes between the scales of consecutive groups
+    auto copy_offsets = [&](const Tile& c, int slot) {
+        const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
+#pragma unroll
+        for (int j = 0; j < kPCopies; ++j)
+            pvoff[j] = (uint32_t)p_row(c, 8 * (kPCopies * wave + j) + (lane >> 3)) * (uint32_t)K + chunk;
+#pragma unroll
+        for (int j = 0; j < kQCopies; ++j) {
+            const int r = 8 * (kQCopies * wave + j) + (lane >> 3);
+            const int src = MODE == B128_W13 ? gsrc[slot][r] : routed_row(c, r) - (c.mb + c.qt * TQ);
+            qvoff[j] = (uint32_t)src * (uint32_t)K + chunk;
+        }
+        qbase = reinterpret_cast<const char*>(g.qq);
+        if constexpr (MODE != B128_W13) qbase += (size_t)(c.mb + c.qt * TQ) * K;
+        pbase = reinterpret_cast<const char*>(g.pq + (size_t)c.e * prows * K);
+        if (q_scales) {
+            svoff = (uint32_t)routed_row(c, 64 * wave + lane) * 4u;
+            sbase = reinterpret_cast<const char*>(g.qs);
+            sstep = (size_t)g.R * 4;
+        } else {
+            int b = MODE == B128_W13 ? (lane & 1) * (g.Np / 128) + c.pt : 2 * c.pt + (lane & 1);
+            if (b >= prows / 128) b = prows / 128 - 1;
+            svoff = (uint32_t)(b * groups) * 4u;
+            sbase = reinterpret_cast<const char*>(g.ps + (size_t)c.e * (prows / 128) * groups);
+            sstep = 4;
+        }
+    };
+    auto dma_p = [&](int kt, int buf, int j) {
+        dma16(lds0 + buf * kBuf + (kPCopies * wave + j) * 1024, pvoff[j], pbase + kt * TK);
+    };
+    auto dma_q = [&](int kt, int buf, int j) {
+        dma16(lds0 + buf * kBuf + kPBytes + (kQCopies * wave + j) * 1024, qvoff[j], qbase + kt * TK);
+    };
+    auto dma_scales = [&](int kt, int buf) {
+        dma4(lsc0 + buf * kSlot + (q_scales ? 256 * wave : TQ * 4), svoff, sbase + kt * sstep);
+    };
+
+    // ------------------------------------------------------------ a stage
+    const int row16 = lane & 15, quad = lane >> 4;
+    // a fragment: 16 rows, lane (row16, quad) the chunks 2 quad and 2 quad + 1 of its row
+    const int c0 = ((2 * quad) ^ (row16 & 7)) * 16, c1 = ((2 * quad + 1) ^ (row16 & 7)) * 16;
+    const int poff = (wp * 128 + row16) * TK, qoff = kPBytes + (wq * 64 + row16) * TK;
+    auto read_frag = [&](const char* row) {
+        const i32x4_t x = *reinterpret_cast<const i32x4_t*>(row + c0);
+        const i32x4_t y = *reinterpret_cast<const i32x4_t*>(row + c1);
+        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    f32x4_t acc[8][4];
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    auto stage = [&](int buf, int next_kt) {
+        const char* base = lds + buf * kBuf;
+        const float* sc = reinterpret_cast<const float*>(lsc + buf * kSlot);
+        i32x8_t qf[4], pf = read_frag(base + poff);
+        float f0[4], f1[4];                              // factors; B128_W13: of gate and up rows
+        const float s0 = sc[TQ + (MODE == B128_W13 ? 0 : wp)], s1 = sc[TQ + 1];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            qf[b] = read_frag(base + qoff + b * 16 * TK);
+            const float sq = sc[wq * 64 + b * 16 + row16];
+            f0[b] = sq * s0;
+            f1[b] = MODE == B128_W13 ? sq * s1 : f0[b];
+        }
+        dma_scales(next_kt, buf ^ 1);
+        f32x4_t part[4];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) {
+            i32x8_t pn = a < 7 ? read_frag(base + poff + (a + 1) * 16 * TK) : pf;
+            f32x4_t now[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                now[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[b], zero, 0, 0, 0, 0, 0, 0);
+                // the last fragment's results, while this one's are computed
+                if (a > 0)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        acc[a - 1][b][z] = __builtin_fmaf(part[b][z], (a - 1) & 1 ? f1[b] : f0[b], acc[a - 1][b][z]);
+            }
+            // neither the instructions nor the FMAs have an ordering edge to anything here and would
+            // be emitted all together: an empty asm that takes their results keeps them in this step
+            asm volatile("" :: "v"(now[0]), "v"(now[1]), "v"(now[2]), "v"(now[3]));
+            if (a > 0) asm volatile("" : "+v"(acc[a - 1][0]), "+v"(acc[a - 1][1]), "+v"(acc[a - 1][2]), "+v"(acc[a - 1][3]));
+            if (a < kPCopies) dma_p(next_kt, buf ^ 1, a);
+            if (a < kQCopies) dma_q(next_kt, buf ^ 1, a);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) part[b] = now[b];
+            pf = pn;
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) acc[7][b][z] = __builtin_fmaf(part[b][z], f1[b], acc[7][b][z]);
+    };
+
+    // ------------------------------------------------------------ epilogues
+    // buf: the buffer that the tile's last stage has been read from
+    auto epilogue_w13 = [&](const Tile& c, int buf) {
+        // a = f(g) u: fragments 2 m hold gate values, 2 m + 1 the up values of the same outputs,
+        // i = 128 pt + 64 wp + 16 m + 4 quad + z of row 64 wq + 16 b + row16
+        char* stg = lds + buf * kBuf;                    // codes [TQ][128], chunks as the stages'
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float v = act_f<kAct>(acc[2 * m][b][z]) * acc[2 * m + 1][b][z];
+                    acc[2 * m][b][z] = v;
+                    const uint32_t t = __float_as_uint(v) & 0x7FFFFFFFu;
+                    top = top > t ? top : t;
+                }
+#pragma unroll
+            for (int o = 16; o < 64; o <<= 1) {
+                const uint32_t t = __shfl_xor(top, o, MOE_WAVE);
+                top = top > t ? top : t;
+            }
+            if (lane < 16) tops[wp][wq * 64 + b * 16 + row16] = top;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int r = wq * 64 + b * 16 + row16;
+            const uint32_t t0 = tops[0][r], t1 = tops[1][r];
+            const float s = block_scale(t0 > t1 ? t0 : t1), inv = 1.0f / s;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                *reinterpret_cast<uint32_t*>(stg + r * 128 + (((4 * wp + m) ^ (r & 7)) * 16) + 4 * quad) =
+                    block_codes4(acc[2 * m][b][0], acc[2 * m][b][1], acc[2 * m][b][2], acc[2 * m][b][3], s, inv);
+            const int rr = c.qt * TQ + r;
+            if (wp == 0 && quad == 0 && rr < c.rows) g.as[(size_t)c.pt * g.R + c.mb + rr] = s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int it = 0; it < TQ / (8 * kWaves); ++it) {
+            const int r = (it * kWaves + wave) * 8 + (lane >> 3), ch = lane & 7, rr = c.qt * TQ + r;
+            const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((ch ^ (r & 7)) * 16));
+            if (rr < c.rows) *reinterpret_cast<uint4*>(g.aq + (size_t)(c.mb + rr) * g.Np + c.pt * 128 + ch * 16) = v;
+        }
+    };
+    auto epilogue_plain = [&](const Tile& c, int buf) {
+        // BF16 rows by way of this wave's 8 KiB of the buffer, stored as whole 256-byte pieces
+        // past the caches (ordinary stores evict operands that the XCD's workgroups share)
+        char* stg = lds + buf * kBuf + wave * 8192;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int bb = 0; bb < 2; ++bb)
+#pragma unroll
+                for (int a = 0; a < 8; ++a) {
+                    const f32x4_t v = acc[a][2 * h + bb];
+                    const int r = bb * 16 + row16, c16 = 2 * a + (quad >> 1);
+                    *reinterpret_cast<uint2*>(stg + r * 256 + ((c16 ^ (r & 15)) * 16) + 8 * (quad & 1)) =
+                        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int r = 4 * it + quad, c16 = row16;
+                const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 256 + ((c16 ^ (r & 15)) * 16));
+                const int rr = c.qt * TQ + wq * 64 + h * 32 + r, p = c.pt * TP + wp * 128 + 8 * c16;
+                if (rr < c.rows && p < g.Np) store_nt(g.out + (size_t)(c.mb + rr) * g.Np + p, v);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
+
+    // ------------------------------------------------------------ stream of stages
+    // Every stage ends with a wait for all of the wave's copies and a barrier: the next one has landed,
+    // and the buffer just read may be copied into.
+    int l_tile = vid, l_kt = 0, gslot = 0;               // the load cursor
+    Tile lc = coords(l_tile), nc = lc;
+    gather_dma(lc, 0);
+    if (l_tile + G < total) { nc = coords(l_tile + G); gather_dma(nc, 1); }
+    if constexpr (MODE == B128_W13) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    copy_offsets(lc, 0);
+    auto advance_load = [&]() {
+        if (++l_kt < groups) return;
+        if (l_tile + G >= total) { l_kt = groups - 1; return; }      // past the end: the last stage again
+        // the new tile's tokens were copied at the last switch, at least a stage's wait ago
+        l_kt = 0;
+        l_tile += G;
+        gslot ^= 1;
+        lc = nc;
+        copy_offsets(lc, gslot);
+        if (l_tile + G < total) { nc = coords(l_tile + G); gather_dma(nc, gslot ^ 1); }
+    };
+    dma_scales(0, 0);
+#pragma unroll
+    for (int j = 0; j < kPCopies; ++j) dma_p(0, 0, j);
+#pragma unroll
+    for (int j = 0; j < kQCopies; ++j) dma_q(0, 0, j);
+    advance_load();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+
+    Tile cc = coords(vid);
+    int buf = 0;
+    for (int c_tile = vid;;) {
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) acc[a][b] = zero;
+        for (int kt = 0; kt < groups; ++kt) {
+            stage(buf, l_kt);
+            advance_load();
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            buf ^= 1;
+        }
+        if constexpr (MODE == B128_W13) epilogue_w13(cc, buf ^ 1);
+        else epilogue_plain(cc, buf ^ 1);
+        c_tile += G;
+        if (c_tile >= total) break;
+        __syncthreads();                                 // the staging rows are copied into again
+        cc = coords(c_tile);
+    }
+}
+
+template <int MODE, int kAct, int TQ> hipError_t launch_t(const Block128GemmArgs& g, int num_cu, hipStream_t s) {
+    const int64_t nPt = MODE == B128_W13 ? g.Np / 128 : (g.Np + TP - 1) / TP;
+    int64_t grid = (g.R / TQ + (g.E < g.R ? g.E : g.R)) * nPt;       // tiles, at most
+    grid = grid < num_cu ? grid : num_cu;
+    if (grid >= 8) grid -= grid % 8;
+    hipLaunchKernelGGL((grouped_gemm_b128<MODE, kAct, TQ>), dim3((unsigned)(grid < 1 ? 1 : grid)), dim3(TQ * 2), 0, s, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_block128(Block128Mode mode, const Block128GemmArgs& g, int num_cu, hipStream_t s) {
+    if (g.E <= 0 || g.E > 256 || (!g.m_indptr && g.E != 1) || g.R < 0 || g.R > 0x7FFFFFFF || g.K <= 0 || g.K % 128 != 0 || g.Np <= 0 || g.Np % 128 != 0) return hipErrorInvalidValue;
+    if (g.R == 0) return hipSuccess;
+    if (mode == B128_PLAIN) return launch_t<B128_PLAIN, kActSwiGLU, 256>(g, num_cu, s);
+    if (g.act == kActGeGLU) return launch_t<B128_W13, kActGeGLU, 256>(g, num_cu, s);
+    if (g.act == kActReGLU) return launch_t<B128_W13, kActReGLU, 256>(g, num_cu, s);
+    return launch_t<B128_W13, kActSwiGLU, 256>(g, num_cu, s);
+}
+
+// The layer's forward: x in 8 bits with its scales by routed row, W13, W2
+hipError_t launch_layer_block128(MxMode mode, const MxGemmArgs& g, int num_cu, hipStream_t s) {
+    const int64_t R = (int64_t)g.T * g.k;
+    if (mode == MX_QUANT_X) {
+        uint8_t* xq = const_cast<uint8_t*>(g.xq);
+        float* xs = reinterpret_cast<float*>(const_cast<uint8_t*>(g.xs));
+        if (!g.xs_rows) return launch_block128_rows(g.x, R, g.d, xq, xs, true, g.m_indptr + g.E, s);
+        const hipError_t e = launch_block128_rows(g.x, g.T, g.d, xq, reinterpret_cast<float*>(g.xs_rows), false, nullptr, s);
+        // (the scales of 128 values are a word, as four MX scales are)
+        return e != hipSuccess ? e : launch_route_scales(g.xs_rows, g.T, g.gather, R, g.d, const_cast<uint8_t*>(g.xs), s);
+    }
+    Block128GemmArgs b{};
+    b.E = g.E; b.R = R; b.m_indptr = g.m_indptr; b.act = g.act;
+    if (mode == MX_W13) {
+        b.K = g.d; b.Np = g.I; b.gather = g.gather;
+        b.pq = g.w13q; b.ps = reinterpret_cast<const float*>(g.w13s);
+        b.qq = g.xq; b.qs = reinterpret_cast<const float*>(g.xs);
+        b.aq = g.aq; b.as = reinterpret_cast<float*>(g.as);
+        return launch_gemm_block128(B128_W13, b, num_cu, s);
+    }
+    if (mode != MX_W2) return hipErrorInvalidValue;
+    b.K = g.I; b.Np = g.d;
+    b.pq = g.w2q; b.ps = reinterpret_cast<const float*>(g.w2s);
+    b.qq = g.aq; b.qs = reinterpret_cast<const float*>(g.as);
+    b.out = g.o;
+    return launch_gemm_block128(B128_PLAIN, b, num_cu, s);
+}
+
+}  // namespace moe

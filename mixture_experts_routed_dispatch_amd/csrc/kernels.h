@@ -70,7 +70,8 @@ hipError_t launch_gemm(GemmMode mode, const GemmArgs& g, int num_cu, hipStream_t
 // MXFP8 forward products (OCP E4M3 codes, E8M0 scale per 32 along K).
 // MX_PLAIN_W13 / MX_WGRAD_W13: MX_PLAIN / MX_WGRAD as a kernel instance of their own (the
 // W13-side backward products), so that traces tell them from the W2 side.
-enum MxMode { MX_W13 = 0, MX_W2 = 1, MX_PLAIN = 2, MX_WGRAD = 3, MX_PLAIN_W13 = 4, MX_WGRAD_W13 = 5 };
+// MX_QUANT_X: x in 8 bits, of layers with weights in blocks of 128 only (see block128 below).
+enum MxMode { MX_W13 = 0, MX_W2 = 1, MX_PLAIN = 2, MX_WGRAD = 3, MX_PLAIN_W13 = 4, MX_WGRAD_W13 = 5, MX_QUANT_X = 6 };
 
 struct MxGemmArgs {
     int T, d, I, E, k;
@@ -105,6 +106,12 @@ struct MxGemmArgs {
     const uint8_t* qs;
     uint16_t* out;
     int accumulate;       // MX_WGRAD: out = bf16(out + bf16(D)) instead of bf16(D)
+    // The forward with weights in blocks of 128 (gemm_block128.hip): MX_QUANT_X, MX_W13 and MX_W2; all
+    // scales are FP32 then, in the same places: xs [d/128, R], as [I/128, R], w13s and w2s
+    // [E, N/128, K/128]
+    int block128;
+    const uint16_t* x;    // MX_QUANT_X: [T, d], or with xs_rows NULL the rows in expert order
+    uint8_t* xs_rows;     // MX_QUANT_X: [T, d/128], the scales by token
 };
 
 hipError_t launch_gemm_mxfp8(MxMode mode, const MxGemmArgs& g, int num_cu, hipStream_t s);
@@ -174,7 +181,17 @@ struct DecodeArgs {
     int act;               // gated activation of decode W13
     const uint8_t* w13_scale;  // MXFP4 weights only: w13 and w2 are codes (mxfp4.hip's layout)
     const uint8_t* w2_scale;
+    // weights in blocks of 128 (the scales above are FP32 then; decode_block128.hip), with T > 1 the
+    // rows in 8 bits and the sorted entries as well
+    int block128;
+    float* a32;            // [T*k, I]
+    uint8_t* xq;           // [T, d]
+    float* xs;             // [T, d/128]
+    uint8_t* aq;           // [T*k, I]
+    float* as;             // [T*k, I/128]
+    void* groups;          // kBlock128GroupBytes
 };
+constexpr size_t kBlock128GroupBytes = 5376;
 
 // With MXFP4 weights W2 is combined into y as well (decode_mxfp4.hip).
 hipError_t launch_decode_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
@@ -219,6 +236,79 @@ inline Mxfp4Matrix mxfp4_w2(const void* w, const void* codes, const void* scales
 // values, then their remainders.
 hipError_t launch_decode4_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
 hipError_t launch_decode4_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
+hipError_t launch_decode4_combine(const DecodeArgs& g, hipStream_t s);
+// The same with weights in blocks of 128, and a product's few rows (R <= kMaxDecodeRows): y [R, N] in
+// BF16 of rows x, in expert order by m_indptr (NULL: one matrix), whose codes go to xq and xs.
+hipError_t launch_decode8_w13(const DecodeArgs& g, int num_cu, hipStream_t s);
+hipError_t launch_decode8_w2(const DecodeArgs& g, int num_cu, hipStream_t s);
+struct Block128RowsArgs {
+    int E, N, K, R;
+    const int32_t* m_indptr;  // [E+1]
+    int32_t* status;          // routing flags, or NULL
+    const uint16_t* x;        // [R, K]
+    const uint8_t* w;         // [E, N, K]
+    const float* ws;          // [E, N/128, K/128]
+    uint16_t* y;              // [R, N]
+    uint8_t* xq;
+    float* xs;                // [R, K/128]
+    void* groups;             // kBlock128GroupBytes
+};
+// Rows that stream the weights instead of going through the grouped products
+inline bool block128_few_rows(int64_t R, int E) { return R <= kMaxDecodeRows && R <= 32 * (int64_t)E; }
+hipError_t launch_block128_few_rows(const Block128RowsArgs& g, int num_cu, hipStream_t s);
+
+// E4M3 codes with one FP32 scale per 128 (block128.hip).  Rows: scales [rows, K/128], or with
+// block_major [K/128, rows]; rows_dev (optional, device): only the first min(rows, *rows_dev) rows.
+// Weights: one scale per 128 x 128, one or two matrices [E, N, K] a launch (w NULL: none).  K and N
+// multiples of 128, tensors 16-byte aligned.
+struct Block128Matrix {
+    uint16_t* w;              // BF16: read by the packing, written by the expansion
+    uint8_t* codes;           // [E, N, K]
+    float* scales;            // [E, N/128, K/128]
+    int64_t units;            // set by the launcher
+    int E, N, K;
+};
+struct Block128Pair {
+    Block128Matrix m[2];
+};
+inline Block128Matrix block128(const void* w, const void* codes, const void* scales, int E, int N, int K) {
+    return {static_cast<uint16_t*>(const_cast<void*>(w)), static_cast<uint8_t*>(const_cast<void*>(codes)),
+            static_cast<float*>(const_cast<void*>(scales)), 0, E, N, K};
+}
+hipError_t launch_block128_rows(const uint16_t* v, int64_t rows, int K, uint8_t* codes, float* scales, bool block_major,
+                                const int32_t* rows_dev, hipStream_t s);
+hipError_t launch_block128_rows_f32(const float* v, int64_t rows, int K, uint8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_block128_pack(Block128Pair g, hipStream_t s);
+hipError_t launch_block128_expand(Block128Pair g, hipStream_t s);
+// m_out [E+1] = m_in, or zeros and (unless NULL) the status flag where it does not rise from 0 to at
+// most R; m_in NULL: 0, R (E = 1)
+hipError_t launch_segments(const int32_t* m_in, int E, int R, int32_t* m_out, int32_t* status, hipStream_t s);
+hipError_t launch_block128_transpose(const uint8_t* codes, const float* scales, int E, int N, int K, uint8_t* codes_t,
+                                     float* scales_t, hipStream_t s);
+
+// Grouped products of such operands (gemm_block128.hip): rows m_indptr[e] .. m_indptr[e+1] with
+// matrix e, E <= 256, K and Np multiples of 128.  Offsets inside one matrix, and in W13 inside the rows'
+// codes, are 32-bit.
+enum Block128Mode { B128_W13 = 0, B128_PLAIN = 1 };
+struct Block128GemmArgs {
+    int E, K, Np;             // Np: outputs, W13: I
+    int64_t R;                // rows of the layouts
+    const int32_t* m_indptr;  // [E+1], or NULL: one matrix, R rows
+    int check;                // 1: m_indptr is the caller's.  Where it does not rise from 0 to at most R,
+    int32_t* status;          // nothing is written and (unless NULL) the flag is set
+    const int32_t* gather;    // W13: [R] the row of qq behind a routed row
+    const uint8_t* pq;        // [E, Np, K]; W13: [E, 2 Np, K]
+    const float* ps;          // [E, .. / 128, K/128]
+    const uint8_t* qq;        // [.., K]
+    const float* qs;          // [K/128, R], by routed row
+    uint16_t* out;            // PLAIN: [R, Np]
+    uint8_t* aq;              // W13: [R, Np] and
+    float* as;                //      [Np/128, R]
+    int act;
+};
+constexpr int kMaxProductRows = 1 << 24;
+hipError_t launch_layer_block128(MxMode mode, const MxGemmArgs& g, int num_cu, hipStream_t s);
+hipError_t launch_gemm_block128(Block128Mode mode, const Block128GemmArgs& g, int num_cu, hipStream_t s);
 
 // block_major: scale word (g, row) (bytes of blocks 4 g .. 4 g + 3) at (g * rows + row) * 4
 // (K a multiple of 128); else scales [rows, K/32].

@@ -164,7 +164,8 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     *out = nullptr;
     const moe_config_t c = *cfg;
     if (c.T < 0 || c.d <= 0 || c.I <= 0 || c.E <= 0 || c.k <= 0) return MOE_ERR_INVALID_ARG;
-    if (c.precision != MOE_BF16 && c.precision != MOE_MXFP8_E4M3 && c.precision != MOE_MXFP4)
+    if (c.precision != MOE_BF16 && c.precision != MOE_MXFP8_E4M3 && c.precision != MOE_MXFP4 &&
+        c.precision != MOE_FP8_BLOCK128)
         return MOE_ERR_INVALID_ARG;
     if (c.training != 0 && c.training != 1) return MOE_ERR_INVALID_ARG;
     if (c.wgrad_accumulate != 0 && c.wgrad_accumulate != 1) return MOE_ERR_INVALID_ARG;
@@ -182,7 +183,9 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     if (c.precision == MOE_MXFP8_E4M3 && (c.d % 256 != 0 || c.I % 128 != 0)) return MOE_ERR_UNSUPPORTED;
     // MXFP4 weights come in tiles of 128 along K and serve inference only
     const bool w4 = c.precision == MOE_MXFP4;
-    if (w4 && (c.training || c.d % 128 != 0 || c.I % 128 != 0)) return MOE_ERR_UNSUPPORTED;
+    // and so do weights in blocks of 128 x 128
+    const bool b128 = c.precision == MOE_FP8_BLOCK128;
+    if ((w4 || b128) && (c.training || c.d % 128 != 0 || c.I % 128 != 0)) return MOE_ERR_UNSUPPORTED;
     // MXFP8 weight gradients address a token-layout operand (features x padded rows) with
     // 32-bit offsets
     if (c.precision == MOE_MXFP8_E4M3 && c.training &&
@@ -194,11 +197,11 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
         return MOE_ERR_UNSUPPORTED;
     // small-batch inference runs the weight-streaming kernels (nvfp4moe README,
     // "MoE layer": batch-one and small-batch decode get their own launch grid)
-    const bool decode_ok = c.training == 0 && (c.precision == MOE_BF16 || w4) && R > 0 &&
+    const bool decode_ok = c.training == 0 && (c.precision == MOE_BF16 || w4 || b128) && R > 0 &&
                            R <= kMaxDecodeRows;
     if (c.path == MOE_PATH_DECODE && !decode_ok) return MOE_ERR_UNSUPPORTED;
     if (c.mega != 0 && c.mega != 1) return MOE_ERR_INVALID_ARG;
-    if (c.mega && (!decode_ok || w4 || c.path == MOE_PATH_PREFILL)) return MOE_ERR_UNSUPPORTED;
+    if (c.mega && (!decode_ok || w4 || b128 || c.path == MOE_PATH_PREFILL)) return MOE_ERR_UNSUPPORTED;
 
     moe_plan_s* p = new (std::nothrow) moe_plan_s();
     if (!p) return MOE_ERR_INVALID_ARG;
@@ -214,12 +217,13 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     p->off_probs = take(sizeof(float) * (size_t)R);
     const bool mx = c.precision == MOE_MXFP8_E4M3;
     const bool mxt = mx && c.training;
+    const bool decode32 = (w4 || b128) && p->decode;
     // a in BF16: the BF16 path's W2 operand; MXFP8 training keeps it for the weight gradient
-    // (the MXFP4 decode keeps the remainder of its rounding as well)
-    p->a_bytes = (w4 && p->decode ? 4 : 2) * (size_t)R * c.I;
-    p->off_a = (!mx || c.training) ? take(p->a_bytes) : 0;
-    // the experts' outputs: BF16, or FP32 in the MXFP4 decode, which rounds y alone
-    p->o_bytes = (w4 && p->decode ? 4 : 2) * (size_t)R * c.d;
+    // (the MXFP4 decode keeps the remainder of its rounding as well; the block-128 one has it in FP32)
+    p->a_bytes = (decode32 ? 4 : 2) * (size_t)R * c.I;
+    p->off_a = (!(mx || b128) || c.training || decode32) ? take(p->a_bytes) : 0;
+    // the experts' outputs: BF16, or FP32 in these decodes, which round y alone
+    p->o_bytes = (decode32 ? 4 : 2) * (size_t)R * c.d;
     p->off_o = take(p->o_bytes);
     const size_t h_bytes = 2 * (size_t)R * 2 * c.I;
     p->off_h = (c.training && !c.recompute_h) ? take(h_bytes) : 0;
@@ -242,11 +246,13 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
             p->off_h = take(h_bytes);
         }
     }
-    p->off_xq = mx ? take((size_t)c.T * c.d) : 0;
-    p->off_xs = mx ? take((size_t)c.T * c.d / 32) : 0;
-    p->off_xsr = mx ? take((size_t)R * c.d / 32) : 0;
-    p->off_aq = mx ? take((size_t)R * c.I) : 0;
-    p->off_as = mx ? take((size_t)R * c.I / 32) : 0;
+    // four E8M0 bytes, or one FP32 scale, for 128 values
+    p->off_xq = mx || b128 ? take((size_t)c.T * c.d) : 0;
+    p->off_xs = mx || b128 ? take((size_t)c.T * c.d / 32) : 0;
+    p->off_xsr = mx || (b128 && !p->decode) ? take((size_t)R * c.d / 32) : 0;
+    p->off_aq = mx || b128 ? take((size_t)R * c.I) : 0;
+    p->off_as = mx || b128 ? take((size_t)R * c.I / 32) : 0;
+    p->off_groups = b128 && p->decode ? take(kBlock128GroupBytes) : 0;
     p->ntok = R + (int64_t)kMxWgradPad * c.E;
     p->tp_feat = (size_t)(c.I > c.d ? c.I : c.d);              // P: a^T (I), then x^T (d)
     p->tq_feat = (size_t)(c.d > 2 * c.I ? c.d : 2 * c.I);      // Q: dO^T (d), then dh^T (2I)
@@ -268,7 +274,7 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
             p->off_h = take(h_bytes);
         }
     }
-    const bool gemms = !mx && !p->decode;
+    const bool gemms = !mx && !b128 && !p->decode;
     p->off_split = take(sizeof(int32_t) * 4 * (kMaxPieces / 2 + 1));
     p->off_part = gemms && c.training ? take(kGemmPartBytes) : 0;
     p->off_mega = c.mega ? take(sizeof(float) * (size_t)R * (c.I / mega_chunk(c.T, c.k)) * c.d) : 0;
@@ -291,7 +297,8 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
     const moe_config_t& c = p->cfg;
     const int64_t R = p->R;
     const bool mx = c.precision == MOE_MXFP8_E4M3;
-    const bool gemms = !mx && !p->decode;
+    const bool b128 = c.precision == MOE_FP8_BLOCK128;
+    const bool gemms = !mx && !b128 && !p->decode;
     std::string out;
     char line[512];
     auto add = [&](const char* fmt, auto... args) {
@@ -299,7 +306,7 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
         out += line;
     };
     add("moe plan: T=%d d=%d I=%d E=%d k=%d, %lld routed rows (T*k), %s, %s, %s path\n", c.T, c.d, c.I, c.E,
-        c.k, (long long)R, mx ? "MXFP8 E4M3" : c.precision == MOE_MXFP4 ? "MXFP4 weights" : "BF16", c.training ? "training" : "inference",
+        c.k, (long long)R, mx ? "MXFP8 E4M3" : c.precision == MOE_MXFP4 ? "MXFP4 weights" : b128 ? "E4M3 with a scale per 128" : "BF16", c.training ? "training" : "inference",
         p->decode ? (c.mega ? "decode (weight-streaming, mega: one fused launch)" : "decode (weight-streaming)")
                   : "grouped-GEMM");
     if (c.training)
@@ -323,7 +330,9 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
     saved_region("gather", sizeof(int32_t) * (size_t)R, "token of each routed row [R]");
     saved_region("slots", sizeof(int32_t) * (size_t)R, "routed row of each (t, j) [T, k]");
     saved_region("probs", sizeof(float) * (size_t)R, "score of each routed row [R]");
-    if (!mx || c.training)
+    if (b128 && p->decode)
+        region("a", p->a_bytes, "scratch", "SwiGLU output [R, I] FP32");
+    else if (!(mx || b128) || c.training)
         saved_region("a", p->a_bytes, mx ? "SwiGLU output [R, I] BF16 (weight-gradient operand)"
                                       : p->a_bytes == 2 * (size_t)R * c.I ? "SwiGLU output [R, I] BF16"
                                                                           : "SwiGLU output [R, I] BF16 and its remainder");
@@ -359,6 +368,14 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
             region("dys", 2 * (size_t)R * c.d, "backward",
                    "probs * dy[gather] [R, d] BF16 (weight-gradient operand)");
         }
+    }
+    if (b128) {
+        region("xq", (size_t)c.T * c.d, "scratch", "E4M3 codes of x [T, d]");
+        region("xs", (size_t)c.T * c.d / 32, "scratch", "FP32 scales of x [T, d/128]");
+        region("xs_routed", p->decode ? 0 : (size_t)R * c.d / 32, "scratch", "scales of x[gather], block-major [d/128, R]");
+        region("aq", (size_t)R * c.I, "scratch", "E4M3 codes of a [R, I]");
+        region("as", (size_t)R * c.I / 32, "scratch", p->decode ? "FP32 scales of a [R, I/128]" : "FP32 scales of a (block-major)");
+        region("groups", p->decode ? kBlock128GroupBytes : 0, "scratch", "routed entries in expert order");
     }
     if (mx) {
         region("xq", (size_t)c.T * c.d, "scratch", "E4M3 codes of x [T, d]");
@@ -448,8 +465,8 @@ moe_status_t moe_prepare_weights_backward(moe_plan_t p, const void* w13, const v
     return MOE_OK;
 }
 
-// the kernels read MXFP4 codes 16 bytes and scales a word at a time
-static bool mxfp4_aligned(const moe_weights_t* w) {
+// the kernels read codes 16 bytes and scales a word at a time
+static bool prepared_aligned(const moe_weights_t* w) {
     auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     return aligned(w->w13) && aligned(w->w2) && aligned(w->w13_scale) && aligned(w->w2_scale);
 }
@@ -459,10 +476,11 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
     if (!p || !w) return MOE_ERR_INVALID_ARG;
     const moe_config_t& c = p->cfg;
     if (c.T > 0 && (!x || !ids || !scores || !y || !w->w13 || !w->w2)) return MOE_ERR_INVALID_ARG;
-    const bool w4 = c.precision == MOE_MXFP4;
-    if (c.T > 0 && (w4 || c.precision == MOE_MXFP8_E4M3) && (!w->w13_scale || !w->w2_scale))
+    const bool w4 = c.precision == MOE_MXFP4, b128 = c.precision == MOE_FP8_BLOCK128;
+    if (c.T > 0 && c.precision != MOE_BF16 && (!w->w13_scale || !w->w2_scale)) return MOE_ERR_INVALID_ARG;
+    if (c.T > 0 && (w4 || b128) && !prepared_aligned(w)) return MOE_ERR_INVALID_ARG;
+    if (c.T > 0 && b128 && (reinterpret_cast<uintptr_t>(x) % 16 != 0 || reinterpret_cast<uintptr_t>(y) % 16 != 0))
         return MOE_ERR_INVALID_ARG;
-    if (c.T > 0 && w4 && !mxfp4_aligned(w)) return MOE_ERR_INVALID_ARG;
     if (!p->ws) return MOE_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     p->have_saved_forward = false;
@@ -483,9 +501,16 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         dg.o = p->at<uint16_t>(p->off_o);
         dg.y = static_cast<uint16_t*>(y);
         dg.status = p->at<int32_t>(p->off_status);
-        if (w4) {
+        if (w4 || b128) {
             dg.w13_scale = w->w13_scale;
             dg.w2_scale = w->w2_scale;
+        }
+        if (b128) {
+            dg.block128 = 1;
+            dg.a32 = p->at<float>(p->off_a);
+            dg.xq = p->at<uint8_t>(p->off_xq); dg.xs = p->at<float>(p->off_xs);
+            dg.aq = p->at<uint8_t>(p->off_aq); dg.as = p->at<float>(p->off_as);
+            dg.groups = p->at<char>(p->off_groups);
         }
         if (c.mega) {
             hipError_t e = staged(p, MOE_STAGE_MEGA, s, [&] {
@@ -495,13 +520,13 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         }
         hipError_t e = staged(p, MOE_STAGE_DECODE_W13, s, [&] { return launch_decode_w13(dg, p->num_cu, s); });
         if (e != hipSuccess) return MOE_ERR_HIP;
-        if (c.T == 1 && !w4) {
+        if (c.T == 1 && !w4 && !b128) {
             e = staged(p, MOE_STAGE_DECODE_W2, s, [&] { return launch_decode_w2_one(dg, p->num_cu, s); });
             return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
         }
         e = staged(p, MOE_STAGE_DECODE_W2, s, [&] { return launch_decode_w2(dg, p->num_cu, s); });
         if (e != hipSuccess) return MOE_ERR_HIP;
-        if (w4) return MOE_OK;                         // combined
+        if (w4 || b128) return MOE_OK;                 // combined
         e = staged(p, MOE_STAGE_COMBINE, s, [&] {
             return launch_combine(dg.o, nullptr, scores, c.T, c.k, c.d, dg.y, s);
         });
@@ -517,20 +542,16 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
     });
     if (e != hipSuccess) return MOE_ERR_HIP;
 
-    if (c.precision == MOE_MXFP8_E4M3) {
+    if (c.precision == MOE_MXFP8_E4M3 || b128) {
         // MXFP8 (blog post "What it is selling": activations quantized after routing,
         // prepared weights): x is quantized per token row, which equals quantizing the
         // gathered rows since every MX block lies inside one row; the scales are then
         // copied out per routed row, block-major, so that a W13 tile's scale words for one
-        // K group are contiguous
+        // K group are contiguous; with weights in blocks of 128 the same, one FP32 scale in the place of
+        // four E8M0 bytes
         uint8_t* xq = p->at<uint8_t>(p->off_xq);
         uint8_t* xs = p->at<uint8_t>(p->off_xs);
         uint8_t* xsr = p->at<uint8_t>(p->off_xsr);
-        e = staged(p, MOE_STAGE_QUANT_X, s, [&] {
-            hipError_t qe = launch_quantize_mxfp8(static_cast<const uint16_t*>(x), c.T, c.d, xq, xs, false, s);
-            return qe != hipSuccess ? qe : launch_route_scales(xs, c.T, gather, p->R, c.d, xsr, s);
-        });
-        if (e != hipSuccess) return MOE_ERR_HIP;
         MxGemmArgs mg{};
         mg.T = c.T; mg.d = c.d; mg.I = c.I; mg.E = c.E; mg.k = c.k;
         mg.act = c.activation;
@@ -540,6 +561,14 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         mg.w2q = static_cast<const uint8_t*>(w->w2); mg.w2s = w->w2_scale;
         mg.aq = p->at<uint8_t>(p->off_aq); mg.as = p->at<uint8_t>(p->off_as);
         mg.o = p->at<uint16_t>(p->off_o);
+        mg.block128 = b128;
+        mg.x = static_cast<const uint16_t*>(x); mg.xs_rows = xs;
+        e = staged(p, MOE_STAGE_QUANT_X, s, [&] {
+            if (b128) return launch_gemm_mxfp8(MX_QUANT_X, mg, p->num_cu, s);
+            hipError_t qe = launch_quantize_mxfp8(static_cast<const uint16_t*>(x), c.T, c.d, xq, xs, false, s);
+            return qe != hipSuccess ? qe : launch_route_scales(xs, c.T, gather, p->R, c.d, xsr, s);
+        });
+        if (e != hipSuccess) return MOE_ERR_HIP;
         if (c.training && !c.recompute_h) {
             // kept for the backward: h for the activation backward, a for dW2
             mg.h_out = p->at<uint16_t>(p->off_h);
@@ -621,9 +650,11 @@ moe_status_t moe_forward_routed(moe_plan_t p, const void* x_rows, const int32_t*
     if (c.training || p->decode) return MOE_ERR_UNSUPPORTED;
     if (p->R * c.d * 2 >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;   // 32-bit row offsets into x_rows
     if (c.T > 0 && (!x_rows || !m_indptr || !out || !w->w13 || !w->w2)) return MOE_ERR_INVALID_ARG;
-    const bool w4 = c.precision == MOE_MXFP4;
-    if (c.T > 0 && (mx || w4) && (!w->w13_scale || !w->w2_scale)) return MOE_ERR_INVALID_ARG;
-    if (c.T > 0 && w4 && !mxfp4_aligned(w)) return MOE_ERR_INVALID_ARG;
+    const bool w4 = c.precision == MOE_MXFP4, b128 = c.precision == MOE_FP8_BLOCK128;
+    if (c.T > 0 && (mx || w4 || b128) && (!w->w13_scale || !w->w2_scale)) return MOE_ERR_INVALID_ARG;
+    if (c.T > 0 && (w4 || b128) && !prepared_aligned(w)) return MOE_ERR_INVALID_ARG;
+    if (c.T > 0 && b128 && (reinterpret_cast<uintptr_t>(x_rows) % 16 != 0 || reinterpret_cast<uintptr_t>(out) % 16 != 0))
+        return MOE_ERR_INVALID_ARG;
     if (!p->ws) return MOE_ERR_WORKSPACE;
     p->have_saved_forward = false;
     p->status_word = p->at<int32_t>(p->off_status);
@@ -635,17 +666,12 @@ moe_status_t moe_forward_routed(moe_plan_t p, const void* x_rows, const int32_t*
         return launch_routed_prep(m_indptr, c.E, p->R, mi, gather, p->at<int32_t>(p->off_status), s);
     });
     if (e != hipSuccess) return MOE_ERR_HIP;
-    if (mx) {
+    if (mx || b128) {
         // the m_indptr[E] rows are quantized as they stand, their scales written
         // block-major over the routed rows (the layout W13 copies); the codes take the
         // `o` region, which W2 does not use here since it writes the caller's rows
         uint8_t* xq = p->at<uint8_t>(p->off_o);
         uint8_t* xsr = p->at<uint8_t>(p->off_xsr);
-        e = staged(p, MOE_STAGE_QUANT_X, s, [&] {
-            return launch_quantize_mxfp8(static_cast<const uint16_t*>(x_rows), p->R, c.d, xq, xsr, true, s,
-                                         mi + c.E);
-        });
-        if (e != hipSuccess) return MOE_ERR_HIP;
         MxGemmArgs mg{};
         mg.T = c.T; mg.d = c.d; mg.I = c.I; mg.E = c.E; mg.k = c.k;
         mg.act = c.activation;
@@ -655,6 +681,14 @@ moe_status_t moe_forward_routed(moe_plan_t p, const void* x_rows, const int32_t*
         mg.w2q = static_cast<const uint8_t*>(w->w2); mg.w2s = w->w2_scale;
         mg.aq = p->at<uint8_t>(p->off_aq); mg.as = p->at<uint8_t>(p->off_as);
         mg.o = static_cast<uint16_t*>(out);
+        mg.block128 = b128;
+        mg.x = static_cast<const uint16_t*>(x_rows);
+        e = staged(p, MOE_STAGE_QUANT_X, s, [&] {
+            if (b128) return launch_gemm_mxfp8(MX_QUANT_X, mg, p->num_cu, s);
+            return launch_quantize_mxfp8(static_cast<const uint16_t*>(x_rows), p->R, c.d, xq, xsr, true, s,
+                                         mi + c.E);
+        });
+        if (e != hipSuccess) return MOE_ERR_HIP;
         e = staged(p, MOE_STAGE_W13, s, [&] { return launch_gemm_mxfp8(MX_W13, mg, p->num_cu, s); });
         if (e != hipSuccess) return MOE_ERR_HIP;
         e = staged(p, MOE_STAGE_W2, s, [&] { return launch_gemm_mxfp8(MX_W2, mg, p->num_cu, s); });

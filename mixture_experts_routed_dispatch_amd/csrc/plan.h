@@ -3,12 +3,25 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <vector>
 
 #include "../../include/moe.h"
 
 constexpr size_t kMaxProfileRecords = 4096;
 constexpr int kMaxExperts = 256;             // nvfp4moe README, "Limits"
+
+// compute units of the current device, looked up once per device
+inline int device_cus() {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
+    if (dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
+    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 struct moe_plan_s {
     moe_config_t cfg;
@@ -23,6 +36,7 @@ struct moe_plan_s {
     size_t tp_feat, tq_feat;           // features of the largest P / Q token-layout operand
     int64_t ntok;                      // token-layout rows: T*k + 128 E
     size_t off_part, off_split;        // split weight-gradient tiles: partial sums, descriptors
+    size_t off_groups;                 // block-128 decode: the entries in expert order
     size_t off_we;                     // MXFP4 on the grouped-GEMM path: a product's weights as BF16
     size_t a_bytes, o_bytes;           // of the regions of W13 outputs and expert outputs
     size_t off_mega;                   // mega decode: FP32 partial expert outputs [T*k, I / chunk, d]

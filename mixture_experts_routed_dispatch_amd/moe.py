@@ -30,6 +30,7 @@ MOE_STATIC_SCRATCH_BYTES = 32 << 20
 MOE_BF16 = 0
 MOE_MXFP8_E4M3 = 1
 MOE_MXFP4 = 2
+MOE_FP8_BLOCK128 = 3
 
 MOE_PATH_AUTO = 0
 MOE_PATH_PREFILL = 1
@@ -50,7 +51,9 @@ EXPORTS = ("moe_plan", "moe_workspace_bytes", "moe_bind_workspace", "moe_plan_de
            "moe_backward", "moe_get_status", "moe_status_string", "moe_profile", "moe_plan_explain",
            "moe_profile_read", "moe_expand_weights",
            "moe_router_workspace_bytes", "moe_router_forward", "moe_router_backward",
-           "moe_norm_workspace_bytes", "moe_norm_forward", "moe_norm_backward")
+           "moe_norm_workspace_bytes", "moe_norm_forward", "moe_norm_backward",
+           "moe_quantize_block128", "moe_product_workspace_bytes", "moe_product_prepare_weights",
+           "moe_product_expand_weights", "moe_product_forward", "moe_product_backward")
 
 STAGES = ("dispatch", "quant_x", "w13", "w2", "combine", "score_grad", "dgrad_w2", "wgrad_w2",
           "dgrad_w13", "wgrad_w13", "dx_combine", "decode_w13", "decode_w2", "wgrad_rows", "recompute_h",
@@ -88,6 +91,11 @@ class NormConfig(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("gate", ctypes.c_int32),
                 ("residual_f32", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("residual_scale", ctypes.c_float)]
+
+
+class ProductConfig(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("training", ctypes.c_int32), ("wgrad_accumulate", ctypes.c_int32)]
 
 
 _lib = None
@@ -143,6 +151,19 @@ def lib():
         L.moe_norm_forward.restype = ctypes.c_int
         L.moe_norm_backward.argtypes = [norm] + [vp] * 13 + [sz, vp]
         L.moe_norm_backward.restype = ctypes.c_int
+        product = ctypes.POINTER(ProductConfig)
+        L.moe_quantize_block128.argtypes = [vp, i64, i32, vp, vp, vp]
+        L.moe_quantize_block128.restype = ctypes.c_int
+        L.moe_product_workspace_bytes.argtypes = [product]
+        L.moe_product_workspace_bytes.restype = sz
+        L.moe_product_prepare_weights.argtypes = [product] + [vp] * 4
+        L.moe_product_prepare_weights.restype = ctypes.c_int
+        L.moe_product_expand_weights.argtypes = [product] + [vp] * 4
+        L.moe_product_expand_weights.restype = ctypes.c_int
+        L.moe_product_forward.argtypes = [product] + [vp] * 7 + [sz, vp]
+        L.moe_product_forward.restype = ctypes.c_int
+        L.moe_product_backward.argtypes = [product] + [vp] * 9 + [sz, vp]
+        L.moe_product_backward.restype = ctypes.c_int
         L.moe_get_status.argtypes = [vp, ctypes.POINTER(i32), i32, vp]
         L.moe_get_status.restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -268,6 +289,33 @@ def moe_norm_backward(cfg: NormConfig, dz, dh, z, y, w_post, gate, w_pre, dx, dy
                                 workspace, workspace_bytes, stream), "moe_norm_backward")
 
 
+def moe_quantize_block128(v, rows, K, codes, scales, stream=0):
+    _ok(lib().moe_quantize_block128(v, rows, K, codes, scales, stream), "moe_quantize_block128")
+
+
+def moe_product_workspace_bytes(cfg: ProductConfig) -> int:
+    return int(lib().moe_product_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_product_prepare_weights(cfg: ProductConfig, w, w_q, w_s, stream=0):
+    _ok(lib().moe_product_prepare_weights(ctypes.byref(cfg), w, w_q, w_s, stream), "moe_product_prepare_weights")
+
+
+def moe_product_expand_weights(cfg: ProductConfig, w_q, w_s, w, stream=0):
+    _ok(lib().moe_product_expand_weights(ctypes.byref(cfg), w_q, w_s, w, stream), "moe_product_expand_weights")
+
+
+def moe_product_forward(cfg: ProductConfig, x, m_indptr, w_q, w_s, y, status, workspace, workspace_bytes, stream=0):
+    _ok(lib().moe_product_forward(ctypes.byref(cfg), x, m_indptr, w_q, w_s, y, status, workspace, workspace_bytes, stream),
+        "moe_product_forward")
+
+
+def moe_product_backward(cfg: ProductConfig, dy, x, m_indptr, w_q, w_s, dx, dw, status, workspace, workspace_bytes,
+                         stream=0):
+    _ok(lib().moe_product_backward(ctypes.byref(cfg), dy, x, m_indptr, w_q, w_s, dx, dw, status, workspace,
+                                   workspace_bytes, stream), "moe_product_backward")
+
+
 def moe_get_status(plan, clear=True, stream=0):
     """Returns (status, device_flags); synchronises the stream."""
     flags = ctypes.c_int32(0)
@@ -321,6 +369,8 @@ class Layer:
     """One plan plus its torch-allocated workspace; all compute goes through libmoe.  Tensors that a
     call makes come from the memory of the stream that writes them (`stream`, else the current one)."""
 
+    _block128 = None                   # shapes of the weights' scales, with MOE_FP8_BLOCK128
+
     def __init__(self, T, d, I, E, k, precision=MOE_BF16, training=False, path=MOE_PATH_AUTO,
                  device="cuda", wgrad_accumulate=False, recompute_h=False, activation=MOE_ACT_SWIGLU,
                  mega=False):
@@ -338,6 +388,8 @@ class Layer:
             self._mxfp4 = ((_dense(E, I * d), _dense(E, 2 * I // 16, (d + 511) // 512, 64, 4)),
                            (_dense(E, d * I // 2), _dense(E, d // 16, (I + 511) // 512, 64, 4)))
             self._mxfp4_sizes = tuple(math.prod(shape) for shape, _ in sum(self._mxfp4, ()))
+        if precision == MOE_FP8_BLOCK128:
+            self._block128 = (E, 2 * I // 128, d // 128), (E, d // 128, I // 128)
         nbytes = moe_workspace_bytes(self.plan)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         moe_bind_workspace(self.plan, _ptr(self.workspace), self.workspace.numel())
@@ -374,6 +426,8 @@ class Layer:
             y = _new(self._rows, torch.bfloat16, x.device, stream)
         if self._mxfp4 is not None:
             self._check_mxfp4(w13, w13_scale, w2, w2_scale, x, ids, scores, y, stream)
+        if self._block128 is not None:
+            self._check_block128(w13, w13_scale, w2, w2_scale, (x, ids, scores, y), stream)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward(self.plan, _ptr(x), _ptr(ids), _ptr(scores), w, _ptr(y), _stream(stream))
         return y
@@ -388,6 +442,8 @@ class Layer:
             out = _new(_dense(self.T * self.k, self.d), torch.bfloat16, x_rows.device, stream)
         if self._mxfp4 is not None:
             self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out, out, stream)
+        if self._block128 is not None:
+            self._check_block128(w13, w13_scale, w2, w2_scale, (x_rows, m_indptr, out), stream)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward_routed(self.plan, _ptr(x_rows), _ptr(m_indptr), w, _ptr(out), _stream(stream))
         return out
@@ -415,7 +471,8 @@ class Layer:
 
     def prepare_weights(self, w13, w2, stream=None):
         """BF16 weights -> (w13_q, w13_s, w2_q, w2_s): MXFP8 codes and scales, or on an
-        MXFP4 layer MXFP4 ones in the decode kernels' tile layout."""
+        MXFP4 layer MXFP4 ones in the decode kernels' tile layout, or with MOE_FP8_BLOCK128 codes and the
+        FP32 scales of their 128 x 128 squares."""
         import torch
         dev = w13.device
         E, I, d = self.E, self.I, self.d
@@ -427,6 +484,17 @@ class Layer:
             _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
             _check("w2", w2, (E, d, I), torch.bfloat16, dev)
             w13_q, w13_s, w2_q, w2_s = (_new(n, torch.uint8, dev, stream) for n in n13 + n2)
+            moe_prepare_weights(self.plan, w13.data_ptr(), w2.data_ptr(), w13_q.data_ptr(), w13_s.data_ptr(),
+                                w2_q.data_ptr(), w2_s.data_ptr(), _stream(stream))
+            return w13_q, w13_s, w2_q, w2_s
+        if self._block128 is not None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+            if stream is not None:
+                _check_stream(stream, dev.index)
+            _check("w13", w13, (E, 2 * I, d), torch.bfloat16, dev)
+            _check("w2", w2, (E, d, I), torch.bfloat16, dev)
+            w13_q, w2_q = (_new(n, torch.uint8, dev, stream) for n in self._weights)
+            w13_s, w2_s = (_new(_dense(*n), torch.float32, dev, stream) for n in self._block128)
             moe_prepare_weights(self.plan, w13.data_ptr(), w2.data_ptr(), w13_q.data_ptr(), w13_s.data_ptr(),
                                 w2_q.data_ptr(), w2_s.data_ptr(), _stream(stream))
             return w13_q, w13_s, w2_q, w2_s
@@ -460,9 +528,36 @@ class Layer:
             _check(name, t, shape, torch.uint8, dev)
         raise ValueError("the current device is %s; x, ids, scores or the output is elsewhere" % dev)
 
-    def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
-        """The BF16 weights (w13, w2) that an MXFP4 layer's prepared weights stand for."""
+    def _check_block128(self, w13_q, w13_s, w2_q, w2_s, others, stream):
+        """Codes and scales of this layer's sizes, they, the other tensors and the stream on the current
+        device, or ValueError (a missing tensor is left to the call, which refuses it)."""
         import torch
+        index = torch.cuda.current_device()
+        if stream is not None:
+            _check_stream(stream, index)
+        if w13_q is None or w13_s is None or w2_q is None or w2_s is None:
+            return
+        (n13, n2), (s13, s2) = self._weights, self._block128
+        if not (w13_q.shape == n13[0] and w2_q.shape == n2[0] and w13_s.shape == s13 and w2_s.shape == s2
+                and w13_q.dtype in _codes8() and w2_q.dtype in _codes8()
+                and w13_s.dtype is torch.float32 and w2_s.dtype is torch.float32
+                and w13_q.is_contiguous() and w2_q.is_contiguous() and w13_s.is_contiguous() and w2_s.is_contiguous()
+                and index == w13_q.get_device() == w2_q.get_device() == w13_s.get_device() == w2_s.get_device()):
+            dev = torch.device("cuda", index)
+            _check_codes("w13_q", w13_q, n13[0], dev)
+            _check("w13_s", w13_s, s13, torch.float32, dev)
+            _check_codes("w2_q", w2_q, n2[0], dev)
+            _check("w2_s", w2_s, s2, torch.float32, dev)
+        for t in others:
+            if t is not None and t.get_device() != index:
+                raise ValueError("the current device is cuda:%d; x, ids, scores or the output is elsewhere" % index)
+
+    def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
+        """The BF16 weights (w13, w2) that the prepared weights of an MXFP4 or MOE_FP8_BLOCK128 layer
+        stand for."""
+        import torch
+        if self._block128 is not None:
+            self._check_block128(w13_q, w13_s, w2_q, w2_s, (), stream)
         if self._mxfp4 is not None:
             self._check_mxfp4(w13_q, w13_s, w2_q, w2_s, w13_q, w13_s, w2_q, w2_s, stream)
         w13, w2 = (_new(n, torch.bfloat16, w13_q.device, stream) for n in self._weights)
@@ -525,8 +620,26 @@ def _check(name, t, shape, dtype, device):
         "" if t.is_contiguous() else ", not contiguous"))
 
 
+_codes = None
+
+
+def _codes8():
+    """The types that hold E4M3 codes."""
+    global _codes
+    if _codes is None:
+        import torch
+        _codes = torch.uint8, torch.float8_e4m3fn
+    return _codes
+
+
+def _check_codes(name, t, shape, device):
+    """_check for E4M3 codes."""
+    import torch
+    _check(name, t, shape, t.dtype if t.dtype in _codes8() else torch.uint8, device)
+
+
 class _OnDevice:
-    """What Router and BlockNorm share: their device, a workspace there, and calls made with
+    """What Router, BlockNorm and Product share: their device, a workspace there, and calls made with
     that device current and their outputs allocated on the stream that writes them.  The workspace
     belongs to the stream that the object was made on.  Calls on other streams, and captured ones, take
     one of their own from their stream's (the graph's) memory, so that calls of one object may overlap."""
@@ -709,3 +822,106 @@ class BlockNorm(_OnDevice):
                           dx.data_ptr(), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), room.data_ptr(),
                           self._workspace_bytes, s)
         return dx, dy, dw_post, dgate, dw_pre
+
+
+class Product(_OnDevice):
+    """Rows [R, K] in BF16 times weights [E, N, K] in E4M3 with one FP32 scale per 128 x 128: one matrix, or
+    with m_indptr (int32 [E+1] on the device) the matrix of each segment of the rows.  See the section on
+    products in include/moe.h.  Weights are codes (uint8 or float8_e4m3fn) [E, N, K] and scales f32
+    [E, N/128, K/128], from prepare_weights or from a checkpoint that holds them so."""
+
+    def __init__(self, R, N, K, E=1, training=False, wgrad_accumulate=False, device="cuda"):
+        import torch
+        self.R, self.N, self.K, self.E = R, N, K, E
+        self._in, self._out, self._weights = _dense(R, K), _dense(R, N), _dense(E, N, K)
+        self._scales = _dense(E, N // 128, K // 128)
+        self._cfg = ProductConfig(R, N, K, E, int(bool(training)), int(bool(wgrad_accumulate)))
+        nbytes = moe_product_workspace_bytes(self._cfg)
+        if not nbytes:                                 # the reason, from the call that names it
+            moe_product_forward(self._cfg, 0, 0, 0, 0, 0, 0, 0, 0)
+        super().__init__(device, nbytes)
+        self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _check_args(self, w_q, w_s, m_indptr):
+        import torch
+        if w_q is not None:
+            _check_codes("w_q", w_q, self._weights[0], self.device)
+        if w_s is not None:
+            _check("w_s", w_s, self._scales[0], torch.float32, self.device)
+        if m_indptr is not None:
+            _check("m_indptr", m_indptr, (self.E + 1,), torch.int32, self.device)
+
+    def prepare_weights(self, w, stream=None):
+        """BF16 weights [E, N, K] -> (codes uint8, scales f32)."""
+        import torch
+        _check("w", w, self._weights[0], torch.bfloat16, self.device)
+        return self._call(self._prepare, stream, w)
+
+    def _prepare(self, s, w):
+        import torch
+        w_q, w_s = _new(self._weights, torch.uint8, self.device), _new(self._scales, torch.float32, self.device)
+        moe_product_prepare_weights(self._cfg, w.data_ptr(), w_q.data_ptr(), w_s.data_ptr(), s)
+        return w_q, w_s
+
+    def expand_weights(self, w_q, w_s, stream=None):
+        """The BF16 weights that codes and scales stand for."""
+        self._check_args(w_q, w_s, None)
+        return self._call(self._expand, stream, w_q, w_s)
+
+    def _expand(self, s, w_q, w_s):
+        import torch
+        w = _new(self._weights, torch.bfloat16, self.device)
+        moe_product_expand_weights(self._cfg, w_q.data_ptr(), w_s.data_ptr(), w.data_ptr(), s)
+        return w
+
+    def forward(self, x, w_q, w_s, m_indptr=None, y=None, stream=None):
+        """y BF16 [R, N]; rows behind m_indptr[E] are not written."""
+        import torch
+        _check("x", x, self._in[0], torch.bfloat16, self.device)
+        self._check_args(w_q, w_s, m_indptr)
+        if y is not None:
+            _check("y", y, self._out[0], torch.bfloat16, self.device)
+        return self._call(self._forward, stream, x, w_q, w_s, m_indptr, y)
+
+    def _forward(self, s, x, w_q, w_s, m_indptr, y):
+        import torch
+        if y is None:
+            y = _new(self._out, torch.bfloat16, self.device)
+        room = self._room(s)
+        moe_product_forward(self._cfg, x.data_ptr(), _ptr(m_indptr), w_q.data_ptr(), w_s.data_ptr(), y.data_ptr(),
+                            self._status.data_ptr(), room.data_ptr(), self._workspace_bytes, s)
+        return y
+
+    def backward(self, dy, x, w_q, w_s, m_indptr=None, dx=None, dw=None, need_dx=True, need_dw=True, stream=None):
+        """(dx BF16 [R, K], dw BF16 [E, N, K]), None where it is not needed; x may be None without dw,
+        the weights without dx.  dx and dw may be given (with wgrad_accumulate dw has to be)."""
+        import torch
+        _check("dy", dy, self._out[0], torch.bfloat16, self.device)
+        if x is not None:
+            _check("x", x, self._in[0], torch.bfloat16, self.device)
+        self._check_args(w_q, w_s, m_indptr)
+        for name, t, shape in (("dx", dx, self._in[0]), ("dw", dw, self._weights[0])):
+            if t is not None:
+                _check(name, t, shape, torch.bfloat16, self.device)
+        if need_dw and dw is None and self._cfg.wgrad_accumulate:
+            raise ValueError("dw: the gradients to add to are needed")
+        return self._call(self._backward, stream, dy, x, w_q, w_s, m_indptr, dx, dw, need_dx, need_dw)
+
+    def _backward(self, s, dy, x, w_q, w_s, m_indptr, dx, dw, need_dx, need_dw):
+        import torch
+        bf16 = torch.bfloat16
+        dx = None if not need_dx else _new(self._in, bf16, self.device) if dx is None else dx
+        dw = None if not need_dw else _new(self._weights, bf16, self.device) if dw is None else dw
+        room = self._room(s)
+        moe_product_backward(self._cfg, dy.data_ptr(), _ptr(x), _ptr(m_indptr), _ptr(w_q), _ptr(w_s), _ptr(dx), _ptr(dw),
+                             self._status.data_ptr(), room.data_ptr(), self._workspace_bytes, s)
+        return dx, dw
+
+    def status(self, clear=True):
+        """(status, device flags) of the calls so far; waits for the device's work."""
+        import torch
+        torch.cuda.synchronize(self.device)
+        flags = int(self._status.item())
+        if clear and flags:
+            self._status.zero_()
+        return (MOE_ERR_ROUTING if flags else MOE_OK), flags
