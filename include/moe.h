@@ -398,6 +398,11 @@ moe_status_t moe_product_backward(const moe_product_config_t* cfg, const void* d
  * A NaN key counts as -inf in the choice.  A NaN logit has one, and makes the row's softmax (with sigmoid:
  * its own score and the row's p) NaN; so does +inf with softmax.  With softmax and a bias all keys of such
  * a row are NaN: its ids are 0 .. k-1.  Biases may be infinite.  A score s below 2^-126 counts as 0.
+ * With groups > 0 the choice is limited: expert e is in group e / (E / groups); a group's score is the sum
+ * of its group_top (1 or 2) largest keys, those with the bias (0 without one): s + bias, ordered as in 64
+ * bits, or with group_top 1 and no bias z; the experts of the top_groups groups of largest score can be
+ * chosen, ties to the lowest group.  (A key of -inf makes a sum of two -inf; a NaN sum counts as -inf.)
+ * Scores, p, counts, the loss and the gradient are what they are without groups.
  * Stateless: a config, caller-owned buffers and a workspace that holds nothing between calls;
  * calls that overlap need a workspace each. */
 #define MOE_SCORE_SOFTMAX 0
@@ -411,6 +416,9 @@ typedef struct {
     int32_t logits_f32;    /* 1: logits and dlogits FP32, 0: BF16 */
     float scale;           /* factor on the scores, finite */
     float balance_coef;    /* factor of the balance loss, finite */
+    int32_t groups;        /* 0: the choice is free; else 1..32, a divisor of E, of size >= group_top */
+    int32_t top_groups;    /* groups that stay, 1..groups, with k experts at least (0 without groups) */
+    int32_t group_top;     /* keys that make a group's score, 1 or 2 (0 without groups) */
 } moe_router_config_t;
 
 /* Bytes of workspace that moe_router_forward needs for counts, prob_sums or loss; 0 for an

@@ -62,7 +62,17 @@ static moe_status_t router_check(const moe_router_config_t* c) {
     if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
     if ((c->normalize != 0 && c->normalize != 1) || (c->logits_f32 != 0 && c->logits_f32 != 1)) return MOE_ERR_INVALID_ARG;
     if (!std::isfinite(c->scale) || !std::isfinite(c->balance_coef)) return MOE_ERR_INVALID_ARG;
+    if (c->groups < 0 || c->top_groups < 0 || c->group_top < 0) return MOE_ERR_INVALID_ARG;
+    if (c->groups == 0 ? c->top_groups != 0 || c->group_top != 0
+                       : c->top_groups < 1 || c->top_groups > c->groups || c->group_top < 1 || c->group_top > 2)
+        return MOE_ERR_INVALID_ARG;
     if (c->E > kMaxExperts || c->k > c->E || c->k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+    if (c->groups > 0) {
+        // groups of one size, which hold the keys that rank them, and enough experts in the chosen ones
+        if (c->groups > kMaxRouterGroups || c->E % c->groups != 0) return MOE_ERR_UNSUPPORTED;
+        const int size = c->E / c->groups;
+        if (c->group_top > size || c->k > c->top_groups * size) return MOE_ERR_UNSUPPORTED;
+    }
     return MOE_OK;
 }
 
@@ -85,6 +95,7 @@ moe_status_t moe_router_forward(const moe_router_config_t* c, const void* logits
     g.scale = c->scale; g.coef = c->balance_coef;
     g.logits = logits; g.bias = bias; g.mask = mask;
     g.ids = ids; g.scores = scores;
+    g.groups = c->groups; g.top_groups = c->top_groups; g.group_top = c->group_top;
     g.counts = counts; g.psum = prob_sums; g.loss = loss;
     if (counts || prob_sums || loss) {
         if (!workspace || workspace_bytes < moe_router_workspace_bytes(c)) return MOE_ERR_WORKSPACE;

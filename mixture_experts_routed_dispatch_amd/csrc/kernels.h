@@ -339,8 +339,10 @@ struct RouterArgs {
     float* part_sums;
     double* shares;           // [16, 2], with part_counts
     int32_t* ticket;          // [1], with part_counts
-    int vec, bias_vec, stride;  // set by the launcher
+    int groups, top_groups, group_top;   // groups 0: none; at most kMaxRouterGroups
+    int vec, bias_vec, stride, group_size, group_magic;  // set by the launcher
 };
+constexpr int kMaxRouterGroups = 32;
 int router_blocks(int64_t T);
 hipError_t launch_route(RouterArgs g, bool sigmoid, bool f32, hipStream_t s);
 

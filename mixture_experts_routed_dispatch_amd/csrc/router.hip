@@ -4,6 +4,8 @@
 // With z = logits[t], s = softmax(z) or sigmoid(z), p_e = s_e / sum_e' s_e' (softmax: p = s):
 //   ids      the k experts of the largest key, descending, ties to the lowest index; the key
 //            is z_e itself, or s_e + bias_e when a selection bias is given (-inf where z_e is)
+//            With groups (E / groups consecutive experts each) only those of the top_groups groups with the
+//            largest sum of their group_top largest keys s_e + bias_e can be chosen, ties to the lowest group.
 //   scores   scale s_j, divided by the sum of the chosen s with `normalize`
 //   counts_e tokens that chose e;  P_e = sum_t p_te  (rows that the mask leaves out count
 //            nowhere; N = sum counts / k rows remain)
@@ -30,9 +32,15 @@
 // 22.2 us, and 113 while all of k > 12 took the maxima and settled near keys for the whole row; k = 32,
 // which takes the maxima, 214.
 //
+// The groups' sums are merged from the two largest keys of each lane's pieces, which lie in one group where
+// its size is a multiple of theirs, by way of LDS: a lane to a group, up to two.  Keys of closed groups
+// leave the choice before its bound is taken.
+//
 // With a bias the keys s + b have to be ordered as in exact arithmetic.  They are compared in
 // FP32; where two that matter lie closer than FP32's error, they are computed again in 64
 // bits: of the candidates only, or in the other way of all.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -254,10 +262,10 @@ __device__ __forceinline__ double exact_sum(const void* logits, int64_t row, int
 // the k largest by keys in 64 bits, each computed when it is compared (rare: few registers
 // matter more than time)
 template <int kV, bool kSig>
-__device__ __forceinline__ void take_top_exact(const RouterArgs& g, int64_t row, int i0, bool f32, int* sel) {
+__device__ __forceinline__ void take_top_exact(const RouterArgs& g, int64_t row, int i0, bool f32, uint32_t open, int* sel) {
     float zmax;
     const double sum = exact_sum<kV, kSig>(g.logits, row, i0, g.E, zmax, f32);
-    uint32_t taken = 0;
+    uint32_t taken = ~open;
     for (int j = 0; j < g.k; ++j) {
         double m = -(double)INFINITY;
         int at = 1 << 20;
@@ -314,8 +322,9 @@ __device__ __forceinline__ void count_above(float a, float b, float ra, float rb
 }
 // A bound that at least k of the row's keys reach: the k-th largest of the lanes' largest keys, or
 // of their two largest.  It is the smallest of those with fewer than k above it.
-template <int kV> __device__ __forceinline__ float bound_of(const float key[kV], int k) {
-    if (__builtin_expect(k <= kOneK, 1)) {
+// With groups few lanes may be left: always of their two largest.
+template <int kV, bool kGroups> __device__ __forceinline__ float bound_of(const float key[kV], int k) {
+    if (!kGroups && __builtin_expect(k <= kOneK, 1)) {
         float a = key[0];
 #pragma unroll
         for (int i = 1; i < kV; ++i) a = __builtin_fmaxf(a, key[i]);
@@ -336,9 +345,10 @@ template <int kV> __device__ __forceinline__ float bound_of(const float key[kV],
 }
 // Indices of the row's candidates, which reach the bound, into list, ascending; returns how many
 // there are (more than kCand: the list is not to be used).  slack: how far below the bound a key
-// still counts.
+// still counts.  open: bit i, the lane's i-th key can be chosen.
 template <int kV>
-__device__ __forceinline__ int find_candidates(const float key[kV], float bound, int i0, int E, float slack, int* list) {
+__device__ __forceinline__ int find_candidates(const float key[kV], float bound, int i0, int E, float slack, uint32_t open,
+                                               int* list) {
     bound -= slack * __builtin_fmaxf(1.0f, __builtin_fabsf(bound));
     if (!(bound > -INFINITY)) bound = -INFINITY;        // +inf gives NaN: then every key counts
     uint32_t m = 0;                                     // a NaN key is a candidate, which counts as -inf
@@ -347,7 +357,7 @@ __device__ __forceinline__ int find_candidates(const float key[kV], float bound,
     auto exist = [&](int room) { return room > 7 ? 0xFFu : room > 0 ? (1u << room) - 1 : 0u; };
     uint32_t all = exist(E - i0);
     if constexpr (kV == 16) all |= exist(E - i0 - 128) << 8;
-    m &= all;
+    m &= all & open;
     // candidates of the lanes below, of each half of the row: row_shr, 0 past the row
     const uint32_t n = (uint32_t)__builtin_popcount(m & 0xFF) | (uint32_t)__builtin_popcount(m >> 8) << 16;
     uint32_t incl = n;
@@ -435,6 +445,148 @@ __device__ __forceinline__ void place_candidates(const RouterArgs& g, int64_t t,
     }
 }
 
+// The keys of a row's groups.  Which groups are open is the same for the 16 lanes: a bit for each.
+constexpr int kMaxGroups = kMaxRouterGroups;
+struct Two {
+    float a, b;                                         // the largest and the second, as choice keys
+};
+__device__ __forceinline__ void add(Two& t, float v) {
+    t.b = v > t.a ? t.a : __builtin_fmaxf(t.b, v);
+    t.a = __builtin_fmaxf(t.a, v);
+}
+__device__ __forceinline__ int group_of(const RouterArgs& g, int e) { return e * g.group_magic >> 16; }
+
+// The two largest keys of the groups l16 and l16 + 16 (those that there are) of a row.  pieces: this
+// row's LDS.
+template <int kV>
+__device__ __forceinline__ void group_tops(const RouterArgs& g, const float key[kV], int i0, float2* pieces, Two (&top)[2]) {
+    constexpr int kP = kV < 8 ? kV : 8;                 // keys of a piece
+    const int l16 = threadIdx.x & 15, size = g.group_size;
+    top[0] = top[1] = {-INFINITY, -INFINITY};
+    if (size % kP == 0) {
+#pragma unroll
+        for (int h = 0; h < kV / kP; ++h) {
+            Two t = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kP; ++i) add(t, choice_key(key[h * kP + i]));
+            pieces[l16 + 16 * h] = make_float2(t.a, t.b);
+        }
+        wave_fence();
+        const int n = size / kP;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (l16 + 16 * h < g.groups)
+                for (int i = 0; i < n; ++i) {
+                    const float2 p = pieces[(l16 + 16 * h) * n + i];
+                    add(top[h], p.x);
+                    add(top[h], p.y);
+                }
+        return;
+    }
+    // groups of other sizes one after another: each lane's two, then the row's
+#pragma unroll 1
+    for (int q = 0; q < g.groups; ++q) {
+        Two t = {-INFINITY, -INFINITY};
+        const int first = q * size - i0;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const int at = ahead(i) - first;
+            if (at >= 0 && at < size) add(t, choice_key(key[i]));
+        }
+        auto turn = [&](auto ctrl) {
+            const float a = __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(t.a)));
+            const float b = __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(t.b)));
+            add(t, a);
+            add(t, b);
+        };
+        turn(std::integral_constant<int, 0x128>());
+        turn(std::integral_constant<int, 0x124>());
+        turn(std::integral_constant<int, 0x122>());
+        turn(std::integral_constant<int, 0x121>());
+        if (q == l16) top[0] = t;
+        if (q == l16 + 16) top[1] = t;
+    }
+}
+
+// The open groups by their sums v[h] of the groups l16 + 16 h: those with fewer than top_groups before them.
+template <typename T>
+__device__ __forceinline__ uint32_t rank_groups(const RouterArgs& g, const T (&v)[2], T* sums) {
+    const int l16 = threadIdx.x & 15;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) sums[l16 + 16 * h] = v[h];
+    wave_fence();
+    int before[2] = {0, 0};
+    for (int c = 0; c < g.groups; ++c) {
+        const T o = sums[c];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) before[h] += o > v[h] || (o == v[h] && c < l16 + 16 * h);
+    }
+    wave_fence();
+    const int shift = threadIdx.x & 48;
+    const uint64_t lo = __ballot(l16 < g.groups && before[0] < g.top_groups);
+    const uint64_t hi = __ballot(l16 + 16 < g.groups && before[1] < g.top_groups);
+    return (uint32_t)(lo >> shift & 0xFFFF) | (uint32_t)(hi >> shift & 0xFFFF) << 16;
+}
+
+// The same by sums in 64 bits, a lane adding up its groups' keys.
+template <int kV, bool kF32, bool kSig, bool kBias>
+__device__ __attribute__((noinline)) uint32_t open_groups_exact(const RouterArgs& g, int64_t row, int i0, double* sums) {
+    float zmax;
+    const double sum = exact_sum<kV, kSig>(g.logits, row, i0, g.E, zmax, kF32);
+    const int l16 = threadIdx.x & 15;
+    double v[2];
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        double a = -(double)INFINITY, b = a;
+        if (l16 + 16 * h < g.groups)
+#pragma unroll 1
+            for (int i = 0; i < g.group_size; ++i) {
+                const int e = (l16 + 16 * h) * g.group_size + i;
+                const double key = exact_key<kSig>(ld_logit(g.logits, row + e, kF32), kBias ? g.bias[e] : 0.0f, zmax, sum);
+                b = key > a ? a : key > b ? key : b;
+                a = key > a ? key : a;
+            }
+        v[h] = choice_key(g.group_top == 2 ? a + b : a);
+    }
+    return rank_groups<double>(g, v, sums);
+}
+
+// The open groups of a row from its FP32 keys.  Sums of keys that rounding may have brought into a wrong
+// order (kNear for each of the two, relative to the largest key that enters any) go to 64 bits where
+// such a sum lies on either side of the border.  Logits order exactly, one a group.
+template <int kV, bool kF32, bool kSig, bool kBias>
+__device__ __forceinline__ uint32_t open_groups(const RouterArgs& g, int64_t row, const float key[kV], const float s[kV], int i0,
+                                                float2* pieces, float* sums, double* sums64) {
+    const bool by_score = !kBias && g.group_top == 2;
+    float k[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) k[i] = by_score ? key_score(s[i], key[i]) : key[i];
+    Two top[2];
+    group_tops<kV>(g, k, i0, pieces, top);
+    float v[2], most = 1.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        v[h] = choice_key(g.group_top == 2 ? top[h].a + top[h].b : top[h].a);
+        if (top[h].a > -INFINITY) most = __builtin_fmaxf(most, __builtin_fabsf(top[h].a));
+        if (top[h].b > -INFINITY && g.group_top == 2) most = __builtin_fmaxf(most, __builtin_fabsf(top[h].b));
+    }
+    const uint32_t open = rank_groups<float>(g, v, sums);
+    if (!kBias && !by_score) return open;
+    float least = INFINITY, over = -INFINITY;           // the smallest open sum, the largest closed one
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int q = (threadIdx.x & 15) + 16 * h;
+        if (q >= g.groups) continue;
+        if (open >> q & 1) least = __builtin_fminf(least, v[h]);
+        else over = __builtin_fmaxf(over, v[h]);
+    }
+    least = -row_max(-least);
+    over = row_max(over);
+    const bool near = g.top_groups < g.groups && !(least - over > 2 * kNear * row_max(most));
+    if (__builtin_expect(!__ballot(near), 1)) return open;
+    return open_groups_exact<kV, kF32, kSig, kBias>(g, row, i0, sums64);
+}
+
 // the loss from sum counts_e P_e and sum counts_e
 __device__ __forceinline__ float loss_value(const RouterArgs& g, double a, double n) {
     n /= g.k;
@@ -453,12 +605,14 @@ __device__ __forceinline__ void write_loss(const RouterArgs& g, int count, float
     }
 }
 
-template <int kThr, int kV, bool kF32, bool kSig, bool kBias>
+template <int kThr, int kV, bool kF32, bool kSig, bool kBias, bool kGroups>
 __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
     constexpr int kR = kThr / 16;
     __shared__ int sel[kR][kCand];
     __shared__ __attribute__((aligned(16))) float keys[kR][kCand];
-    __shared__ double keys64[kBias ? kR : 1][kCand];
+    __shared__ double keys64[kBias || kGroups ? kR : 1][kCand];
+    __shared__ float2 pieces[kGroups ? kR : 1][kMaxGroups];
+    static_assert(kMaxGroups <= kCand, "keys and keys64 hold the groups' sums too");
     __shared__ int cnt[256];
     __shared__ float sums[kThr / MOE_WAVE][256];
     __shared__ double part[4][2];
@@ -489,8 +643,21 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) z[i] += s[i];  // keys from here on
         }
+        uint32_t open = 0xFFFFFFFFu;                    // bit i: the lane's i-th key can be chosen
+        if constexpr (kGroups) {
+            const uint32_t groups = open_groups<kV, kF32, kSig, kBias>(g, t * E, z, s, i0, pieces[row], keys[row], keys64[row]);
+            wave_fence();
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int e = i0 + ahead(i);
+                if (e < E && !(groups >> group_of(g, e) & 1)) {
+                    open &= ~(1u << i);
+                    z[i] = -INFINITY;
+                }
+            }
+        }
         int n = kCand + 1;
-        if (k <= kTwoK) n = find_candidates<kV>(z, bound_of<kV>(z, k), i0, E, kBias ? kNear : 0.0f, sel[row]);
+        if (k <= kTwoK) n = find_candidates<kV>(z, bound_of<kV, kGroups>(z, k), i0, E, kBias ? kNear : 0.0f, open, sel[row]);
         // the ways marked unlikely lie behind the usual one, which a wave walks through once: in their
         // places between its parts they cost 16384 rows 0.5 to 1 us of instruction fetches
         bool placed = !__ballot(n > kCand);
@@ -498,14 +665,14 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
         if (__builtin_expect(!placed, 0)) {
             uint32_t key[kV];
 #pragma unroll
-            for (int i = 0; i < kV; ++i) key[i] = ahead(i) < E - i0 ? order_key(z[i]) : 0u;
+            for (int i = 0; i < kV; ++i) key[i] = ahead(i) < E - i0 && (open >> i & 1) ? order_key(z[i]) : 0u;
             wave_fence();
             last = take_top<kV>(key, k, i0, sel[row]);
             wave_fence();
             if constexpr (kBias) {
                 // that key is the best bound; the candidates go to 64 bits only if they have to
                 int* list = reinterpret_cast<int*>(keys[row]);
-                n = find_candidates<kV>(z, key_value(last), i0, E, kNear, list);
+                n = find_candidates<kV>(z, key_value(last), i0, E, kNear, open, list);
                 placed = !__ballot(n > kCand);
                 wave_fence();
                 if (placed) {
@@ -541,7 +708,7 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
 #pragma unroll 1
                 for (int i = 0; i < kV; ++i) {
                     const int e = i0 + ahead(i);
-                    if (e >= E) continue;
+                    if (e >= E || !(open >> i & 1)) continue;
                     const float zi = ld_logit(g.logits, t * E + e, kF32), bi = g.bias[e];
                     const float ki = choice_key(key_score(one_score<kSig>(zi, base, inv), zi) + bi);
                     near |= __builtin_fabsf(ki - k_last) <= reach && !(zi == z_last && bi == b_last);
@@ -556,7 +723,7 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
                 }
                 if (__ballot(near)) {
                     wave_fence();
-                    take_top_exact<kV, kSig>(g, t * E, i0, kF32, sel[row]);
+                    take_top_exact<kV, kSig>(g, t * E, i0, kF32, open, sel[row]);
                     wave_fence();
                 }
             }
@@ -819,18 +986,23 @@ bool aligned_rows(const void* a, const void* b, int E, bool f32) {
     return E % v == 0 && reinterpret_cast<uintptr_t>(a) % bytes == 0 && reinterpret_cast<uintptr_t>(b) % bytes == 0;
 }
 
-template <int kThr, int kV, bool kF32>
+template <int kThr, int kV, bool kF32, bool kGroups>
 void launch_route_t(const RouterArgs& g, int grid, bool sig, hipStream_t s) {
     const dim3 gd(grid), bd(kThr);
-    if (sig && g.bias) hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, true, true>), gd, bd, 0, s, g);
-    else if (sig) hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, true, false>), gd, bd, 0, s, g);
-    else if (g.bias) hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, false, true>), gd, bd, 0, s, g);
-    else hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, false, false>), gd, bd, 0, s, g);
+    if (sig && g.bias) hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, true, true, kGroups>), gd, bd, 0, s, g);
+    else if (sig) hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, true, false, kGroups>), gd, bd, 0, s, g);
+    else if (g.bias) hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, false, true, kGroups>), gd, bd, 0, s, g);
+    else hipLaunchKernelGGL((route_kernel<kThr, kV, kF32, false, false, kGroups>), gd, bd, 0, s, g);
 }
 template <int kV, bool kF32>
 void launch_route_v(const RouterArgs& g, int grid, bool sig, hipStream_t s) {
-    if (wide_blocks(g.T)) launch_route_t<kWide, kV, kF32>(g, grid, sig, s);
-    else launch_route_t<kThreads, kV, kF32>(g, grid, sig, s);
+    if (g.groups) {
+        if (wide_blocks(g.T)) launch_route_t<kWide, kV, kF32, true>(g, grid, sig, s);
+        else launch_route_t<kThreads, kV, kF32, true>(g, grid, sig, s);
+    } else {
+        if (wide_blocks(g.T)) launch_route_t<kWide, kV, kF32, false>(g, grid, sig, s);
+        else launch_route_t<kThreads, kV, kF32, false>(g, grid, sig, s);
+    }
 }
 template <int kV>
 void launch_route_grad_v(const RouterGradArgs& g, int grid, bool sig, bool f32, hipStream_t s) {
@@ -856,6 +1028,11 @@ hipError_t launch_route(RouterArgs g, bool sigmoid, bool f32, hipStream_t s) {
     g.vec = aligned_rows(g.logits, g.logits, g.E, f32);
     g.bias_vec = aligned_rows(g.bias, g.bias, g.E, true);
     g.stride = (g.E + 3) & ~3;
+    if (g.groups) {
+        if (g.groups < 0 || g.groups > kMaxGroups || g.E % g.groups != 0) return hipErrorInvalidValue;
+        g.group_size = g.E / g.groups;
+        g.group_magic = 65536 / g.group_size + 1;       // e / group_size = e * magic >> 16 for e < 256
+    }
     const int grid = router_blocks(g.T);
     switch (per_lane(g.E) * 2 + (f32 ? 1 : 0)) {
         case 8: launch_route_v<4, false>(g, grid, sigmoid, s); break;

@@ -84,7 +84,8 @@ class MoeWeights(ctypes.Structure):
 class RouterConfig(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("score", ctypes.c_int32), ("normalize", ctypes.c_int32), ("logits_f32", ctypes.c_int32),
-                ("scale", ctypes.c_float), ("balance_coef", ctypes.c_float)]
+                ("scale", ctypes.c_float), ("balance_coef", ctypes.c_float),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32)]
 
 
 class NormConfig(ctypes.Structure):
@@ -678,12 +679,15 @@ class _OnDevice:
 
 class Router(_OnDevice):
     """Logits [T, E] (FP32 or BF16) -> ids, scores, per-expert counts and the balance loss, and
-    the gradient; see the router section of include/moe.h for the formulas."""
+    the gradient; see the router section of include/moe.h for the formulas.  With groups, only experts of
+    the top_groups groups whose group_top largest keys have the largest sum are chosen."""
 
-    def __init__(self, T, E, k, score=MOE_SCORE_SOFTMAX, normalize=True, scale=1.0, balance_coef=0.0, device="cuda"):
+    def __init__(self, T, E, k, score=MOE_SCORE_SOFTMAX, normalize=True, scale=1.0, balance_coef=0.0, device="cuda",
+                 groups=0, top_groups=0, group_top=0):
         self.T, self.E, self.k = T, E, k
         self._per_choice, self._per_expert = _dense(T, k), _dense(E)
-        self._cfg = {f32: RouterConfig(T, E, k, int(score), int(bool(normalize)), int(f32), scale, balance_coef)
+        self._cfg = {f32: RouterConfig(T, E, k, int(score), int(bool(normalize)), int(f32), scale, balance_coef,
+                                       int(groups), int(top_groups), int(group_top))
                      for f32 in (False, True)}
         nbytes = moe_router_workspace_bytes(self._cfg[True])
         if not nbytes:                                 # the reason, from the call that names it
