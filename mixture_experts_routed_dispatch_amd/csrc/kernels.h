@@ -340,7 +340,7 @@ struct RouterArgs {
     double* shares;           // [16, 2], with part_counts
     int32_t* ticket;          // [1], with part_counts
     int groups, top_groups, group_top;   // groups 0: none; at most kMaxRouterGroups
-    int vec, bias_vec, stride, group_size, group_magic;  // set by the launcher
+    int vec, bias_vec, stride, group_size, group_magic, group_lanes, group_shift;  // set by the launcher
 };
 constexpr int kMaxRouterGroups = 32;
 int router_blocks(int64_t T);

@@ -32,9 +32,8 @@
 // 22.2 us, and 113 while all of k > 12 took the maxima and settled near keys for the whole row; k = 32,
 // which takes the maxima, 214.
 //
-// The groups' sums are merged from the two largest keys of each lane's pieces, which lie in one group where
-// its size is a multiple of theirs, by way of LDS: a lane to a group, up to two.  Keys of closed groups
-// leave the choice before its bound is taken.
+// The groups' sums are merged from the two largest keys of each lane's pieces; keys of closed groups leave the
+// choice before its bound is taken.
 //
 // With a bias the keys s + b have to be ordered as in exact arithmetic.  They are compared in
 // FP32; where two that matter lie closer than FP32's error, they are computed again in 64
@@ -456,135 +455,208 @@ __device__ __forceinline__ void add(Two& t, float v) {
 }
 __device__ __forceinline__ int group_of(const RouterArgs& g, int e) { return e * g.group_magic >> 16; }
 
-// The two largest keys of the groups l16 and l16 + 16 (those that there are) of a row.  pieces: this
-// row's LDS.
-template <int kV>
-__device__ __forceinline__ void group_tops(const RouterArgs& g, const float key[kV], int i0, float2* pieces, Two (&top)[2]) {
-    constexpr int kP = kV < 8 ? kV : 8;                 // keys of a piece
-    const int l16 = threadIdx.x & 15, size = g.group_size;
-    top[0] = top[1] = {-INFINITY, -INFINITY};
-    if (size % kP == 0) {
-#pragma unroll
-        for (int h = 0; h < kV / kP; ++h) {
-            Two t = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < kP; ++i) add(t, choice_key(key[h * kP + i]));
-            pieces[l16 + 16 * h] = make_float2(t.a, t.b);
-        }
-        wave_fence();
-        const int n = size / kP;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (l16 + 16 * h < g.groups)
-                for (int i = 0; i < n; ++i) {
-                    const float2 p = pieces[(l16 + 16 * h) * n + i];
-                    add(top[h], p.x);
-                    add(top[h], p.y);
-                }
-        return;
-    }
-    // groups of other sizes one after another: each lane's two, then the row's
-#pragma unroll 1
-    for (int q = 0; q < g.groups; ++q) {
-        Two t = {-INFINITY, -INFINITY};
-        const int first = q * size - i0;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int at = ahead(i) - first;
-            if (at >= 0 && at < size) add(t, choice_key(key[i]));
-        }
-        auto turn = [&](auto ctrl) {
-            const float a = __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(t.a)));
-            const float b = __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(t.b)));
-            add(t, a);
-            add(t, b);
-        };
-        turn(std::integral_constant<int, 0x128>());
-        turn(std::integral_constant<int, 0x124>());
-        turn(std::integral_constant<int, 0x122>());
-        turn(std::integral_constant<int, 0x121>());
-        if (q == l16) top[0] = t;
-        if (q == l16 + 16) top[1] = t;
-    }
+// The other lanes' two largest, by DPP, into t
+template <int kCtrl> __device__ __forceinline__ void merge(Two& t) {
+    const float a = __uint_as_float(dpp<kCtrl>(__float_as_uint(t.a))), b = __uint_as_float(dpp<kCtrl>(__float_as_uint(t.b)));
+    add(t, a);
+    add(t, b);
 }
-
-// The open groups by their sums v[h] of the groups l16 + 16 h: those with fewer than top_groups before them.
-template <typename T>
-__device__ __forceinline__ uint32_t rank_groups(const RouterArgs& g, const T (&v)[2], T* sums) {
-    const int l16 = threadIdx.x & 15;
+__device__ __forceinline__ float sum_of(const RouterArgs& g, const Two& t) {
+    return choice_key(g.group_top == 2 ? t.a + t.b : t.a);
+}
+// Groups with a larger sum than v, or the same and a lower index than q, of the row's sums (as many as g.groups
+// rounded up to 4)
+template <typename T> __device__ __forceinline__ int groups_before(const RouterArgs& g, const T* sums, T v, int q) {
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+    int n = 0;
+    for (int c = 0; c < g.groups; c += 4) {
+        const vec4 o = *reinterpret_cast<const vec4*>(sums + c);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) sums[l16 + 16 * h] = v[h];
-    wave_fence();
-    int before[2] = {0, 0};
-    for (int c = 0; c < g.groups; ++c) {
-        const T o = sums[c];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) before[h] += o > v[h] || (o == v[h] && c < l16 + 16 * h);
+        for (int i = 0; i < 4; ++i) n += o[i] > v || (o[i] == v && c + i < q);
     }
+    return n;
+}
+// The open groups, a bit for each, by the sums of the groups l16 and l16 + 16
+template <typename T> __device__ __forceinline__ uint32_t rank_groups(const RouterArgs& g, T v0, T v1, T* sums) {
+    const int l16 = threadIdx.x & 15, shift = threadIdx.x & 48;
+    sums[l16] = l16 < g.groups ? v0 : -(T)INFINITY;
+    sums[l16 + 16] = l16 + 16 < g.groups ? v1 : -(T)INFINITY;
     wave_fence();
-    const int shift = threadIdx.x & 48;
-    const uint64_t lo = __ballot(l16 < g.groups && before[0] < g.top_groups);
-    const uint64_t hi = __ballot(l16 + 16 < g.groups && before[1] < g.top_groups);
+    const uint64_t lo = __ballot(l16 < g.groups && groups_before<T>(g, sums, v0, l16) < g.top_groups);
+    const uint64_t hi = __ballot(l16 + 16 < g.groups && groups_before<T>(g, sums, v1, l16 + 16) < g.top_groups);
+    wave_fence();
     return (uint32_t)(lo >> shift & 0xFFFF) | (uint32_t)(hi >> shift & 0xFFFF) << 16;
 }
+// The lane's keys in open groups
+template <int kV> __device__ __forceinline__ uint32_t open_keys(const RouterArgs& g, uint32_t groups, int i0) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        const int e = i0 + ahead(i);
+        m |= e < g.E ? (groups >> group_of(g, e) & 1) << i : 0u;
+    }
+    return m;
+}
 
-// The same by sums in 64 bits, a lane adding up its groups' keys.
+// The open groups by sums in 64 bits.  key: the FP32 keys; least[h]: what a key of the lane's h-th piece reaches
+// if it may be one of its group's two (-inf or NaN: all).  Up to 32 such keys of a row are computed again, a lane
+// two of them; where there are more, or the groups are no whole pieces, a lane goes through its groups' keys.
 template <int kV, bool kF32, bool kSig, bool kBias>
-__device__ __attribute__((noinline)) uint32_t open_groups_exact(const RouterArgs& g, int64_t row, int i0, double* sums) {
+__device__ __forceinline__ uint32_t open_groups_exact(const RouterArgs& g, int64_t row, const float key[kV], int i0, bool pieces,
+                                                      float least0, float least1, int* list, double* sums) {
     float zmax;
     const double sum = exact_sum<kV, kSig>(g.logits, row, i0, g.E, zmax, kF32);
     const int l16 = threadIdx.x & 15;
-    double v[2];
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        double a = -(double)INFINITY, b = a;
-        if (l16 + 16 * h < g.groups)
-#pragma unroll 1
-            for (int i = 0; i < g.group_size; ++i) {
-                const int e = (l16 + 16 * h) * g.group_size + i;
-                const double key = exact_key<kSig>(ld_logit(g.logits, row + e, kF32), kBias ? g.bias[e] : 0.0f, zmax, sum);
-                b = key > a ? a : key > b ? key : b;
-                a = key > a ? key : a;
-            }
-        v[h] = choice_key(g.group_top == 2 ? a + b : a);
+    auto exact = [&](int e) {
+        return exact_key<kSig>(ld_logit(g.logits, row + e, kF32), kBias ? g.bias[e] : 0.0f, zmax, sum);
+    };
+    auto next = [](double& a, double& b, double k) {
+        b = k > a ? a : k > b ? k : b;
+        a = k > a ? k : a;
+    };
+    double a0 = -(double)INFINITY, b0 = a0, a1 = a0, b1 = a0;
+    int n = kCand + 1;
+    if (pieces) {
+        float in[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) in[i] = key[i] < (i < 8 ? least0 : least1) ? -1.0f : 1.0f;
+        n = find_candidates<kV>(in, 0.0f, i0, g.E, 0.0f, 0xFFFFFFFFu, list);
     }
-    return rank_groups<double>(g, v, sums);
+    if (__builtin_expect(!__ballot(n > kCand), 1)) {
+        wave_fence();
+        const double k0 = l16 < n ? exact(list[l16]) : 0.0, k1 = l16 + 16 < n ? exact(list[l16 + 16]) : 0.0;
+        sums[l16] = k0;
+        sums[l16 + 16] = k1;
+        wave_fence();
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
+            const int q = group_of(g, list[c]);
+            if (q == l16) next(a0, b0, sums[c]);
+            if (q == l16 + 16) next(a1, b1, sums[c]);
+        }
+        wave_fence();
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < g.group_size; ++i) {
+            if (l16 < g.groups) next(a0, b0, exact(l16 * g.group_size + i));
+            if (l16 + 16 < g.groups) next(a1, b1, exact((l16 + 16) * g.group_size + i));
+        }
+    }
+    const bool two = g.group_top == 2;
+    return rank_groups<double>(g, choice_key(two ? a0 + b0 : a0), choice_key(two ? a1 + b1 : a1), sums);
 }
 
-// The open groups of a row from its FP32 keys.  Sums of keys that rounding may have brought into a wrong
-// order (kNear for each of the two, relative to the largest key that enters any) go to 64 bits where
-// such a sum lies on either side of the border.  Logits order exactly, one a group.
+// The lane's keys that lie in the open groups of a row, from its FP32 keys.  Sums of keys that rounding may have
+// brought into a wrong order (kNear for each of the two, relative to the largest key that enters any) go
+// to 64 bits where such a sum lies on either side of the border.  Logits order exactly, one a group.
+//
+// A group of 1, 2, 4, 8 or 16 of the lanes' pieces (g.group_lanes) is merged by DPP, and its lanes know whether it is
+// open.  (All sizes by way of LDS, a lane to a group: 16384 x 256 23.6 us against XX.)
+// z: the keys of the choice, in which NaN becomes -inf.
 template <int kV, bool kF32, bool kSig, bool kBias>
-__device__ __forceinline__ uint32_t open_groups(const RouterArgs& g, int64_t row, const float key[kV], const float s[kV], int i0,
-                                                float2* pieces, float* sums, double* sums64) {
+__device__ __forceinline__ uint32_t open_groups(const RouterArgs& g, int64_t row, float z[kV], const float s[kV], int i0,
+                                                int* list, float* sums, double* sums64) {
+    constexpr int kP = kV < 8 ? kV : 8, kH = kV / kP;   // keys of a piece, pieces of a lane
+    const int l16 = threadIdx.x & 15;
     const bool by_score = !kBias && g.group_top == 2;
-    float k[kV];
+    float key[kV];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) k[i] = by_score ? key_score(s[i], key[i]) : key[i];
-    Two top[2];
-    group_tops<kV>(g, k, i0, pieces, top);
-    float v[2], most = 1.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        v[h] = choice_key(g.group_top == 2 ? top[h].a + top[h].b : top[h].a);
-        if (top[h].a > -INFINITY) most = __builtin_fmaxf(most, __builtin_fabsf(top[h].a));
-        if (top[h].b > -INFINITY && g.group_top == 2) most = __builtin_fmaxf(most, __builtin_fabsf(top[h].b));
+    for (int i = 0; i < kV; ++i) {
+        key[i] = z[i] = choice_key(z[i]);
+        if constexpr (!kBias) key[i] = by_score ? choice_key(key_score(s[i], z[i])) : z[i];
     }
-    const uint32_t open = rank_groups<float>(g, v, sums);
+    float most = 1.0f, border, over;                    // the smallest open sum, the largest closed one
+    uint32_t open;
+    float least0 = -INFINITY, least1 = -INFINITY;
+    auto enter = [&](const Two& t) {
+        if (t.a > -INFINITY) most = __builtin_fmaxf(most, __builtin_fabsf(t.a));
+        if (t.b > -INFINITY && g.group_top == 2) most = __builtin_fmaxf(most, __builtin_fabsf(t.b));
+    };
+    if (__builtin_expect(g.group_lanes > 0, 1)) {
+        Two t[kH];
+        float v[kH];
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+            t[h] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kP; ++i) add(t[h], key[h * kP + i]);
+        }
+        // lanes of one group: the neighbour, the other pair, the other four, the other eight
+        if (g.group_lanes > 1)
+#pragma unroll
+            for (int h = 0; h < kH; ++h) merge<0xB1>(t[h]);
+        if (g.group_lanes > 2)
+#pragma unroll
+            for (int h = 0; h < kH; ++h) merge<0x4E>(t[h]);
+        if (g.group_lanes > 4)
+#pragma unroll
+            for (int h = 0; h < kH; ++h) merge<0x141>(t[h]);
+        if (g.group_lanes > 8)
+#pragma unroll
+            for (int h = 0; h < kH; ++h) merge<0x140>(t[h]);
+        sums[l16] = sums[l16 + 16] = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+            v[h] = sum_of(g, t[h]);
+            enter(t[h]);
+            sums[(l16 + 16 * h) >> g.group_shift] = v[h];
+        }
+        wave_fence();
+        open = 0;
+        border = INFINITY;
+        over = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+            const int q = (l16 + 16 * h) >> g.group_shift;
+            if (q >= g.groups) continue;
+            if (groups_before<float>(g, sums, v[h], q) < g.top_groups) {
+                open |= ((1u << kP) - 1) << (kP * h);
+                border = __builtin_fminf(border, v[h]);
+            } else {
+                over = __builtin_fmaxf(over, v[h]);
+            }
+        }
+        wave_fence();
+        least0 = g.group_top == 2 ? t[0].b : t[0].a;
+        least1 = kH > 1 ? (g.group_top == 2 ? t[kH - 1].b : t[kH - 1].a) : least0;
+    } else {
+        // groups of other sizes one after another: each lane's two, then the row's; a lane keeps two groups'
+        Two t0 = {-INFINITY, -INFINITY}, t1 = t0;
+#pragma unroll 1
+        for (int q = 0; q < g.groups; ++q) {
+            Two t = {-INFINITY, -INFINITY};
+            const int first = q * g.group_size - i0;
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                if ((unsigned)(ahead(i) - first) < (unsigned)g.group_size) add(t, key[i]);
+            merge<0xB1>(t);
+            merge<0x4E>(t);
+            merge<0x141>(t);
+            merge<0x140>(t);
+            if (q == l16) t0 = t;
+            if (q == l16 + 16) t1 = t;
+        }
+        enter(t0);
+        enter(t1);
+        const float v0 = sum_of(g, t0), v1 = sum_of(g, t1);
+        const uint32_t groups = rank_groups<float>(g, v0, v1, sums);
+        open = open_keys<kV>(g, groups, i0);
+        border = INFINITY;
+        over = -INFINITY;
+        if (l16 < g.groups) (groups >> l16 & 1 ? border : over) = v0;
+        if (l16 + 16 < g.groups) {
+            if (groups >> (l16 + 16) & 1) border = __builtin_fminf(border, v1);
+            else over = __builtin_fmaxf(over, v1);
+        }
+    }
     if (!kBias && !by_score) return open;
-    float least = INFINITY, over = -INFINITY;           // the smallest open sum, the largest closed one
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int q = (threadIdx.x & 15) + 16 * h;
-        if (q >= g.groups) continue;
-        if (open >> q & 1) least = __builtin_fminf(least, v[h]);
-        else over = __builtin_fmaxf(over, v[h]);
-    }
-    least = -row_max(-least);
+    border = -row_max(-border);
     over = row_max(over);
-    const bool near = g.top_groups < g.groups && !(least - over > 2 * kNear * row_max(most));
+    most = row_max(most);
+    const bool near = g.top_groups < g.groups && !(border - over > 2 * kNear * most);
     if (__builtin_expect(!__ballot(near), 1)) return open;
-    return open_groups_exact<kV, kF32, kSig, kBias>(g, row, i0, sums64);
+    return open_keys<kV>(g, open_groups_exact<kV, kF32, kSig, kBias>(g, row, key, i0, g.group_lanes > 0, least0 - kNear * most,
+                                                                     least1 - kNear * most, list, sums64), i0);
 }
 
 // the loss from sum counts_e P_e and sum counts_e
@@ -610,8 +682,7 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
     constexpr int kR = kThr / 16;
     __shared__ int sel[kR][kCand];
     __shared__ __attribute__((aligned(16))) float keys[kR][kCand];
-    __shared__ double keys64[kBias || kGroups ? kR : 1][kCand];
-    __shared__ float2 pieces[kGroups ? kR : 1][kMaxGroups];
+    __shared__ __attribute__((aligned(32))) double keys64[kBias || kGroups ? kR : 1][kCand];
     static_assert(kMaxGroups <= kCand, "keys and keys64 hold the groups' sums too");
     __shared__ int cnt[256];
     __shared__ float sums[kThr / MOE_WAVE][256];
@@ -645,16 +716,10 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouterArgs g) {
         }
         uint32_t open = 0xFFFFFFFFu;                    // bit i: the lane's i-th key can be chosen
         if constexpr (kGroups) {
-            const uint32_t groups = open_groups<kV, kF32, kSig, kBias>(g, t * E, z, s, i0, pieces[row], keys[row], keys64[row]);
+            open = open_groups<kV, kF32, kSig, kBias>(g, t * E, z, s, i0, sel[row], keys[row], keys64[row]);
             wave_fence();
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const int e = i0 + ahead(i);
-                if (e < E && !(groups >> group_of(g, e) & 1)) {
-                    open &= ~(1u << i);
-                    z[i] = -INFINITY;
-                }
-            }
+            for (int i = 0; i < kV; ++i) z[i] = open >> i & 1 ? z[i] : -INFINITY;
         }
         int n = kCand + 1;
         if (k <= kTwoK) n = find_candidates<kV>(z, bound_of<kV, kGroups>(z, k), i0, E, kBias ? kNear : 0.0f, open, sel[row]);
@@ -1032,6 +1097,11 @@ hipError_t launch_route(RouterArgs g, bool sigmoid, bool f32, hipStream_t s) {
         if (g.groups < 0 || g.groups > kMaxGroups || g.E % g.groups != 0) return hipErrorInvalidValue;
         g.group_size = g.E / g.groups;
         g.group_magic = 65536 / g.group_size + 1;       // e / group_size = e * magic >> 16 for e < 256
+        const int piece = per_lane(g.E) < 8 ? per_lane(g.E) : 8, lanes = g.group_size / piece;
+        if (g.group_size % piece == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0) {
+            g.group_lanes = lanes;
+            g.group_shift = __builtin_ctz(lanes);
+        }
     }
     const int grid = router_blocks(g.T);
     switch (per_lane(g.E) * 2 + (f32 ? 1 : 0)) {
