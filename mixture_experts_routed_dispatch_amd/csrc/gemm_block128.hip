@@ -21,8 +21,9 @@
 // Workgroup tile 256 (P) x TQ (rows), waves of 128 x 64, a stage of 128 K in LDS while the next one
 // is copied into the other buffer by direct global-to-LDS copies, one continuous stream of stages per
 // workgroup over its tiles (the next tile's first stage is copied during the last of this one).
-// LDS rows are 128 bytes, 16-byte chunk c of row r at slot c ^ (r & 7): eight consecutive rows' same
-// chunks meet all banks once.
+// LDS rows are 128 bytes, 16-byte chunk c of row r at slot c ^ (r / 2 % 8): the same chunk of 16
+// consecutive rows, which a quarter of a wave reads, meets all 64 banks once.  (At slot c ^ (r & 7) half of the
+// reads' cycles were conflicts.)
 #include "block128.h"
 
 namespace moe {
@@ -49,6 +50,7 @@ __device__ __forceinline__ void tile_order(int local, int nQt, int nPt, int& pt,
 struct Tile {
     int e, mb, rows, pt, qt;
 };
+__device__ __forceinline__ int swz(int r) { return r >> 1 & 7; }
 
 template <int MODE, int kAct, int TQ>
 __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs g) {
@@ -158,15 +160,16 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     const bool q_scales = wave < TQ / 64;
     size_t sstep = 0;                                    // bytes between the scales of consecutive groups
     auto copy_offsets = [&](const Tile& c, int slot) {
-        const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
 #pragma unroll
-        for (int j = 0; j < kPCopies; ++j)
-            pvoff[j] = (uint32_t)p_row(c, 8 * (kPCopies * wave + j) + (lane >> 3)) * (uint32_t)K + chunk;
+        for (int j = 0; j < kPCopies; ++j) {
+            const int r = 8 * (kPCopies * wave + j) + (lane >> 3);
+            pvoff[j] = (uint32_t)p_row(c, r) * (uint32_t)K + 16 * ((lane & 7) ^ swz(r));
+        }
 #pragma unroll
         for (int j = 0; j < kQCopies; ++j) {
             const int r = 8 * (kQCopies * wave + j) + (lane >> 3);
             const int src = MODE == B128_W13 ? gsrc[slot][r] : routed_row(c, r) - (c.mb + c.qt * TQ);
-            qvoff[j] = (uint32_t)src * (uint32_t)K + chunk;
+            qvoff[j] = (uint32_t)src * (uint32_t)K + 16 * ((lane & 7) ^ swz(r));
         }
         qbase = reinterpret_cast<const char*>(g.qq);
         if constexpr (MODE != B128_W13) qbase += (size_t)(c.mb + c.qt * TQ) * K;
@@ -195,8 +198,8 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
 
     // ------------------------------------------------------------ a stage
     const int row16 = lane & 15, quad = lane >> 4;
-    // a fragment: 16 rows, lane (row16, quad) the chunks 2 quad and 2 quad + 1 of its row
-    const int c0 = ((2 * quad) ^ (row16 & 7)) * 16, c1 = ((2 * quad + 1) ^ (row16 & 7)) * 16;
+    // a fragment: 16 rows, lane (row16, quad) the chunks quad and quad + 4 of its row
+    const int c0 = (quad ^ swz(row16)) * 16, c1 = c0 ^ 64;
     const int poff = (wp * 128 + row16) * TK, qoff = kPBytes + (wq * 64 + row16) * TK;
     auto read_frag = [&](const char* row) {
         const i32x4_t x = *reinterpret_cast<const i32x4_t*>(row + c0);
@@ -283,7 +286,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
             const float s = block_scale(t0 > t1 ? t0 : t1), inv = 1.0f / s;
 #pragma unroll
             for (int m = 0; m < 4; ++m)
-                *reinterpret_cast<uint32_t*>(stg + r * 128 + (((4 * wp + m) ^ (r & 7)) * 16) + 4 * quad) =
+                *reinterpret_cast<uint32_t*>(stg + r * 128 + (((4 * wp + m) ^ swz(r)) * 16) + 4 * quad) =
                     block_codes4(acc[2 * m][b][0], acc[2 * m][b][1], acc[2 * m][b][2], acc[2 * m][b][3], s, inv);
             const int rr = c.qt * TQ + r;
             if (wp == 0 && quad == 0 && rr < c.rows) g.as[(size_t)c.pt * g.R + c.mb + rr] = s;
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
 #pragma unroll
         for (int it = 0; it < TQ / (8 * kWaves); ++it) {
             const int r = (it * kWaves + wave) * 8 + (lane >> 3), ch = lane & 7, rr = c.qt * TQ + r;
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((ch ^ (r & 7)) * 16));
+            const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((ch ^ swz(r)) * 16));
             if (rr < c.rows) *reinterpret_cast<uint4*>(g.aq + (size_t)(c.mb + rr) * g.Np + c.pt * 128 + ch * 16) = v;
         }
     };
