@@ -68,6 +68,13 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wp = wave & 1, wq = wave >> 1;
+    // The lane id read afresh where code runs once per tile: offsets that depend on it, hoisted out of the loop
+    // over tiles, would be spilled, and a reload waits for every copy in flight.
+    auto fresh_lane = []() {
+        int l;
+        asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+        return l;
+    };
     const int E = g.E, K = g.K, groups = K / TK;
     const int nPt = MODE == B128_W13 ? g.Np / 128 : (g.Np + TP - 1) / TP;
     const int prows = MODE == B128_W13 ? 2 * g.Np : g.Np;        // P rows of an expert
@@ -102,6 +109,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
 
     auto coords = [&](int tile) {
         // largest e with cum[e] <= tile = number of e in [1, E) with cum[e] <= tile
+        const int lane = fresh_lane();
         int lo = 0;
 #pragma unroll
         for (int base = 1; base < 257; base += 64) {
@@ -116,15 +124,15 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
         tile_order(tile - __builtin_amdgcn_readfirstlane(cum[lo]), (c.rows + TQ - 1) / TQ, nPt, c.pt, c.qt);
         return c;
     };
-    // row of P behind tile row r (clamped to the last)
+    // row of P behind tile row r.  A wave's 32 rows follow one another, or are 16 and 16.
     auto p_row = [&](const Tile& c, int r) {
         if constexpr (MODE == B128_W13) {
             // 16-row pieces: gate rows 128 pt + 16 j .., then the up rows of the same outputs
             const int i = c.pt * 128 + (r >> 5) * 16 + (r & 15);
             return (r & 16) ? g.Np + i : i;
         } else {
-            const int p = c.pt * TP + r;
-            return p < g.Np ? p : g.Np - 1;
+            // a second half past the last row is the first again
+            return c.pt * TP + (c.pt * TP + 128 < g.Np ? r : r & 127);
         }
     };
     // routed row behind tile row r (clamped to the expert's last)
@@ -147,6 +155,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     // A wave copies the tokens of the rows whose data it copies itself, a tile ahead.
     auto gather_dma = [&](const Tile& c, int slot) {
         if constexpr (MODE == B128_W13) {
+            const int lane = fresh_lane();
             const int r = 8 * kQCopies * wave + lane % (8 * kQCopies);
             const uint32_t dst = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) int*)&gsrc[slot][8 * kQCopies * wave];
             if (lane < 8 * kQCopies) dma4(dst, (uint32_t)routed_row(c, r) * 4u, reinterpret_cast<const char*>(g.gather));
@@ -155,13 +164,15 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     // Data: a wave copies consecutive 1 KiB pieces of either operand; lane l fetches 16 bytes that land
     // at piece + 16 l = row l / 8 of the piece, slot l % 8.  Scales: waves 0 .. TQ/64 - 1 one word
     // each of 64 rows, the others the words of the two squares of P that the tile meets.
-    uint32_t pvoff[kPCopies], qvoff[kQCopies], svoff;
+    static_assert(kPCopies == 4, "32 rows a wave");
+    uint32_t pvoff[2], qvoff[kQCopies], svoff;           // P: of even and odd pieces, the others by scalar offsets
     const char *pbase = nullptr, *qbase = nullptr, *sbase = nullptr;
     const bool q_scales = wave < TQ / 64;
     size_t sstep = 0;                                    // bytes between the scales of consecutive groups
     auto copy_offsets = [&](const Tile& c, int slot) {
+        const int lane = fresh_lane();
 #pragma unroll
-        for (int j = 0; j < kPCopies; ++j) {
+        for (int j = 0; j < 2; ++j) {
             const int r = 8 * (kPCopies * wave + j) + (lane >> 3);
             pvoff[j] = (uint32_t)p_row(c, r) * (uint32_t)K + 16 * ((lane & 7) ^ swz(r));
         }
@@ -187,7 +198,8 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
         }
     };
     auto dma_p = [&](int kt, int buf, int j) {
-        dma16(lds0 + buf * kBuf + (kPCopies * wave + j) * 1024, pvoff[j], pbase + kt * TK);
+        const size_t rows16 = (size_t)(MODE == B128_W13 ? g.Np : 16) * K;
+        dma16(lds0 + buf * kBuf + (kPCopies * wave + j) * 1024, pvoff[j & 1], pbase + kt * TK + (j >> 1) * rows16);
     };
     auto dma_q = [&](int kt, int buf, int j) {
         dma16(lds0 + buf * kBuf + kPBytes + (kQCopies * wave + j) * 1024, qvoff[j], qbase + kt * TK);
@@ -208,43 +220,74 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     };
     f32x4_t acc[8][4];
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    auto stage = [&](int buf, int next_kt) {
-        const char* base = lds + buf * kBuf;
-        const float* sc = reinterpret_cast<const float*>(lsc + buf * kSlot);
-        i32x8_t qf[4], pf = read_frag(base + poff);
+    i32x8_t qf[4], pf;                                   // the rows' fragments, the next one of P
+    float sq[4], sp[2];                                  // scales: of this lane's rows, of the wave's squares of P
+    auto read_q = [&](int buf, int b) {
+        qf[b] = read_frag(lds + buf * kBuf + qoff + b * 16 * TK);
+        sq[b] = reinterpret_cast<const float*>(lsc + buf * kSlot)[wq * 64 + b * 16 + row16];
+    };
+    auto read_p = [&](int buf, int a) { return read_frag(lds + buf * kBuf + poff + a * 16 * TK); };
+    auto read_sp = [&](int buf) {
+        const float* sc = reinterpret_cast<const float*>(lsc + buf * kSlot) + TQ;
+        sp[0] = sc[MODE == B128_W13 ? 0 : wp];
+        sp[1] = MODE == B128_W13 ? sc[1] : sp[0];
+    };
+    auto read_first = [&](int buf) {
+        pf = read_p(buf, 0);
+        read_sp(buf);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) read_q(buf, b);
+    };
+    // One stage from buffer buf, whose first fragments have been read: eight steps of one fragment of P.  A step
+    // issues its four products, each followed by the FMAs of the step before, reads the next fragment and
+    // issues copies of the stage at next_kt into the other buffer.  Before the last step everything of
+    // this buffer has been read and the next stage has landed (a barrier); unless the tile ends, that
+    // step reads the next stage's first fragments.
+    auto stage = [&](auto last_tag, int buf, int next_kt) {
+        constexpr bool kLast = decltype(last_tag)::value;
         float f0[4], f1[4];                              // factors; B128_W13: of gate and up rows
-        const float s0 = sc[TQ + (MODE == B128_W13 ? 0 : wp)], s1 = sc[TQ + 1];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            qf[b] = read_frag(base + qoff + b * 16 * TK);
-            const float sq = sc[wq * 64 + b * 16 + row16];
-            f0[b] = sq * s0;
-            f1[b] = MODE == B128_W13 ? sq * s1 : f0[b];
+            f0[b] = sq[b] * sp[0];
+            f1[b] = MODE == B128_W13 ? sq[b] * sp[1] : f0[b];
         }
-        dma_scales(next_kt, buf ^ 1);
         f32x4_t part[4];
 #pragma unroll
         for (int a = 0; a < 8; ++a) {
-            i32x8_t pn = a < 7 ? read_frag(base + poff + (a + 1) * 16 * TK) : pf;
-            f32x4_t now[4];
+            i32x8_t pn = pf;
+            if (a == 7) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __syncthreads();
+                if constexpr (!kLast) {
+                    pn = read_p(buf ^ 1, 0);
+                    read_sp(buf ^ 1);
+                }
+            } else {
+                pn = read_p(buf, a + 1);
+            }
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                now[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[b], zero, 0, 0, 0, 0, 0, 0);
+                const f32x4_t now = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[b], zero, 0, 0, 0, 0, 0, 0);
                 // the last fragment's results, while this one's are computed
                 if (a > 0)
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
                         acc[a - 1][b][z] = __builtin_fmaf(part[b][z], (a - 1) & 1 ? f1[b] : f0[b], acc[a - 1][b][z]);
+                // neither the products nor the FMAs have an ordering edge to anything here and would be
+                // emitted all together: an empty asm that takes their results keeps them in this step
+                asm volatile("" :: "v"(now));
+                if (a > 0) asm volatile("" : "+v"(acc[a - 1][b]));
+                part[b] = now;
+                if constexpr (!kLast) {
+                    if (a == 7) read_q(buf ^ 1, b);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                if (b == 1 && a < kPCopies) dma_p(next_kt, buf ^ 1, a);
+                if (b == 3 && a < kQCopies) dma_q(next_kt, buf ^ 1, a);
+                if (b == 3 && a == 4) dma_scales(next_kt, buf ^ 1);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            // neither the instructions nor the FMAs have an ordering edge to anything here and would
-            // be emitted all together: an empty asm that takes their results keeps them in this step
-            asm volatile("" :: "v"(now[0]), "v"(now[1]), "v"(now[2]), "v"(now[3]));
-            if (a > 0) asm volatile("" : "+v"(acc[a - 1][0]), "+v"(acc[a - 1][1]), "+v"(acc[a - 1][2]), "+v"(acc[a - 1][3]));
-            if (a < kPCopies) dma_p(next_kt, buf ^ 1, a);
-            if (a < kQCopies) dma_q(next_kt, buf ^ 1, a);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) part[b] = now[b];
             pf = pn;
         }
 #pragma unroll
@@ -258,6 +301,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     auto epilogue_w13 = [&](const Tile& c, int buf) {
         // a = f(g) u: fragments 2 m hold gate values, 2 m + 1 the up values of the same outputs,
         // i = 128 pt + 64 wp + 16 m + 4 quad + z of row 64 wq + 16 b + row16
+        const int lane = fresh_lane(), row16 = lane & 15, quad = lane >> 4;
         char* stg = lds + buf * kBuf;                    // codes [TQ][128], chunks as the stages'
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -302,6 +346,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     auto epilogue_plain = [&](const Tile& c, int buf) {
         // BF16 rows by way of this wave's 8 KiB of the buffer, stored as whole 256-byte pieces
         // past the caches (ordinary stores evict operands that the XCD's workgroups share)
+        const int lane = fresh_lane(), row16 = lane & 15, quad = lane >> 4;
         char* stg = lds + buf * kBuf + wave * 8192;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -329,8 +374,6 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     };
 
     // ------------------------------------------------------------ stream of stages
-    // Every stage ends with a wait for all of the wave's copies and a barrier: the next one has landed,
-    // and the buffer just read may be copied into.
     int l_tile = vid, l_kt = 0, gslot = 0;               // the load cursor
     Tile lc = coords(l_tile), nc = lc;
     gather_dma(lc, 0);
@@ -359,24 +402,27 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
 
     Tile cc = coords(vid);
     int buf = 0;
+    read_first(0);
     for (int c_tile = vid;;) {
 #pragma unroll
         for (int a = 0; a < 8; ++a)
 #pragma unroll
             for (int b = 0; b < 4; ++b) acc[a][b] = zero;
-        for (int kt = 0; kt < groups; ++kt) {
-            stage(buf, l_kt);
+        for (int kt = 1; kt < groups; ++kt) {
+            stage(std::false_type(), buf, l_kt);
             advance_load();
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
             buf ^= 1;
         }
-        if constexpr (MODE == B128_W13) epilogue_w13(cc, buf ^ 1);
-        else epilogue_plain(cc, buf ^ 1);
+        stage(std::true_type(), buf, l_kt);
+        advance_load();
+        if constexpr (MODE == B128_W13) epilogue_w13(cc, buf);
+        else epilogue_plain(cc, buf);
+        buf ^= 1;
         c_tile += G;
         if (c_tile >= total) break;
         __syncthreads();                                 // the staging rows are copied into again
         cc = coords(c_tile);
+        read_first(buf);
     }
 }
 
