@@ -13,26 +13,30 @@ namespace {
 // The scale of a block from the bits of its largest magnitude (magnitudes of floats order like
 // their bits, infinities and NaN above all): amax / 448 rounded once, at least 2^-100, which keeps
 // the quotients' remainders below exact; NaN for a block that holds an infinity or NaN, so that
-// what is computed from it is NaN.
+// what is computed from it is NaN.  With r = 1 / 448 rounded, the quotient a r plus its remainder times r
+// is the correctly rounded one (Markstein's theorem; where a is too small for that the floor holds).
 __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-    if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-    return __builtin_fmaxf(__uint_as_float(amax_bits) / 448.0f, 0x1p-100f);
+    constexpr float r = 1.0f / 448.0f;
+    const float a = __uint_as_float(amax_bits), q = a * r;
+    const float s = __builtin_fmaxf(__builtin_fmaf(__builtin_fmaf(-q, 448.0f, a), r, q), 0x1p-100f);
+    return amax_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : s;
 }
+// 1 / s within an ulp, for block_quotient
+__device__ __forceinline__ float block_inverse(float s) { return __builtin_amdgcn_rcpf(s); }
 
 // v / s for |v| <= 448 s (1 + 2^-24), as a float that rounds to the same E4M3 value as the exact
 // quotient does (nearest, ties to even).  q is within an ulp of the quotient.  Where it is not the
 // quotient itself and its last bit is 0, it goes one ulp towards the quotient: E4M3 values and the
 // midpoints between them have that bit 0, so none of them lies between the result and the
 // quotient.  The sign of the remainder v - q s is that of the exact one, which fma rounds once.
-// inv = 1 / s within an ulp.
 __device__ __forceinline__ float block_quotient(float v, float s, float inv) {
     const float a = __builtin_fabsf(v);
     float q = a * inv;
     q = __builtin_fmaf(__builtin_fmaf(-q, s, a), inv, q);
     const float rest = __builtin_fmaf(-q, s, a);
     uint32_t b = __float_as_uint(q);
-    const uint32_t towards = rest > 0.0f ? b + 1 : b - 1;      // rest < 0 only where q > 0
-    b = rest != 0.0f && (b & 1) == 0 ? towards : b;
+    b -= rest < 0.0f;                                  // (only where q > 0)
+    b |= rest != 0.0f;
     return __builtin_copysignf(__uint_as_float(b), v);
 }
 

@@ -16,25 +16,50 @@ constexpr int kThreads = 256;
 constexpr int kB = 128;
 
 // 16 lanes hold a block of a row, 8 elements each; a wave takes four consecutive blocks.
-// rows_dev (optional): only the first *rows_dev rows (at most rows).
-__global__ __launch_bounds__(kThreads) void rows_kernel(const uint16_t* __restrict__ v, int64_t rows, int groups,
-                                                        const int32_t* __restrict__ rows_dev, bool block_major,
+__global__ __launch_bounds__(kThreads) void rows_kernel(const uint16_t* __restrict__ v, int64_t blocks,
                                                         uint8_t* __restrict__ codes, float* __restrict__ scales) {
+    const int64_t step = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < blocks * 16; i += step) {
+        const uint4 x = *reinterpret_cast<const uint4*>(v + i * 8);
+        const float s = block_scale(max16(bf16_amax_bits(x)));
+        *reinterpret_cast<uint2*>(codes + i * 8) = block_codes8(x, s, block_inverse(s));
+        if ((threadIdx.x & 15) == 0) scales[i >> 4] = s;
+    }
+}
+
+// The same with block-major scales: a workgroup takes four blocks of 16 rows, a wave the four of every fourth row, and
+// writes 16 consecutive scales at a time.  (Each wave the scales of its own four blocks: 65536 x 1536 83 us against
+// XX.)  rows_dev (optional): only the first *rows_dev rows (at most rows).
+__global__ __launch_bounds__(kThreads) void rows_block_major_kernel(const uint16_t* __restrict__ v, int64_t rows, int groups,
+                                                                    const int32_t* __restrict__ rows_dev,
+                                                                    uint8_t* __restrict__ codes, float* __restrict__ scales) {
+    __shared__ float sc[4][16];
     int64_t n = rows;
     if (rows_dev) {
         n = *rows_dev;
         n = n < 0 ? 0 : n < rows ? n : rows;
     }
-    const int64_t pieces = n * groups * 16, step = (int64_t)gridDim.x * kThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < pieces; i += step) {
-        const uint4 x = *reinterpret_cast<const uint4*>(v + i * 8);
-        const float s = block_scale(max16(bf16_amax_bits(x)));
-        *reinterpret_cast<uint2*>(codes + i * 8) = block_codes8(x, s, 1.0f / s);
-        if ((threadIdx.x & 15) == 0) {
-            const int64_t b = i >> 4, row = b / groups, g = b - row * groups;
-            scales[block_major ? g * rows + row : b] = s;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, block = lane >> 4;
+    const uint32_t spans = (uint32_t)(groups + 3) / 4, rg = blockIdx.x / spans, span = blockIdx.x - rg * spans;
+    const int64_t row0 = (int64_t)rg * 16;
+    if (row0 >= n) return;
+    const int g = 4 * span + block;
+    const bool in = g < groups;
+    const int64_t at = (row0 + wave) * groups * kB + 512 * span + 8 * lane;
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (in && row0 + wave + 4 * u < n) x[u] = *reinterpret_cast<const uint4*>(v + at + (int64_t)4 * u * groups * kB);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (in && row0 + wave + 4 * u < n) {
+            const float s = block_scale(max16(bf16_amax_bits(x[u])));
+            *reinterpret_cast<uint2*>(codes + at + (int64_t)4 * u * groups * kB) = block_codes8(x[u], s, block_inverse(s));
+            if ((lane & 15) == 0) sc[block][wave + 4 * u] = s;
         }
-    }
+    __syncthreads();
+    const int b = threadIdx.x >> 4, r = threadIdx.x & 15;
+    if (threadIdx.x < 64 && 4 * (int)span + b < groups && row0 + r < n) scales[(int64_t)(4 * span + b) * rows + row0 + r] = sc[b][r];
 }
 
 // the same of FP32 rows, row-major scales
@@ -53,7 +78,7 @@ __global__ __launch_bounds__(kThreads) void rows_f32_kernel(const float* __restr
                 top = top > m ? top : m;
             }
         }
-        const float s = block_scale(max16(top)), inv = 1.0f / s;
+        const float s = block_scale(max16(top)), inv = block_inverse(s);
         *reinterpret_cast<uint2*>(codes + i * 8) = make_uint2(block_codes4(x[0][0], x[0][1], x[0][2], x[0][3], s, inv),
                                                               block_codes4(x[1][0], x[1][1], x[1][2], x[1][3], s, inv));
         if ((threadIdx.x & 15) == 0) scales[i >> 4] = s;
@@ -88,7 +113,7 @@ __global__ __launch_bounds__(kThreads) void squares_kernel(Block128Pair args) {
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kThreads / MOE_WAVE; ++w) top = top > tops[w] ? top : tops[w];
-        const float s = block_scale(top), inv = 1.0f / s;
+        const float s = block_scale(top), inv = block_inverse(s);
 #pragma unroll
         for (int r = 0; r < 8; ++r)
             *reinterpret_cast<uint2*>(m.codes + at + (int64_t)4 * r * m.K) = block_codes8(x[r], s, inv);
@@ -178,11 +203,16 @@ int grid_of(int64_t n, int64_t most) { return (int)(n < 1 ? 1 : n < most ? n : m
 
 hipError_t launch_block128_rows(const uint16_t* v, int64_t rows, int K, uint8_t* codes, float* scales, bool block_major,
                                 const int32_t* rows_dev, hipStream_t s) {
-    if (rows < 0 || K <= 0 || K % kB != 0) return hipErrorInvalidValue;
+    if (rows < 0 || K <= 0 || K % kB != 0 || (rows_dev && !block_major)) return hipErrorInvalidValue;
     if (rows == 0) return hipSuccess;
-    const int64_t wgs = (rows * (K / 8) + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(rows_kernel, dim3(grid_of(wgs, 65536)), dim3(kThreads), 0, s, v, rows, K / kB, rows_dev,
-                       block_major, codes, scales);
+    if (block_major) {
+        const int64_t wgs = (rows + 15) / 16 * ((K / kB + 3) / 4);
+        if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(rows_block_major_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, v, rows, K / kB, rows_dev, codes, scales);
+    } else {
+        const int64_t wgs = (rows * (K / 8) + kThreads - 1) / kThreads;
+        hipLaunchKernelGGL(rows_kernel, dim3(grid_of(wgs, 65536)), dim3(kThreads), 0, s, v, rows * (K / kB), codes, scales);
+    }
     return hipGetLastError();
 }
 

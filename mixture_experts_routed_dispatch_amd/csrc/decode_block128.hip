@@ -47,7 +47,7 @@ __device__ __forceinline__ void quantize_rows(const uint16_t* x, int64_t blocks,
     for (int64_t i = first; i < blocks * 16; i += step) {
         const uint4 v = *reinterpret_cast<const uint4*>(x + i * 8);
         const float s = block_scale(max16(bf16_amax_bits(v)));
-        *reinterpret_cast<uint2*>(xq + i * 8) = block_codes8(v, s, 1.0f / s);
+        *reinterpret_cast<uint2*>(xq + i * 8) = block_codes8(v, s, block_inverse(s));
         if ((i & 15) == 0) xs[i >> 4] = s;
     }
 }
@@ -119,7 +119,7 @@ template <int kTiles, typename Row0>
 __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], __amdgpu_buffer_rsrc_t codes, const float* scales,
                                               Row0&& row0, int K, __amdgpu_buffer_rsrc_t rows, __amdgpu_buffer_rsrc_t row_scales,
                                               uint32_t ro, uint32_t so, int s0, int s1) {
-    constexpr int kDepth = 2;
+    constexpr int kDepth = kTiles == 1 ? 4 : 2;          // operand sets, all but one on their way
     const int lane = threadIdx.x & 63, S = K / 128;
     uint32_t co = (uint32_t)(lane & 15) * K + 16u * (lane >> 4);
     ro += 16u * (lane >> 4);
@@ -148,12 +148,13 @@ __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], __amdgpu_b
     };
     if (s0 >= s1) return;
     Operands8<kTiles> w[kDepth];
-    load(w[0], s0);
+#pragma unroll
+    for (int u = 0; u < kDepth - 1; ++u) load(w[u], s0 + u);
     for (int s = s0; s < s1; s += kDepth) {
 #pragma unroll
         for (int u = 0; u < kDepth; ++u) {
             if (s + u >= s1) return;
-            load(w[(u + 1) % kDepth], s + u + 1);
+            load(w[(u + kDepth - 1) % kDepth], s + u + kDepth - 1);
             products(w[u]);
         }
     }
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(kThreads, kWGs) void product_rows(Block128RowsArgs 
 // (lanes 16 j .. 16 j + 15: block j)
 __device__ __forceinline__ float stage_bf16(const uint4 v, char* at) {
     const float s = block_scale(max16(bf16_amax_bits(v)));
-    *reinterpret_cast<uint2*>(at + 8 * (threadIdx.x & 63)) = block_codes8(v, s, 1.0f / s);
+    *reinterpret_cast<uint2*>(at + 8 * (threadIdx.x & 63)) = block_codes8(v, s, block_inverse(s));
     return s;
 }
 __device__ __forceinline__ float stage_f32(f32x4_t a, f32x4_t b, char* at) {
@@ -269,7 +270,7 @@ __device__ __forceinline__ float stage_f32(f32x4_t a, f32x4_t b, char* at) {
         top = top > ma ? top : ma;
         top = top > mb ? top : mb;
     }
-    const float s = block_scale(max16(top)), inv = 1.0f / s;
+    const float s = block_scale(max16(top)), inv = block_inverse(s);
     *reinterpret_cast<uint2*>(at + 8 * (threadIdx.x & 63)) =
         make_uint2(block_codes4(a[0], a[1], a[2], a[3], s, inv), block_codes4(b[0], b[1], b[2], b[3], s, inv));
     return s;
@@ -278,8 +279,54 @@ __device__ __forceinline__ float of_block(float s, int j) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s), 16 * j));
 }
 
-// A workgroup per (slot, 16 outputs), its four waves a quarter of K each.  Every column of the
-// instruction is the token.
+// kT tiles of 16 weight rows times one row in BF16: this wave's share s0 .. s1 of K's steps, kChunk at a time.
+// The row's piece is loaded before the weights, so that it is quantized while they are on their way (loads
+// come back in order).  Every column of the instruction is the row.  row0(t): tile t's first row; scale(t): the
+// scales of its squares along K.
+template <int kT, int kChunk, typename Row0, typename Scale>
+__device__ __forceinline__ void one_row(f32x4_t (&acc)[kT], __amdgpu_buffer_rsrc_t codes, Row0&& row0, Scale&& scale, int K,
+                                        __amdgpu_buffer_rsrc_t xr, char* stage, int s0, int s1) {
+    static_assert(kChunk % 4 == 0, "a load of the row is four blocks");
+    const int lane = threadIdx.x & 63, quad = lane >> 4;
+    const uint32_t co = (uint32_t)(lane & 15) * K + 16u * quad;
+    for (int s = s0; s < s1; s += kChunk) {
+        i32x4_t c[kT][kChunk][2], x[kChunk / 4];
+        float f[kT][kChunk];
+        // past s1 a row's pieces belong to the next wave, or lie past the resource's end: not used
+#pragma unroll
+        for (int h = 0; h < kChunk / 4; ++h) x[h] = load16(xr, 16u * lane, 256 * (s + 4 * h), 0);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j)
+            if (s + j < s1)
+#pragma unroll
+                for (int t = 0; t < kT; ++t) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) c[t][j][h] = load16(codes, co, row0(t) * K + 128 * (s + j) + 64 * h, kNonTemporal);
+                    f[t][j] = scale(t)[s + j];
+                }
+        float xs[kChunk / 4];
+#pragma unroll
+        for (int h = 0; h < kChunk / 4; ++h) xs[h] = stage_bf16(__builtin_bit_cast(uint4, x[h]), stage + 512 * h);
+        wave_fence();
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j)
+            if (s + j < s1) {
+                const char* b = stage + 128 * j + 16 * quad;
+                const i32x8_t xv = join(*reinterpret_cast<const i32x4_t*>(b), *reinterpret_cast<const i32x4_t*>(b + 64));
+                const float sx = of_block(xs[j / 4], j & 3);
+#pragma unroll
+                for (int t = 0; t < kT; ++t) {
+                    const f32x4_t p = mma128(join(c[t][j][0], c[t][j][1]), xv);
+                    const float ff = sx * f[t][j];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) acc[t][z] = __builtin_fmaf(p[z], ff, acc[t][z]);
+                }
+            }
+        wave_fence();
+    }
+}
+
+// A workgroup per (slot, 16 outputs), its four waves a quarter of K each.
 template <int kAct>
 __global__ __launch_bounds__(kThreads, 3) void decode8_w13_one(DecodeArgs g) {
     __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
@@ -290,47 +337,12 @@ __global__ __launch_bounds__(kThreads, 3) void decode8_w13_one(DecodeArgs g) {
     if ((unsigned)e >= (unsigned)g.E) return;
     const int lane = threadIdx.x & 63, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int d = g.d, S = d / 128, i0 = 16 * blockIdx.x;
-    const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
     const size_t matrix = (size_t)2 * g.I * d;
-    const __amdgpu_buffer_rsrc_t codes = rows_rsrc(reinterpret_cast<const uint8_t*>(g.w13) + e * matrix, (uint32_t)matrix);
-    const __amdgpu_buffer_rsrc_t xr = rows_rsrc(g.x, (uint32_t)d * 2u);
     const float* ws = reinterpret_cast<const float*>(g.w13_scale) + (size_t)e * (2 * g.I / 128) * S + i0 / 128 * S;
-    const uint32_t co = (uint32_t)(lane & 15) * d + 16u * quad;
-    const int up = g.I / 128 * S;                        // from a gate square's scale to the up square's
     f32x4_t acc[2] = {};
-    for (int s = s0; s < s1; s += 4) {
-        i32x4_t c[2][4][2];
-        float f[2][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (s + j < s1)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        c[t][j][h] = load16(codes, co, (t * g.I + i0) * d + 128 * (s + j) + 64 * h, kNonTemporal);
-                    f[t][j] = ws[t * up + s + j];
-                }
-        // past s1 a row's pieces belong to the next wave, or lie past the resource's end: not used
-        const uint4 x = __builtin_bit_cast(uint4, load16(xr, 16u * lane, 256 * s, 0));
-        const float xs = stage_bf16(x, stage[wave]);
-        wave_fence();
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (s + j < s1) {
-                const char* b = stage[wave] + 128 * j + 16 * quad;
-                const i32x8_t xv = join(*reinterpret_cast<const i32x4_t*>(b), *reinterpret_cast<const i32x4_t*>(b + 64));
-                const float sx = of_block(xs, j);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const f32x4_t p = mma128(join(c[t][j][0], c[t][j][1]), xv);
-                    const float ff = sx * f[t][j];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) acc[t][z] = __builtin_fmaf(p[z], ff, acc[t][z]);
-                }
-            }
-        wave_fence();
-    }
+    one_row<2, 4>(acc, rows_rsrc(reinterpret_cast<const uint8_t*>(g.w13) + e * matrix, (uint32_t)matrix),
+                  [&](int t) { return t * g.I + i0; }, [&](int t) { return ws + t * (g.I / 128 * S); }, d,
+                  rows_rsrc(g.x, (uint32_t)d * 2u), stage[wave], S * wave / kWaves, S * (wave + 1) / kWaves);
     const f32x4_t gate = reduce_waves<true>(acc[0], red, par), uv = reduce_waves<true>(acc[1], red, par);
     if (threadIdx.x < MOE_WAVE && (lane & 15) == 0) {
         f32x4_t v;
@@ -340,11 +352,28 @@ __global__ __launch_bounds__(kThreads, 3) void decode8_w13_one(DecodeArgs g) {
     }
 }
 
+// One row through one matrix: a workgroup for 16 outputs.
+__global__ __launch_bounds__(kThreads, 3) void product_one(Block128RowsArgs g) {
+    __shared__ f32x4_t red[2][kWaves][MOE_WAVE];
+    __shared__ __attribute__((aligned(16))) char stage[kWaves][1024];
+    int par = 0;
+    const int lane = threadIdx.x & 63, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int K = g.K, S = K / 128, n0 = 16 * blockIdx.x;
+    const float* ws = g.ws + n0 / 128 * S;
+    f32x4_t acc[1] = {};
+    one_row<1, 8>(acc, rows_rsrc(g.w, (uint32_t)g.N * (uint32_t)K), [&](int) { return n0; }, [&](int) { return ws; }, K,
+                  rows_rsrc(g.x, (uint32_t)K * 2u), stage[wave], S * wave / kWaves, S * (wave + 1) / kWaves);
+    const f32x4_t v = reduce_waves<true>(acc[0], red, par);
+    if (threadIdx.x < MOE_WAVE && (lane & 15) == 0)
+        *reinterpret_cast<uint2*>(g.y + n0 + 4 * quad) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+
 // W2 of all k experts and the combine, 8 output features per workgroup: rows 0 .. 7 of the instruction
 // are those features of expert 2 p, rows 8 .. 15 of expert 2 p + 1; even columns are a_2p, odd ones
 // a_2p+1 (half of the results belong to no expert and are not used).
 __global__ __launch_bounds__(kThreads, 2) void decode8_w2_one(DecodeArgs g) {
-    __shared__ __attribute__((aligned(16))) char stage[kWaves][2][512];
+    constexpr int kChunk = 8;
+    __shared__ __attribute__((aligned(16))) char stage[kWaves][2][128 * kChunk];
     __shared__ float ov[kMaxTopK][8];
     __shared__ float sc[kMaxTopK];
     const int tid = threadIdx.x, lane = tid & 63, row16 = lane & 15, quad = lane >> 4;
@@ -370,11 +399,19 @@ __global__ __launch_bounds__(kThreads, 2) void decode8_w2_one(DecodeArgs g) {
             const uint32_t ax = ex >= 0 ? (uint32_t)(2 * p * I) * 4u + 32u * lane : kNoRow;
             const uint32_t ay = ey >= 0 ? (uint32_t)((2 * p + 1) * I) * 4u + 32u * lane : kNoRow;
             f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-            for (int s = 0; s < S; s += 4) {
-                i32x4_t c[4][2], a[4];
-                float fx[4], fy[4];
+            // kChunk steps at a time; a's pieces are loaded before the weights, as in one_row
+            for (int s = 0; s < S; s += kChunk) {
+                i32x4_t c[kChunk][2], a[kChunk / 4][4];
+                float fx[kChunk], fy[kChunk];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int q = 0; q < kChunk / 4; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        a[q][h] = load16(ar, s + 4 * q < S ? ax + 16u * h : kNoRow, 512 * (s + 4 * q), 0);
+                        a[q][2 + h] = load16(ar, s + 4 * q < S ? ay + 16u * h : kNoRow, 512 * (s + 4 * q), 0);
+                    }
+#pragma unroll
+                for (int j = 0; j < kChunk; ++j)
                     if (s + j < S) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
@@ -382,21 +419,20 @@ __global__ __launch_bounds__(kThreads, 2) void decode8_w2_one(DecodeArgs g) {
                         fx[j] = wsx[s + j];
                         fy[j] = wsy[s + j];
                     }
+                float sx[kChunk / 4], sy[kChunk / 4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    a[h] = load16(ar, ax + 16u * h, 512 * s, 0);
-                    a[2 + h] = load16(ar, ay + 16u * h, 512 * s, 0);
+                for (int q = 0; q < kChunk / 4; ++q) {
+                    sx[q] = stage_f32(__builtin_bit_cast(f32x4_t, a[q][0]), __builtin_bit_cast(f32x4_t, a[q][1]), stage[wave][0] + 512 * q);
+                    sy[q] = stage_f32(__builtin_bit_cast(f32x4_t, a[q][2]), __builtin_bit_cast(f32x4_t, a[q][3]), stage[wave][1] + 512 * q);
                 }
-                const float sx = stage_f32(__builtin_bit_cast(f32x4_t, a[0]), __builtin_bit_cast(f32x4_t, a[1]), stage[wave][0]);
-                const float sy = stage_f32(__builtin_bit_cast(f32x4_t, a[2]), __builtin_bit_cast(f32x4_t, a[3]), stage[wave][1]);
                 wave_fence();
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < kChunk; ++j)
                     if (s + j < S) {
                         const char* b = stage[wave][row16 & 1] + 128 * j + 16 * quad;
                         const f32x4_t r = mma128(join(c[j][0], c[j][1]), join(*reinterpret_cast<const i32x4_t*>(b),
                                                                               *reinterpret_cast<const i32x4_t*>(b + 64)));
-                        const float f = quad < 2 ? fx[j] * of_block(sx, j) : fy[j] * of_block(sy, j);
+                        const float f = quad < 2 ? fx[j] * of_block(sx[j / 4], j & 3) : fy[j] * of_block(sy[j / 4], j & 3);
 #pragma unroll
                         for (int z = 0; z < 4; ++z) acc[z] = __builtin_fmaf(r[z], f, acc[z]);
                     }
@@ -464,6 +500,10 @@ hipError_t launch_decode8_w2(const DecodeArgs& g, int num_cu, hipStream_t s) {
 hipError_t launch_block128_few_rows(const Block128RowsArgs& g, int num_cu, hipStream_t s) {
     if (g.R <= 0) return hipSuccess;
     if (g.R > kMaxDecodeRows || g.E <= 0 || g.E > 256 || g.N % 128 != 0 || g.K % 128 != 0) return hipErrorInvalidValue;
+    if (g.R == 1 && !g.m_indptr) {
+        hipLaunchKernelGGL(product_one, dim3(g.N / 16), dim3(kThreads), 0, s, g);
+        return hipGetLastError();
+    }
     const int pieces = (g.R * (g.K / 8) + kThreads - 1) / kThreads;
     hipLaunchKernelGGL(product_prepare, dim3(1 + (pieces < 1024 ? pieces : 1024)), dim3(kThreads), 0, s, g);
     const hipError_t e = hipGetLastError();

@@ -327,7 +327,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
         for (int b = 0; b < 4; ++b) {
             const int r = wq * 64 + b * 16 + row16;
             const uint32_t t0 = tops[0][r], t1 = tops[1][r];
-            const float s = block_scale(t0 > t1 ? t0 : t1), inv = 1.0f / s;
+            const float s = block_scale(t0 > t1 ? t0 : t1), inv = block_inverse(s);
 #pragma unroll
             for (int m = 0; m < 4; ++m)
                 *reinterpret_cast<uint32_t*>(stg + r * 128 + (((4 * wp + m) ^ swz(r)) * 16) + 4 * quad) =

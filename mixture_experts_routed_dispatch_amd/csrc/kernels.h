@@ -258,7 +258,8 @@ inline bool block128_few_rows(int64_t R, int E) { return R <= kMaxDecodeRows && 
 hipError_t launch_block128_few_rows(const Block128RowsArgs& g, int num_cu, hipStream_t s);
 
 // E4M3 codes with one FP32 scale per 128 (block128.hip).  Rows: scales [rows, K/128], or with
-// block_major [K/128, rows]; rows_dev (optional, device): only the first min(rows, *rows_dev) rows.
+// block_major [K/128, rows]; rows_dev (optional, device, with block_major): only the first
+// min(rows, *rows_dev) rows.
 // Weights: one scale per 128 x 128, one or two matrices [E, N, K] a launch (w NULL: none).  K and N
 // multiples of 128, tensors 16-byte aligned.
 struct Block128Matrix {
