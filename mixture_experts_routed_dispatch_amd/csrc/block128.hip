@@ -146,15 +146,27 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Block128Pair args) {
     }
 }
 
+// m_out [E+1] = m_in where it rises from 0 to at most R, else zeros and the flag; m_in NULL: 0, R.  By one workgroup.
+__device__ __forceinline__ void write_segments(const Segments& g) {
+    bool bad = false;
+    for (int i = threadIdx.x; g.in && i <= g.E; i += kThreads) bad |= i == 0 ? g.in[0] != 0 : g.in[i] < g.in[i - 1] || g.in[i] > g.R;
+    bad = __syncthreads_or(bad);
+    for (int i = threadIdx.x; i <= g.E; i += kThreads) g.out[i] = bad ? 0 : g.in ? g.in[i] : i == 0 ? 0 : g.R;
+    if (bad && threadIdx.x == 0 && g.status) atomicOr(g.status, kDevBadIndptr);
+}
+__global__ __launch_bounds__(kThreads) void segments_kernel(Segments g) { write_segments(g); }
+
 // Transpose of codes [E, N, K] to [E, K, N] and of their scales, a 128 x 128 square a workgroup, by
-// way of LDS (row stride 132: a column's bytes meet different banks).
+// way of LDS (row stride 132: a column's bytes meet different banks).  seg (out NULL: none) is written along
+// with it, which saves a launch.
 constexpr int kLd = 132;
 __global__ __launch_bounds__(kThreads) void transpose_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
                                                              int N, int K, uint8_t* __restrict__ codes_t,
-                                                             float* __restrict__ scales_t) {
+                                                             float* __restrict__ scales_t, Segments seg) {
     __shared__ uint32_t tile[kB * kLd / 4];
     const int t = threadIdx.x, bk = blockIdx.x, bn = blockIdx.y;
     const int64_t e = blockIdx.z;
+    if (seg.out && bk == 0 && bn == 0 && e == 0) write_segments(seg);
     const uint8_t* src = codes + (e * N + bn * kB) * K + bk * kB;
     uint8_t* dst = codes_t + (e * K + bk * kB) * N + bn * kB;
 #pragma unroll
@@ -180,16 +192,6 @@ __global__ __launch_bounds__(kThreads) void transpose_kernel(const uint8_t* __re
         *reinterpret_cast<uint4*>(dst + (int64_t)(4 * c + j) * N + 16 * g) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     if (t == 0) scales_t[(e * (K / kB) + bk) * (N / kB) + bn] = scales[(e * (N / kB) + bn) * (K / kB) + bk];
-}
-
-__global__ __launch_bounds__(kThreads) void segments_kernel(const int32_t* __restrict__ m_in, int E, int R,
-                                                            int32_t* __restrict__ m_out, int32_t* __restrict__ status) {
-    bool bad = false;
-    for (int i = threadIdx.x; m_in && i <= E; i += kThreads)
-        bad |= i == 0 ? m_in[0] != 0 : m_in[i] < m_in[i - 1] || m_in[i] > R;
-    bad = __syncthreads_or(bad);
-    for (int i = threadIdx.x; i <= E; i += kThreads) m_out[i] = bad ? 0 : m_in ? m_in[i] : i == 0 ? 0 : R;
-    if (bad && threadIdx.x == 0 && status) atomicOr(status, kDevBadIndptr);
 }
 
 bool shapes_ok(const Block128Pair& g) {
@@ -239,16 +241,17 @@ hipError_t launch_block128_expand(Block128Pair g, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_segments(const int32_t* m_in, int E, int R, int32_t* m_out, int32_t* status, hipStream_t s) {
-    if (E <= 0 || E > 256 || R < 0 || (!m_in && E != 1)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(segments_kernel, dim3(1), dim3(kThreads), 0, s, m_in, E, R, m_out, status);
+hipError_t launch_segments(const Segments& g, hipStream_t s) {
+    if (g.E <= 0 || g.E > 256 || g.R < 0 || (!g.in && g.E != 1)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(segments_kernel, dim3(1), dim3(kThreads), 0, s, g);
     return hipGetLastError();
 }
 
 hipError_t launch_block128_transpose(const uint8_t* codes, const float* scales, int E, int N, int K, uint8_t* codes_t,
-                                     float* scales_t, hipStream_t s) {
+                                     float* scales_t, const Segments& seg, hipStream_t s) {
+    if (seg.out && (seg.E <= 0 || seg.E > 256 || seg.R < 0 || (!seg.in && seg.E != 1))) return hipErrorInvalidValue;
     if (E <= 0 || N <= 0 || K <= 0 || N % kB != 0 || K % kB != 0 || N / kB > 65535 || E > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(transpose_kernel, dim3(K / kB, N / kB, E), dim3(kThreads), 0, s, codes, scales, N, K, codes_t, scales_t);
+    hipLaunchKernelGGL(transpose_kernel, dim3(K / kB, N / kB, E), dim3(kThreads), 0, s, codes, scales, N, K, codes_t, scales_t, seg);
     return hipGetLastError();
 }
 

@@ -77,13 +77,19 @@ __device__ __forceinline__ void tile_order(int local, int nQt, int nPt, int& pt,
     qt = gi * kQGroup + (rem - pt * gsz);
 }
 
+// pieces of an expert with kp padded rows
+__device__ __forceinline__ int mx_pieces(int most, int kp) { return most < kp / kMxWgradPad ? most : kp / kMxWgradPad; }
+
 struct TileCtx {
     int e, mb, rows, pt, qt, nk;
     int koff, kp;                      // MX_WGRAD: the expert's token-layout offset and padded rows
+    int k0, slot;                      // split MX_WGRAD: the piece's first stage and its partial sums' slot
 };
 
 // kProd only names the instance (1: the W13-side product of MX_PLAIN / MX_WGRAD), so that
-// per-kernel traces and counters tell the two backward products of a mode apart.
+// per-kernel traces and counters tell the two backward products of a mode apart; but 2 is the split MX_WGRAD:
+// an expert's rows are cut into up to g.pieces pieces (whole units of 128 padded rows), each a work item of its own
+// with FP32 partial sums in g.part, for few matrices of few tiles (one of 2048 x 2048 has 64).
 template <int MODE, int kAct = kActSwiGLU, bool kSave = false, int kProd = 0>
 __global__ __launch_bounds__(NTHR, 1) void grouped_gemm_mx(MxGemmArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[NBUF * BUFB];
@@ -94,6 +100,7 @@ __global__ __launch_bounds__(NTHR, 1) void grouped_gemm_mx(MxGemmArgs g) {
     __shared__ int wtot[NTHR / MOE_WAVE];
     __shared__ int worder[256], wkp[256], wkoff[256];   // MX_WGRAD: work order, padded rows, offsets
     constexpr bool kWgrad = MODE == MX_WGRAD;
+    constexpr bool kSplit = kWgrad && kProd == 2;
     // W13 and the weight gradients: the next tile's first stage skips its wait (below)
     constexpr bool kEarlyWait = MODE == MX_W13 || MODE == MX_WGRAD;
 
@@ -149,7 +156,8 @@ __global__ __launch_bounds__(NTHR, 1) void grouped_gemm_mx(MxGemmArgs g) {
             worder[rank] = tid;
         }
         __syncthreads();
-        block_scan(tid < E ? nQt * nPt : 0, cum);
+        if constexpr (kSplit) block_scan(tid < E ? nQt * nPt * mx_pieces(g.pieces, wkp[worder[tid]]) : 0, cum);
+        else block_scan(tid < E ? nQt * nPt : 0, cum);
     } else {
         int cnt = 0;
         if (tid < E) {
@@ -179,11 +187,21 @@ __global__ __launch_bounds__(NTHR, 1) void grouped_gemm_mx(MxGemmArgs g) {
             c.e = __builtin_amdgcn_readfirstlane(worder[lo]);
             c.mb = 0;
             c.rows = g.Nq;                            // q rows of the tile are features
-            c.qt = local / nPt;
-            c.pt = local - c.qt * nPt;
             c.kp = __builtin_amdgcn_readfirstlane(wkp[c.e]);
             c.koff = __builtin_amdgcn_readfirstlane(wkoff[c.e]);
+            int tile_of = local;
+            c.k0 = c.slot = 0;
             c.nk = c.kp / TKB;                        // even: kp is a multiple of 128
+            if constexpr (kSplit) {
+                const int units = c.kp / kMxWgradPad, n = mx_pieces(g.pieces, c.kp), piece = local / (nQt * nPt);
+                tile_of -= piece * nQt * nPt;
+                const int u0 = (int)((int64_t)units * piece / n), u1 = (int)((int64_t)units * (piece + 1) / n);
+                c.k0 = 2 * u0;
+                c.nk = 2 * (u1 - u0);                 // at least one unit
+                c.slot = c.e * g.pieces + piece;
+            }
+            c.qt = tile_of / nPt;
+            c.pt = tile_of - c.qt * nPt;
         } else {
             c.e = lo;
             c.mb = mptr[lo];
@@ -281,6 +299,12 @@ __global__ __launch_bounds__(NTHR, 1) void grouped_gemm_mx(MxGemmArgs g) {
             qsbase_e = reinterpret_cast<const char*>(qscale + (size_t)c.koff * g.Nq / 32);
             pscale_stride = (size_t)g.Np * 4;
             qscale_stride = (size_t)g.Nq * 4;
+            if constexpr (kSplit) {
+                pbase_e += c.k0 * TKB;
+                qbase_e += c.k0 * TKB;
+                psbase_e += (size_t)(c.k0 / 2) * pscale_stride;
+                qsbase_e += (size_t)(c.k0 / 2) * qscale_stride;
+            }
         } else {
             pbase_e = reinterpret_cast<const char*>(pdata + (size_t)c.e * prows_e * K);
             psbase_e = reinterpret_cast<const char*>(pscale + (size_t)c.e * prows_e * 4);
@@ -472,6 +496,35 @@ __global__ __launch_bounds__(NTHR, 1) void grouped_gemm_mx(MxGemmArgs g) {
                     __builtin_amdgcn_s_waitcnt(0xc07f);
                 }
             }
+        } else if constexpr (kSplit) {
+            // the piece's sums [Nq, Np] in FP32 through LDS (as below), 64 columns of 32 rows at a time
+            float* obase = g.part + (size_t)c.slot * g.Nq * g.Np;
+            char* stg = lds + buf * BUFB + wave * 8192;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int a2 = 0; a2 < 2; ++a2)
+#pragma unroll
+                        for (int grp = 0; grp < 4; ++grp) {
+                            const int c16 = 8 * a2 + 2 * grp + (ln >> 5);
+                            const f32x16_t& v = acc[2 * h + a2][b];
+                            const f32x4_t w = {v[4 * grp], v[4 * grp + 1], v[4 * grp + 2], v[4 * grp + 3]};
+                            *reinterpret_cast<f32x4_t*>(stg + q_in * 256 + ((c16 ^ (q_in & 15)) << 4)) = w;
+                        }
+                    __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+                    for (int it = 0; it < 8; ++it) {
+                        const int row = 4 * it + (ln >> 4);
+                        const int c16 = ln & 15;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stg + row * 256 + ((c16 ^ (row & 15)) << 4));
+                        const int rr = c.qt * TQ + wq * 128 + b * 32 + row;
+                        const int p = c.pt * TP + wp * 128 + h * 64 + 4 * c16;
+                        if (rr < c.rows && p < g.Np) *reinterpret_cast<uint4*>(obase + (size_t)rr * g.Np + p) = v;
+                    }
+                    __builtin_amdgcn_s_waitcnt(0xc07f);
+                }
         } else {
             // o [R, d] (MX_PLAIN: [R, Np]; MX_WGRAD: expert e's [Nq, Np]) in BF16 through
             // LDS (this wave's 8 KiB of the stage buffer just consumed), stored as whole
@@ -646,7 +699,7 @@ hipError_t launch_mx_mode(const MxGemmArgs& g, int num_cu, hipStream_t s) {
     if constexpr (MODE == MX_W13) tiles = (R / TQ + g.E) * (g.I / 128);
     else if constexpr (MODE == MX_W2) tiles = (R / TQ + g.E) * (g.d / TP);
     else if constexpr (MODE == MX_PLAIN) tiles = (R / TQ + g.E) * ((g.Np + TP - 1) / TP);
-    else tiles = (int64_t)g.E * ((g.Np + TP - 1) / TP) * ((g.Nq + TQ - 1) / TQ);
+    else tiles = (int64_t)g.E * ((g.Np + TP - 1) / TP) * ((g.Nq + TQ - 1) / TQ) * (kProd == 2 ? g.pieces : 1);
     int64_t grid = tiles < num_cu ? tiles : num_cu;
     if (grid >= 8) grid -= grid % 8;
     if (grid < 1) grid = 1;
@@ -658,6 +711,32 @@ hipError_t launch_mx_mode(const MxGemmArgs& g, int num_cu, hipStream_t s) {
     return launch_mx_act<MODE, kActSwiGLU, kProd>(g, gd, s);
 }
 
+// Weight gradients from their pieces' sums, in piece order, and rounded (or added to what is there as in
+// MX_WGRAD's epilogue); eight elements a thread.
+__global__ __launch_bounds__(NTHR) void sum_pieces_kernel(MxGemmArgs g) {
+    const size_t n = (size_t)g.Nq * g.Np;
+    const size_t i = ((size_t)blockIdx.x * NTHR + threadIdx.x) * 8;
+    const int e = blockIdx.y;
+    if (i >= n) return;
+    const int rows = g.m_indptr[e + 1] - g.m_indptr[e];
+    const int pieces = mx_pieces(g.pieces, ((rows > 0 ? rows : 1) + kMxWgradPad - 1) / kMxWgradPad * kMxWgradPad);
+    const float* src = g.part + (size_t)e * g.pieces * n + i;
+    f32x4_t lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+    for (int p = 0; p < pieces; ++p) {
+        lo += *reinterpret_cast<const f32x4_t*>(src + p * n);
+        hi += *reinterpret_cast<const f32x4_t*>(src + p * n + 4);
+    }
+    uint32_t nv[4] = {pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]), pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
+    uint4* dst = reinterpret_cast<uint4*>(g.out + e * n + i);
+    if (g.accumulate) {
+        const uint4 o = *dst;
+        const uint32_t ov[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int z = 0; z < 4; ++z) nv[z] = pack_bf16(bf16lo(ov[z]) + bf16lo(nv[z]), bf16hi(ov[z]) + bf16hi(nv[z]));
+    }
+    *dst = make_uint4(nv[0], nv[1], nv[2], nv[3]);
+}
+
 }  // namespace
 
 hipError_t launch_gemm_mxfp8(MxMode mode, const MxGemmArgs& g, int num_cu, hipStream_t s) {
@@ -667,7 +746,14 @@ hipError_t launch_gemm_mxfp8(MxMode mode, const MxGemmArgs& g, int num_cu, hipSt
         case MX_W13: return launch_mx_mode<MX_W13>(g, num_cu, s);
         case MX_W2: return launch_mx_mode<MX_W2>(g, num_cu, s);
         case MX_PLAIN: return launch_mx_mode<MX_PLAIN>(g, num_cu, s);
-        case MX_WGRAD: return launch_mx_mode<MX_WGRAD>(g, num_cu, s);
+        case MX_WGRAD: {
+            if (g.pieces <= 1) return launch_mx_mode<MX_WGRAD>(g, num_cu, s);
+            const hipError_t e = launch_mx_mode<MX_WGRAD, 2>(g, num_cu, s);
+            if (e != hipSuccess) return e;
+            const int64_t wgs = ((int64_t)g.Nq * g.Np / 8 + NTHR - 1) / NTHR;
+            hipLaunchKernelGGL(sum_pieces_kernel, dim3((unsigned)wgs, g.E), dim3(NTHR), 0, s, g);
+            return hipGetLastError();
+        }
         case MX_PLAIN_W13: return launch_mx_mode<MX_PLAIN, 1>(g, num_cu, s);
         case MX_WGRAD_W13: return launch_mx_mode<MX_WGRAD, 1>(g, num_cu, s);
     }

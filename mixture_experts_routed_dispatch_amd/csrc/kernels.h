@@ -106,6 +106,8 @@ struct MxGemmArgs {
     const uint8_t* qs;
     uint16_t* out;
     int accumulate;       // MX_WGRAD: out = bf16(out + bf16(D)) instead of bf16(D)
+    int pieces;           // MX_WGRAD: over 1, an expert's rows are cut into up to so many pieces, which are
+    float* part;          // summed up in FP32 here [E, pieces, Nq, Np] (Nq Np a multiple of 8)
     // The forward with weights in blocks of 128 (gemm_block128.hip): MX_QUANT_X, MX_W13 and MX_W2; all
     // scales are FP32 then, in the same places: xs [d/128, R], as [I/128, R], w13s and w2s
     // [E, N/128, K/128]
@@ -281,11 +283,17 @@ hipError_t launch_block128_rows(const uint16_t* v, int64_t rows, int K, uint8_t*
 hipError_t launch_block128_rows_f32(const float* v, int64_t rows, int K, uint8_t* codes, float* scales, hipStream_t s);
 hipError_t launch_block128_pack(Block128Pair g, hipStream_t s);
 hipError_t launch_block128_expand(Block128Pair g, hipStream_t s);
-// m_out [E+1] = m_in, or zeros and (unless NULL) the status flag where it does not rise from 0 to at
-// most R; m_in NULL: 0, R (E = 1)
-hipError_t launch_segments(const int32_t* m_in, int E, int R, int32_t* m_out, int32_t* status, hipStream_t s);
+// out [E+1] = in, or zeros and (unless NULL) the status flag where it does not rise from 0 to at most R;
+// in NULL: 0, R (E = 1)
+struct Segments {
+    const int32_t* in;
+    int32_t* out;
+    int32_t* status;
+    int E, R;
+};
+hipError_t launch_segments(const Segments& g, hipStream_t s);
 hipError_t launch_block128_transpose(const uint8_t* codes, const float* scales, int E, int N, int K, uint8_t* codes_t,
-                                     float* scales_t, hipStream_t s);
+                                     float* scales_t, const Segments& seg, hipStream_t s);
 
 // Grouped products of such operands (gemm_block128.hip): rows m_indptr[e] .. m_indptr[e+1] with
 // matrix e, E <= 256, K and Np multiples of 128.  Offsets inside one matrix, and in W13 inside the rows'

@@ -26,8 +26,17 @@ static moe_status_t product_check(const moe_product_config_t* c) {
 
 namespace {
 struct Room {
-    size_t q, qs, groups, starts, wt, wts, tp, tps, tq, tqs, bytes;
+    size_t q, qs, groups, starts, wt, wts, tp, tps, tq, tqs, part, bytes;
 };
+// Pieces into which the rows of a weight gradient are cut: as many as fill the chip with tiles of 256 x 256, of
+// 1024 rows at least on average
+int grad_pieces(const moe_product_config_t& c) {
+    constexpr int kUnits = 256, kMost = 8, kRows = 1024;
+    const int64_t tiles = (int64_t)c.E * ((c.N + 255) / 256) * ((c.K + 255) / 256), rows = c.R / c.E / kRows;
+    int64_t n = kUnits / tiles;
+    n = n < rows ? n : rows;
+    return (int)(n < 1 ? 1 : n < kMost ? n : kMost);
+}
 Room room_of(const moe_product_config_t& c) {
     Room r{};
     size_t off = 0;
@@ -45,6 +54,8 @@ Room room_of(const moe_product_config_t& c) {
         r.tps = take(tokens * c.K / 32);
         r.tq = take(tokens * c.N);
         r.tqs = take(tokens * c.N / 32);
+        const int pieces = grad_pieces(c);
+        r.part = take(pieces > 1 ? sizeof(float) * pieces * weights : 0);
     }
     r.bytes = off;
     return r;
@@ -137,14 +148,16 @@ moe_status_t moe_product_backward(const moe_product_config_t* c, const void* dy,
     // no rows: every matrix' segment is empty, whatever m_indptr holds
     const int E = c->E, R = c->R;
     int32_t* starts = reinterpret_cast<int32_t*>(ws + r.starts);
+    const Segments seg{m_indptr, starts, status, E, R};
     if (R == 0) {
         if (launch_fill_i32(starts, E + 1, 0, s) != hipSuccess) return MOE_ERR_HIP;
-    } else if (launch_segments(m_indptr, E, R, starts, status, s) != hipSuccess) {
+    } else if (!dx && launch_segments(seg, s) != hipSuccess) {
         return MOE_ERR_HIP;
     }
     if (dx && R > 0) {
         // dx = dy W: the matrices transposed, dy quantized along N
-        if (launch_block128_transpose(w_q, w_s, E, c->N, c->K, codes(r.wt), scales(r.wts), s) != hipSuccess) return MOE_ERR_HIP;
+        if (launch_block128_transpose(w_q, w_s, E, c->N, c->K, codes(r.wt), scales(r.wts), seg, s) != hipSuccess)
+            return MOE_ERR_HIP;
         if (launch_block128_rows(static_cast<const uint16_t*>(dy), R, c->N, codes(r.q), scales(r.qs), true, starts + E, s) != hipSuccess)
             return MOE_ERR_HIP;
         Block128GemmArgs g{};
@@ -167,6 +180,8 @@ moe_status_t moe_product_backward(const moe_product_config_t* c, const void* dy,
         g.pq = codes(r.tp); g.ps = codes(r.tps); g.qq = codes(r.tq); g.qs = codes(r.tqs);
         g.out = static_cast<uint16_t*>(dw);
         g.accumulate = c->wgrad_accumulate;
+        g.pieces = grad_pieces(*c);
+        g.part = reinterpret_cast<float*>(ws + r.part);
         if (launch_gemm_mxfp8(MX_WGRAD, g, cus, s) != hipSuccess) return MOE_ERR_HIP;
     }
     return MOE_OK;
