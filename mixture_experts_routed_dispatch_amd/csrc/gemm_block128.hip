@@ -18,7 +18,7 @@
 // the vector unit and lie in its registers, which limits a wave to 128 x 64 outputs (the MXFP8
 // products, whose scales the matrix unit applies, have 128 x 128).
 //
-// Workgroup tile 256 (P) x TQ (rows), waves of 128 x 64, a stage of 128 K in LDS while the next one
+// Workgroup tile 256 (P) x TQ (rows: 256, 192 or 128), eight waves of 128 x TQ / 4, a stage of 128 K in LDS while the next one
 // is copied into the other buffer by direct global-to-LDS copies, one continuous stream of stages per
 // workgroup over its tiles (the next tile's first stage is copied during the last of this one).
 // LDS rows are 128 bytes, 16-byte chunk c of row r at slot c ^ (r / 2 % 8): the same chunk of 16
@@ -53,11 +53,12 @@ struct Tile {
 __device__ __forceinline__ int swz(int r) { return r >> 1 & 7; }
 
 template <int MODE, int kAct, int TQ>
-__global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs g) {
-    constexpr int kWaves = TQ / 64 * 2, kThr = kWaves * MOE_WAVE;
+__global__ __launch_bounds__(512, 1) void grouped_gemm_b128(Block128GemmArgs g) {
+    constexpr int kWaves = 8, kThr = kWaves * MOE_WAVE;
+    constexpr int kNB = TQ / 64;                         // fragments of 16 rows a wave
     constexpr int kBuf = kPBytes + TQ * TK;              // a stage: P then Q
     constexpr int kSlot = TQ * 4 + 256;                  // its scales: TQ words of Q, 64 of P
-    constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = TQ * TK / 1024 / kWaves;   // of 1 KiB a wave
+    constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kNB;          // of 1 KiB a wave
     __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf];
     __shared__ __attribute__((aligned(1024))) char lsc[2 * kSlot];
     __shared__ uint32_t tops[2][TQ];                     // B128_W13: magnitudes of a row's two halves
@@ -212,19 +213,19 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     const int row16 = lane & 15, quad = lane >> 4;
     // a fragment: 16 rows, lane (row16, quad) the chunks quad and quad + 4 of its row
     const int c0 = (quad ^ swz(row16)) * 16, c1 = c0 ^ 64;
-    const int poff = (wp * 128 + row16) * TK, qoff = kPBytes + (wq * 64 + row16) * TK;
+    const int poff = (wp * 128 + row16) * TK, qoff = kPBytes + (wq * 16 * kNB + row16) * TK;
     auto read_frag = [&](const char* row) {
         const i32x4_t x = *reinterpret_cast<const i32x4_t*>(row + c0);
         const i32x4_t y = *reinterpret_cast<const i32x4_t*>(row + c1);
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    f32x4_t acc[8][4];
+    f32x4_t acc[8][kNB];
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    i32x8_t qf[4], pf;                                   // the rows' fragments, the next one of P
-    float sq[4], sp[2];                                  // scales: of this lane's rows, of the wave's squares of P
+    i32x8_t qf[kNB], pf;                                   // the rows' fragments, the next one of P
+    float sq[kNB], sp[2];                                  // scales: of this lane's rows, of the wave's squares of P
     auto read_q = [&](int buf, int b) {
         qf[b] = read_frag(lds + buf * kBuf + qoff + b * 16 * TK);
-        sq[b] = reinterpret_cast<const float*>(lsc + buf * kSlot)[wq * 64 + b * 16 + row16];
+        sq[b] = reinterpret_cast<const float*>(lsc + buf * kSlot)[wq * 16 * kNB + b * 16 + row16];
     };
     auto read_p = [&](int buf, int a) { return read_frag(lds + buf * kBuf + poff + a * 16 * TK); };
     auto read_sp = [&](int buf) {
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
         pf = read_p(buf, 0);
         read_sp(buf);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) read_q(buf, b);
+        for (int b = 0; b < kNB; ++b) read_q(buf, b);
     };
     // One stage from buffer buf, whose first fragments have been read: eight steps of one fragment of P.  A step
     // issues its four products, each followed by the FMAs of the step before, reads the next fragment and
@@ -245,13 +246,13 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
     // step reads the next stage's first fragments.
     auto stage = [&](auto last_tag, int buf, int next_kt) {
         constexpr bool kLast = decltype(last_tag)::value;
-        float f0[4], f1[4];                              // factors; B128_W13: of gate and up rows
+        float f0[kNB], f1[kNB];                              // factors; B128_W13: of gate and up rows
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < kNB; ++b) {
             f0[b] = sq[b] * sp[0];
             f1[b] = MODE == B128_W13 ? sq[b] * sp[1] : f0[b];
         }
-        f32x4_t part[4];
+        f32x4_t part[kNB];
 #pragma unroll
         for (int a = 0; a < 8; ++a) {
             i32x8_t pn = pf;
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
                 pn = read_p(buf, a + 1);
             }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < kNB; ++b) {
                 const f32x4_t now = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[b], zero, 0, 0, 0, 0, 0, 0);
                 // the last fragment's results, while this one's are computed
                 if (a > 0)
@@ -283,15 +284,15 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
                 }
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-                if (b == 1 && a < kPCopies) dma_p(next_kt, buf ^ 1, a);
-                if (b == 3 && a < kQCopies) dma_q(next_kt, buf ^ 1, a);
-                if (b == 3 && a == 4) dma_scales(next_kt, buf ^ 1);
+                if (b == (kNB > 2 ? 1 : 0) && a < kPCopies) dma_p(next_kt, buf ^ 1, a);
+                if (b == kNB - 1 && a < kQCopies) dma_q(next_kt, buf ^ 1, a);
+                if (b == kNB - 1 && a == 4) dma_scales(next_kt, buf ^ 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
             pf = pn;
         }
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < kNB; ++b)
 #pragma unroll
             for (int z = 0; z < 4; ++z) acc[7][b][z] = __builtin_fmaf(part[b][z], f1[b], acc[7][b][z]);
     };
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
         const int lane = fresh_lane(), row16 = lane & 15, quad = lane >> 4;
         char* stg = lds + buf * kBuf;                    // codes [TQ][128], chunks as the stages'
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < kNB; ++b) {
             uint32_t top = 0;
 #pragma unroll
             for (int m = 0; m < 4; ++m)
@@ -320,12 +321,12 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
                 const uint32_t t = __shfl_xor(top, o, MOE_WAVE);
                 top = top > t ? top : t;
             }
-            if (lane < 16) tops[wp][wq * 64 + b * 16 + row16] = top;
+            if (lane < 16) tops[wp][wq * 16 * kNB + b * 16 + row16] = top;
         }
         __syncthreads();
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int r = wq * 64 + b * 16 + row16;
+        for (int b = 0; b < kNB; ++b) {
+            const int r = wq * 16 * kNB + b * 16 + row16;
             const uint32_t t0 = tops[0][r], t1 = tops[1][r];
             const float s = block_scale(t0 > t1 ? t0 : t1), inv = block_inverse(s);
 #pragma unroll
@@ -344,28 +345,26 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
         }
     };
     auto epilogue_plain = [&](const Tile& c, int buf) {
-        // BF16 rows by way of this wave's 8 KiB of the buffer, stored as whole 256-byte pieces
+        // BF16 rows by way of this wave's 4 KiB of the buffer, 16 at a time, stored as whole 256-byte pieces
         // past the caches (ordinary stores evict operands that the XCD's workgroups share)
         const int lane = fresh_lane(), row16 = lane & 15, quad = lane >> 4;
-        char* stg = lds + buf * kBuf + wave * 8192;
+        char* stg = lds + buf * kBuf + wave * 4096;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int b = 0; b < kNB; ++b) {
 #pragma unroll
-            for (int bb = 0; bb < 2; ++bb)
-#pragma unroll
-                for (int a = 0; a < 8; ++a) {
-                    const f32x4_t v = acc[a][2 * h + bb];
-                    const int r = bb * 16 + row16, c16 = 2 * a + (quad >> 1);
-                    *reinterpret_cast<uint2*>(stg + r * 256 + ((c16 ^ (r & 15)) * 16) + 8 * (quad & 1)) =
-                        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-                }
+            for (int a = 0; a < 8; ++a) {
+                const f32x4_t v = acc[a][b];
+                const int c16 = 2 * a + (quad >> 1);
+                *reinterpret_cast<uint2*>(stg + row16 * 256 + ((c16 ^ row16) * 16) + 8 * (quad & 1)) =
+                    make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int it = 0; it < 8; ++it) {
+            for (int it = 0; it < 4; ++it) {
                 const int r = 4 * it + quad, c16 = row16;
-                const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 256 + ((c16 ^ (r & 15)) * 16));
-                const int rr = c.qt * TQ + wq * 64 + h * 32 + r, p = c.pt * TP + wp * 128 + 8 * c16;
+                const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 256 + ((c16 ^ r) * 16));
+                const int rr = c.qt * TQ + wq * 16 * kNB + b * 16 + r, p = c.pt * TP + wp * 128 + 8 * c16;
                 if (rr < c.rows && p < g.Np) store_nt(g.out + (size_t)(c.mb + rr) * g.Np + p, v);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -407,7 +406,7 @@ __global__ __launch_bounds__(TQ * 2, 1) void grouped_gemm_b128(Block128GemmArgs 
 #pragma unroll
         for (int a = 0; a < 8; ++a)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) acc[a][b] = zero;
+            for (int b = 0; b < kNB; ++b) acc[a][b] = zero;
         for (int kt = 1; kt < groups; ++kt) {
             stage(std::false_type(), buf, l_kt);
             advance_load();
@@ -431,8 +430,34 @@ template <int MODE, int kAct, int TQ> hipError_t launch_t(const Block128GemmArgs
     int64_t grid = (g.R / TQ + (g.E < g.R ? g.E : g.R)) * nPt;       // tiles, at most
     grid = grid < num_cu ? grid : num_cu;
     if (grid >= 8) grid -= grid % 8;
-    hipLaunchKernelGGL((grouped_gemm_b128<MODE, kAct, TQ>), dim3((unsigned)(grid < 1 ? 1 : grid)), dim3(TQ * 2), 0, s, g);
+    hipLaunchKernelGGL((grouped_gemm_b128<MODE, kAct, TQ>), dim3((unsigned)(grid < 1 ? 1 : grid)), dim3(512), 0, s, g);
     return hipGetLastError();
+}
+
+template <int TQ> hipError_t launch_act(Block128Mode mode, const Block128GemmArgs& g, int num_cu, hipStream_t s) {
+    if (mode == B128_PLAIN) return launch_t<B128_PLAIN, kActSwiGLU, TQ>(g, num_cu, s);
+    if (g.act == kActGeGLU) return launch_t<B128_W13, kActGeGLU, TQ>(g, num_cu, s);
+    if (g.act == kActReGLU) return launch_t<B128_W13, kActReGLU, TQ>(g, num_cu, s);
+    return launch_t<B128_W13, kActSwiGLU, TQ>(g, num_cu, s);
+}
+
+// Rows of a tile: those with which the tiles' rounds over the chip take the least time, when one of 256 rows takes 1.
+// The rows of several experts are taken to fill their last tiles by half, and their rounds, whose number is
+// not known here, are not rounded up.  (4096 outputs of 2048 inputs: 2000 rows
+// 36.2, 33.2 and 30.2 us with 256, 192 and 128, 6000 rows 72.5, 64.2 and 70.9, 20000 rows 182, 194 and 218; 128
+// experts, 2048 routed rows in all: 152, 142 and 129.)
+int rows_of_tile(Block128Mode mode, const Block128GemmArgs& g, int num_cu) {
+    const int64_t nPt = mode == B128_W13 ? g.Np / 128 : (g.Np + TP - 1) / TP;
+    int best = 256;
+    float least = 0.f;
+    for (int tq = 256; tq >= 128; tq -= 64) {
+        const int64_t tiles = g.E == 1 ? (g.R + tq - 1) / tq : g.R / tq + (g.E < g.R ? g.E : g.R) / 2 + 1;
+        float t = (float)(tiles * nPt) / (float)num_cu;
+        t = g.E == 1 ? (float)((tiles * nPt + num_cu - 1) / num_cu) : t > 1.0f ? t : 1.0f;
+        t *= tq == 256 ? 1.0f : tq == 192 ? 0.88f : 0.7f;
+        if (tq == 256 || t < least) { least = t; best = tq; }
+    }
+    return best;
 }
 
 }  // namespace
@@ -440,10 +465,11 @@ template <int MODE, int kAct, int TQ> hipError_t launch_t(const Block128GemmArgs
 hipError_t launch_gemm_block128(Block128Mode mode, const Block128GemmArgs& g, int num_cu, hipStream_t s) {
     if (g.E <= 0 || g.E > 256 || (!g.m_indptr && g.E != 1) || g.R < 0 || g.R > 0x7FFFFFFF || g.K <= 0 || g.K % 128 != 0 || g.Np <= 0 || g.Np % 128 != 0) return hipErrorInvalidValue;
     if (g.R == 0) return hipSuccess;
-    if (mode == B128_PLAIN) return launch_t<B128_PLAIN, kActSwiGLU, 256>(g, num_cu, s);
-    if (g.act == kActGeGLU) return launch_t<B128_W13, kActGeGLU, 256>(g, num_cu, s);
-    if (g.act == kActReGLU) return launch_t<B128_W13, kActReGLU, 256>(g, num_cu, s);
-    return launch_t<B128_W13, kActSwiGLU, 256>(g, num_cu, s);
+    switch (rows_of_tile(mode, g, num_cu)) {
+        case 128: return launch_act<128>(mode, g, num_cu, s);
+        case 192: return launch_act<192>(mode, g, num_cu, s);
+        default: return launch_act<256>(mode, g, num_cu, s);
+    }
 }
 
 // The layer's forward: x in 8 bits with its scales by routed row, W13, W2
