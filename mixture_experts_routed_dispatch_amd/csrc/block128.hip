@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const uint16_t* __restri
 
 // The same with block-major scales: a workgroup takes four blocks of 16 rows, a wave the four of every fourth row, and
 // writes 16 consecutive scales at a time.  (Each wave the scales of its own four blocks: 65536 x 1536 83 us against
-// XX.)  rows_dev (optional): only the first *rows_dev rows (at most rows).
+// 66.)  rows_dev (optional): only the first *rows_dev rows (at most rows).
 __global__ __launch_bounds__(kThreads) void rows_block_major_kernel(const uint16_t* __restrict__ v, int64_t rows, int groups,
                                                                     const int32_t* __restrict__ rows_dev,
                                                                     uint8_t* __restrict__ codes, float* __restrict__ scales) {

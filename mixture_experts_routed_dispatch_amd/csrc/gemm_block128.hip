@@ -8,8 +8,13 @@
 //   mode       P                          Q                      K    output
 //   B128_W13   W13_e, gate/up row pairs   xq[gather[r]]          d    a = f(g) u quantized along I: codes [R, I],
 //                                                                     scales [I/128, R]
-//   B128_PLAIN rows of a matrix           routed rows            Kp   BF16 [R, Np]: W2, and a product's forward
-//                                                                     and input gradient
+//   B128_W2    W2_e rows                  aq[r]                  I    o in 16-bit integers, in units of a 32767th of
+//                                                                     the largest of a row's block of 128: [R, d],
+//                                                                     [R, d/128].  As many bytes as BF16, whose rounding
+//                                                                     would add as much again to y's error; this adds a
+//                                                                     hundredth
+//   B128_PLAIN rows of a matrix           routed rows            Kp   BF16 [R, Np]: a product's forward and input gradient,
+//                                                                     W2 of rows in expert order
 //
 // The inner sum is one v_mfma_f32_16x16x128_f8f6f4 with a zero third operand; its four results a
 // lane are multiplied with their scale and added in FP32.  The rows are the instruction's columns: a
@@ -344,19 +349,45 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_b128(Block128GemmArgs g) 
             if (rr < c.rows) *reinterpret_cast<uint4*>(g.aq + (size_t)(c.mb + rr) * g.Np + c.pt * 128 + ch * 16) = v;
         }
     };
-    auto epilogue_plain = [&](const Tile& c, int buf) {
-        // BF16 rows by way of this wave's 4 KiB of the buffer, 16 at a time, stored as whole 256-byte pieces
-        // past the caches (ordinary stores evict operands that the XCD's workgroups share)
+    auto epilogue_rows = [&](const Tile& c, int buf) {
+        // rows in BF16 (B128_W2: integers) by way of this wave's 4 KiB of the buffer, 16 at a time, stored as
+        // whole 256-byte pieces past the caches (ordinary stores evict operands that the XCD's workgroups share)
         const int lane = fresh_lane(), row16 = lane & 15, quad = lane >> 4;
         char* stg = lds + buf * kBuf + wave * 4096;
 #pragma unroll
         for (int b = 0; b < kNB; ++b) {
+            float inv = 0.f;
+            if constexpr (MODE == B128_W2) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int a = 0; a < 8; ++a)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t t = __float_as_uint(acc[a][b][z]) & 0x7FFFFFFFu;
+                        top = top > t ? top : t;
+                    }
+#pragma unroll
+                for (int o = 16; o < 64; o <<= 1) {
+                    const uint32_t t = __shfl_xor(top, o, MOE_WAVE);
+                    top = top > t ? top : t;
+                }
+                // a row that holds an infinity or NaN is NaN; one below 2^-120 is zero
+                const bool some = top >= 0x03800000u && top < 0x7F800000u;
+                inv = some ? __builtin_amdgcn_rcpf(__uint_as_float(top)) : 0.f;
+                const float unit = some ? __uint_as_float(top) * (1.0f / 32767.0f) : top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
+                const int rr = c.qt * TQ + wq * 16 * kNB + b * 16 + row16, p = c.pt * TP + wp * 128;
+                if (quad == 0 && rr < c.rows && p < g.Np) g.os[(size_t)(c.mb + rr) * (g.Np / 128) + p / 128] = unit;
+            }
+            auto pack = [&](float x, float y) {
+                if constexpr (MODE == B128_W2) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_i16(x * inv, y * inv));
+                else return pack_bf16(x, y);
+            };
 #pragma unroll
             for (int a = 0; a < 8; ++a) {
                 const f32x4_t v = acc[a][b];
                 const int c16 = 2 * a + (quad >> 1);
                 *reinterpret_cast<uint2*>(stg + row16 * 256 + ((c16 ^ row16) * 16) + 8 * (quad & 1)) =
-                    make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                    make_uint2(pack(v[0], v[1]), pack(v[2], v[3]));
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -415,7 +446,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_b128(Block128GemmArgs g) 
         stage(std::true_type(), buf, l_kt);
         advance_load();
         if constexpr (MODE == B128_W13) epilogue_w13(cc, buf);
-        else epilogue_plain(cc, buf);
+        else epilogue_rows(cc, buf);
         buf ^= 1;
         c_tile += G;
         if (c_tile >= total) break;
@@ -436,9 +467,31 @@ template <int MODE, int kAct, int TQ> hipError_t launch_t(const Block128GemmArgs
 
 template <int TQ> hipError_t launch_act(Block128Mode mode, const Block128GemmArgs& g, int num_cu, hipStream_t s) {
     if (mode == B128_PLAIN) return launch_t<B128_PLAIN, kActSwiGLU, TQ>(g, num_cu, s);
+    if (mode == B128_W2) return launch_t<B128_W2, kActSwiGLU, TQ>(g, num_cu, s);
     if (g.act == kActGeGLU) return launch_t<B128_W13, kActGeGLU, TQ>(g, num_cu, s);
     if (g.act == kActReGLU) return launch_t<B128_W13, kActReGLU, TQ>(g, num_cu, s);
     return launch_t<B128_W13, kActSwiGLU, TQ>(g, num_cu, s);
+}
+
+// y[t] = sum_j s[t][j] o[slots[t][j]] in FP32, j ascending from +0.0, of o in integers; eight columns a thread.  Reading
+// o is its time: 65536 rows of 2048 52 us, 268 MB at 5.1 TB/s (58 with loads that stay in the caches).
+__global__ __launch_bounds__(256) void combine16_kernel(MxGemmArgs g) {
+    const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x, d = g.d;
+    if (8 * c >= d) return;
+    float y[8] = {};
+#pragma unroll 8
+    for (int j = 0; j < g.k; ++j) {
+        const size_t r = (size_t)g.slots[(size_t)t * g.k + j];
+        const u32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(g.o + r * d + 8 * c));
+        const float f = g.os[r * (d / 128) + c / 16], w = g.scores[(size_t)t * g.k + j];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            y[2 * z] = __builtin_fmaf(w, f * (float)(int16_t)(u[z] & 0xFFFFu), y[2 * z]);
+            y[2 * z + 1] = __builtin_fmaf(w, f * (float)((int32_t)u[z] >> 16), y[2 * z + 1]);
+        }
+    }
+    *reinterpret_cast<uint4*>(g.y + (size_t)t * d + 8 * c) =
+        make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
 }
 
 // Rows of a tile: those with which the tiles' rounds over the chip take the least time, when one of 256 rows takes 1.
@@ -472,7 +525,7 @@ hipError_t launch_gemm_block128(Block128Mode mode, const Block128GemmArgs& g, in
     }
 }
 
-// The layer's forward: x in 8 bits with its scales by routed row, W13, W2
+// The layer's forward: x in 8 bits with its scales by routed row, W13, W2, the combine
 hipError_t launch_layer_block128(MxMode mode, const MxGemmArgs& g, int num_cu, hipStream_t s) {
     const int64_t R = (int64_t)g.T * g.k;
     if (mode == MX_QUANT_X) {
@@ -492,12 +545,16 @@ hipError_t launch_layer_block128(MxMode mode, const MxGemmArgs& g, int num_cu, h
         b.aq = g.aq; b.as = reinterpret_cast<float*>(g.as);
         return launch_gemm_block128(B128_W13, b, num_cu, s);
     }
+    if (mode == MX_COMBINE) {
+        if (g.T > 0) hipLaunchKernelGGL(combine16_kernel, dim3((g.d / 8 + 255) / 256, g.T), dim3(256), 0, s, g);
+        return hipGetLastError();
+    }
     if (mode != MX_W2) return hipErrorInvalidValue;
     b.K = g.I; b.Np = g.d;
     b.pq = g.w2q; b.ps = reinterpret_cast<const float*>(g.w2s);
     b.qq = g.aq; b.qs = reinterpret_cast<const float*>(g.as);
-    b.out = g.o;
-    return launch_gemm_block128(B128_PLAIN, b, num_cu, s);
+    b.out = g.o; b.os = g.os;
+    return launch_gemm_block128(g.os ? B128_W2 : B128_PLAIN, b, num_cu, s);
 }
 
 }  // namespace moe

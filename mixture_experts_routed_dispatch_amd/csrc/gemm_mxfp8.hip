@@ -742,7 +742,8 @@ __global__ __launch_bounds__(NTHR) void sum_pieces_kernel(MxGemmArgs g) {
 hipError_t launch_gemm_mxfp8(MxMode mode, const MxGemmArgs& g, int num_cu, hipStream_t s) {
     if (g.block128) return launch_layer_block128(mode, g, num_cu, s);
     switch (mode) {
-        case MX_QUANT_X: break;
+        case MX_QUANT_X:
+        case MX_COMBINE: break;
         case MX_W13: return launch_mx_mode<MX_W13>(g, num_cu, s);
         case MX_W2: return launch_mx_mode<MX_W2>(g, num_cu, s);
         case MX_PLAIN: return launch_mx_mode<MX_PLAIN>(g, num_cu, s);

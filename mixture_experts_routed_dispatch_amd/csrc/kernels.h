@@ -70,8 +70,8 @@ hipError_t launch_gemm(GemmMode mode, const GemmArgs& g, int num_cu, hipStream_t
 // MXFP8 forward products (OCP E4M3 codes, E8M0 scale per 32 along K).
 // MX_PLAIN_W13 / MX_WGRAD_W13: MX_PLAIN / MX_WGRAD as a kernel instance of their own (the
 // W13-side backward products), so that traces tell them from the W2 side.
-// MX_QUANT_X: x in 8 bits, of layers with weights in blocks of 128 only (see block128 below).
-enum MxMode { MX_W13 = 0, MX_W2 = 1, MX_PLAIN = 2, MX_WGRAD = 3, MX_PLAIN_W13 = 4, MX_WGRAD_W13 = 5, MX_QUANT_X = 6 };
+// MX_QUANT_X and MX_COMBINE: x in 8 bits, and y, of layers with weights in blocks of 128 only (see block128 below).
+enum MxMode { MX_W13 = 0, MX_W2 = 1, MX_PLAIN = 2, MX_WGRAD = 3, MX_PLAIN_W13 = 4, MX_WGRAD_W13 = 5, MX_QUANT_X = 6, MX_COMBINE = 7 };
 
 struct MxGemmArgs {
     int T, d, I, E, k;
@@ -114,6 +114,11 @@ struct MxGemmArgs {
     int block128;
     const uint16_t* x;    // MX_QUANT_X: [T, d], or with xs_rows NULL the rows in expert order
     uint8_t* xs_rows;     // MX_QUANT_X: [T, d/128], the scales by token
+    float* os;            // MX_W2: NULL: o is BF16; else [R, d/128], the largest magnitudes / 32767 of o's blocks of 128,
+                          // whose values are 16-bit integers in units of that
+    const int32_t* slots; // MX_COMBINE: y[t] = sum_j scores[t][j] o[slots[t][j]], in FP32, j ascending
+    const float* scores;
+    uint16_t* y;
 };
 
 hipError_t launch_gemm_mxfp8(MxMode mode, const MxGemmArgs& g, int num_cu, hipStream_t s);
@@ -299,7 +304,8 @@ hipError_t launch_block128_transpose(const uint8_t* codes, const float* scales, 
 // Grouped products of such operands (gemm_block128.hip): rows m_indptr[e] .. m_indptr[e+1] with
 // matrix e, E <= 256, K and Np multiples of 128.  Offsets inside one matrix, and in W13 inside the rows'
 // codes, are 32-bit.
-enum Block128Mode { B128_W13 = 0, B128_PLAIN = 1 };
+// B128_W2: as PLAIN, but out holds 16-bit integers in units of os (MxGemmArgs).
+enum Block128Mode { B128_W13 = 0, B128_PLAIN = 1, B128_W2 = 2 };
 struct Block128GemmArgs {
     int E, K, Np;             // Np: outputs, W13: I
     int64_t R;                // rows of the layouts
@@ -311,7 +317,8 @@ struct Block128GemmArgs {
     const float* ps;          // [E, .. / 128, K/128]
     const uint8_t* qq;        // [.., K]
     const float* qs;          // [K/128, R], by routed row
-    uint16_t* out;            // PLAIN: [R, Np]
+    uint16_t* out;            // PLAIN, W2: [R, Np]
+    float* os;                // W2: [R, Np/128]
     uint8_t* aq;              // W13: [R, Np] and
     float* as;                //      [Np/128, R]
     int act;

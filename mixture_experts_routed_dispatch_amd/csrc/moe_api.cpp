@@ -253,6 +253,7 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     p->off_aq = mx || b128 ? take((size_t)R * c.I) : 0;
     p->off_as = mx || b128 ? take((size_t)R * c.I / 32) : 0;
     p->off_groups = b128 && p->decode ? take(kBlock128GroupBytes) : 0;
+    p->off_os = b128 && !p->decode ? take((size_t)R * c.d / 32) : 0;
     p->ntok = R + (int64_t)kMxWgradPad * c.E;
     p->tp_feat = (size_t)(c.I > c.d ? c.I : c.d);              // P: a^T (I), then x^T (d)
     p->tq_feat = (size_t)(c.d > 2 * c.I ? c.d : 2 * c.I);      // Q: dO^T (d), then dh^T (2I)
@@ -339,7 +340,7 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
     if (p->dh_aliased)
         region("o", 2 * (size_t)R * c.d, "fwd/bwd", "expert outputs [R, d] BF16; in the backward dh (g, u gradient [R, 2I])");
     else
-        saved_region("o", p->o_bytes, p->o_bytes == 2 * (size_t)R * c.d ? "expert outputs [R, d] BF16" : "expert outputs [R, d] FP32");
+        saved_region("o", p->o_bytes, p->o_bytes != 2 * (size_t)R * c.d ? "expert outputs [R, d] FP32" : b128 ? "expert outputs [R, d], 16-bit integers" : "expert outputs [R, d] BF16");
     if (c.training) {
         const size_t hb = 2 * (size_t)R * 2 * c.I;
         if (c.recompute_h)
@@ -376,6 +377,7 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
         region("aq", (size_t)R * c.I, "scratch", "E4M3 codes of a [R, I]");
         region("as", (size_t)R * c.I / 32, "scratch", p->decode ? "FP32 scales of a [R, I/128]" : "FP32 scales of a (block-major)");
         region("groups", p->decode ? kBlock128GroupBytes : 0, "scratch", "routed entries in expert order");
+        region("os", p->decode ? 0 : (size_t)R * c.d / 32, "scratch", "units of o's blocks of 128 [R, d/128] FP32");
     }
     if (mx) {
         region("xq", (size_t)c.T * c.d, "scratch", "E4M3 codes of x [T, d]");
@@ -563,6 +565,10 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         mg.o = p->at<uint16_t>(p->off_o);
         mg.block128 = b128;
         mg.x = static_cast<const uint16_t*>(x); mg.xs_rows = xs;
+        if (b128) {
+            mg.os = p->at<float>(p->off_os);
+            mg.slots = slots; mg.scores = scores; mg.y = static_cast<uint16_t*>(y);
+        }
         e = staged(p, MOE_STAGE_QUANT_X, s, [&] {
             if (b128) return launch_gemm_mxfp8(MX_QUANT_X, mg, p->num_cu, s);
             hipError_t qe = launch_quantize_mxfp8(static_cast<const uint16_t*>(x), c.T, c.d, xq, xs, false, s);
@@ -579,6 +585,7 @@ moe_status_t moe_forward(moe_plan_t p, const void* x, const int32_t* ids, const 
         e = staged(p, MOE_STAGE_W2, s, [&] { return launch_gemm_mxfp8(MX_W2, mg, p->num_cu, s); });
         if (e != hipSuccess) return MOE_ERR_HIP;
         e = staged(p, MOE_STAGE_COMBINE, s, [&] {
+            if (b128) return launch_gemm_mxfp8(MX_COMBINE, mg, p->num_cu, s);
             return launch_combine(p->at<uint16_t>(p->off_o), slots, scores, c.T, c.k, c.d,
                                   static_cast<uint16_t*>(y), s);
         });

@@ -551,7 +551,7 @@ __device__ __forceinline__ uint32_t open_groups_exact(const RouterArgs& g, int64
 // to 64 bits where such a sum lies on either side of the border.  Logits order exactly, one a group.
 //
 // A group of 1, 2, 4, 8 or 16 of the lanes' pieces (g.group_lanes) is merged by DPP, and its lanes know whether it is
-// open.  (All sizes by way of LDS, a lane to a group: 16384 x 256 23.6 us against XX.)
+// open.  Other sizes go group by group.  (All sizes so: 16384 x 256, 8 groups, sigmoid and bias 37.7 us against 25.3.)
 // z: the keys of the choice, in which NaN becomes -inf.
 template <int kV, bool kF32, bool kSig, bool kBias>
 __device__ __forceinline__ uint32_t open_groups(const RouterArgs& g, int64_t row, float z[kV], const float s[kV], int i0,
