@@ -164,10 +164,10 @@ __global__ __launch_bounds__(kThreads) void transpose_kernel(const uint8_t* __re
                                                              int N, int K, uint8_t* __restrict__ codes_t,
                                                              float* __restrict__ scales_t, Segments seg) {
     __shared__ uint32_t tile[kB * kLd / 4];
-    const int t = threadIdx.x, bk = blockIdx.x, bn = blockIdx.y;
-    const int64_t e = blockIdx.z;
-    if (seg.out && bk == 0 && bn == 0 && e == 0) write_segments(seg);
-    const uint8_t* src = codes + (e * N + bn * kB) * K + bk * kB;
+    const int t = threadIdx.x, bn = blockIdx.x / (K / kB), bk = blockIdx.x - bn * (K / kB);
+    const int64_t e = blockIdx.y;
+    if (seg.out && blockIdx.x == 0 && e == 0) write_segments(seg);
+    const uint8_t* src = codes + (e * N + (int64_t)bn * kB) * K + bk * kB;
     uint8_t* dst = codes_t + (e * K + bk * kB) * N + bn * kB;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -250,8 +250,8 @@ hipError_t launch_segments(const Segments& g, hipStream_t s) {
 hipError_t launch_block128_transpose(const uint8_t* codes, const float* scales, int E, int N, int K, uint8_t* codes_t,
                                      float* scales_t, const Segments& seg, hipStream_t s) {
     if (seg.out && (seg.E <= 0 || seg.E > 256 || seg.R < 0 || (!seg.in && seg.E != 1))) return hipErrorInvalidValue;
-    if (E <= 0 || N <= 0 || K <= 0 || N % kB != 0 || K % kB != 0 || N / kB > 65535 || E > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(transpose_kernel, dim3(K / kB, N / kB, E), dim3(kThreads), 0, s, codes, scales, N, K, codes_t, scales_t, seg);
+    if (E <= 0 || N <= 0 || K <= 0 || N % kB != 0 || K % kB != 0 || E > 65535) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(transpose_kernel, dim3(K / kB * (N / kB), E), dim3(kThreads), 0, s, codes, scales, N, K, codes_t, scales_t, seg);
     return hipGetLastError();
 }
 

@@ -476,7 +476,7 @@ template <int TQ> hipError_t launch_act(Block128Mode mode, const Block128GemmArg
 // y[t] = sum_j s[t][j] o[slots[t][j]] in FP32, j ascending from +0.0, of o in integers; eight columns a thread.  Reading
 // o is its time: 65536 rows of 2048 52 us, 268 MB at 5.1 TB/s (58 with loads that stay in the caches).
 __global__ __launch_bounds__(256) void combine16_kernel(MxGemmArgs g) {
-    const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x, d = g.d;
+    const int t = blockIdx.x, c = blockIdx.y * 256 + threadIdx.x, d = g.d;
     if (8 * c >= d) return;
     float y[8] = {};
 #pragma unroll 8
@@ -546,7 +546,7 @@ hipError_t launch_layer_block128(MxMode mode, const MxGemmArgs& g, int num_cu, h
         return launch_gemm_block128(B128_W13, b, num_cu, s);
     }
     if (mode == MX_COMBINE) {
-        if (g.T > 0) hipLaunchKernelGGL(combine16_kernel, dim3((g.d / 8 + 255) / 256, g.T), dim3(256), 0, s, g);
+        if (g.T > 0) hipLaunchKernelGGL(combine16_kernel, dim3(g.T, (g.d / 8 + 255) / 256), dim3(g.d < 2048 ? (g.d / 8 + 63) & ~63 : 256), 0, s, g);
         return hipGetLastError();
     }
     if (mode != MX_W2) return hipErrorInvalidValue;

@@ -892,7 +892,7 @@ class Product(_OnDevice):
         if y is None:
             y = _new(self._out, torch.bfloat16, self.device)
         room = self._room(s)
-        moe_product_forward(self._cfg, x.data_ptr(), _ptr(m_indptr), w_q.data_ptr(), w_s.data_ptr(), y.data_ptr(),
+        moe_product_forward(self._cfg, x.data_ptr(), _ptr(m_indptr), _ptr(w_q), _ptr(w_s), y.data_ptr(),
                             self._status.data_ptr(), room.data_ptr(), self._workspace_bytes, s)
         return y
 
