@@ -153,6 +153,18 @@ hipError_t launch_mx_transpose_quant(const uint16_t* src, int segs, int K, int N
                                      const int32_t* gather, const float* probs, int T, bool weights,
                                      uint8_t* codes, uint8_t* scales, hipStream_t s);
 
+// Rows v [R, N] of E segments in MXFP8 along each segment's rows, as launch_mx_transpose_quant writes them, and
+// (row_codes, row_scales not NULL) in blocks of 128 along N: codes [R, N], scales [N/128, R].
+struct RowsColumnsArgs {
+    const uint16_t* v;
+    const int32_t* m_indptr;     // checked
+    int64_t R;
+    int E, N;
+    uint8_t *codes, *scales, *row_codes;
+    float* row_scales;
+};
+hipError_t launch_rows_and_columns(const RowsColumnsArgs& g, hipStream_t s);
+
 // y[t] = sum_j w[t][j] * src[slots[t][j]] (w = NULL means weight 1; slots = NULL means
 // row t*k + j), FP32, j ascending.
 hipError_t launch_combine(const uint16_t* src, const int32_t* slots, const float* w, int T, int k,

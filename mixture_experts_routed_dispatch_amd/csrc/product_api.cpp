@@ -158,8 +158,14 @@ moe_status_t moe_product_backward(const moe_product_config_t* c, const void* dy,
         // dx = dy W: the matrices transposed, dy quantized along N
         if (launch_block128_transpose(w_q, w_s, E, c->N, c->K, codes(r.wt), scales(r.wts), seg, s) != hipSuccess)
             return MOE_ERR_HIP;
-        if (launch_block128_rows(static_cast<const uint16_t*>(dy), R, c->N, codes(r.q), scales(r.qs), true, starts + E, s) != hipSuccess)
+        if (dw) {                                        // with dy along the rows, for dw, from the same reads
+            const RowsColumnsArgs both{static_cast<const uint16_t*>(dy), starts, R, E, c->N, codes(r.tq), codes(r.tqs),
+                                       codes(r.q), scales(r.qs)};
+            if (launch_rows_and_columns(both, s) != hipSuccess) return MOE_ERR_HIP;
+        } else if (launch_block128_rows(static_cast<const uint16_t*>(dy), R, c->N, codes(r.q), scales(r.qs), true, starts + E,
+                                        s) != hipSuccess) {
             return MOE_ERR_HIP;
+        }
         Block128GemmArgs g{};
         g.E = E; g.K = c->N; g.Np = c->K; g.R = R;
         g.m_indptr = starts;
@@ -169,11 +175,12 @@ moe_status_t moe_product_backward(const moe_product_config_t* c, const void* dy,
     }
     if (dw) {
         // dW_e = sum_r dy[r] x[r]^T: both operands along the rows, in MXFP8
-        if (launch_mx_transpose_quant(static_cast<const uint16_t*>(x), E, R, c->K, starts, nullptr, nullptr, 0, false,
-                                      codes(r.tp), codes(r.tps), s) != hipSuccess ||
-            launch_mx_transpose_quant(static_cast<const uint16_t*>(dy), E, R, c->N, starts, nullptr, nullptr, 0, false,
-                                      codes(r.tq), codes(r.tqs), s) != hipSuccess)
-            return MOE_ERR_HIP;
+        RowsColumnsArgs t{static_cast<const uint16_t*>(x), starts, R, E, c->K, codes(r.tp), codes(r.tps), nullptr, nullptr};
+        if (launch_rows_and_columns(t, s) != hipSuccess) return MOE_ERR_HIP;
+        if (!dx || R == 0) {
+            t.v = static_cast<const uint16_t*>(dy); t.N = c->N; t.codes = codes(r.tq); t.scales = codes(r.tqs);
+            if (launch_rows_and_columns(t, s) != hipSuccess) return MOE_ERR_HIP;
+        }
         MxGemmArgs g{};
         g.T = R; g.k = 1; g.E = E; g.m_indptr = starts;
         g.Np = c->K; g.Nq = c->N;
