@@ -40,11 +40,29 @@ __device__ __forceinline__ float block_quotient(float v, float s, float inv) {
     return __builtin_copysignf(__uint_as_float(b), v);
 }
 
-// Codes of four values.  With a NaN scale they are some E4M3 numbers: what is multiplied with that
-// scale is NaN whatever they are.
+// Codes of four values.  With a NaN scale they are any codes: what is multiplied with that scale is NaN whatever they are.
+// v inv is within three of its own last places of the quotient (the reciprocal's ulp and a rounding), so that it
+// rounds as the quotient does unless a midpoint between two E4M3 values is that near: from 2^-6 on, where these have
+// three bits behind the point, one whose 20 last bits are 0x80000.  Such values, and smaller ones, are settled by
+// block_quotient.  (Every value that way: a layer of 16384 x 4096 x 2048, 64 experts, 3658 us against 3612.)  What is above 448 by
+// those last places rounds to it.
 __device__ __forceinline__ uint32_t block_codes4(float a, float b, float c, float d, float s, float inv) {
-    return e4m3_pack4(block_quotient(a, s, inv), block_quotient(b, s, inv), block_quotient(c, s, inv),
-                      block_quotient(d, s, inv));
+    const float v[4] = {a, b, c, d};
+    float q[4], least = INFINITY;
+    uint32_t near = 0xFFFFFFFFu;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        q[z] = v[z] * inv;
+        const uint32_t t = (__float_as_uint(q[z]) << 12) - (0x7FFFCu << 12);
+        near = near < t ? near : t;
+        least = __builtin_fminf(least, __builtin_fabsf(q[z]));
+    }
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+    if (__builtin_expect(near < 8u << 12 || least < 0x1p-6f, 0))
+        return e4m3_pack4(block_quotient(a, s, inv), block_quotient(b, s, inv), block_quotient(c, s, inv),
+                          block_quotient(d, s, inv));
+    return (uint32_t)w;
 }
 // largest magnitude, as bits, of eight BF16 values
 __device__ __forceinline__ uint32_t bf16_amax_bits(uint4 v) {
