@@ -371,9 +371,10 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_b128(Block128GemmArgs g) 
                     const uint32_t t = __shfl_xor(top, o, MOE_WAVE);
                     top = top > t ? top : t;
                 }
-                // a row that holds an infinity or NaN is NaN; one below 2^-120 is zero
+                // a row that holds an infinity or NaN is NaN; one below 2^-120 is zero.  (The reciprocal's own result
+                // is not to be a denormal, which it flushes.)
                 const bool some = top >= 0x03800000u && top < 0x7F800000u;
-                inv = some ? __builtin_amdgcn_rcpf(__uint_as_float(top)) : 0.f;
+                inv = some ? __builtin_amdgcn_rcpf(__uint_as_float(top) * 0.25f) * 0.25f : 0.f;
                 const float unit = some ? __uint_as_float(top) * (1.0f / 32767.0f) : top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
                 const int rr = c.qt * TQ + wq * 16 * kNB + b * 16 + row16, p = c.pt * TP + wp * 128;
                 if (quad == 0 && rr < c.rows && p < g.Np) g.os[(size_t)(c.mb + rr) * (g.Np / 128) + p / 128] = unit;

@@ -353,6 +353,26 @@ def test_layer_on_weights_with_any_scales(moe):
         assert close(y, want, 2.5e-3)
 
 
+@pytest.mark.parametrize("power", [125, -115])
+@pytest.mark.parametrize("T", [1, 20, 400])
+def test_layer_outputs_of_any_size(moe, T, power):
+    """Expert outputs near the largest numbers, and near the smallest of full precision."""
+    from tests import block128_ref as ref
+    layer, x, ids, scores, p = layer_case(moe, T, 256, 128, 8, 2)
+    p[3].mul_(2.0 ** power)
+    y = layer.forward(x, ids, scores, p[0], p[2], p[1], p[3])
+    assert close(y, ref.layer(x, ids, scores, ref.matrix(p[0], p[1]), ref.matrix(p[2], p[3])), 2.5e-3)
+
+
+def test_layer_of_no_tokens(moe):
+    import torch
+    layer = moe.Layer(0, 256, 128, 8, 2, precision=moe.MOE_FP8_BLOCK128)
+    p = layer.prepare_weights(randn(1, 8, 256, 256), randn(2, 8, 256, 128))
+    none = lambda n, t: torch.empty(0, n, dtype=t, device=dev())
+    y = layer.forward(none(256, torch.bfloat16), none(2, torch.int32), none(2, torch.float32), p[0], p[2], p[1], p[3])
+    assert y.shape == (0, 256) and layer.status() == (moe.MOE_OK, 0)
+
+
 def test_layer_rows_in_expert_order(moe):
     import torch
     from tests import block128_ref as ref
