@@ -12,8 +12,8 @@
 // a block of it is the work of several workgroups; a launch quantizes it; W2 and the combine follow.
 // One token: two launches, whose workgroups quantize x and a for themselves.
 //
-// d = 2048, I = 768, k = 8: one token 8.4 + 6.4 us for 25 + 13 MB, a round trip of loads each; 32 tokens of 60 experts W13
-// 40.6 us (4.7 TB/s), W2 24.2 (4.0 TB/s), the three small launches 4.6-4.9 each.  A product of one row of 4096 x 4096: 5.5 us.
+// d = 2048, I = 768, k = 8: one token 8.1 + 6.8 us for 25 + 13 MB, a round trip of loads each; 32 tokens of 68 experts W13
+// 39.2 us (5.5 TB/s), W2 21.2 (5.0 TB/s), the three small launches 4.6-4.8 each.  A product of one row of 4096 x 4096: 5.8 us.
 #include "block128.h"
 #include "decode_common.h"
 
