@@ -273,7 +273,7 @@ struct Block128RowsArgs {
     void* groups;             // kBlock128GroupBytes
 };
 // Rows that stream the weights instead of going through the grouped products: up to 128 of one matrix (4096 x 2048:
-// 18.0 us against 23.3, with 256 rows 28.3 against 24.1), up to 256 of several (16 of 1536 x 2048: 20.1 against 25.0)
+// 17.1 us against 23.3, with 256 rows 28.3 against 24.1), up to 256 of several (16 of 1536 x 2048: 20.1 against 25.0)
 inline bool block128_few_rows(int64_t R, int E) { return R <= kMaxDecodeRows && R <= 128 * (int64_t)E; }
 hipError_t launch_block128_few_rows(const Block128RowsArgs& g, int num_cu, hipStream_t s);
 
