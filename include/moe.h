@@ -378,8 +378,8 @@ moe_status_t moe_product_forward(const moe_product_config_t* cfg, const void* x,
                                  const uint8_t* w_q, const float* w_s, void* y, int32_t* status, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
-/* dx BF16 [R, K] and dw BF16 [E, N, K] (+0.0 for experts with no row), either of which may be NULL; x is
- * read for dw, the weights for dx.  With a broken m_indptr every expert counts as empty. */
+/* dx BF16 [R, K] and dw BF16 [E, N, K] (+0.0 for experts with no row), either of which may be NULL (with R = 0,
+ * where dx is empty, both); x is read for dw, the weights for dx.  With a broken m_indptr every expert counts as empty. */
 moe_status_t moe_product_backward(const moe_product_config_t* cfg, const void* dy, const void* x,
                                   const int32_t* m_indptr, const uint8_t* w_q, const float* w_s, void* dx, void* dw,
                                   int32_t* status, void* workspace, size_t workspace_bytes, void* stream);

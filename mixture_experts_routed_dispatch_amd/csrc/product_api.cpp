@@ -133,6 +133,7 @@ moe_status_t moe_product_backward(const moe_product_config_t* c, const void* dy,
     const moe_status_t st = product_check(c);
     if (st != MOE_OK) return st;
     if (!c->training) return MOE_ERR_STATE;
+    if (c->R == 0 && !dw) return MOE_OK;                 // dx is empty (so that its pointer may be null)
     if (!dx && !dw) return MOE_ERR_INVALID_ARG;
     if (c->R > 0 && (!dy || (dw && !x) || (dx && (!w_q || !w_s)) || (!m_indptr && c->E != 1))) return MOE_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(x) || !aligned16(w_q) || !aligned4(w_s) || !aligned16(dx) || !aligned16(dw))
