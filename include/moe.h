@@ -346,7 +346,8 @@ moe_status_t moe_backward(moe_plan_t plan, const void* dy, const void* x, const 
  * for dx, dy along N, a block being 128 elements of a row; a weight's block is 128 x 128.  A product is
  * the sum over blocks of (sum of code products) x scale x scale, in FP32, rounded once to BF16.
  * For dW the operands are quantized along the expert's rows instead, in MXFP8: blocks of 32 rows,
- * counted from the expert's first, by moe_quantize_mxfp8's rule (which makes an infinity or NaN finite). */
+ * counted from the expert's first, by moe_quantize_mxfp8's rule; but a block that holds an infinity or NaN is NaN,
+ * and so are the row (from dy) or the column (from x) of its expert's dW that it enters. */
 typedef struct {
     int32_t R;                 /* rows, 0 .. 2^24 */
     int32_t N;                 /* outputs; a multiple of 128 */

@@ -19,6 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint16_t* __restrict__ v,
                                                             int64_t nblocks, int kb_row, int64_t rows,
@@ -100,11 +101,8 @@ __global__ void __launch_bounds__(kThreads) route_scales_kernel(const uint32_t* 
     }
 }
 
-// One MX block of 32 FP32 values: E8M0 scale byte and 32 E4M3 codes (8 words).
-__device__ __forceinline__ uint32_t quant_block32(const float* v, uint32_t out[8]) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
+// One MX block of 32 FP32 values: E8M0 scale byte and 32 E4M3 codes (8 words), from its largest magnitude.
+__device__ __forceinline__ uint32_t quant_block32(const float* v, float amax, uint32_t out[8]) {
     const uint32_t sb = e8m0_scale(amax);
     const int sh = 127 - (int)sb;
 #pragma unroll
@@ -112,6 +110,12 @@ __device__ __forceinline__ uint32_t quant_block32(const float* v, uint32_t out[8
         out[i] = e4m3_pack4(__builtin_ldexpf(v[4 * i], sh), __builtin_ldexpf(v[4 * i + 1], sh),
                             __builtin_ldexpf(v[4 * i + 2], sh), __builtin_ldexpf(v[4 * i + 3], sh));
     return sb;
+}
+__device__ __forceinline__ uint32_t quant_block32(const float* v, uint32_t out[8]) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
+    return quant_block32(v, amax, out);
 }
 
 __device__ __forceinline__ void store_codes32(uint8_t* dst, const uint32_t w[8]) {
@@ -429,13 +433,20 @@ __global__ __launch_bounds__(kThreads, 4) void rows_and_columns_kernel(RowsColum
         const int64_t n = (int64_t)ft * kTile + 2 * pair;
         uint8_t* dst = g.codes + at.koff * N + n * at.kp + at.kt * kTile + 32 * b;
         uint8_t* sd = g.scales + at.koff * N / 32 + ((int64_t)at.kt * N + n) * 4 + b;
+        // both columns' largest magnitudes; as integers, they have infinities and NaN above all
+        u16x2_t top = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2_t, w[j] & 0x7FFF7FFFu));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = h ? bf16hi(w[j]) : bf16lo(w[j]);
             uint32_t out[8];
-            sd[4 * h] = (uint8_t)quant_block32(v, out);
+            sd[4 * h] = (uint8_t)quant_block32(v, bf16_to_f32(top[h]), out);
+            // a block that holds an infinity or NaN: all its codes are NaN, and so is its row or column of dW
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[i] = top[h] >= 0x7F80u ? 0x7F7F7F7Fu : out[i];
             store_codes32(dst + h * at.kp, out);
         }
     }

@@ -3,8 +3,8 @@ unlike size, arguments of wrong form, the status word, operands that end with th
 bounds that tests/test_gpu_block128.py derives."""
 import pytest
 
-from tests.gpu_util import dev
-from tests.test_gpu_block128 import moe, randn  # noqa: F401
+from tests.gpu_util import dev, say
+from tests.test_gpu_block128 import INF, NAN, moe, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +27,35 @@ def test_gradients_of_no_rows(moe, need, E):
             assert torch.equal(dw, before) if add else (dw == 0).all()
         else:
             assert dw is None
+
+
+@pytest.mark.parametrize("R,N,K,E", [(70, 128, 256, 1), (300, 256, 384, 3), (4099, 256, 128, 1)])
+def test_not_finite_rows_reach_the_weight_gradient(moe, R, N, K, E):
+    """An infinity or NaN of dy makes its matrix' row of dW NaN, one of x its column, and nothing else; rows behind
+    the last segment are not read."""
+    import torch
+    say("not finite", R, N, K, E)
+    p = moe.Product(R, N, K, E=E, training=True)
+    x, dy, w = randn(R, R, K), randn(R + 1, R, N, std=0.1), randn(N, E, N, K)
+    w_q, w_s = p.prepare_weights(w)
+    m = torch.tensor([0, R - 5, R - 5, R - 2][:E] + [R - 2], dtype=torch.int32, device=dev())
+    good = [p.backward(dy, x, w_q, w_s, m_indptr=m), (None, p.backward(dy, x, None, None, m_indptr=m, need_dx=False)[1])]
+    assert torch.equal(good[0][1], good[1][1])
+    last = R - 6                                         # in matrix 0, in its last block of 32 rows
+    dy[1, 3], dy[40, 77], dy[last, N - 1], dy[33, N - 2] = NAN, INF, -INF, -NAN
+    x[0, K - 1], x[35, 64], x[last, 5] = -INF, NAN, INF
+    dy[R - 1, 9], x[R - 2, 9] = NAN, INF
+    bad = torch.zeros(E, N, K, dtype=torch.bool, device=dev())
+    for n in (3, 77, N - 1, N - 2):
+        bad[0, n] = True
+    for k in (K - 1, 64, 5):
+        bad[0, :, k] = True
+    bad_dx = torch.zeros(R, K, dtype=torch.bool, device=dev())
+    for r in (1, 40, 33, last):
+        bad_dx[r] = True
+    dx, dw = p.backward(dy, x, w_q, w_s, m_indptr=m)
+    _, only = p.backward(dy, x, None, None, m_indptr=m, need_dx=False)
+    for got in (dw, only):
+        assert torch.equal(got.isnan(), bad) and torch.equal(got[~bad], good[0][1][~bad])
+    live = slice(0, R - 2)
+    assert torch.equal(dx[live].isnan(), bad_dx[live]) and torch.equal(dx[live][~bad_dx[live]], good[0][0][live][~bad_dx[live]])
