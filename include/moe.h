@@ -261,9 +261,9 @@ moe_status_t moe_prepare_weights_backward(moe_plan_t plan, const void* w13_bf16,
  * to BF16 (nvfp4moe README, "MoE layer": the timed path).  y is BF16 [T, d].
  * With FP8_BLOCK128 every product's operands are in 8 bits on either path: x by
  * moe_quantize_block128's rule, and the activation's output a, from its FP32 value, by the same
- * rule along I.  y is added up from expert outputs of 32 bits on the decode path,
- * of 16 bits, integers with a scale per row and 128, on the other (128 that hold an infinity or NaN are NaN, 128 below
- * 2^-120 are 0).
+ * rule along I.  y is added up from expert outputs of 32 bits on the decode path, on the other of FP16 in units of a
+ * power of two per row and 128 (each within 2^-11 of itself, or a 2^-39th of the largest of its 128; 128 that hold
+ * an infinity or NaN are NaN).
  * BF16 plans take BF16 weights; MXFP8 plans take the prepared codes in w13 / w2
  * and their E8M0 scales in w13_scale / w2_scale (moe_prepare_weights layout;
  * NULL scales are MOE_ERR_INVALID_ARG).  Plans with T*k <= 256 (BF16, inference)

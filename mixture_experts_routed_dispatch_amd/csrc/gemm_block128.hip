@@ -8,11 +8,13 @@
 //   mode       P                          Q                      K    output
 //   B128_W13   W13_e, gate/up row pairs   xq[gather[r]]          d    a = f(g) u quantized along I: codes [R, I],
 //                                                                     scales [I/128, R]
-//   B128_W2    W2_e rows                  aq[r]                  I    o in 16-bit integers, in units of a 32767th of
-//                                                                     the largest of a row's block of 128: [R, d],
-//                                                                     [R, d/128].  As many bytes as BF16, whose rounding
-//                                                                     would add as much again to y's error; this adds a
-//                                                                     hundredth
+//   B128_W2    W2_e rows                  aq[r]                  I    o in FP16, in units of a power of two that puts the
+//                                                                     largest of a row's block of 128 into 2^14 .. 2^15:
+//                                                                     [R, d], [R, d/128].  Within 2^-11 of each value
+//                                                                     down to a 2^-29th of the block's largest, in as many bytes
+//                                                                     as BF16 (2^-8).  (Integers in units of the largest are
+//                                                                     closer where all are of one size, but lose the
+//                                                                     others beside one 2^12 times as large: 3.5e-2)
 //   B128_PLAIN rows of a matrix           routed rows            Kp   BF16 [R, Np]: a product's forward and input gradient,
 //                                                                     W2 of rows in expert order
 //
@@ -43,6 +45,12 @@ constexpr int TP = 256, TK = 128;
 constexpr int kPBytes = TP * TK;
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+// two floats in FP16, nearest even, the first in the low half
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const f32x2_t v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
+}
 
 // Order of an expert's tiles: as in the MXFP8 products, groups of kQGroup row tiles, inside a group
 // the P tiles with the group's row tiles fastest, so that the tiles that an XCD runs at a time share
@@ -355,7 +363,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_b128(Block128GemmArgs g) 
         }
     };
     auto epilogue_rows = [&](const Tile& c, int buf) {
-        // rows in BF16 (B128_W2: integers) by way of this wave's 4 KiB of the buffer, 16 at a time, stored as
+        // rows in BF16 (B128_W2: scaled FP16) by way of this wave's 4 KiB of the buffer, 16 at a time, stored as
         // whole 256-byte pieces past the caches (ordinary stores evict operands that the XCD's workgroups share)
         const int lane = fresh_lane(), row16 = lane & 15, quad = lane >> 4;
         char* stg = lds + buf * kBuf + wave * 4096;
@@ -376,16 +384,16 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_b128(Block128GemmArgs g) 
                     const uint32_t t = __shfl_xor(top, o, MOE_WAVE);
                     top = top > t ? top : t;
                 }
-                // a row that holds an infinity or NaN is NaN; one below 2^-120 is zero.  (The reciprocal's own result
-                // is not to be a denormal, which it flushes.)
-                const bool some = top >= 0x03800000u && top < 0x7F800000u;
-                inv = some ? __builtin_amdgcn_rcpf(__uint_as_float(top) * 0.25f) * 0.25f : 0.f;
-                const float unit = some ? __uint_as_float(top) * (1.0f / 32767.0f) : top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
+                // the unit's exponent, biased: at least 1, so that neither it nor its inverse is a denormal.  128 that
+                // hold an infinity or NaN are NaN.
+                const uint32_t e = top >> 23, ue = (e > 15u ? e : 15u) - 14u;
+                inv = __uint_as_float((254u - ue) << 23);
+                const float unit = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : ue << 23);
                 const int rr = c.qt * TQ + wq * 16 * kNB + b * 16 + row16, p = c.pt * TP + wp * 128;
                 if (quad == 0 && rr < c.rows && p < g.Np) g.os[(size_t)(c.mb + rr) * (g.Np / 128) + p / 128] = unit;
             }
             auto pack = [&](float x, float y) {
-                if constexpr (MODE == B128_W2) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_i16(x * inv, y * inv));
+                if constexpr (MODE == B128_W2) return pack_f16(x * inv, y * inv);
                 else return pack_bf16(x, y);
             };
 #pragma unroll
@@ -479,7 +487,7 @@ template <int TQ> hipError_t launch_act(Block128Mode mode, const Block128GemmArg
     return launch_t<B128_W13, kActSwiGLU, TQ>(g, num_cu, s);
 }
 
-// y[t] = sum_j s[t][j] o[slots[t][j]] in FP32, j ascending from +0.0, of o in integers; eight columns a thread.  Reading
+// y[t] = sum_j s[t][j] o[slots[t][j]] in FP32, j ascending from +0.0, of o in scaled FP16; eight columns a thread.  Reading
 // o is its time: 65536 rows of 2048 52 us, 268 MB at 5.1 TB/s (58 with loads that stay in the caches).
 __global__ __launch_bounds__(256) void combine16_kernel(MxGemmArgs g) {
     const int t = blockIdx.x, c = blockIdx.y * 256 + threadIdx.x, d = g.d;
@@ -492,8 +500,10 @@ __global__ __launch_bounds__(256) void combine16_kernel(MxGemmArgs g) {
         const float f = g.os[r * (d / 128) + c / 16], w = g.scores[(size_t)t * g.k + j];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-            y[2 * z] = __builtin_fmaf(w, f * (float)(int16_t)(u[z] & 0xFFFFu), y[2 * z]);
-            y[2 * z + 1] = __builtin_fmaf(w, f * (float)((int32_t)u[z] >> 16), y[2 * z + 1]);
+            const uint32_t word = u[z];                  // (a bit cast of u[z] itself takes u[0])
+            const f16x2_t h = __builtin_bit_cast(f16x2_t, word);
+            y[2 * z] = __builtin_fmaf(w, f * (float)h[0], y[2 * z]);
+            y[2 * z + 1] = __builtin_fmaf(w, f * (float)h[1], y[2 * z + 1]);
         }
     }
     *reinterpret_cast<uint4*>(g.y + (size_t)t * d + 8 * c) =

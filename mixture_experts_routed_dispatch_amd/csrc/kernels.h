@@ -114,8 +114,8 @@ struct MxGemmArgs {
     int block128;
     const uint16_t* x;    // MX_QUANT_X: [T, d], or with xs_rows NULL the rows in expert order
     uint8_t* xs_rows;     // MX_QUANT_X: [T, d/128], the scales by token
-    float* os;            // MX_W2: NULL: o is BF16; else [R, d/128], the largest magnitudes / 32767 of o's blocks of 128,
-                          // whose values are 16-bit integers in units of that
+    float* os;            // MX_W2: NULL: o is BF16; else [R, d/128], powers of two in whose units o's blocks of 128
+                          // are FP16
     const int32_t* slots; // MX_COMBINE: y[t] = sum_j scores[t][j] o[slots[t][j]], in FP32, j ascending
     const float* scores;
     uint16_t* y;
@@ -316,7 +316,7 @@ hipError_t launch_block128_transpose(const uint8_t* codes, const float* scales, 
 // Grouped products of such operands (gemm_block128.hip): rows m_indptr[e] .. m_indptr[e+1] with
 // matrix e, E <= 256, K and Np multiples of 128.  Offsets inside one matrix, and in W13 inside the rows'
 // codes, are 32-bit.
-// B128_W2: as PLAIN, but out holds 16-bit integers in units of os (MxGemmArgs).
+// B128_W2: as PLAIN, but out holds FP16 in units of os (MxGemmArgs).
 enum Block128Mode { B128_W13 = 0, B128_PLAIN = 1, B128_W2 = 2 };
 struct Block128GemmArgs {
     int E, K, Np;             // Np: outputs, W13: I

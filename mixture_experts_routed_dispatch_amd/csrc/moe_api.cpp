@@ -340,7 +340,7 @@ size_t moe_plan_explain(moe_plan_t p, char* buf, size_t len) {
     if (p->dh_aliased)
         region("o", 2 * (size_t)R * c.d, "fwd/bwd", "expert outputs [R, d] BF16; in the backward dh (g, u gradient [R, 2I])");
     else
-        saved_region("o", p->o_bytes, p->o_bytes != 2 * (size_t)R * c.d ? "expert outputs [R, d] FP32" : b128 ? "expert outputs [R, d], 16-bit integers" : "expert outputs [R, d] BF16");
+        saved_region("o", p->o_bytes, p->o_bytes != 2 * (size_t)R * c.d ? "expert outputs [R, d] FP32" : b128 ? "expert outputs [R, d], scaled FP16 (bits in 16-bit integers)" : "expert outputs [R, d] BF16");
     if (c.training) {
         const size_t hb = 2 * (size_t)R * 2 * c.I;
         if (c.recompute_h)

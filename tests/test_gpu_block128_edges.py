@@ -4,7 +4,7 @@ bounds that tests/test_gpu_block128.py derives."""
 import pytest
 
 from tests.gpu_util import dev, say
-from tests.test_gpu_block128 import INF, NAN, moe, randn  # noqa: F401
+from tests.test_gpu_block128 import INF, NAN, layer_case, moe, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,26 @@ def test_not_finite_rows_reach_the_weight_gradient(moe, R, N, K, E):
         assert torch.equal(got.isnan(), bad) and torch.equal(got[~bad], good[0][1][~bad])
     live = slice(0, R - 2)
     assert torch.equal(dx[live].isnan(), bad_dx[live]) and torch.equal(dx[live][~bad_dx[live]], good[0][0][live][~bad_dx[live]])
+
+
+@pytest.mark.parametrize("T,k", [(20, 2), (400, 2)])
+@pytest.mark.parametrize("power", [8, 12])
+def test_columns_beside_a_large_one(moe, T, k, power):
+    """One output in every 128 is 2^power the others' size: the others are as exact as without it, on either path.  (FP16
+    in units of a power of two is off by at most 2^-11 of each value: 2^-12 of the norm, where the bound leaves 1.5e-3.)"""
+    import torch
+    from tests import block128_ref as ref
+    d, I, E = 384, 256, 8
+    layer, x, ids, scores, p = layer_case(moe, T, d, I, E, k)
+    w2 = randn(77, E, d, I, std=I ** -0.5)
+    w2[:, 37::128] *= 2.0 ** power
+    _, _, q2, s2 = layer.prepare_weights(randn(78, E, 2 * I, d, std=d ** -0.5), w2)
+    y = layer.forward(x, ids, scores, p[0], q2, p[1], s2)
+    want = ref.layer(x, ids, scores, ref.matrix(p[0], p[1]), ref.matrix(q2, s2))
+    small = torch.ones(d, dtype=torch.bool, device=dev())
+    small[37::128] = False
+    for cols in (small, ~small):
+        a, b = y[:, cols].double(), want[:, cols]
+        rel = float((a - b).norm() / b.norm())
+        say("  T %d, 2^%d: rel %.2e" % (T, power, rel))
+        assert rel <= 2.5e-3
