@@ -371,6 +371,7 @@ class Layer:
     call makes come from the memory of the stream that writes them (`stream`, else the current one)."""
 
     _block128 = None                   # shapes of the weights' scales, with MOE_FP8_BLOCK128
+    _forward_args = _routed_args = None  # and what _check_rows takes of a call's other tensors
 
     def __init__(self, T, d, I, E, k, precision=MOE_BF16, training=False, path=MOE_PATH_AUTO,
                  device="cuda", wgrad_accumulate=False, recompute_h=False, activation=MOE_ACT_SWIGLU,
@@ -390,10 +391,21 @@ class Layer:
                            (_dense(E, d * I // 2), _dense(E, d // 16, (I + 511) // 512, 64, 4)))
             self._mxfp4_sizes = tuple(math.prod(shape) for shape, _ in sum(self._mxfp4, ()))
         if precision == MOE_FP8_BLOCK128:
-            self._block128 = (E, 2 * I // 128, d // 128), (E, d // 128, I // 128)
+            self._set_block128()
         nbytes = moe_workspace_bytes(self.plan)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         moe_bind_workspace(self.plan, _ptr(self.workspace), self.workspace.numel())
+
+    def _set_block128(self):
+        import torch
+        T, d, I, E, k, bf16, i32 = self.T, self.d, self.I, self.E, self.k, torch.bfloat16, torch.int32
+        self._block128 = (E, 2 * I // 128, d // 128), (E, d // 128, I // 128)
+        row, per_choice = (bf16, (T, d), T * d), (T, k)
+        self._forward_args = (("x", *row), ("ids", i32, per_choice, T * k), ("scores", torch.float32, per_choice, T * k),
+                              ("y", *row))
+        # x_rows and out may end with the last segment's rows
+        rows = bf16, (T * k, d), None
+        self._routed_args = ("x_rows", *rows), ("m_indptr", i32, (E + 1,), E + 1), ("out", *rows)
 
     def explain(self) -> str:
         return moe_plan_explain(self.plan)
@@ -428,7 +440,7 @@ class Layer:
         if self._mxfp4 is not None:
             self._check_mxfp4(w13, w13_scale, w2, w2_scale, x, ids, scores, y, stream)
         if self._block128 is not None:
-            self._check_block128(w13, w13_scale, w2, w2_scale, (x, ids, scores, y), stream)
+            self._check_block128(w13, w13_scale, w2, w2_scale, (x, ids, scores, y), self._forward_args, stream)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward(self.plan, _ptr(x), _ptr(ids), _ptr(scores), w, _ptr(y), _stream(stream))
         return y
@@ -444,7 +456,7 @@ class Layer:
         if self._mxfp4 is not None:
             self._check_mxfp4(w13, w13_scale, w2, w2_scale, x_rows, m_indptr, out, out, stream)
         if self._block128 is not None:
-            self._check_block128(w13, w13_scale, w2, w2_scale, (x_rows, m_indptr, out), stream)
+            self._check_block128(w13, w13_scale, w2, w2_scale, (x_rows, m_indptr, out), self._routed_args, stream)
         w = weights(_ptr(w13), _ptr(w2), _ptr(w13_scale), _ptr(w2_scale))
         moe_forward_routed(self.plan, _ptr(x_rows), _ptr(m_indptr), w, _ptr(out), _stream(stream))
         return out
@@ -529,9 +541,9 @@ class Layer:
             _check(name, t, shape, torch.uint8, dev)
         raise ValueError("the current device is %s; x, ids, scores or the output is elsewhere" % dev)
 
-    def _check_block128(self, w13_q, w13_s, w2_q, w2_s, others, stream):
-        """Codes and scales of this layer's sizes, they, the other tensors and the stream on the current
-        device, or ValueError (a missing tensor is left to the call, which refuses it)."""
+    def _check_block128(self, w13_q, w13_s, w2_q, w2_s, others, args, stream):
+        """Codes and scales of this layer's sizes, the other tensors as args says, they and the stream on the
+        current device, or ValueError (a missing tensor is left to the call, which refuses it)."""
         import torch
         index = torch.cuda.current_device()
         if stream is not None:
@@ -549,16 +561,19 @@ class Layer:
             _check("w13_s", w13_s, s13, torch.float32, dev)
             _check_codes("w2_q", w2_q, n2[0], dev)
             _check("w2_s", w2_s, s2, torch.float32, dev)
-        for t in others:
-            if t is not None and t.get_device() != index:
-                raise ValueError("the current device is cuda:%d; x, ids, scores or the output is elsewhere" % index)
+        for t, arg in zip(others, args or _no_args):
+            if t is not None:
+                if t.get_device() != index:
+                    raise ValueError("the current device is cuda:%d; x, ids, scores or the output is elsewhere" % index)
+                if arg is not None and not (t.dtype is arg[1] and t.shape == arg[2] and t.is_contiguous()):
+                    _check_rows(t, *arg)
 
     def expand_weights(self, w13_q, w13_s, w2_q, w2_s, stream=None):
         """The BF16 weights (w13, w2) that the prepared weights of an MXFP4 or MOE_FP8_BLOCK128 layer
         stand for."""
         import torch
         if self._block128 is not None:
-            self._check_block128(w13_q, w13_s, w2_q, w2_s, (), stream)
+            self._check_block128(w13_q, w13_s, w2_q, w2_s, (), None, stream)
         if self._mxfp4 is not None:
             self._check_mxfp4(w13_q, w13_s, w2_q, w2_s, w13_q, w13_s, w2_q, w2_s, stream)
         w13, w2 = (_new(n, torch.bfloat16, w13_q.device, stream) for n in self._weights)
@@ -619,6 +634,19 @@ def _check(name, t, shape, dtype, device):
     raise ValueError("%s: a contiguous %s tensor of shape %s on %s is needed, got %s %s on %s%s" % (
         name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
         "" if t.is_contiguous() else ", not contiguous"))
+
+
+_no_args = (None,) * 4
+
+
+def _check_rows(t, name, dtype, shape, numel):
+    """A dense tensor of this type, of rows as long as the shape's (or flat), `numel` elements in all unless that is
+    None, or ValueError: the kernels address it by the plan's sizes."""
+    if (t.dtype is dtype and t.is_contiguous() and (numel is None or t.numel() == numel)
+            and (t.dim() == 1 or t.shape[-1:] == shape[-1:])):
+        return
+    raise ValueError("%s: a contiguous %s tensor of shape %s is needed, got %s %s%s" % (
+        name, dtype, shape, t.dtype, tuple(t.shape), "" if t.is_contiguous() else ", not contiguous"))
 
 
 _codes = None
