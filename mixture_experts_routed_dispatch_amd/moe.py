@@ -860,7 +860,8 @@ class Product(_OnDevice):
     """Rows [R, K] in BF16 times weights [E, N, K] in E4M3 with one FP32 scale per 128 x 128: one matrix, or
     with m_indptr (int32 [E+1] on the device) the matrix of each segment of the rows.  See the section on
     products in include/moe.h.  Weights are codes (uint8 or float8_e4m3fn) [E, N, K] and scales f32
-    [E, N/128, K/128], from prepare_weights or from a checkpoint that holds them so."""
+    [E, N/128, K/128], from prepare_weights or from a checkpoint that holds them so.  Calls may be captured; the
+    object is made before."""
 
     def __init__(self, R, N, K, E=1, training=False, wgrad_accumulate=False, device="cuda"):
         import torch
@@ -872,7 +873,15 @@ class Product(_OnDevice):
         if not nbytes:                                 # the reason, from the call that names it
             moe_product_forward(self._cfg, 0, 0, 0, 0, 0, 0, 0, 0)
         super().__init__(device, nbytes)
+        if self._own is None:
+            raise RuntimeError("a Product is made before a capture, not in it: its status word would be cleared by each replay")
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._wait()
+
+    def _wait(self):
+        """The status word is cleared: calls on any stream may set it from now on."""
+        import torch
+        torch.cuda.current_stream(self.device).synchronize()
 
     def _check_args(self, w_q, w_s, m_indptr):
         import torch
@@ -956,4 +965,5 @@ class Product(_OnDevice):
         flags = int(self._status.item())
         if clear and flags:
             self._status.zero_()
+            self._wait()
         return (MOE_ERR_ROUTING if flags else MOE_OK), flags

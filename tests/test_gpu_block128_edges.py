@@ -4,7 +4,7 @@ bounds that tests/test_gpu_block128.py derives."""
 import pytest
 
 from tests.gpu_util import dev, say
-from tests.test_gpu_block128 import INF, NAN, layer_case, moe, randn  # noqa: F401
+from tests.test_gpu_block128 import INF, NAN, layer_case, moe, randn, routing, starts, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,44 @@ def test_columns_beside_a_large_one(moe, T, k, power):
         rel = float((a - b).norm() / b.norm())
         say("  T %d, 2^%d: rel %.2e" % (T, power, rel))
         assert rel <= 2.5e-3
+
+
+def test_the_status_word_is_clear_before_the_first_call(moe):
+    """A flag that a call on another stream sets right after the object was made stays set, however late the stream
+    is that the object was made on."""
+    import torch
+    x, m = randn(0, 300, 128), torch.tensor([0, 200, 100, 300], dtype=torch.int32, device=dev())
+    first = moe.Product(300, 128, 128, E=3)
+    w_q, w_s = first.prepare_weights(randn(1, 3, 128, 128))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                        # some 10 ms of the current stream
+    p = moe.Product(300, 128, 128, E=3)
+    y = torch.empty(300, 128, dtype=torch.bfloat16, device=dev())
+    p.forward(x, w_q, w_s, m_indptr=m, y=y, stream=side)
+    assert p.status() == (moe.MOE_ERR_ROUTING, moe.MOE_DEV_BAD_INDPTR)
+    assert p.status() == (moe.MOE_OK, 0)
+    # and one right after the word was read and cleared
+    p.forward(x, w_q, w_s, m_indptr=m, y=y, stream=side)
+    p.status()
+    p.forward(x, w_q, w_s, m_indptr=m, y=y, stream=side)
+    assert p.status() == (moe.MOE_ERR_ROUTING, moe.MOE_DEV_BAD_INDPTR)
+
+
+def test_products_are_made_before_a_capture(moe):
+    """Made while its stream is captured, a product's clear of the status word would be replayed with every graph."""
+    import torch
+    p = moe.Product(4, 128, 128)
+    x, (w_q, w_s) = randn(0, 4, 128), p.prepare_weights(randn(1, 1, 128, 128))
+    want = p.forward(x, w_q, w_s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="captur"):
+            moe.Product(4, 128, 128)
+        y = p.forward(x, w_q, w_s)
+    for _ in range(2):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
