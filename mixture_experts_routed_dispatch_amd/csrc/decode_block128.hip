@@ -140,7 +140,7 @@ template <int kTiles, typename Row0>
 __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], __amdgpu_buffer_rsrc_t codes, const float* scales,
                                               Row0&& row0, int K, __amdgpu_buffer_rsrc_t rows, __amdgpu_buffer_rsrc_t row_scales,
                                               uint32_t ro, uint32_t so, int s0, int s1) {
-    constexpr int kDepth = kTiles == 1 ? 4 : 2;          // operand sets, all but one on their way
+    constexpr int kDepth = kTiles == 1 ? 4 : 2;          // operand sets, all but one on their way (kAhead of run_items at most)
     const int lane = threadIdx.x & 63, S = K / 128;
     uint32_t co = line_offset(K);
     ro += 16u * (lane >> 4);
@@ -202,7 +202,11 @@ __device__ __forceinline__ void run_items(const Groups* groups, Partials8<kTiles
     const int lane = threadIdx.x & 63, col = lane & 15, S = K / 128;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
-    const __amdgpu_buffer_rsrc_t rr = rows_rsrc(rows, nrows * (uint32_t)K), sr = rows_rsrc(row_scales, nrows * (uint32_t)S * 4u);
+    // The loads ahead of tile_products pass the last step by up to kAhead, at kNoRow: with their scalar offsets inside the range,
+    // they are past its end whether it counts these or not.  Lanes with a row stay within the rows.
+    constexpr uint32_t kAhead = 4;
+    const __amdgpu_buffer_rsrc_t rr = rows_rsrc(rows, nrows * (uint32_t)K + 128u * kAhead);
+    const __amdgpu_buffer_rsrc_t sr = rows_rsrc(row_scales, (nrows * (uint32_t)S + kAhead) * 4u);
     const int items = __builtin_amdgcn_readfirstlane(groups->n) * per;
     int half = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -313,9 +317,10 @@ __device__ __forceinline__ void one_row(f32x4_t (&acc)[kT], __amdgpu_buffer_rsrc
     for (int s = s0; s < s1; s += kChunk) {
         i32x4_t c[kT][kChunk][2], x[kChunk / 4];
         float f[kT][kChunk];
-        // past s1 a row's pieces belong to the next wave, or lie past the resource's end: not used
+        // past s1 a row's pieces belong to the next wave, or lie past the resource's end: not used.  (The whole offset is the
+        // lane's, which a resource's range is checked against whether it counts the scalar offset or not.)
 #pragma unroll
-        for (int h = 0; h < kChunk / 4; ++h) x[h] = load16(xr, 16u * lane, 256 * (s + 4 * h), 0);
+        for (int h = 0; h < kChunk / 4; ++h) x[h] = load16(xr, 16u * lane + 256u * (s + 4 * h), 0, 0);
 #pragma unroll
         for (int j = 0; j < kChunk; ++j)
             if (s + j < s1)
@@ -424,6 +429,7 @@ __global__ __launch_bounds__(kThreads, 2) void decode8_w2_one(DecodeArgs g) {
             for (int s = 0; s < S; s += kChunk) {
                 i32x4_t c[kChunk][2], a[kChunk / 4][4];
                 float fx[kChunk], fy[kChunk];
+                // (a load's blocks past S are another row's, or what follows a in the workspace: not used)
 #pragma unroll
                 for (int q = 0; q < kChunk / 4; ++q)
 #pragma unroll

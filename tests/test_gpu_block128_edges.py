@@ -4,7 +4,7 @@ bounds that tests/test_gpu_block128.py derives."""
 import pytest
 
 from tests.gpu_util import dev, say
-from tests.test_gpu_block128 import INF, NAN, layer_case, moe, randn, routing, starts, within  # noqa: F401
+from tests.test_gpu_block128 import INF, NAN, layer_case, moe, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,42 @@ def test_products_are_made_before_a_capture(moe):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def last_of(t):
+    """t at the end of a buffer, NaN (all bits set) right before and behind it."""
+    import torch
+    n = t.numel()
+    room = torch.full((n + 8192,), -1, dtype=torch.int16, device=dev()).view(torch.bfloat16)
+    out = room[4096:4096 + n].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("K", [128, 256, 384, 640, 1152])
+@pytest.mark.parametrize("R,E", [(1, 1), (1, 3), (2, 1), (2, 2), (3, 1), (19, 3)])
+def test_few_rows_of_few_steps(moe, R, E, K):
+    """Rows whose loads ahead, and whose last whole load, would pass their end: waves of no steps, of one, of a part of a
+    load; a segment of all rows, empty ones around it."""
+    import torch
+    from tests import block128_ref as ref
+    N = 256
+    p = moe.Product(R, N, K, E=E)
+    x = last_of(randn(R, R, K))
+    w_q, w_s = p.prepare_weights(randn(K, E, N, K, std=K ** -0.5))
+    for first in range(E):
+        m = None if E == 1 else torch.tensor([0] * (first + 1) + [R] * (E - first), dtype=torch.int32, device=dev())
+        y = p.forward(x, w_q, w_s, m_indptr=m)
+        assert within(y, ref.rows_value(x), ref.matrix(w_q, w_s)[first])
+
+
+@pytest.mark.parametrize("T,d,I,k", [(1, 128, 128, 1), (1, 384, 640, 1), (1, 640, 1152, 3), (2, 128, 128, 1), (2, 384, 128, 1)])
+def test_decode_of_few_steps(moe, T, d, I, k):
+    from tests import block128_ref as ref
+    layer, x, ids, scores, p = layer_case(moe, T, d, I, 5, k)
+    x = last_of(x)
+    y = layer.forward(x, ids, scores, p[0], p[2], p[1], p[3])
+    want = ref.layer(x, ids, scores, ref.matrix(p[0], p[1]), ref.matrix(p[2], p[3]))
+    rel = float((y.double() - want).norm() / want.norm())
+    say("  rel %.2e" % rel)
+    assert rel <= 2.5e-3
