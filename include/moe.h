@@ -32,6 +32,10 @@
  *     Routing errors found on the device (an id outside [0, E) or repeated in
  *     a row) set a sticky flag read by moe_get_status; outputs of that call are
  *     then unspecified.
+ *   - A program is built with the header of the library that it runs with.  The
+ *     structs carry no size or version and have grown at their ends (last:
+ *     moe_router_config_t by groups, top_groups and group_top, 32 to 44 bytes); a
+ *     struct of an earlier header is read past its end.
  */
 #ifndef MOE_H
 #define MOE_H

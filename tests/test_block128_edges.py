@@ -66,3 +66,26 @@ def test_tensors_of_the_layer(monkeypatch):
             with pytest.raises(ValueError, match="^" + name + ": "):
                 f(**{name: t})
     assert not called
+
+
+def test_structs_of_the_binding_are_those_of_the_header(tmp_path):
+    """The library reads structs of the header's size: the binding's have that size, field by field."""
+    import ctypes
+    import os
+    import subprocess
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    pairs = [("moe_config_t", moe.MoeConfig), ("moe_weights_t", moe.MoeWeights), ("moe_router_config_t", moe.RouterConfig),
+             ("moe_norm_config_t", moe.NormConfig), ("moe_product_config_t", moe.ProductConfig)]
+    lines = []
+    for c, py in pairs:
+        lines.append('printf("%%d\\n", (int)sizeof(%s));' % c)
+        lines += ['printf("%%d\\n", (int)offsetof(%s, %s));' % (c, f[0]) for f in py._fields_]
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include "moe.h"\nint main(void) { %s return 0; }\n' % " ".join(lines))
+    subprocess.run(["gcc", "-I", include, str(src), "-o", str(tmp_path / "sizes")], check=True)
+    out = list(map(int, subprocess.run([str(tmp_path / "sizes")], check=True, capture_output=True, text=True).stdout.split()))
+    want = []
+    for _, py in pairs:
+        want.append(ctypes.sizeof(py))
+        want += [getattr(py, f[0]).offset for f in py._fields_]
+    assert out == want and ctypes.sizeof(moe.RouterConfig) == 44
