@@ -378,7 +378,8 @@ moe_status_t moe_product_expand_weights(const moe_product_config_t* cfg, const u
 /* x, y BF16 [R, K], [R, N]; m_indptr int32 [E+1] on the device, the experts' first rows: from 0, not
  * falling, at most R (NULL with E = 1: all rows).  Rows behind m_indptr[E] are not written.  An m_indptr
  * that breaks this is caught on the device: no row is written, and MOE_DEV_BAD_INDPTR is set in *status
- * (device int32, or NULL).  All pointers but m_indptr, scales and status 16-byte aligned. */
+ * (device int32, or NULL).  All pointers but m_indptr, scales and status 16-byte aligned.
+ * Here and in the gradients, outputs overlap no input. */
 moe_status_t moe_product_forward(const moe_product_config_t* cfg, const void* x, const int32_t* m_indptr,
                                  const uint8_t* w_q, const float* w_s, void* y, int32_t* status, void* workspace,
                                  size_t workspace_bytes, void* stream);

@@ -162,3 +162,28 @@ def test_decode_of_few_steps(moe, T, d, I, k):
     rel = float((y.double() - want).norm() / want.norm())
     say("  rel %.2e" % rel)
     assert rel <= 2.5e-3
+
+
+def test_the_most_rows(moe):
+    """2^24 rows, the last of them in a segment of their own: outputs and gradients equal those of a short call."""
+    import torch
+    R, N, K, n = 1 << 24, 128, 128, 700
+    p, few = moe.Product(R, N, K, E=2, training=True), moe.Product(n, N, K, training=True)
+    q, s = p.prepare_weights(randn(0, 2, N, K, std=K ** -0.5))
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device=dev())
+    dy = torch.zeros(R, N, dtype=torch.bfloat16, device=dev())
+    x[-n:], dy[-n:] = randn(1, n, K), randn(2, n, N)
+    m = torch.tensor([0, R - n, R], dtype=torch.int32, device=dev())
+    y = p.forward(x, q, s, m_indptr=m)
+    xs, dys, qs, ss = x[-n:].clone(), dy[-n:].clone(), q[1:].clone(), s[1:].clone()
+    assert torch.equal(y[-n:], few.forward(xs, qs, ss)) and not y[:-n].any()
+    del y
+    dx, dw = p.backward(dy, x, q, s, m_indptr=m)
+    a, b = few.backward(dys, xs, qs, ss)
+    assert torch.equal(dx[-n:], a) and not dx[:-n].any()
+    # The long product adds its rows up in five pieces.  700 rows are 11 steps of 64 and those pieces: up to 16 additions on
+    # either side, each off by at most 2^-23 of the terms' magnitudes; so both may round to BF16 a step apart
+    terms = dys.double().abs().T @ xs.double().abs() * 1.13          # (values in 8 bits are up to a sixteenth larger)
+    err = (dw[1].double() - b[0].double()).abs()
+    assert (dw[0] == 0).all() and bool((err <= 2.0 ** -7 * b[0].double().abs() + 32 * 2.0 ** -23 * terms).all())
+    assert p.status() == (moe.MOE_OK, 0)
