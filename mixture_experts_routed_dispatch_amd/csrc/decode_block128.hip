@@ -12,8 +12,9 @@
 // a block of it is the work of several workgroups; a launch quantizes it; W2 and the combine follow.
 // One token: two launches, whose workgroups quantize x and a for themselves.
 //
-// d = 2048, I = 768, k = 8: one token 8.1 + 6.8 us for 25 + 13 MB, a round trip of loads each; 32 tokens of 68 experts W13
-// 39.2 us (5.5 TB/s), W2 21.2 (5.0 TB/s), the three small launches 4.6-4.8 each.  A product of one row of 4096 x 4096: 5.8 us.
+// d = 2048, I = 768, k = 8: one token 12.9 us a call in a graph for 25 + 13 MB (traced, 8 to 9.5 and 6.8), a round trip of loads
+// each; 32 tokens of 68 experts W13 39.1 us (5.5 TB/s), W2 21.2 (5.1 TB/s), the three small launches 4.7-4.8 each.  A product
+// of one row of 4096 x 4096: 5.6 us.
 #include "block128.h"
 #include "decode_common.h"
 
@@ -39,7 +40,7 @@ __device__ __forceinline__ void wave_fence() {
 
 // 16 weight rows x 128 of K as an operand, from two loads of whole lines: lane (n, q) has loaded bytes 16 q + 64 (n / 8) .. of row
 // n % 8 (r0) and of row 8 + n % 8 (r1); lanes n and n ^ 8 exchange one of them.  (Loads of 64 bytes of each of 16 rows, two of
-// which share a line: layer of 32 tokens 82 us against 69, one token in a graph 16.7 against 14.8.)
+// which share a line: layer of 32 tokens of 68 experts 81 us against 69, one token in a graph 13.4 against 12.9.)
 __device__ __forceinline__ i32x8_t join_lines(i32x4_t r0, i32x4_t r1) {
     i32x4_t a, b;
 #pragma unroll

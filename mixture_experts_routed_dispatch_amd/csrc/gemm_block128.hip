@@ -32,10 +32,10 @@
 // consecutive rows, which a quarter of a wave reads, meets all 64 banks once.  (At slot c ^ (r & 7) half of the
 // reads' cycles were conflicts.)
 //
-// Bound by the matrix unit at the clock that its power leaves (busy 52-62 % at 1.7-1.95 GHz) and by the copies and LDS reads
-// beside it.  16384 tokens of 4096 x 2048, 64 experts, k = 8: W13 2.13 ms, W2 1.18 ms, 2.07 and 1.86 PFLOP/s;
-// 65536 rows of 4096 x 4096 1.05 ms, 2.09 PFLOP/s; 8192 tokens of 2048 x 768, 16 experts: 233 and 136 us, where a tile's few
-// stages (16 and 6) leave its epilogue a larger share.
+// Bound by the matrix unit at the clock that its power leaves and by the copies and LDS reads beside it.  16384 tokens of 4096 x
+// 2048, 64 experts, k = 8: W13 2.12 ms, W2 1.19 ms, 2.08 and 1.85 PFLOP/s (matrix unit busy 54 and 48 % at 1.9 GHz);
+// 65536 rows of 4096 x 4096 1.05 to 1.09 ms, 2.0-2.1 PFLOP/s (59 % at 1.6 GHz); 8192 tokens of 2048 x 768, 16 experts: 227 and 132 us
+// (44 and 36 % at 2.0 and 2.1 GHz), where a tile's few stages (16 and 6) leave its epilogue a larger share.
 #include "block128.h"
 
 namespace moe {

@@ -384,11 +384,11 @@ __global__ __launch_bounds__(kThreads) void mx_transpose_quant_kernel(const uint
 
 // The token layout's quantization of plain rows, and (kRows) their own quantization along N in blocks of 128 from the
 // same reads.  A workgroup takes 128 rows and walks every gridDim.y-th tile of 128 columns; the other three of a CU
-// work while it loads (its own next tile's loads in flight, at 156 registers and two others: 20.2 us against 17.9).
+// work while it loads (its own next tile's loads in flight, at 156 registers and two others: an eighth slower).
 // A row's 128 values are 16 lanes' 16 bytes: its scale, and its codes, need no more.  They go into LDS as they are, the
 // 16-byte pieces of rows 32 b .. turned by 4 b, so that a thread, which quantizes two columns' 32 values of block b, four of
-// which write 128 consecutive bytes, meets no bank twice in a wave.  Memory bounds it: 8192 x 2048 both ways 17.9 us, the
-// columns alone 12.1 (rows and columns apart 13 and 14.8), 65536 x 1536 both ways 99.7, 65536 x 2048 columns 87.1, 4.6 TB/s.
+// which write 128 consecutive bytes, meets no bank twice in a wave.  Memory bounds it: 8192 x 2048 both ways 20.4 us, the
+// columns alone 12.0 (rows and columns apart 13 and 14.8), 65536 x 1536 both ways 92.5, 65536 x 2048 columns 87.4, 4.6 TB/s.
 constexpr int kRowsColumnsWgs = 2048;    // 65536 x 2048: 87 us, one tile a workgroup 99
 template <bool kRows>
 __global__ __launch_bounds__(kThreads, 4) void rows_and_columns_kernel(RowsColumnsArgs g) {
