@@ -2,8 +2,8 @@
 // (block128.hip), up to 256 rows: the expert layer's decode (T*k <= 256) and a product of few rows.
 //
 // The same quantities as on the grouped-GEMM path (gemm_block128.hip): rows in E4M3 with a scale per
-// 128, sums of 128 products by one v_mfma_f32_16x16x128_f8f6f4, times their scales added in FP32.  Here
-// the weights are the instruction's rows: a wave takes 16 weight rows x 128 of K (2 KiB) with two
+// 128, sums of 128 products by one v_mfma_f32_16x16x128_f8f6f4 (the layer's W13: by four BF16 instructions, exact), times
+// their scales added in FP32.  Here the weights are the instruction's rows: a wave takes 16 weight rows x 128 of K (2 KiB) with two
 // 16-byte loads a lane, and up to 16 rows of the batch are its columns.  Lane (n, q) of either operand
 // holds bytes 16 q .. + 15 and 64 + 16 q .. + 15 of the 128 (the instruction's order of K is free as long
 // as both agree).  The time is that of streaming the weights.
@@ -12,8 +12,8 @@
 // a block of it is the work of several workgroups; a launch quantizes it; W2 and the combine follow.
 // One token: two launches, whose workgroups quantize x and a for themselves.
 //
-// d = 2048, I = 768, k = 8: one token 12.9 us a call in a graph for 25 + 13 MB (traced, 8 to 9.5 and 6.8), a round trip of loads
-// each; 32 tokens of 68 experts W13 39.1 us (5.5 TB/s), W2 21.2 (5.1 TB/s), the three small launches 4.7-4.8 each.  A product
+// d = 2048, I = 768, k = 8: one token 13.3 us a call in a graph for 25 + 13 MB (traced, 8 to 9.5 and 6.8), a round trip of loads
+// each; 32 tokens of 68 experts W13 39.8 us (5.5 TB/s), W2 21.2 (5.1 TB/s), the three small launches 4.7-4.8 each.  A product
 // of one row of 4096 x 4096: 5.6 us.
 #include "block128.h"
 #include "decode_common.h"
@@ -29,6 +29,27 @@ __device__ __forceinline__ f32x4_t mma128(i32x8_t a, i32x8_t b) {
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
+// The same to FP32's precision: E4M3 values are BF16 numbers, and the BF16 instruction keeps their products whole (error
+// 2^-26.7 of the sums in rms, against 2^-16 of the instruction above, which drops what lies below 2^-13 of the largest of eight
+// products).  W13 takes it: of a's elements whose sums are off by 2^-16, 2^-9.3 fall on the other side of a border between
+// their E4M3 codes, and with few rows a single one can be 3e-3 of y.  The weights' loads hide most of it (one token in a
+// graph 12.9 -> 13.3 us, 32 tokens of 68 experts 68.6 -> 69.4).
+__device__ __forceinline__ bf16x8_t to_bf16(int a, int b) {
+    auto two = [](int w, auto high) { return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, decltype(high)::value)); };
+    const i32x4_t v = {two(a, std::false_type()), two(a, std::true_type()), two(b, std::false_type()), two(b, std::true_type())};
+    return __builtin_bit_cast(bf16x8_t, v);
+}
+__device__ __forceinline__ f32x4_t mma128_exact(i32x8_t a, i32x8_t b) {
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16(a[2 * i], a[2 * i + 1]), to_bf16(b[2 * i], b[2 * i + 1]), s, 0, 0, 0);
+    return s;
+}
+template <bool kExact> __device__ __forceinline__ f32x4_t mma(i32x8_t a, i32x8_t b) {
+    if constexpr (kExact) return mma128_exact(a, b);
+    else return mma128(a, b);
+}
 __device__ __forceinline__ i32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, int offset, int policy) {
     return policy ? __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, kNonTemporal))
                   : __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0));
@@ -40,7 +61,8 @@ __device__ __forceinline__ void wave_fence() {
 
 // 16 weight rows x 128 of K as an operand, from two loads of whole lines: lane (n, q) has loaded bytes 16 q + 64 (n / 8) .. of row
 // n % 8 (r0) and of row 8 + n % 8 (r1); lanes n and n ^ 8 exchange one of them.  (Loads of 64 bytes of each of 16 rows, two of
-// which share a line: layer of 32 tokens of 68 experts 81 us against 69, one token in a graph 13.4 against 12.9.)
+// which share a line: layer of 32 tokens of 68 experts 81 us against 69, one token in a graph 13.4 against 12.9, both
+// without W13's exact sums.)
 __device__ __forceinline__ i32x8_t join_lines(i32x4_t r0, i32x4_t r1) {
     i32x4_t a, b;
 #pragma unroll
@@ -137,7 +159,7 @@ template <int kTiles> struct Operands8 {
     i32x4_t c[kTiles][2], x[2];
     float xs, ws[kTiles];
 };
-template <int kTiles, typename Row0>
+template <int kTiles, bool kExact, typename Row0>
 __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], __amdgpu_buffer_rsrc_t codes, const float* scales,
                                               Row0&& row0, int K, __amdgpu_buffer_rsrc_t rows, __amdgpu_buffer_rsrc_t row_scales,
                                               uint32_t ro, uint32_t so, int s0, int s1) {
@@ -162,7 +184,7 @@ __device__ __forceinline__ void tile_products(f32x4_t (&acc)[kTiles], __amdgpu_b
         const i32x8_t x = join(w.x[0], w.x[1]);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-            const f32x4_t p = mma128(join_lines(w.c[t][0], w.c[t][1]), x);
+            const f32x4_t p = mma<kExact>(join_lines(w.c[t][0], w.c[t][1]), x);
             const float f = w.xs * w.ws[t];
 #pragma unroll
             for (int z = 0; z < 4; ++z) acc[t][z] = __builtin_fmaf(p[z], f, acc[t][z]);
@@ -196,7 +218,7 @@ __device__ __forceinline__ f32x4_t sum_waves(const f32x4_t (&p)[kWaves][kTiles][
     for (int w = 1; w < kWaves; ++w) s += p[w][t][lane];
     return s;
 }
-template <int kTiles, typename Row0, typename Row, typename Store>
+template <int kTiles, bool kExact, typename Row0, typename Row, typename Store>
 __device__ __forceinline__ void run_items(const Groups* groups, Partials8<kTiles>& part, const uint8_t* codes, const float* scales,
                                           int N, int K, int per, const uint8_t* rows, const float* row_scales, uint32_t nrows,
                                           Row0&& row0, Row&& row, Store&& store) {
@@ -216,7 +238,7 @@ __device__ __forceinline__ void run_items(const Groups* groups, Partials8<kTiles
         const int M = __builtin_amdgcn_readfirstlane(groups->g[q].z);
         const uint32_t r = col < M ? (uint32_t)row(groups->ent[first + col]) : 0u;
         f32x4_t acc[kTiles] = {};
-        tile_products<kTiles>(acc, rows_rsrc(codes + (size_t)e * N * K, (uint32_t)N * (uint32_t)K),
+        tile_products<kTiles, kExact>(acc, rows_rsrc(codes + (size_t)e * N * K, (uint32_t)N * (uint32_t)K),
                               scales + (size_t)e * (N / 128) * S, [&](int t) { return row0(blk, t); }, K, rr, sr,
                               col < M ? r * (uint32_t)K : kNoRow, col < M ? r * (uint32_t)S * 4u : kNoRow, s0, s1);
         // one barrier: the other half is written next, and read only after the next barrier
@@ -235,7 +257,7 @@ template <int kAct>
 __global__ __launch_bounds__(kThreads, kWGs) void decode8_w13(DecodeArgs g) {
     __shared__ Partials8<kTiles> part;
     const int wave = threadIdx.x >> 6, quad = (threadIdx.x & 63) >> 4, I = g.I, k = g.k;
-    run_items<kTiles>(static_cast<const Groups*>(g.groups), part, reinterpret_cast<const uint8_t*>(g.w13),
+    run_items<kTiles, true>(static_cast<const Groups*>(g.groups), part, reinterpret_cast<const uint8_t*>(g.w13),
                       reinterpret_cast<const float*>(g.w13_scale), 2 * I, g.d, I / 32, g.xq, g.xs, (uint32_t)g.T,
                       [&](int blk, int t) { return (t >> 1) * I + 32 * blk + 16 * (t & 1); },
                       [&](int entry) { return entry / k; },
@@ -254,7 +276,7 @@ __global__ __launch_bounds__(kThreads, kWGs) void decode8_w13(DecodeArgs g) {
 __global__ __launch_bounds__(kThreads, kWGs) void decode8_w2(DecodeArgs g) {
     __shared__ Partials8<kTiles> part;
     const int wave = threadIdx.x >> 6, quad = (threadIdx.x & 63) >> 4, d = g.d;
-    run_items<kTiles>(static_cast<const Groups*>(g.groups), part, reinterpret_cast<const uint8_t*>(g.w2),
+    run_items<kTiles, false>(static_cast<const Groups*>(g.groups), part, reinterpret_cast<const uint8_t*>(g.w2),
                       reinterpret_cast<const float*>(g.w2_scale), d, g.I, d / 64, g.aq, g.as, (uint32_t)(g.T * g.k),
                       [](int blk, int t) { return 64 * blk + 16 * t; }, [](int entry) { return entry; },
                       [&](int entry, int blk, const f32x4_t (&p)[kWaves][kTiles][MOE_WAVE]) {
@@ -268,7 +290,7 @@ template <int kT>
 __global__ __launch_bounds__(kThreads, kWGs) void product_rows(Block128RowsArgs g) {
     __shared__ Partials8<kT> part;
     const int wave = threadIdx.x >> 6, quad = (threadIdx.x & 63) >> 4, N = g.N;
-    run_items<kT>(static_cast<const Groups*>(g.groups), part, g.w, g.ws, N, g.K, N / (16 * kT), g.xq, g.xs, (uint32_t)g.R,
+    run_items<kT, false>(static_cast<const Groups*>(g.groups), part, g.w, g.ws, N, g.K, N / (16 * kT), g.xq, g.xs, (uint32_t)g.R,
                   [](int blk, int t) { return 16 * (kT * blk + t); }, [](int entry) { return entry; },
                   [&](int entry, int blk, const f32x4_t (&p)[kWaves][kT][MOE_WAVE]) {
         if (wave >= kT) return;
@@ -309,7 +331,7 @@ __device__ __forceinline__ float of_block(float s, int j) {
 // The row's piece is loaded before the weights, so that it is quantized while they are on their way (loads
 // come back in order).  Every column of the instruction is the row.  row0(t): tile t's first row; scale(t): the
 // scales of its squares along K.
-template <int kT, int kChunk, typename Row0, typename Scale>
+template <int kT, int kChunk, bool kExact, typename Row0, typename Scale>
 __device__ __forceinline__ void one_row(f32x4_t (&acc)[kT], __amdgpu_buffer_rsrc_t codes, Row0&& row0, Scale&& scale, int K,
                                         __amdgpu_buffer_rsrc_t xr, char* stage, int s0, int s1) {
     static_assert(kChunk % 4 == 0, "a load of the row is four blocks");
@@ -343,7 +365,7 @@ __device__ __forceinline__ void one_row(f32x4_t (&acc)[kT], __amdgpu_buffer_rsrc
                 const float sx = of_block(xs[j / 4], j & 3);
 #pragma unroll
                 for (int t = 0; t < kT; ++t) {
-                    const f32x4_t p = mma128(join_lines(c[t][j][0], c[t][j][1]), xv);
+                    const f32x4_t p = mma<kExact>(join_lines(c[t][j][0], c[t][j][1]), xv);
                     const float ff = sx * f[t][j];
 #pragma unroll
                     for (int z = 0; z < 4; ++z) acc[t][z] = __builtin_fmaf(p[z], ff, acc[t][z]);
@@ -367,7 +389,7 @@ __global__ __launch_bounds__(kThreads, 3) void decode8_w13_one(DecodeArgs g) {
     const size_t matrix = (size_t)2 * g.I * d;
     const float* ws = reinterpret_cast<const float*>(g.w13_scale) + (size_t)e * (2 * g.I / 128) * S + i0 / 128 * S;
     f32x4_t acc[2] = {};
-    one_row<2, 4>(acc, rows_rsrc(reinterpret_cast<const uint8_t*>(g.w13) + e * matrix, (uint32_t)matrix),
+    one_row<2, 4, true>(acc, rows_rsrc(reinterpret_cast<const uint8_t*>(g.w13) + e * matrix, (uint32_t)matrix),
                   [&](int t) { return t * g.I + i0; }, [&](int t) { return ws + t * (g.I / 128 * S); }, d,
                   rows_rsrc(g.x, (uint32_t)d * 2u), stage[wave], S * wave / kWaves, S * (wave + 1) / kWaves);
     const f32x4_t gate = reduce_waves<true>(acc[0], red, par), uv = reduce_waves<true>(acc[1], red, par);
@@ -388,7 +410,7 @@ __global__ __launch_bounds__(kThreads, 3) void product_one(Block128RowsArgs g) {
     const int K = g.K, S = K / 128, n0 = 16 * blockIdx.x;
     const float* ws = g.ws + n0 / 128 * S;
     f32x4_t acc[1] = {};
-    one_row<1, 8>(acc, rows_rsrc(g.w, (uint32_t)g.N * (uint32_t)K), [&](int) { return n0; }, [&](int) { return ws; }, K,
+    one_row<1, 8, false>(acc, rows_rsrc(g.w, (uint32_t)g.N * (uint32_t)K), [&](int) { return n0; }, [&](int) { return ws; }, K,
                   rows_rsrc(g.x, (uint32_t)K * 2u), stage[wave], S * wave / kWaves, S * (wave + 1) / kWaves);
     const f32x4_t v = reduce_waves<true>(acc[0], red, par);
     if (threadIdx.x < MOE_WAVE && (lane & 15) == 0)

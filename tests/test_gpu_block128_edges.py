@@ -4,7 +4,7 @@ bounds that tests/test_gpu_block128.py derives."""
 import pytest
 
 from tests.gpu_util import dev, say
-from tests.test_gpu_block128 import INF, NAN, layer_case, moe, randn, within  # noqa: F401
+from tests.test_gpu_block128 import INF, NAN, layer_case, moe, randn, routing, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -187,3 +187,36 @@ def test_the_most_rows(moe):
     err = (dw[1].double() - b[0].double()).abs()
     assert (dw[0] == 0).all() and bool((err <= 2.0 ** -7 * b[0].double().abs() + 32 * 2.0 ** -23 * terms).all())
     assert p.status() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("T,calls", [(256, 1), (24, 8), (1, 64)])
+@pytest.mark.parametrize("act", [0, 2])
+def test_decode_sums_hold_their_digits(moe, T, calls, act):
+    """The activation's output in 8 bits, seen through W2 = 1: its codes are those of the sums in 64 bits.  FP32 sums of 2048
+    terms are off by about 2^-23 of their rms; the borders between codes lie 2^-4 to 2^-3 of a value apart, so that 2^-19 of
+    the elements of that size fall on the other side, and of those down to a sixteenth of it 2^-15.  (Sums off by 2^-16 move
+    2^-9.3: 861 of 524288.)"""
+    import torch
+    from tests import block128_ref as ref
+    d, E = 2048, 4
+    layer = moe.Layer(T, d, d, E, 1, precision=moe.MOE_FP8_BLOCK128, activation=act)
+    w13_q, w13_s, _, _ = layer.prepare_weights(randn(1, E, 2 * d, d, std=d ** -0.5), randn(2, E, d, d))
+    one = torch.eye(d, device=dev()).expand(E, d, d).contiguous()
+    w2_q = one.to(torch.float8_e4m3fn).view(torch.uint8)
+    w2_s = torch.ones(E, d // 128, d // 128, device=dev())
+    w13 = ref.matrix(w13_q, w13_s)
+    moved = total = 0
+    for seed in range(calls):
+        x = randn(100 + seed, T, d)
+        ids, scores = routing(seed, T, E, 1)
+        y = layer.forward(x, ids, scores, w13_q, w2_q, w13_s, w2_s).double()
+        xv = ref.rows_value(x)
+        for e in range(E):
+            t = (ids[:, 0] == e).nonzero()[:, 0]
+            gu = xv[t] @ w13[e].T
+            want = ref.rows_value(ref.act(act, gu[:, :d]) * gu[:, d:])
+            # y rounds to BF16; a neighbouring code is a sixteenth of the value away at least
+            moved += int(((y[t] - want).abs() > 2.0 ** -6 * want.abs()).sum())
+            total += want.numel()
+    say("  %d of %d elements moved" % (moved, total))
+    assert moved <= total * 2.0 ** -15
