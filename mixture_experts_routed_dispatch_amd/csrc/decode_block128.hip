@@ -12,8 +12,8 @@
 // a block of it is the work of several workgroups; a launch quantizes it; W2 and the combine follow.
 // One token: two launches, whose workgroups quantize x and a for themselves.
 //
-// d = 2048, I = 768, k = 8: one token 13.3 us a call in a graph for 25 + 13 MB (traced, 8 to 9.5 and 6.8), a round trip of loads
-// each; 32 tokens of 68 experts W13 39.8 us (5.5 TB/s), W2 21.2 (5.1 TB/s), the three small launches 4.7-4.8 each.  A product
+// d = 2048, I = 768, k = 8: one token 13.3 us a call in a graph for 25 + 13 MB (traced, 8.1 to 9.5 and 6.3 to 6.8), a round trip of loads
+// each; 32 tokens of 68 experts W13 39.9 us (5.4 TB/s), W2 21.2 (5.1 TB/s), the three small launches 4.6-5.5 each.  A product
 // of one row of 4096 x 4096: 5.6 us.
 #include "block128.h"
 #include "decode_common.h"
